@@ -415,6 +415,155 @@ MOER_API moer_status moer_kmeans_balanced(const float* sig, int32_t N, int32_t d
 MOER_API moer_status moer_idf_fit(const moer_dims* d, const int32_t* req_cnt, int32_t R, float* idf,
                          moer_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Router operators around the statistics: scored gates with their weights
+ * and gradient, the block plan of a batch, and the experts' token lists.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of router logits. */
+typedef enum moer_dtype { MOER_F32 = 0, MOER_BF16 = 1, MOER_F16 = 2 } moer_dtype;
+
+/* How logits become scores. */
+typedef enum moer_score_fn { MOER_SCORE_SOFTMAX = 0, MOER_SCORE_SIGMOID = 1 } moer_score_fn;
+
+typedef struct moer_score_opts {
+  int32_t dtype;      /* moer_dtype of the logits (and of their gradient)               */
+  int32_t score;      /* moer_score_fn                                                  */
+  int32_t renorm;     /* 1: the k weights are divided by their sum; 0: left as they are */
+  int32_t n_group;    /* groups of E / n_group neighbouring experts: 1 .. 32, divides E  */
+  int32_t top_group;  /* groups a token may choose from: 1 .. n_group, >= k experts      */
+  int32_t group_best; /* 1 or 2: how many of a group's best choice scores rank it        */
+  float scale;        /* factor on the weights, finite                                   */
+} moer_score_opts;
+
+/* Scored top-k gate: routers that turn logits into scores, balance experts by
+ * a bias, limit a token to some expert groups and weigh the chosen experts.
+ *   No passage of the pages corresponds to these gates (the pages keep the
+ *   model's own gate, [ELDR] section "Key idea"); the ids have the layout of
+ *   moer_topk_signature's, so moer_ids_signature and what follows take them.
+ * Per layer l and token t, over the E logits x of the row:
+ *   s_e   score: softmax of the row, or 1 / (1 + exp(-x_e)); 0 for an expert
+ *         whose logit is -inf or NaN (a masked expert);
+ *   c_e   choice score: s_e + bias[l][e] (fp32) with a bias; the order of x_e
+ *         without one.  A masked expert's is -inf (NaN logit: below -inf)
+ *         whatever its bias;
+ *   groups (n_group > 1): a group's score is the best c of its experts, or
+ *         the sum of its two best (of s without a bias); the top_group best
+ *         groups stay, ties to the lower group;
+ *   topk  the k largest c among the groups that stay, in that order, ties to
+ *         the lower id, NaN below every number;
+ *   w_j   scale * s_j, or with renorm scale * s_j / (sum of the k chosen s)
+ *         (softmax: the softmax over the chosen logits).  Where every chosen
+ *         score is 0 (a row whose experts are all masked) the weights are 0.
+ * logits    row (l, t) starts at element l * ld_layer + t * ld_token; the E
+ *           logits of a row are contiguous.  ld_token >= E; L > 1: ld_layer
+ *           >= E.  [L][T][E] has ld_token = E, ld_layer = T * E; [T][L][E]
+ *           has L * E and E.  Aligned to its element.
+ * bias      [L][E] fp32 or NULL.  It moves the choice only, not the weights.
+ * topk      [L][T][k] uint8 out, 8-byte aligned.
+ * weights   [L][T][k] fp32 out or NULL.
+ * score_sum [L][E] fp32 out or NULL: sum over t of s_e (a balance loss's
+ *           mean score, times T).  Overwritten; summed in a fixed order.
+ * ws        at least moer_score_workspace_bytes(d, T) bytes, 16-byte aligned.
+ * T = 0 writes nothing but a zero score_sum. */
+MOER_API size_t moer_score_workspace_bytes(const moer_dims* d, int64_t T);
+MOER_API moer_status moer_score_topk(const moer_dims* d, const moer_score_opts* o, const void* logits, int64_t T,
+                                     int64_t ld_token, int64_t ld_layer, const float* bias, uint8_t* topk,
+                                     float* weights, float* score_sum, void* ws, size_t ws_bytes,
+                                     moer_stream_t stream);
+
+/* Gradient of moer_score_topk's weights and score sums by the logits, the
+ * choice of experts held fixed (the bias and the groups move only the
+ * choice, so neither enters; o->n_group and the like are checked, not used).
+ * logits, T, ld_token, ld_layer: as in the forward call.
+ * topk        [L][T][k] uint8: the ids that the weights belong to.  An id >= E
+ *             contributes nothing and records MOER_EDATA in ws; a repeated id
+ *             counts as given.
+ * d_weights   [L][T][k] fp32: the loss's gradient by the weights.
+ * d_score_sum [L][E] fp32 or NULL: its gradient by score_sum.
+ * d_logits    out, of the logits' type: row (l, t) at l * ldg_layer + t *
+ *             ldg_token, every one of the E elements written; computed in
+ *             fp32, rounded once.  Masked experts get 0.  May be the logits'
+ *             own buffer with the same strides: each row is read before it
+ *             is written.
+ * ws          at least 256 bytes, 16-byte aligned (the status word). */
+MOER_API moer_status moer_score_topk_grad(const moer_dims* d, const moer_score_opts* o, const void* logits, int64_t T,
+                                          int64_t ld_token, int64_t ld_layer, const uint8_t* topk,
+                                          const float* d_weights, const float* d_score_sum, void* d_logits,
+                                          int64_t ldg_token, int64_t ldg_layer, void* ws, size_t ws_bytes,
+                                          moer_stream_t stream);
+
+/* The block plan of a batch, from its requests' lengths on the GPU: what the
+ * entry points above take as host-made tables, and the KV cache's slots.
+ *   [ELDR] section "Key idea / structure / operation" and the component
+ *   table: counts per KV block, a signature cache co-indexed with the KV
+ *   cache.
+ * Request r holds ctx_len[r] tokens in the KV cache and computes new_len[r]
+ * more; position p lies in its page p / block.  The pages of the held tokens
+ * are in its block table already; the pages it newly needs, ceil((ctx + new)
+ * / block) - ceil(ctx / block), are taken from free_pages in request order
+ * and written to the table.  Its computed tokens form one KV block for each
+ * page that they touch, so a context that ends inside a page continues that
+ * page with a shorter first block.
+ * All pointers are device pointers; those marked "or NULL" are optional. */
+typedef struct moer_block_plan_args {
+  int32_t R;                /* requests, 0 .. 2^20                                        */
+  int32_t block;            /* tokens per KV block and page, 1 .. 255                     */
+  int64_t T;                /* room for computed tokens in the token maps, < 2^31         */
+  int32_t nblk;             /* room for blocks in blk_tab and insert_slot                  */
+  int32_t ncached;          /* room for cached blocks in cache_idx                         */
+  int32_t ld_pages;         /* entries of a row of the block table                         */
+  int32_t n_free;           /* entries of free_pages                                       */
+  const int32_t* new_len;   /* [R], >= 0                                                   */
+  const int32_t* ctx_len;   /* [R], >= 0, or NULL: no request holds any                    */
+  int32_t* pages;           /* [R][ld_pages] block table, in/out; NULL (with ld_pages 0)
+                               where no page ids are asked for                              */
+  const int32_t* free_pages; /* [n_free] page ids, or NULL: the table is complete already  */
+  int32_t* req_off;         /* [R+1] out: CSR of the computed tokens                       */
+  int32_t* req_blk_off;     /* [R+1] out: CSR of their blocks (moer_block_stitch)          */
+  int32_t* blk_tab;         /* [nblk][2] out: (tok0, len) of each block                    */
+  int32_t* insert_slot;     /* [nblk] out or NULL: page of a full block, else -1           */
+  int32_t* req_cache_off;   /* [R+1] out or NULL: CSR of the full held blocks              */
+  int32_t* cache_idx;       /* [ncached] out or NULL: their pages (needs req_cache_off)    */
+  int64_t* slot_map;        /* [T] out or NULL: page * block + offset of each token        */
+  int32_t* tok_req;         /* [T] out or NULL: its request                                */
+  int32_t* tok_pos;         /* [T] out or NULL: its position in the request                */
+  int32_t* totals;          /* [4] out or NULL: tokens, blocks, cached blocks, pages taken */
+} moer_block_plan_args;
+
+/* Entries past the batch's own are written too: -1 in insert_slot, cache_idx,
+ * slot_map, tok_req and tok_pos, (tokens, 0) in blk_tab.  MOER_EDATA is
+ * recorded, and what fits is written, when a length is negative (taken as 0),
+ * when the batch has more tokens, blocks or cached blocks than there is room
+ * for, when a table row is too short for a request, or when free_pages runs
+ * out (the page is then -1, and so are its slots).
+ * ws  at least moer_block_plan_workspace_bytes(R) bytes, 16-byte aligned. */
+MOER_API size_t moer_block_plan_workspace_bytes(int32_t R);
+MOER_API moer_status moer_block_plan(const moer_block_plan_args* a, void* ws, size_t ws_bytes, moer_stream_t stream);
+
+/* The experts' token lists: every layer's (token, choice) pairs in the order
+ * of their experts, the order in which an expert's rows are gathered for its
+ * products.  [GRACE] section 1 (tokens are dispatched to the experts that
+ * they chose).
+ * topk       [L][T][k] uint8, 8-byte aligned; pair p = t * k + j of a layer
+ *            chose expert topk[l][t][j].  An id >= E belongs to no expert and
+ *            records MOER_EDATA in ws.
+ * align      1 .. 1024: each expert's segment is padded to a multiple of it.
+ * expert_off [L][E+1] int32 out: segment e is [off[e], off[e+1]).
+ * order      [L][ld_order] int32 out or NULL: the pairs of each segment in
+ *            ascending order, then -1 up to the segment's end; -1 after the
+ *            last segment.
+ * ld_order   at least T * k + min(E, T * k) * (align - 1).
+ * inv        [L][T][k] int32 out or NULL: the row of each pair in `order`
+ *            (-1 for an id >= E).
+ * Limits: T * k + E * (align - 1) < 2^31.
+ * ws         at least moer_expert_order_workspace_bytes(d, T) bytes, 16-byte
+ *            aligned. */
+MOER_API size_t moer_expert_order_workspace_bytes(const moer_dims* d, int64_t T);
+MOER_API moer_status moer_expert_order(const moer_dims* d, const uint8_t* topk, int64_t T, int32_t align,
+                                       int32_t* expert_off, int32_t* order, int64_t ld_order, int32_t* inv, void* ws,
+                                       size_t ws_bytes, moer_stream_t stream);
+
 /* Waits for `stream`, then returns the status recorded in the workspace
  * (MOER_OK, MOER_EDATA or MOER_ETIMEOUT) and clears it.  `ws` is a device
  * workspace passed to earlier calls. */

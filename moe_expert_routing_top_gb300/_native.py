@@ -29,6 +29,44 @@ class moer_dims(ctypes.Structure):
                 ("block", ctypes.c_int32)]
 
 
+class moer_score_opts(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("score", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("n_group", ctypes.c_int32), ("top_group", ctypes.c_int32), ("group_best", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class moer_block_plan_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("R", "block")] + [("T", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("nblk", "ncached", "ld_pages", "n_free")] +
+                [(n, ctypes.c_void_p) for n in ("new_len", "ctx_len", "pages", "free_pages", "req_off", "req_blk_off",
+                                                "blk_tab", "insert_slot", "req_cache_off", "cache_idx", "slot_map",
+                                                "tok_req", "tok_pos", "totals")])
+
+
+DTYPES = {"f32": 0, "bf16": 1, "f16": 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def make_score_opts(dtype="f32", score="softmax", renorm=True, n_group=1, top_group=1, group_best=1,
+                    scale=1.0) -> moer_score_opts:
+    """Options of a scored gate; `dtype` and `score` by name (DTYPES, SCORES) or by number."""
+    return moer_score_opts(DTYPES.get(dtype, dtype), SCORES.get(score, score), int(renorm), n_group, top_group,
+                           group_best, scale)
+
+
+def make_block_plan(*, R, block, T=0, nblk=0, ncached=0, ld_pages=0, n_free=0, **buffers) -> moer_block_plan_args:
+    """Arguments of moer_block_plan; the buffers (tensors or addresses, by field name) are kept
+    alive on the struct."""
+    a = moer_block_plan_args(R=R, block=block, T=T, nblk=nblk, ncached=ncached, ld_pages=ld_pages, n_free=n_free)
+    names = {n for n, t in moer_block_plan_args._fields_ if t is ctypes.c_void_p}
+    for n, x in buffers.items():
+        if n not in names:
+            raise TypeError(f"moer_block_plan has no buffer {n!r}")
+        setattr(a, n, _ptr(x))
+    a._keepalive = buffers
+    return a
+
+
 def make_dims(E: int, k: int, L: int, mask, block: int = 16) -> moer_dims:
     """Builds the dims struct; the mask array is kept alive on the struct."""
     mask = [int(x) for x in mask]
@@ -46,6 +84,7 @@ def _load():
     vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                              ctypes.c_size_t)
     dp = ctypes.POINTER(moer_dims)
+    op = ctypes.POINTER(moer_score_opts)
     sigs = {
         "moer_workspace_bytes": ([dp, i64, i32, i32, i32], sz),
         "moer_topk_signature": ([dp, vp, i64, vp, i32, vp, vp, vp, vp, sz, vp], ctypes.c_int),
@@ -66,6 +105,13 @@ def _load():
         "moer_replication_plan": ([dp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
         "moer_kmeans_workspace_bytes": ([i32, i32, i32], sz),
         "moer_kmeans_balanced": ([vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+        "moer_score_workspace_bytes": ([dp, i64], sz),
+        "moer_score_topk": ([dp, op, vp, i64, i64, i64, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+        "moer_score_topk_grad": ([dp, op, vp, i64, i64, i64, vp, vp, vp, vp, i64, i64, vp, sz, vp], ctypes.c_int),
+        "moer_block_plan_workspace_bytes": ([i32], sz),
+        "moer_block_plan": ([ctypes.POINTER(moer_block_plan_args), vp, sz, vp], ctypes.c_int),
+        "moer_expert_order_workspace_bytes": ([dp, i64], sz),
+        "moer_expert_order": ([dp, vp, i64, i32, vp, vp, i64, vp, vp, sz, vp], ctypes.c_int),
         "moer_ws_status": ([vp, vp], ctypes.c_int),
         "moer_wait_selftest": ([vp, sz, ctypes.c_uint32, vp], ctypes.c_int),
         "moer_status_str": ([ctypes.c_int], ctypes.c_char_p),
@@ -89,6 +135,9 @@ EXPORTS = ("moer_workspace_bytes", "moer_topk_signature", "moer_topk_signature_n
            "moer_replication_plan", "moer_kmeans_workspace_bytes", "moer_kmeans_balanced",
            "moer_mask_select_workspace_bytes", "moer_mask_select", "moer_spectral_workspace_bytes",
            "moer_spectral_groups",
+           "moer_score_workspace_bytes", "moer_score_topk", "moer_score_topk_grad",
+           "moer_block_plan_workspace_bytes", "moer_block_plan",
+           "moer_expert_order_workspace_bytes", "moer_expert_order",
            "moer_ws_status", "moer_wait_selftest",
            "moer_status_str", "moer_version", "moer_set_extent_checks", "moer_extent_checks",
            "moer_buffer_holds")
@@ -218,6 +267,44 @@ def moer_ids_signature(dims, topk, T, blk_tab, nblk, blk_cnt, affinity, ws, ws_b
     _check("moer_ids_signature", LIB.moer_ids_signature(
         ctypes.byref(dims), _ptr(topk), int(T), _ptr(blk_tab), int(nblk), _ptr(blk_cnt), _ptr(affinity),
         _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moer_score_workspace_bytes(dims, T: int) -> int:
+    return int(LIB.moer_score_workspace_bytes(ctypes.byref(dims), int(T)))
+
+
+def moer_score_topk(dims, opts, logits, T, ld_token, ld_layer, bias, topk, weights, score_sum, ws, ws_bytes,
+                    stream=None) -> None:
+    _check("moer_score_topk", LIB.moer_score_topk(
+        ctypes.byref(dims), ctypes.byref(opts), _ptr(logits), int(T), int(ld_token), int(ld_layer), _ptr(bias),
+        _ptr(topk), _ptr(weights), _ptr(score_sum), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moer_score_topk_grad(dims, opts, logits, T, ld_token, ld_layer, topk, d_weights, d_score_sum, d_logits,
+                         ldg_token, ldg_layer, ws, ws_bytes, stream=None) -> None:
+    _check("moer_score_topk_grad", LIB.moer_score_topk_grad(
+        ctypes.byref(dims), ctypes.byref(opts), _ptr(logits), int(T), int(ld_token), int(ld_layer), _ptr(topk),
+        _ptr(d_weights), _ptr(d_score_sum), _ptr(d_logits), int(ldg_token), int(ldg_layer), _ptr(ws),
+        int(ws_bytes), _stream(stream)))
+
+
+def moer_block_plan_workspace_bytes(R: int) -> int:
+    return int(LIB.moer_block_plan_workspace_bytes(int(R)))
+
+
+def moer_block_plan(args, ws, ws_bytes, stream=None) -> None:
+    """The tables of a batch from its requests' lengths; `args` from make_block_plan."""
+    _check("moer_block_plan", LIB.moer_block_plan(ctypes.byref(args), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moer_expert_order_workspace_bytes(dims, T: int) -> int:
+    return int(LIB.moer_expert_order_workspace_bytes(ctypes.byref(dims), int(T)))
+
+
+def moer_expert_order(dims, topk, T, align, expert_off, order, ld_order, inv, ws, ws_bytes, stream=None) -> None:
+    _check("moer_expert_order", LIB.moer_expert_order(
+        ctypes.byref(dims), _ptr(topk), int(T), int(align), _ptr(expert_off), _ptr(order), int(ld_order),
+        _ptr(inv), _ptr(ws), int(ws_bytes), _stream(stream)))
 
 
 def moer_ws_status(ws, stream=None) -> int:

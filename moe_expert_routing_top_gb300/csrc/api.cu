@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "extent.h"
+#include "score.cuh"
 
 namespace moer {
 size_t spectral_workspace_bytes(int L, int E, int G);
@@ -52,6 +53,14 @@ moer_status affinity_ids_launch(const moer_dims* d, const uint8_t* ids, int64_t 
 moer_status block_counts_launch(const moer_dims* d, const uint8_t* ids, bool mask_only, int64_t T,
                                 const int32_t* blk_tab, int nblk, uint8_t* blk_cnt, uint32_t* status,
                                 cudaStream_t st, bool check);
+size_t score_scratch_bytes(const moer_dims* d, int64_t T);
+moer_status score_topk_launch(ScoreParams p, int dtype, float* score_sum, void* ws, cudaStream_t st);
+moer_status score_grad_launch(const ScoreParams& p, int dtype, cudaStream_t st);
+size_t block_plan_scratch_bytes(int32_t R);
+moer_status block_plan_launch(const moer_block_plan_args* a, void* ws, cudaStream_t st);
+size_t expert_order_scratch_bytes(const moer_dims* d, int64_t T);
+moer_status expert_order_launch(const moer_dims* d, const uint8_t* topk, int64_t T, int32_t align, int32_t* off,
+                                int32_t* order, int64_t ld, int32_t* inv, void* ws, cudaStream_t st);
 
 namespace {
 
@@ -126,6 +135,61 @@ moer_status check_dims(const moer_dims* d, bool need_mask) {
     }
   }
   return MOER_OK;
+}
+
+int elem_bytes(int dtype) { return dtype == MOER_F32 ? 4 : 2; }
+
+moer_status check_score_opts(const moer_dims* d, const moer_score_opts* o) {
+  if (o == nullptr) return MOER_EINVAL;
+  if (o->dtype < MOER_F32 || o->dtype > MOER_F16) return MOER_EINVAL;
+  if (o->score != MOER_SCORE_SOFTMAX && o->score != MOER_SCORE_SIGMOID) return MOER_EINVAL;
+  if (o->renorm != 0 && o->renorm != 1) return MOER_EINVAL;
+  if (!(o->scale - o->scale == 0.f)) return MOER_ERANGE;  // not finite
+  if (o->n_group < 1 || o->n_group > 32 || d->E % o->n_group != 0) return MOER_ERANGE;
+  if (o->top_group < 1 || o->top_group > o->n_group) return MOER_ERANGE;
+  if (o->group_best != 1 && o->group_best != 2) return MOER_ERANGE;
+  const int gs = d->E / o->n_group;
+  if (o->n_group > 1 && o->group_best > gs) return MOER_ESHAPE;
+  if (d->k > o->top_group * gs) return MOER_ESHAPE;
+  return MOER_OK;
+}
+
+// Strides of rows of E elements of `bytes` each: a row's own room, and no
+// address past 62 bits.
+moer_status check_rows(const moer_dims* d, int64_t T, int64_t ld_token, int64_t ld_layer) {
+  constexpr int64_t MOST = int64_t(1) << 46;
+  if (ld_token < d->E || ld_token > MOST) return MOER_ESHAPE;
+  if (d->L > 1 && (ld_layer < d->E || ld_layer > MOST)) return MOER_ESHAPE;
+  return T > 1 && ld_token > (int64_t(1) << 61) / T ? MOER_ESHAPE : MOER_OK;
+}
+// Elements from the first row's start to the last row's end.
+size_t rows_extent(const moer_dims* d, int64_t T, int64_t ld_token, int64_t ld_layer) {
+  return sz(T - 1) * sz(ld_token) + (d->L > 1 ? sz(d->L - 1) * sz(ld_layer) : 0) + sz(d->E);
+}
+// Every row starts on a boundary of `bytes`.
+bool rows_aligned(const moer_dims* d, const void* p, int64_t ld_token, int64_t ld_layer, int elem, size_t bytes) {
+  return aligned(p, bytes) && (ld_token * elem) % (int64_t)bytes == 0 &&
+         (d->L == 1 || (ld_layer * elem) % (int64_t)bytes == 0);
+}
+
+ScoreParams score_params(const moer_dims* d, const moer_score_opts* o, const void* logits, int64_t T,
+                         int64_t ld_token, int64_t ld_layer) {
+  ScoreParams p = {};
+  p.logits = logits;
+  p.T = T;
+  p.ld_token = ld_token;
+  p.ld_layer = d->L > 1 ? ld_layer : 0;
+  p.E = d->E;
+  p.k = d->k;
+  p.L = d->L;
+  p.score = o->score;
+  p.renorm = o->renorm;
+  // with every group kept the groups change nothing
+  p.n_group = o->top_group < o->n_group ? o->n_group : 1;
+  p.top_group = o->top_group < o->n_group ? o->top_group : 1;
+  p.group_best = o->group_best;
+  p.scale = o->scale;
+  return p;
 }
 
 // Extents of the logits-pass buffers (moer_topk_signature and its no-alloc form).
@@ -520,6 +584,174 @@ moer_status moer_kmeans_balanced(const float* sig, int32_t N, int32_t dim, int32
                        reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t moer_score_workspace_bytes(const moer_dims* d, int64_t T) {
+  if (d == nullptr || d->L < 1 || d->E < 1 || T < 1 || T >= (int64_t(1) << 31)) return WS_HEADER;
+  return WS_HEADER + moer::score_scratch_bytes(d, T);
+}
+
+moer_status moer_score_topk(const moer_dims* d, const moer_score_opts* o, const void* logits, int64_t T,
+                            int64_t ld_token, int64_t ld_layer, const float* bias, uint8_t* topk, float* weights,
+                            float* score_sum, void* ws, size_t ws_bytes, moer_stream_t stream) {
+  moer_status s = check_dims(d, false);
+  if (s != MOER_OK) return s;
+  s = check_score_opts(d, o);
+  if (s != MOER_OK) return s;
+  if (T < 0 || T >= (int64_t(1) << 31)) return MOER_ERANGE;
+  if (score_sum != nullptr && !aligned(score_sum, 4)) return MOER_EINVAL;
+  const int eb = elem_bytes(o->dtype);
+  if (T > 0) {
+    if (logits == nullptr || topk == nullptr) return MOER_EINVAL;
+    if (!aligned(logits, eb) || !aligned(topk, 8)) return MOER_EINVAL;
+    if ((bias != nullptr && !aligned(bias, 4)) || (weights != nullptr && !aligned(weights, 4))) return MOER_EINVAL;
+    s = check_rows(d, T, ld_token, ld_layer);
+    if (s != MOER_OK) return s;
+    if (ws == nullptr || !aligned(ws, 16)) return MOER_EINVAL;
+    if (ws_bytes < moer_score_workspace_bytes(d, T)) return MOER_ENOMEM;
+  }
+  {
+    const size_t L = sz(d->L), E = sz(d->E), n = L * sz(T) * sz(d->k);
+    s = T > 0 ? check_extents({{logits, rows_extent(d, T, ld_token, ld_layer) * eb},
+                               {bias, L * E * 4},
+                               {topk, n},
+                               {weights, n * 4},
+                               {score_sum, L * E * 4},
+                               {ws, ws_bytes}})
+              : check_extents({{score_sum, L * E * 4}});
+    if (s != MOER_OK) return s;
+  }
+  ScoreParams p = score_params(d, o, logits, T, ld_token, ld_layer);
+  p.vec = rows_aligned(d, logits, ld_token, ld_layer, eb, 4 * eb);
+  p.bias = bias;
+  p.topk = topk;
+  p.weights = weights;
+  p.status = static_cast<uint32_t*>(ws);
+  return moer::score_topk_launch(p, o->dtype, score_sum, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moer_status moer_score_topk_grad(const moer_dims* d, const moer_score_opts* o, const void* logits, int64_t T,
+                                 int64_t ld_token, int64_t ld_layer, const uint8_t* topk, const float* d_weights,
+                                 const float* d_score_sum, void* d_logits, int64_t ldg_token, int64_t ldg_layer,
+                                 void* ws, size_t ws_bytes, moer_stream_t stream) {
+  moer_status s = check_dims(d, false);
+  if (s != MOER_OK) return s;
+  s = check_score_opts(d, o);
+  if (s != MOER_OK) return s;
+  if (T < 0 || T >= (int64_t(1) << 31)) return MOER_ERANGE;
+  if (T == 0) return MOER_OK;
+  const int eb = elem_bytes(o->dtype);
+  if (logits == nullptr || topk == nullptr || d_weights == nullptr || d_logits == nullptr) return MOER_EINVAL;
+  if (!aligned(logits, eb) || !aligned(d_logits, eb) || !aligned(topk, 8) || !aligned(d_weights, 4) ||
+      (d_score_sum != nullptr && !aligned(d_score_sum, 4)))
+    return MOER_EINVAL;
+  s = check_rows(d, T, ld_token, ld_layer);
+  if (s == MOER_OK) s = check_rows(d, T, ldg_token, ldg_layer);
+  if (s != MOER_OK) return s;
+  if (ws == nullptr || !aligned(ws, 16)) return MOER_EINVAL;
+  if (ws_bytes < WS_HEADER) return MOER_ENOMEM;
+  {
+    const size_t L = sz(d->L), E = sz(d->E), n = L * sz(T) * sz(d->k);
+    s = check_extents({{logits, rows_extent(d, T, ld_token, ld_layer) * eb},
+                       {topk, n},
+                       {d_weights, n * 4},
+                       {d_score_sum, L * E * 4},
+                       {d_logits, rows_extent(d, T, ldg_token, ldg_layer) * eb},
+                       {ws, ws_bytes}});
+    if (s != MOER_OK) return s;
+  }
+  ScoreParams p = score_params(d, o, logits, T, ld_token, ld_layer);
+  p.vec = rows_aligned(d, logits, ld_token, ld_layer, eb, 4 * eb) &&
+          rows_aligned(d, d_logits, ldg_token, ldg_layer, eb, 4 * eb);
+  p.ids = topk;
+  p.d_weights = d_weights;
+  p.d_score_sum = d_score_sum;
+  p.d_logits = d_logits;
+  p.ldg_token = ldg_token;
+  p.ldg_layer = d->L > 1 ? ldg_layer : 0;
+  p.status = static_cast<uint32_t*>(ws);
+  return moer::score_grad_launch(p, o->dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moer_block_plan_workspace_bytes(int32_t R) {
+  return WS_HEADER + (R > 0 ? moer::block_plan_scratch_bytes(R) : 4);
+}
+
+moer_status moer_block_plan(const moer_block_plan_args* a, void* ws, size_t ws_bytes, moer_stream_t stream) {
+  if (a == nullptr) return MOER_EINVAL;
+  if (a->R < 0 || a->R > (1 << 20) || a->block < 1 || a->block > 255) return MOER_ERANGE;
+  if (a->T < 0 || a->T >= (int64_t(1) << 31) || a->nblk < 0 || a->ncached < 0 || a->ld_pages < 0 || a->n_free < 0)
+    return MOER_ERANGE;
+  if (a->req_off == nullptr || a->req_blk_off == nullptr) return MOER_EINVAL;
+  if (a->R > 0 && a->new_len == nullptr) return MOER_EINVAL;
+  if (a->R > 0 && a->pages == nullptr &&
+      (a->ld_pages > 0 || a->free_pages != nullptr || a->insert_slot != nullptr || a->cache_idx != nullptr ||
+       a->slot_map != nullptr))
+    return MOER_EINVAL;
+  if (a->nblk > 0 && a->blk_tab == nullptr) return MOER_EINVAL;
+  if (a->cache_idx != nullptr && a->req_cache_off == nullptr) return MOER_EINVAL;
+  if (a->n_free > 0 && a->free_pages == nullptr) return MOER_EINVAL;
+  const void* const words[] = {a->new_len, a->ctx_len, a->pages, a->free_pages, a->req_off, a->req_blk_off,
+                               a->blk_tab, a->insert_slot, a->req_cache_off, a->cache_idx, a->tok_req, a->tok_pos,
+                               a->totals};
+  for (const void* w : words)
+    if (!aligned(w, 4)) return MOER_EINVAL;
+  if (!aligned(a->slot_map, 8)) return MOER_EINVAL;
+  if (ws == nullptr || !aligned(ws, 16)) return MOER_EINVAL;
+  if (ws_bytes < moer_block_plan_workspace_bytes(a->R)) return MOER_ENOMEM;
+  {
+    const size_t r = sz(a->R), t = sz(a->T), nb = sz(a->nblk);
+    const moer_status s = check_extents({{a->new_len, r * 4},
+                                         {a->ctx_len, r * 4},
+                                         {a->pages, r * sz(a->ld_pages) * 4},
+                                         {a->free_pages, sz(a->n_free) * 4},
+                                         {a->req_off, (r + 1) * 4},
+                                         {a->req_blk_off, (r + 1) * 4},
+                                         {a->blk_tab, nb * 8},
+                                         {a->insert_slot, nb * 4},
+                                         {a->req_cache_off, (r + 1) * 4},
+                                         {a->cache_idx, sz(a->ncached) * 4},
+                                         {a->slot_map, t * 8},
+                                         {a->tok_req, t * 4},
+                                         {a->tok_pos, t * 4},
+                                         {a->totals, 4 * 4},
+                                         {ws, ws_bytes}});
+    if (s != MOER_OK) return s;
+  }
+  return moer::block_plan_launch(a, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moer_expert_order_workspace_bytes(const moer_dims* d, int64_t T) {
+  if (d == nullptr || d->L < 1 || d->E < 1 || d->k < 1 || T < 1 || T >= (int64_t(1) << 31)) return WS_HEADER;
+  return WS_HEADER + moer::expert_order_scratch_bytes(d, T);
+}
+
+moer_status moer_expert_order(const moer_dims* d, const uint8_t* topk, int64_t T, int32_t align, int32_t* expert_off,
+                              int32_t* order, int64_t ld_order, int32_t* inv, void* ws, size_t ws_bytes,
+                              moer_stream_t stream) {
+  moer_status s = check_dims(d, false);
+  if (s != MOER_OK) return s;
+  if (T < 0 || T >= (int64_t(1) << 31) || align < 1 || align > 1024) return MOER_ERANGE;
+  const int64_t N = T * d->k;
+  if (N + (int64_t)d->E * (align - 1) >= (int64_t(1) << 31)) return MOER_ERANGE;
+  if (expert_off == nullptr || !aligned(expert_off, 4)) return MOER_EINVAL;
+  if (T > 0 && (topk == nullptr || !aligned(topk, 8))) return MOER_EINVAL;
+  if ((order != nullptr && !aligned(order, 4)) || (inv != nullptr && !aligned(inv, 4))) return MOER_EINVAL;
+  if (order != nullptr && (ld_order < N + min64(d->E, N) * (align - 1) || ld_order > (int64_t(1) << 40)))
+    return MOER_ESHAPE;
+  if (ws == nullptr || !aligned(ws, 16)) return MOER_EINVAL;
+  if (ws_bytes < moer_expert_order_workspace_bytes(d, T)) return MOER_ENOMEM;
+  {
+    const size_t L = sz(d->L), n = sz(N);
+    s = check_extents({{topk, L * n},
+                       {expert_off, L * (sz(d->E) + 1) * 4},
+                       {order, L * sz(order != nullptr ? ld_order : 0) * 4},
+                       {inv, L * n * 4},
+                       {ws, ws_bytes}});
+    if (s != MOER_OK) return s;
+  }
+  return moer::expert_order_launch(d, topk, T, align, expert_off, order, ld_order, inv, ws,
+                                   reinterpret_cast<cudaStream_t>(stream));
+}
+
 moer_status moer_wait_selftest(void* ws, size_t ws_bytes, uint32_t limit_us, moer_stream_t stream) {
   if (ws == nullptr || !aligned(ws, 16)) return MOER_EINVAL;
   if (ws_bytes < WS_HEADER) return MOER_ENOMEM;
@@ -562,7 +794,7 @@ const char* moer_status_str(moer_status s) {
   return "unknown status";
 }
 
-int32_t moer_version(void) { return 100; }
+int32_t moer_version(void) { return 200; }
 
 void moer_set_extent_checks(int32_t on) { g_extent_checks.store(on ? 1 : 0, std::memory_order_release); }
 

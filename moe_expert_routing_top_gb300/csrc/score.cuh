@@ -1,0 +1,139 @@
+// score.cuh -- the scores of moer_score_topk and its gradient: logit types,
+// the score functions and the parameters that their kernels share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "rank.cuh"
+
+namespace moer {
+
+struct ScoreParams {
+  const void* logits;
+  int64_t T, ld_token, ld_layer;  // strides in elements
+  int E, k, L;
+  int score, renorm, n_group, top_group, group_best;
+  float scale;
+  int vec;             // 1: every row of logits (and gradients) takes 4-element vector access
+  const float* bias;   // [L][E] or NULL
+  uint8_t* topk;       // out [L][T][k]
+  float* weights;      // out [L][T][k] or NULL
+  float* partial;      // [units][E] score sums of each unit, or NULL
+  int span, nspan;     // tokens of a unit, units of a layer
+  // gradient
+  const uint8_t* ids;        // [L][T][k]
+  const float* d_weights;    // [L][T][k]
+  const float* d_score_sum;  // [L][E] or NULL
+  void* d_logits;
+  int64_t ldg_token, ldg_layer;
+  uint32_t* status;
+};
+
+constexpr float NEG_INF = -__builtin_huge_valf();
+
+// ------------------------------------------------------- four logits at once
+// Logits are held as fp32 whatever their type (an exact conversion); a
+// gradient is rounded once, to nearest even, when it is stored.
+template <typename X>
+struct Quad;
+template <>
+struct Quad<float> {
+  using V = float4;
+  __device__ static void get(const V& v, float (&x)[4]) { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
+  __device__ static V put(const float (&x)[4]) { return make_float4(x[0], x[1], x[2], x[3]); }
+  __device__ static float one(float v) { return v; }
+  __device__ static float back(float v) { return v; }
+};
+template <>
+struct Quad<__nv_bfloat16> {
+  using V = uint2;
+  __device__ static void get(const V& v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  }
+  __device__ static V put(const float (&x)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+  __device__ static float one(__nv_bfloat16 v) { return __bfloat162float(v); }
+  __device__ static __nv_bfloat16 back(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Quad<__half> {
+  using V = uint2;
+  __device__ static void get(const V& v, float (&x)[4]) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+  }
+  __device__ static V put(const float (&x)[4]) {
+    const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+  __device__ static float one(__half v) { return __half2float(v); }
+  __device__ static __half back(float v) { return __float2half_rn(v); }
+};
+
+template <typename X>
+__device__ __forceinline__ void load4(const X* p, bool vec, float (&x)[4]) {
+  if (vec) {
+    Quad<X>::get(*reinterpret_cast<const typename Quad<X>::V*>(p), x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = Quad<X>::one(p[j]);
+  }
+}
+template <typename X>
+__device__ __forceinline__ void store4(X* p, bool vec, const float (&x)[4]) {
+  if (vec) {
+    *reinterpret_cast<typename Quad<X>::V*>(p) = Quad<X>::put(x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = Quad<X>::back(x[j]);
+  }
+}
+
+// ------------------------------------------------------------------ scores
+__device__ __forceinline__ float rcp_approx(float x) {  // within 1 ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// A logit that counts: -inf for a masked expert, NaN included.
+__device__ __forceinline__ float live_logit(float x) { return x == x ? x : NEG_INF; }
+// 1 / (1 + exp(-x)): 0 at -inf, 1 at +inf; below x = -87 the result is under
+// the smallest normal number and is 0.
+__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + expf(-x)); }
+// s (1 - s) without the cancellation of 1 - s: t / (1 + t)^2, t = exp(-|x|).
+__device__ __forceinline__ float sigmoid_slope(float x) {
+  const float t = expf(-fabsf(x)), r = rcp_approx(1.f + t);
+  return t * r * r;
+}
+// exp(x - m) for x <= m, where m is the largest of a set: equal infinities
+// give 1 (they share the weight), and a set without any expert gives 0.
+__device__ __forceinline__ float exp_below(float x, float m) {
+  if (x == NEG_INF) return 0.f;
+  return x == m ? 1.f : expf(x - m);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
+  return v;
+}
+
+// Inverse of rank_key for keys of numbers (NaN's key 1 gives -inf: it adds
+// nothing to a group).
+__device__ __forceinline__ float rank_value(uint32_t key) {
+  if (key <= 1u) return NEG_INF;
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
+}
+
+}  // namespace moer
