@@ -621,6 +621,7 @@ moer_status moer_score_topk(const moer_dims* d, const moer_score_opts* o, const 
   }
   ScoreParams p = score_params(d, o, logits, T, ld_token, ld_layer);
   p.vec = rows_aligned(d, logits, ld_token, ld_layer, eb, 4 * eb);
+  p.wide = rows_aligned(d, logits, ld_token, ld_layer, eb, 16);
   p.bias = bias;
   p.topk = topk;
   p.weights = weights;

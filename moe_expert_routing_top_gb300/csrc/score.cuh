@@ -22,6 +22,10 @@ struct ScoreParams {
   float* weights;      // out [L][T][k] or NULL
   float* partial;      // [units][E] score sums of each unit, or NULL
   int span, nspan;     // tokens of a unit, units of a layer
+  int wide;            // 1: rows take 16-byte access (the fast kernel's blocks of 8 logits)
+  // 2^8, known at run time only, so that a key's shift-and-insert stays one
+  // multiply-add (FMA pipe) and off the integer ALU pipe that the networks fill
+  uint32_t key_mul;
   // gradient
   const uint8_t* ids;        // [L][T][k]
   const float* d_weights;    // [L][T][k]

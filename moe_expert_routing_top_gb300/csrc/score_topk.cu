@@ -10,155 +10,34 @@
 // unit order, so the result does not depend on the schedule.
 #include "pdl.cuh"
 #include "score.cuh"
+#include "score_row.cuh"
 
 namespace moer {
+
+cudaError_t score_fast_f32(const ScoreParams& p, cudaStream_t st);
+cudaError_t score_fast_bf16(const ScoreParams& p, cudaStream_t st);
+cudaError_t score_fast_f16(const ScoreParams& p, cudaStream_t st);
 
 namespace {
 constexpr int SC_WARPS = 8;
 constexpr int SC_UNITS = 4864;  // units asked for: 152 SMs x 32
 
-int score_span(int64_t T, int L) {
+constexpr int64_t SC_FAST_ROWS = 4096;  // rows from which the fast kernel is taken
+
+// Tokens of a unit: a multiple of `step`, the rows that a block takes at a time.
+int score_span(int64_t T, int L, int step) {
   const int64_t s = (T * L + SC_UNITS - 1) / SC_UNITS;
-  return (int)((s + SC_WARPS - 1) / SC_WARPS * SC_WARPS);
+  return (int)((s + step - 1) / step * step);
 }
-int score_nspan(int64_t T, int L) {
-  const int s = score_span(T, L);
-  return (int)((T + s - 1) / s);
-}
+int score_nspan(int64_t T, int span) { return (int)((T + span - 1) / span); }
 
-// Best and second-best choice key of each group; lane g returns group g's key.
-template <int NQ>
-__device__ uint32_t group_keys(const ScoreParams& p, const uint32_t (&key)[4 * NQ], int lane) {
-  const int gs = p.E / p.n_group;
-  uint32_t mine = 0u;
-  for (int g = 0; g < p.n_group; ++g) {
-    uint32_t a = 0u, b = 0u;  // the lane's two best keys within the group
-#pragma unroll
-    for (int i = 0; i < 4 * NQ; ++i) {
-      const int e = 4 * (lane + 32 * (i / 4)) + i % 4;
-      if (e / gs == g) {
-        const uint32_t x = key[i];
-        b = max(b, min(a, x));
-        a = max(a, x);
-      }
-    }
-    uint32_t gk = __reduce_max_sync(FULL, a);
-    if (p.group_best == 2) {
-      const int w = __ffs(__ballot_sync(FULL, a == gk)) - 1;  // one instance of the best is used up
-      const uint32_t second = __reduce_max_sync(FULL, lane == w ? b : a);
-      const float sum = rank_value(gk) + rank_value(second);
-      gk = rank_key(sum == sum ? sum : NEG_INF);
-    }
-    if (lane == g) mine = gk;
-  }
-  return mine;
-}
-
-template <typename X, int NQ>
-__device__ void score_row(const ScoreParams& p, const X* row, const float (&bias)[4 * NQ], int64_t out, int lane,
-                          float (&sum)[4 * NQ]) {
-  const bool soft = p.score == MOER_SCORE_SOFTMAX;
-  const bool use_s = p.bias != nullptr || (p.n_group > 1 && p.group_best == 2);  // the choice takes scores
-  const bool dense = p.partial != nullptr || use_s || (soft && !p.renorm);
-  float x[4 * NQ], s[4 * NQ];
-  uint32_t key[4 * NQ];
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    const int e = 4 * (lane + 32 * q);
-    float v[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
-    if (e < p.E) load4<X>(row + e, p.vec != 0, v);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      key[4 * q + j] = e < p.E ? rank_key(v[j]) : 0u;  // of the logit itself
-      x[4 * q + j] = live_logit(v[j]);
-      s[4 * q + j] = 0.f;
-    }
-  }
-  if (dense) {
-    if (soft) {
-      float m = NEG_INF;
-#pragma unroll
-      for (int i = 0; i < 4 * NQ; ++i) m = fmaxf(m, x[i]);
-      m = warp_max(m);
-      float z = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4 * NQ; ++i) {
-        s[i] = exp_below(x[i], m);
-        z += s[i];
-      }
-      z = warp_sum(z);
-      const float r = z > 0.f ? 1.f / z : 0.f;
-#pragma unroll
-      for (int i = 0; i < 4 * NQ; ++i) s[i] *= r;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4 * NQ; ++i) s[i] = sigmoid(x[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4 * NQ; ++i) sum[i] += s[i];
-  }
-  uint32_t ck[4 * NQ];  // keys of the choice scores where those are scores; masked experts keep their logit's key
-#pragma unroll
-  for (int i = 0; i < 4 * NQ; ++i) {
-    ck[i] = key[i];
-    if (use_s && x[i] != NEG_INF) ck[i] = rank_key(s[i] + bias[i]);
-    if (p.bias != nullptr) key[i] = ck[i];
-  }
-  if (p.n_group > 1) {
-    uint32_t gk = group_keys<NQ>(p, ck, lane);
-    unsigned keep = 0u;
-    for (int r = 0; r < p.top_group; ++r) {
-      const uint32_t best = __reduce_max_sync(FULL, gk);
-      const int w = __ffs(__ballot_sync(FULL, gk == best && !((keep >> lane) & 1u) && lane < p.n_group)) - 1;
-      keep |= 1u << w;
-      if (lane == w) gk = 0u;
-    }
-    const int gs = p.E / p.n_group;
-#pragma unroll
-    for (int i = 0; i < 4 * NQ; ++i) {
-      const int e = 4 * (lane + 32 * (i / 4)) + i % 4;
-      if (e < p.E && !((keep >> (e / gs)) & 1u)) key[i] = 0u;
-    }
-  }
-  // lane r holds the r-th choice: its id and its logit or score
-  const bool by_logit = soft && p.renorm;
-  int id = 0;
-  float val = by_logit ? NEG_INF : 0.f;
-  for (int r = 0; r < p.k; ++r) {
-    uint32_t best = 0u;
-    int be = 0xFFFF;
-    float bv = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4 * NQ; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        be = 4 * (lane + 32 * (i / 4)) + i % 4;
-        bv = by_logit ? x[i] : (dense ? s[i] : x[i]);
-      }
-    const uint32_t top = __reduce_max_sync(FULL, best);
-    const int e = (int)__reduce_min_sync(FULL, best == top ? (unsigned)be : 0xFFFFu);
-    const float v = __shfl_sync(FULL, bv, (e / 4) & 31);
-    if (lane == r) id = e, val = v;
-#pragma unroll
-    for (int i = 0; i < 4 * NQ; ++i)
-      if (e == 4 * (lane + 32 * (i / 4)) + i % 4) key[i] = 0u;
-  }
-  if (lane < p.k) p.topk[out * p.k + lane] = (uint8_t)id;
-  if (p.weights != nullptr) {
-    float w;
-    if (by_logit) {
-      const float v = lane < p.k ? val : NEG_INF;
-      const float m = warp_max(v);
-      w = exp_below(v, m);
-    } else {
-      w = lane < p.k ? (dense ? val : sigmoid(val)) : 0.f;
-    }
-    if (p.renorm) {
-      const float z = warp_sum(w);
-      w = z > 0.f ? w / z : 0.f;
-    }
-    if (lane < p.k) p.weights[out * p.k + lane] = p.scale * w;
-  }
+// The fast kernel's options (score_fast.cuh): k <= 8, aligned quads, and groups,
+// where there are any, that are a power of two of blocks on every lane of a row.
+bool fast_supported(const ScoreParams& p) {
+  if (p.k > 8 || p.vec == 0 || p.E < 16 || p.L * p.T < SC_FAST_ROWS) return false;
+  if (p.n_group == 1) return true;
+  const int lanes = p.E <= 64 ? 1 : p.E <= 128 ? 2 : 4, gs = p.E / p.n_group, mb = gs / (8 * lanes);
+  return gs % (8 * lanes) == 0 && (mb & (mb - 1)) == 0 && p.n_group <= 8;
 }
 
 template <typename X, int NQ>
@@ -219,8 +98,9 @@ cudaError_t score_run(const ScoreParams& p, cudaStream_t st) {
 }
 }  // namespace
 
+// The general kernel's units are the more numerous.
 size_t score_scratch_bytes(const moer_dims* d, int64_t T) {
-  return (size_t)d->L * (size_t)score_nspan(T, d->L) * (size_t)d->E * 4;
+  return (size_t)d->L * (size_t)score_nspan(T, score_span(T, d->L, SC_WARPS)) * (size_t)d->E * 4;
 }
 
 moer_status score_topk_launch(ScoreParams p, int dtype, float* score_sum, void* ws, cudaStream_t st) {
@@ -229,12 +109,18 @@ moer_status score_topk_launch(ScoreParams p, int dtype, float* score_sum, void* 
                    cudaMemsetAsync(score_sum, 0, (size_t)p.L * p.E * sizeof(float), st) == cudaSuccess
                ? MOER_OK
                : MOER_ECUDA;
-  p.span = score_span(p.T, p.L);
-  p.nspan = score_nspan(p.T, p.L);
+  const bool fast = fast_supported(p);
+  p.span = score_span(p.T, p.L, !fast ? SC_WARPS : p.E <= 64 ? 128 : p.E <= 128 ? 64 : 32);
+  p.nspan = score_nspan(p.T, p.span);
   p.partial = score_sum != nullptr ? reinterpret_cast<float*>(static_cast<char*>(ws) + WS_HEADER) : nullptr;
-  cudaError_t e = dtype == MOER_F32    ? score_run<float>(p, st)
-                  : dtype == MOER_BF16 ? score_run<__nv_bfloat16>(p, st)
-                                       : score_run<__half>(p, st);
+  p.key_mul = 256u;
+  cudaError_t e;
+  if (fast)
+    e = dtype == MOER_F32 ? score_fast_f32(p, st) : dtype == MOER_BF16 ? score_fast_bf16(p, st) : score_fast_f16(p, st);
+  else
+    e = dtype == MOER_F32    ? score_run<float>(p, st)
+        : dtype == MOER_BF16 ? score_run<__nv_bfloat16>(p, st)
+                             : score_run<__half>(p, st);
   if (e == cudaSuccess && score_sum != nullptr)
     e = launch_pdl(score_sum_kernel, dim3((p.E + 31) / 32, p.L), dim3(256), 0, st, (const float*)p.partial, p.nspan,
                    p.E, score_sum);

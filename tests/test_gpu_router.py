@@ -217,6 +217,61 @@ def test_many_rows_against_the_logits_pass(env):
         assert (np.abs(ss - p) <= 1e-5 * p).all()
 
 
+# Sizes at which the throughput kernel runs (4,096 rows and more), with a ragged last tile
+@pytest.mark.parametrize("E,k", [(16, 3), (24, 8), (32, 8), (60, 5), (64, 6), (72, 4), (96, 8), (128, 8), (128, 1), (160, 7), (192, 8),
+                                 (256, 8), (256, 2)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+def test_throughput_sizes(env, E, k, dtype, score, renorm):
+    torch, _ = env
+    rs = np.random.RandomState(E + k)
+    dev, x = _logits(torch, rs, 2, 2051, E, dtype)
+    for biased in (False, True):
+        bias = rs.normal(0, 0.05, size=(2, E)) if biased else None
+        o = dict(score=score, renorm=renorm, scale=2.5)
+        _check_forward(_forward(env, dev, E, k, dtype, bias=bias, **o), x, k, bias=bias, **o)
+
+
+@pytest.mark.parametrize("E,k,n,keep", [(256, 8, 8, 4), (128, 8, 8, 3), (128, 6, 4, 2), (64, 4, 8, 2), (64, 6, 2, 1), (256, 8, 4, 3), (160, 4, 5, 2),
+                                        (32, 2, 4, 1)])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_throughput_groups(env, E, k, n, keep, best, score, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E + n)
+    dev, x = _logits(torch, rs, 1, 4100, E, dtype)
+    for biased in (False, True):
+        bias = rs.normal(0, 0.05, size=(1, E)) if biased else None
+        o = dict(score=score, renorm=True, n_group=n, top_group=keep, best=best)
+        _check_forward(_forward(env, dev, E, k, dtype, bias=bias, sums=biased, **o), x, k, bias=bias, **o)
+
+
+@pytest.mark.parametrize("special", ["masks", "ties", "inf", "lowest"])
+@pytest.mark.parametrize("E,k,n", [(64, 6, 1), (128, 8, 8), (256, 8, 8), (60, 5, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_throughput_special_values(env, special, E, k, n, score, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E + k + 1)
+    dev, x = _logits(torch, rs, 2, 2100, E, dtype, special=special)
+    for biased in (False, True):
+        bias = rs.normal(0, 0.5, size=(2, E)) if biased else None
+        o = dict(score=score, renorm=biased, n_group=n, top_group=max(1, n // 2), best=1 + (biased and n > 1))
+        _check_forward(_forward(env, dev, E, k, dtype, bias=bias, **o), x, k, bias=bias, **o)
+
+
+@pytest.mark.parametrize("layout", ["token", "odd"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_throughput_layouts(env, layout, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(12)
+    for E, k in ((64, 6), (100, 7), (256, 8)):
+        dev, x = _logits(torch, rs, 3, 1500, E, dtype, layout=layout)
+        bias = rs.normal(0, 0.05, size=(3, E))
+        _check_forward(_forward(env, dev, E, k, dtype, bias=bias, score="sigmoid"), x, k, bias=bias, score="sigmoid")
+
+
 def test_same_bits_twice_and_on_another_stream(env):
     torch, _ = env
     rs = np.random.RandomState(11)
