@@ -55,7 +55,7 @@ moer_status block_counts_launch(const moer_dims* d, const uint8_t* ids, bool mas
                                 cudaStream_t st, bool check);
 size_t score_scratch_bytes(const moer_dims* d, int64_t T);
 moer_status score_topk_launch(ScoreParams p, int dtype, float* score_sum, void* ws, cudaStream_t st);
-moer_status score_grad_launch(const ScoreParams& p, int dtype, cudaStream_t st);
+moer_status score_grad_launch(ScoreParams p, int dtype, cudaStream_t st);
 size_t block_plan_scratch_bytes(int32_t R);
 moer_status block_plan_launch(const moer_block_plan_args* a, void* ws, cudaStream_t st);
 size_t expert_order_scratch_bytes(const moer_dims* d, int64_t T);
@@ -662,6 +662,8 @@ moer_status moer_score_topk_grad(const moer_dims* d, const moer_score_opts* o, c
   ScoreParams p = score_params(d, o, logits, T, ld_token, ld_layer);
   p.vec = rows_aligned(d, logits, ld_token, ld_layer, eb, 4 * eb) &&
           rows_aligned(d, d_logits, ldg_token, ldg_layer, eb, 4 * eb);
+  p.wide = rows_aligned(d, logits, ld_token, ld_layer, eb, 16) &&
+           rows_aligned(d, d_logits, ldg_token, ldg_layer, eb, 16);
   p.ids = topk;
   p.d_weights = d_weights;
   p.d_score_sum = d_score_sum;

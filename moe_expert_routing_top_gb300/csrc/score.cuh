@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "rank.cuh"
 
@@ -99,10 +101,69 @@ __device__ __forceinline__ void store4(X* p, bool vec, const float (&x)[4]) {
   }
 }
 
+// Blocks of 8 logits as they are stored.
+template <int EB>
+struct Raw;
+template <>
+struct Raw<4> {
+  float v[8];
+  template <typename X>
+  __device__ __forceinline__ void load(const float* p, int room, bool) {
+    float4 a = make_float4(NEG_INF, NEG_INF, NEG_INF, NEG_INF), b = a;
+    if (room >= 4) a = *reinterpret_cast<const float4*>(p);
+    if (room >= 8) b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  template <typename X>
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = v[j];
+  }
+};
+template <>
+struct Raw<2> {
+  uint4 v;
+  template <typename X>
+  __device__ __forceinline__ void load(const X* p, int room, bool wide) {
+    constexpr uint32_t LOW = sizeof(X) == 2 && std::is_same<X, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+    v = make_uint4(LOW, LOW, LOW, LOW);
+    if (wide) {
+      if (room >= 8) v = *reinterpret_cast<const uint4*>(p);
+      else if (room >= 4) {
+        const uint2 a = *reinterpret_cast<const uint2*>(p);
+        v.x = a.x, v.y = a.y;
+      }
+    } else {
+      if (room >= 4) {
+        const uint2 a = *reinterpret_cast<const uint2*>(p);
+        v.x = a.x, v.y = a.y;
+      }
+      if (room >= 8) {
+        const uint2 a = *reinterpret_cast<const uint2*>(p + 4);
+        v.z = a.x, v.w = a.y;
+      }
+    }
+  }
+  template <typename X>
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    float a[4], b[4];
+    Quad<X>::get(make_uint2(v.x, v.y), a);
+    Quad<X>::get(make_uint2(v.z, v.w), b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
+  }
+};
+
 // ------------------------------------------------------------------ scores
 __device__ __forceinline__ float rcp_approx(float x) {  // within 1 ulp
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float ex2_approx(float x) {  // 2 units in the last place
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 // A logit that counts: -inf for a masked expert, NaN included.

@@ -12,8 +12,13 @@
 // part at the k chosen experts, so a renormalised gate without score sums
 // reads its chosen logits alone.
 //
-// One warp per row; a lane holds the quads 4 (lane + 32 i) and lane j < k the
-// j-th choice.
+// score_grad_tile_kernel (k <= 8, aligned rows): a warp takes four rows of a layer.
+// The choices go to 8 lanes a row, the dense part to LR lanes a row, each with a
+// block of 8 neighbouring experts, so that both are coalesced and full; the
+// chosen experts' parts reach their blocks through a row of shared memory.
+//
+// score_grad_kernel (any k and alignment): one warp per row; a lane holds the
+// quads 4 (lane + 32 i) and lane j < k the j-th choice.
 #include "pdl.cuh"
 #include "score.cuh"
 
@@ -123,8 +128,195 @@ __global__ void __launch_bounds__(SG_WARPS * 32) score_grad_kernel(const ScorePa
   pdl_release();
 }
 
+constexpr int SGT_WARPS = 8;
+constexpr int SGT_ROWS = 4;  // of a warp at a time
+
+template <int N>
+__device__ __forceinline__ float part_sum(float v) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+  return v;
+}
+template <int N>
+__device__ __forceinline__ float part_max(float v) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
+  return v;
+}
+
+template <typename X>
+__device__ __forceinline__ void store8(X* p, int room, bool wide, const float (&x)[8]) {
+  const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
+  if constexpr (sizeof(X) == 2) {
+    if (wide && room >= 8) {
+      const uint2 u = Quad<X>::put(a), v = Quad<X>::put(b);
+      *reinterpret_cast<uint4*>(p) = make_uint4(u.x, u.y, v.x, v.y);
+      return;
+    }
+  }
+  if (room >= 4) store4<X>(p, true, a);
+  if (room >= 8) store4<X>(p + 4, true, b);
+}
+
+template <typename X, int LR, bool DENSE>
+__global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const ScoreParams p) {
+  constexpr int EB = sizeof(X);
+  constexpr int RS = 32 / LR;               // rows of a step of the dense part
+  constexpr int STEPS = SGT_ROWS / RS;
+  constexpr int PITCH = 8 * LR;
+  // expert e of a row lies at (e / 8) * 4 + e % 4, the upper half of its block 4 LR further on:
+  // a lane's two vector accesses are then free of bank conflicts
+  __shared__ __align__(16) float chosen[SGT_WARPS][SGT_ROWS][PITCH];
+  __shared__ uint8_t owner[SGT_WARPS][SGT_ROWS][PITCH];
+  __shared__ float4 scalar[SGT_WARPS][SGT_ROWS];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = blockIdx.x / p.nspan, unit = blockIdx.x - l * p.nspan;
+  const bool soft = p.score == MOER_SCORE_SOFTMAX;
+  const X* base = static_cast<const X*>(p.logits) + l * p.ld_layer;
+  X* obase = static_cast<X*>(p.d_logits) + l * p.ldg_layer;
+  const int rc = lane >> 3, j = lane & 7;    // the lane's choice
+  const int rd = lane / LR, blk = lane % LR; // its block
+  const int room = p.E - 8 * blk;
+  float a[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    a[i] = DENSE && p.d_score_sum != nullptr && 8 * blk + i < p.E ? p.d_score_sum[(size_t)l * p.E + 8 * blk + i] : 0.f;
+  const int64_t t1 = min64(p.T, (int64_t)(unit + 1) * p.span);
+  for (int64_t t0 = (int64_t)unit * p.span + warp * SGT_ROWS; t0 < t1; t0 += SGT_WARPS * SGT_ROWS) {
+    Raw<EB> raw[STEPS];
+    if (DENSE)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const int64_t t = min64(t0 + s * RS + rd, t1 - 1);
+        raw[s].template load<X>(base + t * p.ld_token + 8 * blk, room, p.wide != 0);
+      }
+    const int64_t tc = t0 + rc;
+    int id = 0;
+    float g = 0.f, xj = NEG_INF;
+    bool ok = tc < t1 && j < p.k;
+    if (ok) {
+      const int64_t at = ((int64_t)l * p.T + tc) * p.k + j;
+      id = p.ids[at];
+      g = p.scale * p.d_weights[at];
+      ok = id < p.E;
+      if (ok)
+        xj = live_logit(Quad<X>::one(base[tc * p.ld_token + id]));
+      else
+        atomicOr(p.status, WS_BIT_EDATA), g = 0.f, id = 0;
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      float4* z = reinterpret_cast<float4*>(chosen[warp][s * RS + rd]);
+      z[blk] = make_float4(0.f, 0.f, 0.f, 0.f);
+      z[LR + blk] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const int slot = (id >> 3) * 4 + (id & 3) + ((id & 4) != 0 ? 4 * LR : 0);
+    if (ok) owner[warp][rc][slot] = (uint8_t)j;
+    float v[STEPS][8], rz[STEPS], dot[STEPS];
+    if constexpr (DENSE) {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        raw[s].template get<X>(v[s]);
+        if (soft) {
+          float m = NEG_INF;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m = fmaxf(m, v[s][i]);
+          m = part_max<LR>(m);
+          // no expert, or one at +inf: with exact comparisons
+          const bool edge = __any_sync(FULL, !(fabsf(m) < 3e38f));
+          float z = 0.f, d = 0.f;
+          const float mm = m * LOG2E;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x = fmaxf(v[s][i], NEG_INF);  // NaN -> -inf
+            v[s][i] = edge ? exp_below(x, m) : ex2_approx(fmaf(x, LOG2E, -mm));
+            z += v[s][i];
+            d = fmaf(a[i], v[s][i], d);
+          }
+          z = part_sum<LR>(z);
+          rz[s] = z > 0.f ? 1.f / z : 0.f;
+          dot[s] = part_sum<LR>(d) * rz[s];
+          if (blk == 0) scalar[warp][s * RS + rd] = make_float4(m, rz[s], 0.f, 0.f);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[s][i] = a[i] * sigmoid_slope(live_logit(v[s][i]));
+        }
+      }
+    }
+    __syncwarp();
+    // the part at the chosen expert
+    float dj;
+    if (soft) {
+      if (p.renorm) {
+        const float q0 = exp_below(xj, part_max<8>(xj)), z = part_sum<8>(q0);
+        const float q = z > 0.f ? q0 / z : 0.f;
+        dj = q * (g - part_sum<8>(g * q));
+      } else {
+        const float4 mr = scalar[warp][rc];
+        dj = g * exp_below(xj, mr.x) * mr.y;
+        const float dg = part_sum<8>(dj);
+        __syncwarp();
+        if (j == 0) scalar[warp][rc].z = dg;
+      }
+    } else {
+      dj = g;
+      if (p.renorm) {
+        const float s = ok ? sigmoid(xj) : 0.f;
+        const float z = part_sum<8>(s), rs = z > 0.f ? 1.f / z : 0.f;
+        dj = (g - part_sum<8>(g * s) * rs) * rs;
+      }
+      dj *= sigmoid_slope(xj);
+    }
+    float* at = &chosen[warp][rc][slot];
+    const bool lost = ok && owner[warp][rc][slot] != j;  // an id that is repeated in its row
+    if (ok) *at = dj;
+    if (__any_sync(FULL, lost)) {
+      if (ok) *at = 0.f;
+      __syncwarp();
+      for (int i = 0; i < 8; ++i) {
+        if (ok && j == i) *at += dj;
+        __syncwarp();
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int r = s * RS + rd;
+      const float4* z = reinterpret_cast<const float4*>(chosen[warp][r]);
+      const float4 lo = z[blk], hi = z[LR + blk];
+      float dx[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      if constexpr (DENSE) {
+        if (soft) {
+          const float d = dot[s] + (p.renorm ? 0.f : scalar[warp][r].z);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dx[i] += v[s][i] * rz[s] * (a[i] - d);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dx[i] += v[s][i];
+        }
+      }
+      if (t0 + r < t1) store8<X>(obase + (t0 + r) * p.ldg_token + 8 * blk, room, p.wide != 0, dx);
+    }
+    __syncwarp();
+  }
+  pdl_release();
+}
+
+template <typename X, int LR>
+cudaError_t grad_tile_run(const ScoreParams& p, cudaStream_t st) {
+  const bool dense = p.d_score_sum != nullptr || (p.score == MOER_SCORE_SOFTMAX && !p.renorm);
+  const dim3 grid((unsigned)(p.L * p.nspan)), block(SGT_WARPS * 32);
+  return dense ? launch_pdl(score_grad_tile_kernel<X, LR, true>, grid, block, 0, st, p)
+               : launch_pdl(score_grad_tile_kernel<X, LR, false>, grid, block, 0, st, p);
+}
+
 template <typename X>
 cudaError_t grad_run(const ScoreParams& p, cudaStream_t st) {
+  if (p.k <= 8 && p.vec != 0)
+    return p.E <= 64    ? grad_tile_run<X, 8>(p, st)
+           : p.E <= 128 ? grad_tile_run<X, 16>(p, st)
+                        : grad_tile_run<X, 32>(p, st);
   const int64_t rows = (int64_t)p.L * p.T;
   const int64_t want = (rows + SG_WARPS - 1) / SG_WARPS;
   const int sms = device_sm_count();
@@ -135,7 +327,12 @@ cudaError_t grad_run(const ScoreParams& p, cudaStream_t st) {
 }
 }  // namespace
 
-moer_status score_grad_launch(const ScoreParams& p, int dtype, cudaStream_t st) {
+moer_status score_grad_launch(ScoreParams p, int dtype, cudaStream_t st) {
+  // units of a layer's tokens, a multiple of the rows that a block takes at a time
+  constexpr int STEP = SGT_WARPS * SGT_ROWS, UNITS = 152 * 32;
+  const int64_t span = ((p.T * p.L + UNITS - 1) / UNITS + STEP - 1) / STEP * STEP;
+  p.span = (int)span;
+  p.nspan = (int)((p.T + span - 1) / span);
   const cudaError_t e = dtype == MOER_F32    ? grad_run<float>(p, st)
                         : dtype == MOER_BF16 ? grad_run<__nv_bfloat16>(p, st)
                                              : grad_run<__half>(p, st);
