@@ -13,7 +13,13 @@
 // held it and from free_pages otherwise, so nothing waits for the table's new
 // entries to be written.
 //
-// Two kernels: the sums, then one pass over tokens, blocks and cached blocks.
+// Two kernels.  The sums: a block scans 4,096 requests, four to a thread, after
+// adding up the lengths of all requests before them by itself (a few
+// thousand requests are a few reads of L2; a chain of blocks would cost more).
+// The fill: a block takes 2,048 neighbouring tokens (then blocks, then cached
+// blocks); two warps find the first and the last one's request by a 32-way
+// search, and a thread searches between them only, once for the four tokens
+// that it writes with vector stores.  It is bound by the stores (16 bytes a token).
 #include "common.cuh"
 #include "pdl.cuh"
 
@@ -21,94 +27,139 @@ namespace moer {
 
 namespace {
 constexpr int BP_SCAN = 1024;
+constexpr int BP_EACH = 4;                     // requests of a thread in the scan
+constexpr int BP_CHUNK = BP_SCAN * BP_EACH;
 constexpr int BP_FILL = 256;
+constexpr int BP_ITEMS = 2048;                 // tokens or blocks of a fill block
 
-struct Sums {
-  int64_t v[4];  // tokens, blocks, cached blocks, pages taken
+struct PlanParams {
+  moer_block_plan_args a;
+  unsigned long long inv;  // ceil(2^64 / B), or 0 for B = 1
+  int32_t* taken_off;      // [R+1]
+  uint32_t* status;
+  int vec;                 // 1: the token maps take vector stores
+  int tok_blocks, blk_blocks;  // fill blocks of tokens, of blocks
 };
 
-__device__ __forceinline__ int64_t ceil_div(int64_t a, int b) { return (a + b - 1) / b; }
-
-__device__ __forceinline__ void request(const moer_block_plan_args& a, int r, int64_t& c, int64_t& n, bool& bad) {
-  n = a.new_len[r];
-  c = a.ctx_len != nullptr ? a.ctx_len[r] : 0;
-  if (n < 0 || c < 0) bad = true;
-  n = max64(n, 0);
-  c = max64(c, 0);
+// x / B for x < 2^32.
+__device__ __forceinline__ uint32_t div_b(const PlanParams& p, uint32_t x) {
+  return p.inv != 0ull ? (uint32_t)__umul64hi((unsigned long long)x, p.inv) : x;
 }
 
-__device__ __forceinline__ Sums sums_of(int64_t c, int64_t n, int B) {
-  Sums s;
-  s.v[0] = n;
-  s.v[1] = n > 0 ? ceil_div(c % B + n, B) : 0;
-  s.v[2] = c / B;
-  s.v[3] = ceil_div(c + n, B) - ceil_div(c, B);
-  return s;
+struct Request {
+  uint32_t c, n;  // tokens held, tokens computed: their sum is below 2^31
+};
+
+__device__ __forceinline__ Request request(const PlanParams& p, int r, bool& bad) {
+  const int n = p.a.new_len[r], c = p.a.ctx_len != nullptr ? p.a.ctx_len[r] : 0;
+  if (n < 0 || c < 0 || max(n, 0) > 0x7FFFFFFF - max(c, 0)) bad = true;
+  const uint32_t held = (uint32_t)max(c, 0);
+  return {held, min((uint32_t)max(n, 0), 0x7FFFFFFFu - held)};  // positions are int32
+}
+
+// Pages that x tokens touch, x < 2^31 + B.
+__device__ __forceinline__ uint32_t pages_of(const PlanParams& p, uint32_t x) {
+  return div_b(p, x + (uint32_t)p.a.block - 1u);
+}
+
+// Tokens, blocks, cached blocks and pages taken of a request.
+__device__ __forceinline__ void sums_of(const PlanParams& p, const Request& q, uint32_t (&s)[4]) {
+  const uint32_t whole = div_b(p, q.c), rest = q.c - whole * (uint32_t)p.a.block;
+  s[0] = q.n;
+  s[1] = q.n > 0u ? pages_of(p, rest + q.n) : 0u;
+  s[2] = whole;
+  s[3] = pages_of(p, q.c + q.n) - pages_of(p, q.c);
 }
 
 __device__ __forceinline__ int32_t clamp32(int64_t v) { return (int32_t)min64(v, 0x7FFFFFFF); }
 
-// One block scans all requests, 1,024 at a time.
-__global__ void __launch_bounds__(BP_SCAN) plan_scan_kernel(const moer_block_plan_args a, int32_t* taken_off,
-                                                            uint32_t* status) {
-  __shared__ int64_t wsum[4][BP_SCAN / 32];
+__global__ void __launch_bounds__(BP_SCAN) plan_scan_kernel(const PlanParams p) {
+  __shared__ int64_t wsum[2][4][BP_SCAN / 32];
   pdl_wait();
+  const moer_block_plan_args& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t base[4] = {0, 0, 0, 0};
+  const int r0 = (int)blockIdx.x * BP_CHUNK + (int)threadIdx.x * BP_EACH;
   bool bad = false;
-  for (int r0 = 0; r0 < a.R; r0 += BP_SCAN) {
-    const int r = r0 + (int)threadIdx.x;
-    int64_t c = 0, n = 0;
-    if (r < a.R) request(a, r, c, n, bad);
-    const Sums s = sums_of(c, n, a.block);
-    int64_t x[4];
+  // the thread's requests, and its share of those before the block's
+  uint32_t s[BP_EACH][4];
+  int64_t x[4] = {0, 0, 0, 0}, before[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      x[q] = s.v[q];
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(FULL, x[q], o);
-        if (lane >= o) x[q] += y;
-      }
-      if (lane == 31) wsum[q][warp] = x[q];
+  for (int i = 0; i < BP_EACH; ++i) {
+    Request q = {0u, 0u};
+    if (r0 + i < a.R) {
+      q = request(p, r0 + i, bad);
+      if (a.pages != nullptr && pages_of(p, q.c + q.n) > (uint32_t)a.ld_pages) bad = true;
     }
-    __syncthreads();
+    sums_of(p, q, s[i]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      int64_t before = 0, all = 0;
-      for (int w = 0; w < BP_SCAN / 32; ++w) {
-        if (w < warp) before += wsum[q][w];
-        all += wsum[q][w];
-      }
-      x[q] += base[q] + before - s.v[q];
-      base[q] += all;
-    }
-    if (r < a.R) {
-      a.req_off[r] = clamp32(x[0]);
-      a.req_blk_off[r] = clamp32(x[1]);
-      if (a.req_cache_off != nullptr) a.req_cache_off[r] = clamp32(x[2]);
-      taken_off[r] = clamp32(x[3]);
-      if (a.pages != nullptr && ceil_div(c + n, a.block) > a.ld_pages) bad = true;
-    }
-    __syncthreads();
+    for (int k = 0; k < 4; ++k) x[k] += s[i][k];
   }
-  if (threadIdx.x == 0) {
-    a.req_off[a.R] = clamp32(base[0]);
-    a.req_blk_off[a.R] = clamp32(base[1]);
-    if (a.req_cache_off != nullptr) a.req_cache_off[a.R] = clamp32(base[2]);
-    taken_off[a.R] = clamp32(base[3]);
+  for (int r = threadIdx.x; r < (int)blockIdx.x * BP_CHUNK; r += BP_SCAN) {
+    uint32_t v[4];
+    sums_of(p, request(p, r, bad), v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) before[k] += v[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    int64_t y = x[k], b = before[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t z = __shfl_up_sync(FULL, y, o);
+      if (lane >= o) y += z;
+    }
+    if (blockIdx.x > 0)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(FULL, b, o);
+    if (lane == 31) wsum[0][k][warp] = y, wsum[1][k][warp] = b;
+    x[k] = y - x[k];  // of the warp's earlier threads
+  }
+  __syncthreads();
+  // one warp for each of the four: the warps' sums, scanned from the sum before the block
+  if (warp < 4) {
+    const int64_t y = wsum[0][warp][lane];
+    int64_t z = y, b = wsum[1][warp][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(FULL, z, o);
+      if (lane >= o) z += u;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(FULL, b, o);
+    wsum[0][warp][lane] = b + z - y;
+    if (lane == 31) wsum[1][warp][0] = b + z;  // up to the block's end
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] += wsum[0][k][warp];
+#pragma unroll
+  for (int i = 0; i < BP_EACH; ++i)
+    if (r0 + i < a.R) {
+      a.req_off[r0 + i] = clamp32(x[0]);
+      a.req_blk_off[r0 + i] = clamp32(x[1]);
+      if (a.req_cache_off != nullptr) a.req_cache_off[r0 + i] = clamp32(x[2]);
+      p.taken_off[r0 + i] = clamp32(x[3]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] += s[i][k];
+    }
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
+    const int64_t t[4] = {wsum[1][0][0], wsum[1][1][0], wsum[1][2][0], wsum[1][3][0]};
+    a.req_off[a.R] = clamp32(t[0]);
+    a.req_blk_off[a.R] = clamp32(t[1]);
+    if (a.req_cache_off != nullptr) a.req_cache_off[a.R] = clamp32(t[2]);
+    p.taken_off[a.R] = clamp32(t[3]);
     if (a.totals != nullptr)
-      for (int q = 0; q < 4; ++q) a.totals[q] = clamp32(base[q]);
-    if (base[0] > a.T || base[1] > a.nblk || (a.cache_idx != nullptr && base[2] > a.ncached) ||
-        (a.free_pages != nullptr && base[3] > a.n_free))
+      for (int k = 0; k < 4; ++k) a.totals[k] = clamp32(t[k]);
+    if (t[0] > a.T || t[1] > a.nblk || (a.cache_idx != nullptr && t[2] > a.ncached) ||
+        (a.free_pages != nullptr && t[3] > a.n_free))
       bad = true;
   }
-  if (bad) atomicOr(status, WS_BIT_EDATA);
+  if (bad) atomicOr(p.status, WS_BIT_EDATA);
   pdl_release();
 }
 
-// Largest r with off[r] <= i, for i < off[R].
-__device__ __forceinline__ int find(const int32_t* off, int R, int64_t i) {
-  int lo = 0, hi = R;
+// Largest r in [lo, hi) with off[r] <= i, where off[lo] <= i.
+__device__ __forceinline__ int find(const int32_t* off, int lo, int hi, int i) {
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (off[mid] <= i)
@@ -119,92 +170,206 @@ __device__ __forceinline__ int find(const int32_t* off, int R, int64_t i) {
   return lo;
 }
 
+// The same over [0, R) by a warp: 32 probes at a time, each step leaves one of
+// 32 parts.  Every lane returns the result.
+__device__ __forceinline__ int find_warp(const int32_t* off, int R, int i) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = R;
+  while (n > 1) {
+    const int part = (n + 31) >> 5;
+    const int at = lo + lane * part;
+    const bool le = lane * part < n && off[at] <= i;
+    const int last = 31 - __clz(__ballot_sync(FULL, le) | 1u);
+    lo += last * part;
+    n = min(part, n - last * part);
+  }
+  return lo;
+}
+
 // The page of a request's page number: held pages from the table, new ones
 // from free_pages (or from the table where that is complete); -1 if there is none.
-__device__ __forceinline__ int page_of(const moer_block_plan_args& a, const int32_t* taken_off, int r, int64_t c,
-                                       int64_t i) {
-  if (i >= a.ld_pages) return -1;
-  const int64_t h = ceil_div(c, a.block);
-  if (a.free_pages != nullptr && i >= h) {
-    const int64_t f = taken_off[r] + (i - h);
+__device__ __forceinline__ int page_of(const PlanParams& p, int r, uint32_t held, uint32_t i) {
+  const moer_block_plan_args& a = p.a;
+  if (i >= (uint32_t)a.ld_pages) return -1;
+  if (a.free_pages != nullptr && i >= held) {
+    const int64_t f = (int64_t)p.taken_off[r] + (i - held);
     return f < a.n_free ? a.free_pages[f] : -1;
   }
   return a.pages[(int64_t)r * a.ld_pages + i];
 }
 
-__global__ void __launch_bounds__(BP_FILL) plan_fill_kernel(const moer_block_plan_args a, const int32_t* taken_off) {
-  pdl_wait();
-  const int64_t T = a.req_off[a.R], nblk = a.req_blk_off[a.R];
-  const int64_t step = (int64_t)gridDim.x * BP_FILL, first = (int64_t)blockIdx.x * BP_FILL + threadIdx.x;
-  bool bad;
-  if (a.slot_map != nullptr || a.tok_req != nullptr || a.tok_pos != nullptr)
-    for (int64_t t = first; t < a.T; t += step) {
-      int64_t slot = -1, pos = -1;
-      int r = -1;
-      if (t < T) {
-        r = find(a.req_off, a.R, t);
-        int64_t c, n;
-        request(a, r, c, n, bad);
-        pos = c + (t - a.req_off[r]);
-        if (a.slot_map != nullptr) {
-          const int page = page_of(a, taken_off, r, c, pos / a.block);
-          if (page >= 0) slot = (int64_t)page * a.block + pos % a.block;
-        }
-      }
-      if (a.slot_map != nullptr) a.slot_map[t] = slot;
-      if (a.tok_req != nullptr) a.tok_req[t] = r;
-      if (a.tok_pos != nullptr) a.tok_pos[t] = (int32_t)pos;
+// Walks over neighbouring tokens: the request, and the slot on its page.
+struct Walk {
+  int r;
+  int64_t end;             // first token past the request
+  uint32_t pos, page_no, held, rest;
+  int page;
+  __device__ __forceinline__ void enter(const PlanParams& p, int request_no, int t) {
+    bool bad;
+    r = request_no;
+    const Request q = request(p, r, bad);
+    const int at = p.a.req_off[r];
+    end = (int64_t)at + q.n;
+    pos = q.c + (uint32_t)(t - at);
+    held = pages_of(p, q.c);
+    page_no = div_b(p, pos);
+    rest = pos - page_no * (uint32_t)p.a.block;
+    if (p.a.slot_map != nullptr) page = page_of(p, r, held, page_no);
+  }
+  // to token t, the one after the last
+  __device__ __forceinline__ void next(const PlanParams& p, int t) {
+    ++pos;
+    if (t >= end) {
+      int q = r + 1;
+      while (p.a.req_off[q + 1] <= t) ++q;  // requests without tokens
+      enter(p, q, t);
+    } else if (++rest == (uint32_t)p.a.block) {
+      rest = 0u;
+      ++page_no;
+      if (p.a.slot_map != nullptr) page = page_of(p, r, held, page_no);
     }
-  for (int64_t b = first; b < a.nblk; b += step) {
-    int tok0 = clamp32(T), len = 0, slot = -1;
-    if (b < nblk) {
-      const int r = find(a.req_blk_off, a.R, b);
-      int64_t c, n;
-      request(a, r, c, n, bad);
-      const int64_t i = c / a.block + (b - a.req_blk_off[r]);
-      const int64_t lo = max64(i * a.block, c), hi = min64((i + 1) * a.block, c + n);
-      tok0 = clamp32(a.req_off[r] + (lo - c));
+  }
+};
+
+__device__ void fill_tokens(const PlanParams& p, int64_t i0, int* range) {
+  const moer_block_plan_args& a = p.a;
+  const int T = a.req_off[a.R];
+  const int n_in = (int)max64(0, min64(BP_ITEMS, T - i0));  // of the block's tokens
+  if (threadIdx.x < 64 && n_in > 0) {
+    const int w = threadIdx.x >> 5;
+    const int r = find_warp(a.req_off, a.R, (int)i0 + (w == 0 ? 0 : n_in - 1));
+    if ((threadIdx.x & 31) == 0) range[w] = r;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int half = 0; half < BP_ITEMS / (4 * BP_FILL); ++half) {
+    const int k = (half * BP_FILL + (int)threadIdx.x) * 4;
+    const int64_t t0 = i0 + k;
+    if (t0 >= a.T) return;
+    int64_t slot[4] = {-1, -1, -1, -1};
+    int req[4] = {-1, -1, -1, -1}, pos[4] = {-1, -1, -1, -1};
+    if (k < n_in) {
+      Walk w;
+      w.enter(p, find(a.req_off, range[0], range[1] + 1, (int)t0), (int)t0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (k + j < n_in) {
+          if (j > 0) w.next(p, (int)t0 + j);
+          req[j] = w.r;
+          pos[j] = (int)w.pos;
+          if (a.slot_map != nullptr && w.page >= 0) slot[j] = (int64_t)w.page * a.block + w.rest;
+        }
+    }
+    if (p.vec != 0 && t0 + 4 <= a.T) {
+      if (a.slot_map != nullptr) {
+        *reinterpret_cast<longlong2*>(a.slot_map + t0) = make_longlong2(slot[0], slot[1]);
+        *reinterpret_cast<longlong2*>(a.slot_map + t0 + 2) = make_longlong2(slot[2], slot[3]);
+      }
+      if (a.tok_req != nullptr) *reinterpret_cast<int4*>(a.tok_req + t0) = make_int4(req[0], req[1], req[2], req[3]);
+      if (a.tok_pos != nullptr) *reinterpret_cast<int4*>(a.tok_pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (t0 + j < a.T) {
+          if (a.slot_map != nullptr) a.slot_map[t0 + j] = slot[j];
+          if (a.tok_req != nullptr) a.tok_req[t0 + j] = req[j];
+          if (a.tok_pos != nullptr) a.tok_pos[t0 + j] = pos[j];
+        }
+    }
+  }
+}
+
+__device__ void fill_blocks(const PlanParams& p, int64_t i0, int* range) {
+  const moer_block_plan_args& a = p.a;
+  const int T = a.req_off[a.R], nblk = a.req_blk_off[a.R];
+  const int n_in = (int)max64(0, min64(BP_ITEMS, nblk - i0));
+  if (threadIdx.x < 64 && n_in > 0) {
+    const int w = threadIdx.x >> 5;
+    const int r = find_warp(a.req_blk_off, a.R, (int)i0 + (w == 0 ? 0 : n_in - 1));
+    if ((threadIdx.x & 31) == 0) range[w] = r;
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < BP_ITEMS && i0 + k < a.nblk; k += BP_FILL) {
+    const int64_t b = i0 + k;
+    int tok0 = T, len = 0, slot = -1;
+    if (k < n_in) {
+      bool bad;
+      const int r = find(a.req_blk_off, range[0], range[1] + 1, (int)b);
+      const Request q = request(p, r, bad);
+      const uint32_t B = (uint32_t)a.block, i = div_b(p, q.c) + (uint32_t)(b - a.req_blk_off[r]);
+      const uint32_t lo = max(i * B, q.c), hi = min(i * B + B, q.c + q.n);
+      tok0 = clamp32((int64_t)a.req_off[r] + (lo - q.c));
       len = (int)(hi - lo);
-      const int page = page_of(a, taken_off, r, c, i);
-      if (len == a.block) slot = page;
-      if (a.free_pages != nullptr && i >= ceil_div(c, a.block) && i < a.ld_pages)
-        a.pages[(int64_t)r * a.ld_pages + i] = page;
+      if (a.pages != nullptr) {
+        const uint32_t held = pages_of(p, q.c);
+        const int page = page_of(p, r, held, i);
+        if (len == a.block) slot = page;
+        if (a.free_pages != nullptr && i >= held && i < (uint32_t)a.ld_pages)
+          a.pages[(int64_t)r * a.ld_pages + i] = page;
+      }
     }
     a.blk_tab[2 * b] = tok0;
     a.blk_tab[2 * b + 1] = len;
     if (a.insert_slot != nullptr) a.insert_slot[b] = slot;
   }
-  if (a.cache_idx != nullptr) {
-    const int64_t nc = a.req_cache_off[a.R];
-    for (int64_t j = first; j < a.ncached; j += step) {
-      int page = -1;
-      if (j < nc) {
-        const int r = find(a.req_cache_off, a.R, j);
-        const int64_t i = j - a.req_cache_off[r];
-        if (i < a.ld_pages) page = a.pages[(int64_t)r * a.ld_pages + i];
-      }
-      a.cache_idx[j] = page;
-    }
+}
+
+__device__ void fill_cached(const PlanParams& p, int64_t i0, int* range) {
+  const moer_block_plan_args& a = p.a;
+  const int nc = a.req_cache_off[a.R];
+  const int n_in = (int)max64(0, min64(BP_ITEMS, nc - i0));
+  if (threadIdx.x < 64 && n_in > 0) {
+    const int w = threadIdx.x >> 5;
+    const int r = find_warp(a.req_cache_off, a.R, (int)i0 + (w == 0 ? 0 : n_in - 1));
+    if ((threadIdx.x & 31) == 0) range[w] = r;
   }
+  __syncthreads();
+  for (int k = threadIdx.x; k < BP_ITEMS && i0 + k < a.ncached; k += BP_FILL) {
+    int page = -1;
+    if (k < n_in) {
+      const int r = find(a.req_cache_off, range[0], range[1] + 1, (int)i0 + k);
+      const int i = (int)i0 + k - a.req_cache_off[r];
+      if (i < a.ld_pages) page = a.pages[(int64_t)r * a.ld_pages + i];
+    }
+    a.cache_idx[i0 + k] = page;
+  }
+}
+
+__global__ void __launch_bounds__(BP_FILL) plan_fill_kernel(const PlanParams p) {
+  __shared__ int range[2];  // requests of the block's first and last item
+  pdl_wait();
+  const int b = (int)blockIdx.x;
+  if (b < p.tok_blocks)
+    fill_tokens(p, (int64_t)b * BP_ITEMS, range);
+  else if (b < p.tok_blocks + p.blk_blocks)
+    fill_blocks(p, (int64_t)(b - p.tok_blocks) * BP_ITEMS, range);
+  else
+    fill_cached(p, (int64_t)(b - p.tok_blocks - p.blk_blocks) * BP_ITEMS, range);
   pdl_release();
 }
+
+bool on16(const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
 }  // namespace
 
 size_t block_plan_scratch_bytes(int32_t R) { return ((size_t)R + 1) * 4; }
 
 moer_status block_plan_launch(const moer_block_plan_args* a, void* ws, cudaStream_t st) {
-  uint32_t* status = static_cast<uint32_t*>(ws);
-  int32_t* taken = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + WS_HEADER);
-  if (launch_pdl(plan_scan_kernel, dim3(1), dim3(BP_SCAN), 0, st, *a, taken, status) != cudaSuccess)
-    return MOER_ECUDA;
-  const int64_t n = max64(max64(a->T, a->nblk), a->ncached);
-  const int sms = device_sm_count();
-  if (sms <= 0) return MOER_ECUDA;
-  const int64_t grid = max64(1, min64((n + BP_FILL - 1) / BP_FILL, (int64_t)sms * 8));
-  return launch_pdl(plan_fill_kernel, dim3((unsigned)grid), dim3(BP_FILL), 0, st, *a, (const int32_t*)taken) ==
-                 cudaSuccess
-             ? MOER_OK
-             : MOER_ECUDA;
+  PlanParams p;
+  p.a = *a;
+  const unsigned long long B = (unsigned long long)a->block;
+  p.inv = B == 1 ? 0ull : ~0ull / B + 1ull;
+  p.status = static_cast<uint32_t*>(ws);
+  p.taken_off = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + WS_HEADER);
+  p.vec = on16(a->slot_map) && on16(a->tok_req) && on16(a->tok_pos);
+  const bool tokens = a->slot_map != nullptr || a->tok_req != nullptr || a->tok_pos != nullptr;
+  auto blocks = [](int64_t n) { return (n + BP_ITEMS - 1) / BP_ITEMS; };
+  p.tok_blocks = tokens ? (int)blocks(a->T) : 0;
+  p.blk_blocks = (int)blocks(a->nblk);
+  const int64_t fill = (int64_t)p.tok_blocks + p.blk_blocks + (a->cache_idx != nullptr ? blocks(a->ncached) : 0);
+  const int scan = a->R > BP_CHUNK ? (a->R + BP_CHUNK - 1) / BP_CHUNK : 1;
+  cudaError_t e = launch_pdl(plan_scan_kernel, dim3(scan), dim3(BP_SCAN), 0, st, p);
+  if (e == cudaSuccess && fill > 0) e = launch_pdl(plan_fill_kernel, dim3((unsigned)fill), dim3(BP_FILL), 0, st, p);
+  return e == cudaSuccess ? MOER_OK : MOER_ECUDA;
 }
 
 }  // namespace moer
