@@ -534,9 +534,10 @@ typedef struct moer_block_plan_args {
 /* Entries past the batch's own are written too: -1 in insert_slot, cache_idx,
  * slot_map, tok_req and tok_pos, (tokens, 0) in blk_tab.  MOER_EDATA is
  * recorded, and what fits is written, when a length is negative (taken as 0),
- * when a request passes 2^31 - 1 tokens (the rest is left out), when the batch has more tokens, blocks or cached blocks than there is room
- * for, when a table row is too short for a request, or when free_pages runs
- * out (the page is then -1, and so are its slots).
+ * when a request passes 2^31 - 1 tokens (the rest is left out), when the
+ * batch has more tokens, blocks or cached blocks than there is room for, when
+ * a table row is too short for a request, or when free_pages runs out (the
+ * page is then -1, and so are its slots).
  * ws  at least moer_block_plan_workspace_bytes(R) bytes, 16-byte aligned. */
 MOER_API size_t moer_block_plan_workspace_bytes(int32_t R);
 MOER_API moer_status moer_block_plan(const moer_block_plan_args* a, void* ws, size_t ws_bytes, moer_stream_t stream);

@@ -151,10 +151,19 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_current = None  # (current device, its current stream's handle), bound at the first call without a stream
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without the stream object that torch.cuda.current_stream()
+        # makes (0.2 instead of 2.9 us a call, a third of a small call's time on the host)
+        global _current
+        if _current is None:
+            import torch
+            torch.cuda.init()
+            _current = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        return _current[1](_current[0]())
     return s if isinstance(s, int) else s.cuda_stream
 
 

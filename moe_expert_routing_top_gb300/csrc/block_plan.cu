@@ -31,19 +31,21 @@ constexpr int BP_EACH = 4;                     // requests of a thread in the sc
 constexpr int BP_CHUNK = BP_SCAN * BP_EACH;
 constexpr int BP_FILL = 256;
 constexpr int BP_ITEMS = 2048;                 // tokens or blocks of a fill block
+constexpr int BP_SMALL = 4;                    // fill blocks that one block does by itself
 
 struct PlanParams {
   moer_block_plan_args a;
-  unsigned long long inv;  // ceil(2^64 / B), or 0 for B = 1
+  uint32_t mul, shift;     // x / B = (x mul) >> (32 + shift) for x < 2^31; shift 32: B = 1
   int32_t* taken_off;      // [R+1]
   uint32_t* status;
   int vec;                 // 1: the token maps take vector stores
   int tok_blocks, blk_blocks;  // fill blocks of tokens, of blocks
 };
 
-// x / B for x < 2^32.
+// x / B for x < 2^31: with s = ceil(log2 B) the multiplier is floor(2^(31 + s) / B) + 1,
+// whose excess over 2^(31 + s) / B, at most 1, times x / 2^(31 + s) stays below 1 / B.
 __device__ __forceinline__ uint32_t div_b(const PlanParams& p, uint32_t x) {
-  return p.inv != 0ull ? (uint32_t)__umul64hi((unsigned long long)x, p.inv) : x;
+  return p.shift < 32u ? __umulhi(x, p.mul) >> p.shift : x;
 }
 
 struct Request {
@@ -57,25 +59,25 @@ __device__ __forceinline__ Request request(const PlanParams& p, int r, bool& bad
   return {held, min((uint32_t)max(n, 0), 0x7FFFFFFFu - held)};  // positions are int32
 }
 
-// Pages that x tokens touch, x < 2^31 + B.
+// Pages that x tokens touch, x < 2^31.
 __device__ __forceinline__ uint32_t pages_of(const PlanParams& p, uint32_t x) {
-  return div_b(p, x + (uint32_t)p.a.block - 1u);
+  return x > 0u ? div_b(p, x - 1u) + 1u : 0u;
 }
 
 // Tokens, blocks, cached blocks and pages taken of a request.
 __device__ __forceinline__ void sums_of(const PlanParams& p, const Request& q, uint32_t (&s)[4]) {
   const uint32_t whole = div_b(p, q.c), rest = q.c - whole * (uint32_t)p.a.block;
   s[0] = q.n;
-  s[1] = q.n > 0u ? pages_of(p, rest + q.n) : 0u;
+  s[1] = q.n > 0u ? pages_of(p, rest + q.n) : 0u;  // rest + n <= c + n
   s[2] = whole;
   s[3] = pages_of(p, q.c + q.n) - pages_of(p, q.c);
 }
 
 __device__ __forceinline__ int32_t clamp32(int64_t v) { return (int32_t)min64(v, 0x7FFFFFFF); }
 
-__global__ void __launch_bounds__(BP_SCAN) plan_scan_kernel(const PlanParams p) {
+// The sums, by gridDim.x blocks of 1,024 threads.
+__device__ __forceinline__ void scan_requests(const PlanParams& p) {
   __shared__ int64_t wsum[2][4][BP_SCAN / 32];
-  pdl_wait();
   const moer_block_plan_args& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r0 = (int)blockIdx.x * BP_CHUNK + (int)threadIdx.x * BP_EACH;
@@ -155,6 +157,11 @@ __global__ void __launch_bounds__(BP_SCAN) plan_scan_kernel(const PlanParams p) 
       bad = true;
   }
   if (bad) atomicOr(p.status, WS_BIT_EDATA);
+}
+
+__global__ void __launch_bounds__(BP_SCAN) plan_scan_kernel(const PlanParams p) {
+  pdl_wait();
+  scan_requests(p);
   pdl_release();
 }
 
@@ -214,7 +221,7 @@ struct Walk {
     held = pages_of(p, q.c);
     page_no = div_b(p, pos);
     rest = pos - page_no * (uint32_t)p.a.block;
-    if (p.a.slot_map != nullptr) page = page_of(p, r, held, page_no);
+    page = p.a.slot_map != nullptr ? page_of(p, r, held, page_no) : -1;
   }
   // to token t, the one after the last
   __device__ __forceinline__ void next(const PlanParams& p, int t) {
@@ -241,24 +248,33 @@ __device__ void fill_tokens(const PlanParams& p, int64_t i0, int* range) {
     if ((threadIdx.x & 31) == 0) range[w] = r;
   }
   __syncthreads();
-#pragma unroll
-  for (int half = 0; half < BP_ITEMS / (4 * BP_FILL); ++half) {
-    const int k = (half * BP_FILL + (int)threadIdx.x) * 4;
+  for (int k = (int)threadIdx.x * 4; k < BP_ITEMS; k += (int)blockDim.x * 4) {
     const int64_t t0 = i0 + k;
-    if (t0 >= a.T) return;
+    if (t0 >= a.T) break;
     int64_t slot[4] = {-1, -1, -1, -1};
     int req[4] = {-1, -1, -1, -1}, pos[4] = {-1, -1, -1, -1};
     if (k < n_in) {
       Walk w;
       w.enter(p, find(a.req_off, range[0], range[1] + 1, (int)t0), (int)t0);
+      if (t0 + 4 <= w.end && w.rest + 4u <= (uint32_t)a.block) {
+        // all four on one page of one request
+        const int64_t s0 = w.page >= 0 ? (int64_t)w.page * a.block + w.rest : -1;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (k + j < n_in) {
-          if (j > 0) w.next(p, (int)t0 + j);
+        for (int j = 0; j < 4; ++j) {
           req[j] = w.r;
-          pos[j] = (int)w.pos;
-          if (a.slot_map != nullptr && w.page >= 0) slot[j] = (int64_t)w.page * a.block + w.rest;
+          pos[j] = (int)w.pos + j;
+          slot[j] = s0 >= 0 ? s0 + j : -1;
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k + j < n_in) {
+            if (j > 0) w.next(p, (int)t0 + j);
+            req[j] = w.r;
+            pos[j] = (int)w.pos;
+            if (w.page >= 0) slot[j] = (int64_t)w.page * a.block + w.rest;
+          }
+      }
     }
     if (p.vec != 0 && t0 + 4 <= a.T) {
       if (a.slot_map != nullptr) {
@@ -289,7 +305,7 @@ __device__ void fill_blocks(const PlanParams& p, int64_t i0, int* range) {
     if ((threadIdx.x & 31) == 0) range[w] = r;
   }
   __syncthreads();
-  for (int k = threadIdx.x; k < BP_ITEMS && i0 + k < a.nblk; k += BP_FILL) {
+  for (int k = threadIdx.x; k < BP_ITEMS && i0 + k < a.nblk; k += (int)blockDim.x) {
     const int64_t b = i0 + k;
     int tok0 = T, len = 0, slot = -1;
     if (k < n_in) {
@@ -324,7 +340,7 @@ __device__ void fill_cached(const PlanParams& p, int64_t i0, int* range) {
     if ((threadIdx.x & 31) == 0) range[w] = r;
   }
   __syncthreads();
-  for (int k = threadIdx.x; k < BP_ITEMS && i0 + k < a.ncached; k += BP_FILL) {
+  for (int k = threadIdx.x; k < BP_ITEMS && i0 + k < a.ncached; k += (int)blockDim.x) {
     int page = -1;
     if (k < n_in) {
       const int r = find(a.req_cache_off, range[0], range[1] + 1, (int)i0 + k);
@@ -348,6 +364,28 @@ __global__ void __launch_bounds__(BP_FILL) plan_fill_kernel(const PlanParams p) 
   pdl_release();
 }
 
+// Small batches: one block makes the sums and then fills the tables itself.
+__global__ void __launch_bounds__(BP_SCAN) plan_small_kernel(const PlanParams p) {
+  __shared__ int range[2];
+  pdl_wait();
+  scan_requests(p);
+  __syncthreads();  // the sums in global memory are this block's own
+  for (int b = 0; b < p.tok_blocks; ++b) {
+    fill_tokens(p, (int64_t)b * BP_ITEMS, range);
+    __syncthreads();
+  }
+  for (int b = 0; b < p.blk_blocks; ++b) {
+    fill_blocks(p, (int64_t)b * BP_ITEMS, range);
+    __syncthreads();
+  }
+  if (p.a.cache_idx != nullptr)
+    for (int64_t i = 0; i < p.a.ncached; i += BP_ITEMS) {
+      fill_cached(p, i, range);
+      __syncthreads();
+    }
+  pdl_release();
+}
+
 bool on16(const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
 }  // namespace
 
@@ -357,7 +395,10 @@ moer_status block_plan_launch(const moer_block_plan_args* a, void* ws, cudaStrea
   PlanParams p;
   p.a = *a;
   const unsigned long long B = (unsigned long long)a->block;
-  p.inv = B == 1 ? 0ull : ~0ull / B + 1ull;
+  uint32_t log = 0u;
+  while ((1ull << log) < B) ++log;
+  p.mul = B == 1 ? 0u : (uint32_t)((1ull << (31u + log)) / B + 1ull);
+  p.shift = B == 1 ? 32u : log - 1u;
   p.status = static_cast<uint32_t*>(ws);
   p.taken_off = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + WS_HEADER);
   p.vec = on16(a->slot_map) && on16(a->tok_req) && on16(a->tok_pos);
@@ -366,6 +407,8 @@ moer_status block_plan_launch(const moer_block_plan_args* a, void* ws, cudaStrea
   p.tok_blocks = tokens ? (int)blocks(a->T) : 0;
   p.blk_blocks = (int)blocks(a->nblk);
   const int64_t fill = (int64_t)p.tok_blocks + p.blk_blocks + (a->cache_idx != nullptr ? blocks(a->ncached) : 0);
+  if (a->R <= BP_CHUNK && fill <= BP_SMALL)
+    return launch_pdl(plan_small_kernel, dim3(1), dim3(BP_SCAN), 0, st, p) == cudaSuccess ? MOER_OK : MOER_ECUDA;
   const int scan = a->R > BP_CHUNK ? (a->R + BP_CHUNK - 1) / BP_CHUNK : 1;
   cudaError_t e = launch_pdl(plan_scan_kernel, dim3(scan), dim3(BP_SCAN), 0, st, p);
   if (e == cudaSuccess && fill > 0) e = launch_pdl(plan_fill_kernel, dim3((unsigned)fill), dim3(BP_FILL), 0, st, p);

@@ -173,10 +173,13 @@ __global__ void __launch_bounds__(EO_THREADS) order_place_kernel(const OrderPara
   for (int e = lane; e < EM; e += 32) count[warp][e] = 0u;
   __syncthreads();
   uint32_t rank[EO_IT];
-  const int w0 = warp * (EO_PAIRS / EO_WARPS);
+  // a warp's pairs: whole rounds of 32, spread over the warps where the chunk is short
+  const int span = (n + EO_THREADS - 1) / EO_THREADS * 32;
+  const int w0 = warp * span;
   bool bad = false;
 #pragma unroll
   for (int it = 0; it < EO_IT; ++it) {
+    if (it * 32 >= span) break;
     const int i = w0 + it * 32 + lane;
     const int e = i < n ? sid[i] : 256;
     const bool ok = e < p.E;
@@ -232,6 +235,7 @@ __global__ void __launch_bounds__(EO_THREADS) order_place_kernel(const OrderPara
   int32_t* inv = p.inv != nullptr ? p.inv + (size_t)l * p.N + i0 : nullptr;
 #pragma unroll
   for (int it = 0; it < EO_IT; ++it) {
+    if (it * 32 >= span) break;
     const int i = w0 + it * 32 + lane;
     if (i < n) {
       const int x = sid[i];

@@ -25,6 +25,7 @@ struct ScoreParams {
   float* partial;      // [units][E] score sums of each unit, or NULL
   int span, nspan;     // tokens of a unit, units of a layer
   int wide;            // 1: rows take 16-byte access (the fast kernel's blocks of 8 logits)
+  int even;            // 2: k = 8, weights on 16 bytes; 1: k even, weights on 8 bytes; 0: neither
   // 2^8, known at run time only, so that a key's shift-and-insert stays one
   // multiply-add (FMA pipe) and off the integer ALU pipe that the networks fill
   uint32_t key_mul;

@@ -11,11 +11,12 @@
 // the binade [2^23, 2^24), whose mantissa bits are n; a multiply-add puts
 // 255 - id below it.  The three steps run on the FMA pipe, while the networks'
 // minima and maxima fill the ALU pipe, which is the kernel's bound.  The range is
-// +-128 for logits (steps of 2^-15) and [-1, 3) for choice scores (5e-7).
+// +-128 for logits (steps of 2^-15) and [-1, 3) for choice scores (5e-7; with
+// biases of at most 1 the first two steps and the bias are one multiply-add).
 //
 // A row's answer is kept only where it is certain: the k-th key above 0, the
 // first below the top of the range, no two neighbours among the k + 1 leading keys
-// of equal n (of scores: within one step) -- but for neighbours within the k whose
+// of equal n (of scores: within two steps) -- but for neighbours within the k whose
 // logits and biases are equal too, a true tie that the id in the key orders
 // (16-bit logits of size 2^-5 and more have exact keys, and need no check) --
 // and, with groups, the last kept group more
@@ -23,9 +24,10 @@
 // the other rows one by one with the exact keys of score_row.cuh.
 //
 // The weights are computed from the chosen logits, read again (they are in L1).
-// A softmax over the row takes its largest logit from the choice and one pass over
-// the registers; score sums take a second pass over the warp's rows from L1, in
-// which a lane owns columns, so that no atomics are needed.
+// A softmax over the row without a renormalisation, and score sums, take a pass
+// over the warp's rows from L1 in which a lane owns eight columns: exponentials
+// against the row's largest logit (from the choice), their sum across the row's
+// lanes, and the columns' sums in registers, so that no atomics are needed.
 #pragma once
 
 #include "pdl.cuh"
@@ -49,14 +51,39 @@ __device__ __forceinline__ bool exact_n(int n) {
   return EB == 2 && abs(n - 4194304) > 1024 && n > 0;
 }
 
-// Keys of a block's choices v = x or score: n = fixed point of v mul + add.
-__device__ __forceinline__ void block_keys(const float (&v)[8], float mul, float add, uint32_t key_mul, int pos,
-                                           int (&c)[8]) {
+// Keys of a block: t holds n in the low 23 bits of a number in [2^23, 2^24); 255 - id goes below n.
+__device__ __forceinline__ void block_ids(const float (&t)[8], uint32_t key_mul, int pos, int (&c)[8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float u = fma_sat(v[j], mul, add);
-    const float t = fmaf(u, 8388607.f, 8388608.f);
-    c[j] = (int)(__float_as_uint(t) * key_mul + (uint32_t)(255 - pos - j));
+  for (int j = 0; j < 8; ++j)
+    asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(c[j]) : "r"(__float_as_uint(t[j])), "r"(key_mul), "r"(255 - pos - j));
+}
+
+// Whether no logit of the blocks is infinite or NaN: the sum of their squares is
+// not (16-bit types in pairs; an f16 logit of 256 and more counts as far too).
+template <typename X, int N>
+__device__ __forceinline__ bool finite_blocks(const Raw<sizeof(X)> (&raw)[N]) {
+  if constexpr (sizeof(X) == 4) {
+    float sq = 0.f;
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sq = fmaf(raw[b].v[j], raw[b].v[j], sq);
+    return sq < 3e38f;
+  } else {
+    using P = typename std::conditional<std::is_same<X, __half>::value, __half2, __nv_bfloat162>::type;
+    uint32_t sq = 0u;
+#pragma unroll
+    for (int b = 0; b < N; ++b) {
+      const uint32_t w[4] = {raw[b].v.x, raw[b].v.y, raw[b].v.z, raw[b].v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const P v = *reinterpret_cast<const P*>(&w[j]);
+        const P s = __hfma2(v, v, *reinterpret_cast<const P*>(&sq));
+        sq = *reinterpret_cast<const uint32_t*>(&s);
+      }
+    }
+    constexpr uint32_t TOP = std::is_same<X, __half>::value ? 0x7C00u : 0x7F80u;  // exponent of infinity and NaN
+    return (sq & TOP) != TOP && (sq >> 16 & TOP) != TOP;
   }
 }
 
@@ -73,182 +100,275 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// BY_SCORE: the choice goes by scores (a bias, or groups ranked by two scores)
-// or there are groups; without it the logits alone order the experts.
-template <typename X, int G, int NB, bool BY_SCORE>
-__global__ void __launch_bounds__(SF_WARPS * 32, 4) score_fast_kernel(const ScoreParams p) {
+// A lane's choices, `own` of them (or OUT): in pairs where k is even (`even` 1: the
+// weights are on 8 bytes; 2: k = 8 and they are on 16, one store of all).
+template <int OUT>
+__device__ __forceinline__ void put_weights(float* to, int own, int even, const float (&w)[OUT]) {
+  if (even == 2) {
+    if constexpr (OUT == 2) {
+      *reinterpret_cast<float2*>(to) = make_float2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < OUT; j += 4)
+        *reinterpret_cast<float4*>(to + j) = make_float4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+    }
+  } else if (even == 1) {
+#pragma unroll
+    for (int j = 0; j < OUT; j += 2)
+      if (j < own) *reinterpret_cast<float2*>(to + j) = make_float2(w[j], w[j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < OUT; ++j)
+      if (j < own) to[j] = w[j];
+  }
+}
+template <int OUT>
+__device__ __forceinline__ void put_ids(uint8_t* to, int own, int even, const int (&id)[OUT]) {
+  if (even == 2) {  // 8 ids a row, on 8 bytes
+    uint32_t v[OUT / 4 + 1];
+    if constexpr (OUT == 2) {
+      *reinterpret_cast<uint16_t*>(to) = (uint16_t)(id[0] | id[1] << 8);
+    } else {
+#pragma unroll
+      for (int j = 0; j < OUT; j += 4)
+        v[j / 4] = (uint32_t)(id[j] | id[j + 1] << 8) | (uint32_t)(id[j + 2] | id[j + 3] << 8) << 16;
+      if constexpr (OUT == 4)
+        *reinterpret_cast<uint32_t*>(to) = v[0];
+      else
+        *reinterpret_cast<uint2*>(to) = make_uint2(v[0], v[1]);
+    }
+  } else if (even == 1) {
+#pragma unroll
+    for (int j = 0; j < OUT; j += 2)
+      if (j < own) *reinterpret_cast<uint16_t*>(to + j) = (uint16_t)(id[j] | id[j + 1] << 8);
+  } else {
+#pragma unroll
+    for (int j = 0; j < OUT; ++j)
+      if (j < own) to[j] = (uint8_t)id[j];
+  }
+}
+
+// What the choice goes by.
+enum ScoreKind {
+  BY_LOGIT = 0,        // the logits alone; weights from the chosen ones
+  BY_LOGIT_DENSE = 1,  // the logits; with the column pass
+  BY_SCORE = 2         // scores (a bias, or groups ranked by two scores), or groups
+};
+
+template <typename X, int G, int NB, int KIND>
+__global__ void __launch_bounds__(SF_WARPS * 32, 5) score_fast_kernel(const ScoreParams p) {
   constexpr int RW = 32 / G;            // rows of a warp at a time
   constexpr int EB = sizeof(X);
-  constexpr int NQ = G > 2 ? 2 : 1;     // quads of a lane in the column passes
+  constexpr int NQ = G > 2 ? 2 : 1;     // quads of a lane on the exact path
   constexpr int OUT = 8 / G;            // choices of a lane
-  __shared__ float sbias[256];
-  __shared__ float part[SF_WARPS][32 * 4 * NQ];
+  constexpr int CL = 8 * G;             // lanes of a row in the column pass
+  constexpr int PF = NB % 4 == 0 ? 4 : NB % 3 == 0 ? 3 : 2;  // blocks in flight: a block's registers take the one PF ahead
+  static_assert(NB % PF == 0, "whole rounds of the block buffers");
+  constexpr int ROUNDS = KIND == BY_SCORE ? 1 : NB / PF;  // unrolled (the longer body: rolled, for the instruction cache)
+  __shared__ __align__(16) float sbias[KIND == BY_SCORE ? 256 : 1];
+  __shared__ float part[SF_WARPS][KIND != BY_LOGIT ? 8 * CL : 1];
+  __shared__ int4 lists[KIND == BY_SCORE ? SF_WARPS : 1][KIND == BY_SCORE ? NB : 1][2][32];  // sorted blocks
   __shared__ float2 row_mr[SF_WARPS][RW];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane % G, rl = lane / G;
   const int l = blockIdx.x / p.nspan, unit = blockIdx.x - l * p.nspan;
   const bool soft = p.score == MOER_SCORE_SOFTMAX;
-  const bool has_bias = BY_SCORE && p.bias != nullptr;
-  const bool use_s = BY_SCORE && (has_bias || (p.n_group > 1 && p.group_best == 2));
-  const bool sums = p.partial != nullptr;
-  const bool dense_soft = soft && (sums || use_s || !p.renorm);
-  if (has_bias)
-    for (int e = threadIdx.x; e < 256; e += SF_WARPS * 32) sbias[e] = e < p.E ? p.bias[(size_t)l * p.E + e] : 0.f;
-  __syncthreads();
-  float acc[4 * NQ];
+  const bool has_bias = KIND == BY_SCORE && p.bias != nullptr;
+  const bool use_s = KIND == BY_SCORE && (has_bias || (p.n_group > 1 && p.group_best == 2));
+  const bool sums = KIND != BY_LOGIT && p.partial != nullptr;
+  const bool columns = KIND != BY_LOGIT && (sums || (soft && !p.renorm));
+  // biases of at most 1 in size: n = s 2^21 + (b + 1) 2^21 in one multiply-add, at most one step off
+  bool tight = true;
+  if (use_s) {
+    bool in = true;
+    for (int e = threadIdx.x; e < 256; e += SF_WARPS * 32) {
+      sbias[e] = has_bias && e < p.E ? p.bias[(size_t)l * p.E + e] : 0.f;
+      in = in && fabsf(sbias[e]) <= 1.f;
+    }
+    tight = __syncthreads_and(in) != 0;
+    if (tight)
+      for (int e = threadIdx.x; e < 256; e += SF_WARPS * 32) sbias[e] = fmaf(sbias[e], 2097152.f, 10485760.f);
+    __syncthreads();
+  }
+  // steps of n that do not settle an order: a score is rounded before its key is
+  const int near = use_s ? 2 : 0;
+  float acc[8];
 #pragma unroll
-  for (int q = 0; q < 4 * NQ; ++q) acc[q] = 0.f;
+  for (int q = 0; q < 8; ++q) acc[q] = 0.f;
   const X* base = static_cast<const X*>(p.logits) + l * p.ld_layer;
   const int64_t t1 = min64(p.T, (int64_t)(unit + 1) * p.span);
-  for (int64_t t0 = (int64_t)unit * p.span + warp * RW; t0 < t1; t0 += SF_WARPS * RW) {
-    const bool live = t0 + rl < t1;
-    const int64_t t = live ? t0 + rl : t1 - 1;
-    const X* row = base + t * p.ld_token;
-    Raw<EB> raw[NB];
+  int64_t t0 = (int64_t)unit * p.span + warp * RW;
+  // rows past the unit's end read its last row again
+  auto row_at = [&](int64_t t) { return base + min64(t + rl, t1 - 1) * p.ld_token; };
+  Raw<EB> raw[PF];
+  const bool full = p.E == 8 * G * NB && p.wide != 0;  // every block whole, on 16 bytes
+  auto fetch = [&](Raw<EB>& to, int b, const X* of) {
+    const int e = 8 * (i + G * b);
+    if (full)
+      to.template load<X>(of + e, 8, true);
+    else
+      to.template load<X>(of + e, p.E - e, p.wide != 0);
+  };
+  const X* row = t0 < t1 ? row_at(t0) : base;
+  if (t0 < t1)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int e = 8 * (i + G * b);
-      raw[b].template load<X>(row + e, p.E - e, p.wide != 0);
-    }
+    for (int j = 0; j < PF; ++j) fetch(raw[j], j, row);
+  for (; t0 < t1; t0 += SF_WARPS * RW) {
+    const bool live = t0 + rl < t1;
+    const bool more = t0 + SF_WARPS * RW < t1;
+    const X* next = more ? row_at(t0 + SF_WARPS * RW) : row;
     int top[8], ninth = INT_MIN;
     bool bad = false;
-    float m = 0.f, rz = 0.f;
-    if constexpr (!BY_SCORE) {
-#pragma unroll
+    float mm = 0.f, rs = 1.f;
+    if (KIND == BY_SCORE && use_s && soft) {
+      // the softmax first: the row from L1 twice, its largest logit and the sum
+      float m = NEG_INF, z = 0.f;
       for (int b = 0; b < NB; ++b) {
+        Raw<EB> again;
+        fetch(again, b, row);
         float x[8];
-        raw[b].template get<X>(x);
+        again.template get<X>(x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, x[j]);
+      }
+      m = row_max<G>(m);
+      bad = !(fabsf(m) < 128.f);  // nothing but masks, or infinities: left to the exact path
+      mm = bad ? 0.f : m * LOG2E;
+      for (int b = 0; b < NB; ++b) {
+        Raw<EB> again;
+        fetch(again, b, row);
+        float x[8];
+        again.template get<X>(x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z += ex2_approx(fmaf(fmaxf(x[j], NEG_INF), LOG2E, -mm));
+      }
+      rs = rcp_approx(row_sum<G>(z));
+    }
+#pragma unroll ROUNDS
+    for (int g = 0; g < NB; g += PF) {
+      const bool last_round = g + PF == NB;
+      bool far = false;  // some logit of the round is infinite or NaN (experts past the row's end are -inf)
+      if (use_s) far = __any_sync(FULL, !finite_blocks<X, PF>(raw));
+#pragma unroll
+      for (int j0 = 0; j0 < PF; ++j0) {
+        const int b = g + j0;
+        float x[8];
+        raw[j0].template get<X>(x);
+        if (!last_round)
+          fetch(raw[j0], b + PF, row);
+        else if (more)
+          fetch(raw[j0], j0, next);
         int c[8];
-        block_keys(x, 1.f / 256.f, 0.5f, p.key_mul, 8 * G * b, c);
+        if (use_s) {
+          uint32_t masked = 0u;
+          if (far) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              x[j] = fmaxf(x[j], NEG_INF);  // NaN -> -inf
+              if (x[j] == NEG_INF) masked |= 1u << j;
+            }
+          }
+          const int e = 8 * (i + G * b);
+          const float4 b0 = *reinterpret_cast<const float4*>(&sbias[e]), b1 = *reinterpret_cast<const float4*>(&sbias[e + 4]);
+          const float bias[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+          if (soft) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = ex2_approx(fmaf(x[j], LOG2E, -mm)) * rs;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = rcp_approx(1.f + ex2_approx(-LOG2E * x[j]));
+          }
+          if (tight) {  // n in one step, the bias holding the rest
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], 2097152.f, bias[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = fmaf(fma_sat(x[j] + bias[j], 0.25f, 0.25f), 8388607.f, 8388608.f);
+          }
+          block_ids(x, p.key_mul, 8 * G * b, c);
+          if (far) {  // masked experts stay out whatever their bias
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if ((masked >> j) & 1u) c[j] &= 255;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = fmaf(fma_sat(x[j], 1.f / 256.f, 0.5f), 8388607.f, 8388608.f);
+          block_ids(x, p.key_mul, 8 * G * b, c);
+        }
         sort8_desc(c);
-        if (b == 0) {
+        if (KIND == BY_SCORE && p.n_group > 1) {
+          lists[warp][b][0][lane] = make_int4(c[0], c[1], c[2], c[3]);
+          lists[warp][b][1][lane] = make_int4(c[4], c[5], c[6], c[7]);
+        } else if (j0 == 0 && g == 0) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) top[j] = c[j];
         } else {
           merge8<true>(top, c, ninth);
         }
       }
-    } else {
-      float v[NB][8];
+    }
+    if (KIND == BY_SCORE && p.n_group > 1) {
+      // a group is mb blocks of every lane of the row
+      const int sh = 31 - __clz(p.E / p.n_group / (8 * G)), mb = 1 << sh;
+      int g1[8], g2[8], gk[8];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) raw[b].template get<X>(v[b]);
-      if (dense_soft) {
-        m = NEG_INF;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) m = fmaxf(m, v[b][j]);
-        m = row_max<G>(m);
-        bad = !(fabsf(m) < 128.f);  // nothing but masks, or infinities: left to the exact path
-        float z = 0.f;
-        const float mm = bad ? 0.f : m * LOG2E;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z += ex2_approx(fmaf(fmaxf(v[b][j], NEG_INF), LOG2E, -mm));
-        rz = rcp_approx(row_sum<G>(z));
-      }
-      if (use_s) {
-        float sq = 0.f;  // infinite or NaN: some logit is
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sq = fmaf(v[b][j], v[b][j], sq);
-        // (experts past the row's end are -inf here)
-        const bool far = __any_sync(FULL, !(sq < 3e38f));
-        const float mm = m * LOG2E;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const int e = 8 * (i + G * b);
-          float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (has_bias) {
-            const float4 b0 = *reinterpret_cast<const float4*>(&sbias[e]), b1 = *reinterpret_cast<const float4*>(&sbias[e + 4]);
-            bias[0] = b0.x, bias[1] = b0.y, bias[2] = b0.z, bias[3] = b0.w;
-            bias[4] = b1.x, bias[5] = b1.y, bias[6] = b1.z, bias[7] = b1.w;
-          }
-          float s[8];
-          if (soft) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] = ex2_approx(fmaf(v[b][j], LOG2E, -mm)) * rz;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float x = far ? fmaxf(v[b][j], NEG_INF) : v[b][j];  // NaN -> -inf
-              s[j] = rcp_approx(1.f + ex2_approx(-LOG2E * x));
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float c = s[j] + bias[j];
-            v[b][j] = far && !(v[b][j] > NEG_INF) ? NEG_INF : c;  // masked experts stay out whatever their bias
-          }
-        }
-      }
-      int key[NB][8];
-      const float mul = use_s ? 0.25f : 1.f / 256.f, add = use_s ? 0.25f : 0.5f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        block_keys(v[b], mul, add, p.key_mul, 8 * G * b, key[b]);
-        sort8_desc(key[b]);
-      }
-      if (p.n_group > 1) {
-        // a group is m blocks of every lane of the row
-        const int sh = 31 - __clz(p.E / p.n_group / (8 * G)), mb = 1 << sh;
-        int g1[8], g2[8], gk[8];
-#pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          g1[b] = b < NB ? key[b < NB ? b : 0][0] >> 8 : -1;
-          g2[b] = b < NB ? key[b < NB ? b : 0][1] >> 8 : -1;
-        }
-#pragma unroll
-        for (int s = 1; s < 8; s *= 2)
-          if (s < mb)
-#pragma unroll
-            for (int b = 0; b < 8; b += 2 * s) {
-              g2[b] = max(max(g2[b], g2[b + s]), min(g1[b], g1[b + s]));
-              g1[b] = max(g1[b], g1[b + s]);
-            }
-#pragma unroll
-        for (int b = 0; b < 8; ++b) {
-#pragma unroll
-          for (int o = 1; o < G; o *= 2) {
-            const int h1 = __shfl_xor_sync(FULL, g1[b], o), h2 = __shfl_xor_sync(FULL, g2[b], o);
-            g2[b] = max(max(g2[b], h2), min(g1[b], h1));
-            g1[b] = max(g1[b], h1);
-          }
-          const bool first = (b & (mb - 1)) == 0 && (b >> sh) < p.n_group;
-          // the second best counts only where there are two numbers to add
-          if (first && p.group_best == 2 && g2[b] <= 0) bad = true;
-          g1[b] += p.group_best == 2 ? g2[b] : 0;
-          gk[b] = first ? g1[b] * 8 + (7 - (b >> sh)) : INT_MIN;
-        }
-        sort8_desc(gk);
-        int thr = gk[0], nxt = gk[1];
-#pragma unroll
-        for (int r = 1; r < 7; ++r)
-          if (r < p.top_group) thr = gk[r], nxt = gk[r + 1];
-        // the sum of two scores' keys can be two steps off either way; equal keys of
-        // logits may stand in either order, unless they hold their logits exactly
-        if ((thr >> 3) - (nxt >> 3) <= (use_s ? 4 : 0) && (use_s || !exact_n<EB>(thr >> 3))) bad = true;
-        int keep = 0;
-#pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          const bool first = (b & (mb - 1)) == 0;
-          keep = first ? (g1[b] * 8 + (7 - (b >> sh)) >= thr ? 1 : 0) : keep;
-          if (b < NB)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) key[b][j] *= keep;  // on the FMA pipe; 0 is below every key
-        }
+      for (int b = 0; b < 8; ++b) {
+        const int2 two = b < NB ? *reinterpret_cast<const int2*>(&lists[warp][b < NB ? b : 0][0][lane]) : make_int2(0, 0);
+        g1[b] = two.x >> 8;
+        g2[b] = two.y >> 8;
       }
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if (b == 0) {
+      for (int s = 1; s < 8; s *= 2)
+        if (s < mb)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top[j] = key[0][j];
-        } else {
-          merge8<true>(top, key[b], ninth);
+          for (int b = 0; b < 8; b += 2 * s) {
+            g2[b] = max(max(g2[b], g2[b + s]), min(g1[b], g1[b + s]));
+            g1[b] = max(g1[b], g1[b + s]);
+          }
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+#pragma unroll
+        for (int o = 1; o < G; o *= 2) {
+          const int h1 = __shfl_xor_sync(FULL, g1[b], o), h2 = __shfl_xor_sync(FULL, g2[b], o);
+          g2[b] = max(max(g2[b], h2), min(g1[b], h1));
+          g1[b] = max(g1[b], h1);
         }
+        const bool first = (b & (mb - 1)) == 0 && (b >> sh) < p.n_group;
+        // the second best counts only where there are two numbers to add
+        if (first && p.group_best == 2 && g2[b] <= 0) bad = true;
+        g1[b] += p.group_best == 2 ? g2[b] : 0;
+        g1[b] = gk[b] = first ? g1[b] * 8 + (7 - (b >> sh)) : INT_MIN;
+      }
+      sort8_desc(gk);
+      int thr = gk[0], nxt = gk[1];
+#pragma unroll
+      for (int r = 1; r < 7; ++r)
+        if (r < p.top_group) thr = gk[r], nxt = gk[r + 1];
+      // the sum of two scores' keys can be three steps off either way; equal keys of
+      // logits may stand in either order, unless they hold their logits exactly
+      if ((thr >> 3) - (nxt >> 3) <= 3 * near && (use_s || !exact_n<EB>(thr >> 3))) bad = true;
+      unsigned keep = 0u;  // the first blocks of the kept groups
+#pragma unroll
+      for (int b = 0; b < 8; ++b)
+        if (g1[b] >= thr) keep |= 1u << b;
+      for (int r = 1; r < mb; r *= 2) keep |= keep << r;  // and the others
+      // their lists, each row's own; a single list's eight are all there is
+      ninth = 0;
+      {
+        const int b0 = __ffs(keep) - 1;
+        keep &= keep - 1u;
+        const int4 u = lists[warp][b0][0][lane], v = lists[warp][b0][1][lane];
+        top[0] = u.x, top[1] = u.y, top[2] = u.z, top[3] = u.w;
+        top[4] = v.x, top[5] = v.y, top[6] = v.z, top[7] = v.w;
+      }
+      for (int q = 1; q < p.top_group * mb; ++q) {
+        const int b0 = __ffs(keep) - 1;
+        keep &= keep - 1u;
+        const int4 u = lists[warp][b0][0][lane], v = lists[warp][b0][1][lane];
+        const int c[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        merge8<true>(top, c, ninth);
       }
     }
     // ids of the row: the lane's own part comes off the inverted position
@@ -264,95 +384,69 @@ __global__ void __launch_bounds__(SF_WARPS * 32, 4) score_fast_kernel(const Scor
       merge8<true>(top, other, ninth);
       ninth = max(ninth, n9);
     }
-    // the lane's choices: j = i, i + G, ...
-    float xj[OUT], bj[OUT];
+    // the lane's choices: i OUT .. i OUT + OUT - 1
+    float xj[OUT];
     int mine[OUT];
-    const int near = use_s ? 1 : 0;     // steps of n that do not settle an order: a score is rounded before its key is
-    int last = top[0], after = top[1];  // the k-th key and the one after it
-#pragma unroll
-    for (int j = 1; j < 8; ++j)
-      if (j < p.k) last = top[j], after = j + 1 < 8 ? top[j + 1 < 8 ? j + 1 : 0] : ninth;
-    bad = bad || last < 256 || (top[0] >> 8) >= 8388607 ||
-          ((last >> 8) - (after >> 8) <= near && (use_s || !exact_n<EB>(last >> 8)));
 #pragma unroll
     for (int jj = 0; jj < OUT; ++jj) {
-      int c = top[jj * G];
+      int c = top[jj];
 #pragma unroll
       for (int g = 1; g < G; ++g)
-        if (i == g) c = top[jj * G + g];
-      mine[jj] = c;
-      const int e = 255 - (c & 255);
-      const bool on = jj * G + i < p.k && e < p.E;
-      xj[jj] = on ? live_logit(Quad<X>::one(row[e])) : NEG_INF;
-      bj[jj] = has_bias ? sbias[e] : 0.f;
+        if (i == g) c = top[g * OUT + jj];
+      mine[jj] = 255 - (c & 255);
+      xj[jj] = NEG_INF;
+      if (i * OUT + jj < p.k && mine[jj] < p.E) xj[jj] = Quad<X>::one(row[mine[jj]]);
     }
-    // neighbours of equal n have to be a true tie
-    bool tie = false;
+    int after = ninth, least = INT_MAX;  // the key after the k-th, the closest two of the k + 1
+#pragma unroll
+    for (int j = 7; j >= 1; --j)
+      if (j >= p.k) after = top[j];
 #pragma unroll
     for (int j = 1; j < 8; ++j)
-      if (j < p.k && (top[j - 1] >> 8) - (top[j] >> 8) <= near && (use_s || !exact_n<EB>(top[j] >> 8))) tie = true;
-    if (__any_sync(FULL, tie)) {
+      if (j < p.k) least = min(least, top[j - 1] - top[j]);
+    int last = top[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j)
+      if (j < p.k) last = top[j];
+    least = min(least, last - after);
+    bad = bad || last < 256 || (top[0] >> 8) >= 8388607;
+    // all leading keys positive logits that their n hold exactly: the ids order equal ones
+    const bool sure = EB == 2 && !use_s && after > (4194304 + 1024) * 256 + 255;
+    if (__any_sync(FULL, !sure && least < 256 * (near + 1))) {
+      // neighbours that the keys do not settle have to be a true tie
+      auto open = [&](int hi, int lo) { return (hi >> 8) - (lo >> 8) <= near && (use_s || !exact_n<EB>(lo >> 8)); };
+      if (open(last, after)) bad = true;
 #pragma unroll
       for (int j = 1; j < 8; ++j) {
-        const int from = rl * G + j % G, prev = rl * G + (j - 1) % G;
-        const float a = __shfl_sync(FULL, xj[j / G], from), b = __shfl_sync(FULL, xj[(j - 1) / G], prev);
-        const float c = __shfl_sync(FULL, bj[j / G], from), d = __shfl_sync(FULL, bj[(j - 1) / G], prev);
-        if (j < p.k && (top[j - 1] >> 8) - (top[j] >> 8) <= near && !(a == b && c == d)) bad = true;
+        const float a = __shfl_sync(FULL, xj[j % OUT], rl * G + j / OUT);
+        const float b = __shfl_sync(FULL, xj[(j - 1) % OUT], rl * G + (j - 1) / OUT);
+        const int ea = 255 - (top[j] & 255), eb = 255 - (top[j - 1] & 255);
+        const bool same = a == b && (!has_bias || (max(ea, eb) < p.E && p.bias[(size_t)l * p.E + ea] == p.bias[(size_t)l * p.E + eb]));
+        if (j < p.k && open(top[j - 1], top[j]) && !same) bad = true;
       }
     }
-    if constexpr (!BY_SCORE) {
-      if (dense_soft) {
-        m = __shfl_sync(FULL, xj[0], rl * G);  // the first choice is the largest logit
-        const float mm = fabsf(m) < 1e30f ? m * LOG2E : 0.f;
-        float z = 0.f;
+    // rows that are not settled, one by one
+    float m = KIND != BY_SCORE ? __shfl_sync(FULL, xj[0], rl * G) : 0.f;  // the first choice is the largest logit
+    if (KIND == BY_SCORE && columns) {
+      if (soft) {  // the largest logit may lie in a group that is dropped
+        m = NEG_INF;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
+          const int e = 8 * (i + G * b);
+          Raw<EB> again;
+          again.template load<X>(row + e, p.E - e, p.wide != 0);
           float x[8];
-          raw[b].template get<X>(x);
+          again.template get<X>(x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) z += ex2_approx(fmaf(fmaxf(x[j], NEG_INF), LOG2E, -mm));
+          for (int j = 0; j < 8; ++j) m = fmaxf(m, x[j]);
         }
-        rz = rcp_approx(row_sum<G>(z));
+        m = row_max<G>(m);
+        bad = bad || !(fabsf(m) < 128.f);
       }
     }
-    const int64_t out = ((int64_t)l * p.T + t) * p.k;
-    const bool write = live && !bad;
-    if (p.weights != nullptr) {
-      float w[OUT], z = 0.f;
-      if (soft) {
-        float mk = m;
-        if (p.renorm) {
-          mk = NEG_INF;
-#pragma unroll
-          for (int jj = 0; jj < OUT; ++jj) mk = fmaxf(mk, xj[jj]);
-          mk = row_max<G>(mk);
-        }
-#pragma unroll
-        for (int jj = 0; jj < OUT; ++jj) w[jj] = exp_below(xj[jj], mk);
-      } else {
-#pragma unroll
-        for (int jj = 0; jj < OUT; ++jj) w[jj] = sigmoid(xj[jj]);
-      }
-#pragma unroll
-      for (int jj = 0; jj < OUT; ++jj) z += w[jj];
-      float f = soft ? rz : 1.f;
-      if (p.renorm) {
-        z = row_sum<G>(z);
-        f = z > 0.f ? 1.f / z : 0.f;
-      }
-      f *= p.scale;
-#pragma unroll
-      for (int jj = 0; jj < OUT; ++jj)
-        if (write && jj * G + i < p.k) p.weights[out + jj * G + i] = w[jj] * f;
-    }
-#pragma unroll
-    for (int jj = 0; jj < OUT; ++jj)
-      if (write && jj * G + i < p.k) p.topk[out + jj * G + i] = (uint8_t)(255 - (mine[jj] & 255));
-    if (sums && i == 0) row_mr[warp][rl] = make_float2(m, rz);
-    // rows that are not settled, one by one
+    if (columns && i == 0) row_mr[warp][rl] = make_float2(m, 0.f);
     unsigned todo = __ballot_sync(FULL, bad && live && i == 0);
     const bool careful = todo != 0u;
-    __syncwarp();
     while (todo != 0u) {
       const int f = (__ffs(todo) - 1) / G;
       todo &= todo - 1;
@@ -360,52 +454,103 @@ __global__ void __launch_bounds__(SF_WARPS * 32, 4) score_fast_kernel(const Scor
 #pragma unroll
       for (int q = 0; q < 4 * NQ; ++q) {
         const int e = 4 * (lane + 32 * (q / 4)) + q % 4;
-        bias[q] = has_bias ? sbias[e & 255] : 0.f;
+        bias[q] = has_bias && e < p.E ? p.bias[(size_t)l * p.E + e] : 0.f;
         none[q] = 0.f;
       }
-      const float2 mr = score_row<X, NQ>(p, base + (t0 + f) * p.ld_token, bias, (int64_t)l * p.T + t0 + f, lane, none);
-      if (sums && lane == 0) row_mr[warp][f] = mr;
-    }
-    if (sums) {
-      // a lane's columns: LR lanes hold a row's quads, 32 / LR rows at a time
-      const int LR = p.E <= 32 ? 8 : p.E <= 64 ? 16 : 32;
-      const int col = lane % LR;
       __syncwarp();
-      const int rows = (int)min64(RW, t1 - t0);
-      for (int r = lane / LR; r < rows; r += 32 / LR) {
-        const X* at = base + (t0 + r) * p.ld_token;
-        const float2 mr = soft ? row_mr[warp][r] : make_float2(0.f, 0.f);
-        const float mm = mr.x * LOG2E;
+      const int64_t at = ((int64_t)l * p.T + t0 + f) * p.k;
+      const float rm = score_row<X, NQ>(p, base + (t0 + f) * p.ld_token, bias, p.topk + at,
+                                        p.weights != nullptr ? p.weights + at : nullptr, lane, none);
+      if (columns && lane == 0) row_mr[warp][f].x = rm;
+    }
+    const int rows = (int)min64(RW, t1 - t0);
+    float rz = 1.f;
+    if (columns) {
+      __syncwarp();
+      const int col = lane % CL, e = 8 * col;
+      const X* at = base + t0 * p.ld_token + e;
+#pragma unroll 2
+      for (int s = 0; s < 8; ++s) {
+        const int r = s * (4 / G) + lane / CL;
+        float x[8];
+        Raw<EB> line;
+        if (full && e < p.E)  // the row may have fewer columns than its lanes own
+          line.template load<X>(at + (int64_t)min(r, rows - 1) * p.ld_token, 8, true);
+        else
+          line.template load<X>(at + (int64_t)min(r, rows - 1) * p.ld_token, p.E - e, p.wide != 0);
+        line.template get<X>(x);
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          const int e = 4 * (col + 32 * q);
-          if (e < p.E) {
-            float x[4];
-            load4<X>(at + e, true, x);
+        for (int j = 0; j < 8; ++j) x[j] = fmaxf(x[j], NEG_INF);  // NaN -> -inf
+        if (soft) {
+          const float mr = row_mr[warp][r].x, mm = mr * LOG2E;
+          float z = 0.f;
+          if (careful) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float v = fmaxf(x[j], NEG_INF);  // NaN -> -inf
-              float s;
-              if (soft)
-                s = (careful ? exp_below(v, mr.x) : ex2_approx(fmaf(v, LOG2E, -mm))) * mr.y;
-              else
-                s = rcp_approx(1.f + ex2_approx(-LOG2E * v));
-              acc[4 * q + j] += s;
-            }
+            for (int j = 0; j < 8; ++j) x[j] = exp_below(x[j], mr);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = ex2_approx(fmaf(x[j], LOG2E, -mm));
           }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z += x[j];
+          z = row_sum<CL>(z);
+          const float rr = z > 0.f ? rcp_approx(z) : 0.f;
+          if (col == 0) row_mr[warp][r].y = rr;
+          if (sums && r < rows)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = fmaf(x[j], rr, acc[j]);
+        } else if (r < rows) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] += rcp_approx(1.f + ex2_approx(-LOG2E * x[j]));
         }
       }
       __syncwarp();
+      if (soft) rz = row_mr[warp][rl].y;
     }
+    // ids and weights of the settled rows (their k-th key is above 0: the chosen
+    // logits are numbers, or +inf only where the first key is out of range)
+    const int64_t out = ((int64_t)l * p.T + t0 + rl) * p.k + i * OUT;
+    const bool write = live && !bad;
+    const int own = p.k - i * OUT;  // choices of this lane, where below OUT
+    float w[OUT];
+    if (p.weights != nullptr) {
+      if (soft) {
+        float mk = m;  // without groups and biases the row's largest logit is the first choice
+        if (KIND == BY_SCORE && p.renorm) {
+          mk = xj[0];
+#pragma unroll
+          for (int jj = 1; jj < OUT; ++jj) mk = fmaxf(mk, xj[jj]);
+          mk = row_max<G>(mk);
+        }
+#pragma unroll
+        for (int jj = 0; jj < OUT; ++jj) w[jj] = ex2_approx(LOG2E * (xj[jj] - mk));
+      } else {
+#pragma unroll
+        for (int jj = 0; jj < OUT; ++jj) w[jj] = rcp_approx(1.f + ex2_approx(-LOG2E * xj[jj]));
+      }
+      float f = soft ? rz : 1.f;
+      if (p.renorm) {
+        float z = 0.f;
+#pragma unroll
+        for (int jj = 0; jj < OUT; ++jj) z += w[jj];
+        z = row_sum<G>(z);
+        f = z > 0.f ? rcp_approx(z) : 0.f;
+      }
+      f *= p.scale;
+#pragma unroll
+      for (int jj = 0; jj < OUT; ++jj) w[jj] *= f;
+      if (write) put_weights<OUT>(p.weights + out, own, p.even, w);
+    }
+    if (write) put_ids<OUT>(p.topk + out, own, p.even, mine);
+    row = next;
   }
   if (sums) {
-    const int LR = p.E <= 32 ? 8 : p.E <= 64 ? 16 : 32;
 #pragma unroll
-    for (int q = 0; q < 4 * NQ; ++q) {
+    for (int q = 0; q < 8; ++q) {
       float v = acc[q];
-      if (LR <= 16) v += __shfl_xor_sync(FULL, v, 16);
-      if (LR <= 8) v += __shfl_xor_sync(FULL, v, 8);
-      part[warp][4 * (lane + 32 * (q / 4)) + q % 4] = v;
+#pragma unroll
+      for (int o = CL; o < 32; o *= 2) v += __shfl_xor_sync(FULL, v, o);
+      if (lane < CL) part[warp][8 * lane + q] = v;
     }
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += SF_WARPS * 32) {
@@ -421,8 +566,10 @@ __global__ void __launch_bounds__(SF_WARPS * 32, 4) score_fast_kernel(const Scor
 template <typename X, int G, int NB>
 cudaError_t score_fast_shape(const ScoreParams& p, cudaStream_t st) {
   const dim3 grid(p.L * p.nspan), block(SF_WARPS * 32);
-  return p.bias != nullptr || p.n_group > 1 ? launch_pdl(score_fast_kernel<X, G, NB, true>, grid, block, 0, st, p)
-                                            : launch_pdl(score_fast_kernel<X, G, NB, false>, grid, block, 0, st, p);
+  if (p.bias != nullptr || p.n_group > 1) return launch_pdl(score_fast_kernel<X, G, NB, BY_SCORE>, grid, block, 0, st, p);
+  if (p.partial != nullptr || (p.score == MOER_SCORE_SOFTMAX && !p.renorm))
+    return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT_DENSE>, grid, block, 0, st, p);
+  return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT>, grid, block, 0, st, p);
 }
 
 template <typename X>

@@ -35,16 +35,16 @@ __device__ uint32_t group_keys(const ScoreParams& p, const uint32_t (&key)[4 * N
   return mine;
 }
 
-// One row by one warp: ids and weights to row `out` of the outputs; with sums
-// wanted, the lane's scores are added to `sum`.  Returns the softmax's largest
-// logit and 1 / sum (0 where every expert is masked) where those were formed.
+// One row by one warp: the k ids and weights to `ids` and `weights` (or NULL); with
+// sums wanted, the lane's scores are added to `sum`.  Returns the softmax's
+// largest logit where it was formed.
 template <typename X, int NQ>
-__device__ float2 score_row(const ScoreParams& p, const X* row, const float (&bias)[4 * NQ], int64_t out, int lane,
-                            float (&sum)[4 * NQ]) {
+__device__ float score_row(const ScoreParams& p, const X* row, const float (&bias)[4 * NQ], uint8_t* ids,
+                           float* weights, int lane, float (&sum)[4 * NQ]) {
   const bool soft = p.score == MOER_SCORE_SOFTMAX;
   const bool use_s = p.bias != nullptr || (p.n_group > 1 && p.group_best == 2);  // the choice takes scores
   const bool dense = p.partial != nullptr || use_s || (soft && !p.renorm);
-  float x[4 * NQ], s[4 * NQ], row_m = NEG_INF, row_r = 0.f;
+  float x[4 * NQ], s[4 * NQ], row_m = NEG_INF;
   uint32_t key[4 * NQ];
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
@@ -73,7 +73,6 @@ __device__ float2 score_row(const ScoreParams& p, const X* row, const float (&bi
       }
       z = warp_sum(z);
       const float r = z > 0.f ? 1.f / z : 0.f;
-      row_r = r;
 #pragma unroll
       for (int i = 0; i < 4 * NQ; ++i) s[i] *= r;
     } else {
@@ -129,8 +128,8 @@ __device__ float2 score_row(const ScoreParams& p, const X* row, const float (&bi
     for (int i = 0; i < 4 * NQ; ++i)
       if (e == 4 * (lane + 32 * (i / 4)) + i % 4) key[i] = 0u;
   }
-  if (lane < p.k) p.topk[out * p.k + lane] = (uint8_t)id;
-  if (p.weights != nullptr) {
+  if (lane < p.k) ids[lane] = (uint8_t)id;
+  if (weights != nullptr) {
     float w;
     if (by_logit) {
       const float v = lane < p.k ? val : NEG_INF;
@@ -143,9 +142,9 @@ __device__ float2 score_row(const ScoreParams& p, const X* row, const float (&bi
       const float z = warp_sum(w);
       w = z > 0.f ? w / z : 0.f;
     }
-    if (lane < p.k) p.weights[out * p.k + lane] = p.scale * w;
+    if (lane < p.k) weights[lane] = p.scale * w;
   }
-  return make_float2(row_m, row_r);
+  return row_m;
 }
 
 }  // namespace moer

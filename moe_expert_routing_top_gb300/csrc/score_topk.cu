@@ -23,6 +23,7 @@ constexpr int SC_WARPS = 8;
 constexpr int SC_UNITS = 4864;  // units asked for: 152 SMs x 32
 
 constexpr int64_t SC_FAST_ROWS = 4096;  // rows from which the fast kernel is taken
+constexpr int SC_FAST_RESIDENT = 5;     // its blocks on an SM
 
 // Tokens of a unit: a multiple of `step`, the rows that a block takes at a time.
 int score_span(int64_t T, int L, int step) {
@@ -30,6 +31,23 @@ int score_span(int64_t T, int L, int step) {
   return (int)((s + step - 1) / step * step);
 }
 int score_nspan(int64_t T, int span) { return (int)((T + span - 1) / span); }
+
+// Tokens of a unit of the fast kernel, whose blocks take `step` rows at a time and
+// are resident `slots` at once: the fewest rounds, a unit's start counted as one,
+// over whole waves of units, and no more units than the general kernel has
+// (the workspace holds a partial sum for each).
+int fast_span(int64_t T, int L, int step, int64_t slots) {
+  const int most = score_nspan(T, score_span(T, L, SC_WARPS));
+  int64_t best = -1, cost = 0;
+  for (int64_t rounds = 1; rounds <= 64 || best < 0; ++rounds) {
+    const int64_t units = (T + rounds * step - 1) / (rounds * step);
+    if (units > most) continue;
+    const int64_t c = (units * L + slots - 1) / slots * (rounds + 1);
+    if (best < 0 || c < cost) best = rounds, cost = c;
+    if (units == 1) break;
+  }
+  return (int)(best * step);
+}
 
 // The fast kernel's options (score_fast.cuh): k <= 8, aligned quads, and groups,
 // where there are any, that are a power of two of blocks on every lane of a row.
@@ -55,8 +73,9 @@ __global__ void __launch_bounds__(SC_WARPS * 32) score_topk_kernel(const ScorePa
   }
   const int64_t t1 = min64(p.T, (int64_t)(u + 1) * p.span);
   for (int64_t t = (int64_t)u * p.span + warp; t < t1; t += SC_WARPS)
-    score_row<X, NQ>(p, static_cast<const X*>(p.logits) + l * p.ld_layer + t * p.ld_token, bias, (int64_t)l * p.T + t,
-                     lane, sum);
+    score_row<X, NQ>(p, static_cast<const X*>(p.logits) + l * p.ld_layer + t * p.ld_token, bias,
+                     p.topk + ((int64_t)l * p.T + t) * p.k,
+                     p.weights != nullptr ? p.weights + ((int64_t)l * p.T + t) * p.k : nullptr, lane, sum);
   if (p.partial != nullptr) {
 #pragma unroll
     for (int i = 0; i < 4 * NQ; ++i) part[warp][4 * (lane + 32 * (i / 4)) + i % 4] = sum[i];
@@ -110,10 +129,18 @@ moer_status score_topk_launch(ScoreParams p, int dtype, float* score_sum, void* 
                ? MOER_OK
                : MOER_ECUDA;
   const bool fast = fast_supported(p);
-  p.span = score_span(p.T, p.L, !fast ? SC_WARPS : p.E <= 64 ? 128 : p.E <= 128 ? 64 : 32);
+  if (fast) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return MOER_ECUDA;
+    p.span = fast_span(p.T, p.L, p.E <= 64 ? 128 : p.E <= 128 ? 64 : 32, (int64_t)sms * SC_FAST_RESIDENT);
+  } else {
+    p.span = score_span(p.T, p.L, SC_WARPS);
+  }
   p.nspan = score_nspan(p.T, p.span);
   p.partial = score_sum != nullptr ? reinterpret_cast<float*>(static_cast<char*>(ws) + WS_HEADER) : nullptr;
   p.key_mul = 256u;
+  const uintptr_t w = reinterpret_cast<uintptr_t>(p.weights);
+  p.even = p.k == 8 && w % 16 == 0 ? 2 : p.k % 2 == 0 && w % 8 == 0 ? 1 : 0;
   cudaError_t e;
   if (fast)
     e = dtype == MOER_F32 ? score_fast_f32(p, st) : dtype == MOER_BF16 ? score_fast_bf16(p, st) : score_fast_f16(p, st);
