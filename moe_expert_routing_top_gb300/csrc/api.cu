@@ -585,7 +585,7 @@ moer_status moer_kmeans_balanced(const float* sig, int32_t N, int32_t dim, int32
 }
 
 size_t moer_score_workspace_bytes(const moer_dims* d, int64_t T) {
-  if (d == nullptr || d->L < 1 || d->E < 1 || T < 1 || T >= (int64_t(1) << 31)) return WS_HEADER;
+  if (check_dims(d, false) != MOER_OK || T < 1 || T >= (int64_t(1) << 31)) return WS_HEADER;
   return WS_HEADER + moer::score_scratch_bytes(d, T);
 }
 
@@ -675,7 +675,7 @@ moer_status moer_score_topk_grad(const moer_dims* d, const moer_score_opts* o, c
 }
 
 size_t moer_block_plan_workspace_bytes(int32_t R) {
-  return WS_HEADER + (R > 0 ? moer::block_plan_scratch_bytes(R) : 4);
+  return WS_HEADER + moer::block_plan_scratch_bytes(R > 0 ? R : 0);
 }
 
 moer_status moer_block_plan(const moer_block_plan_args* a, void* ws, size_t ws_bytes, moer_stream_t stream) {
@@ -723,7 +723,7 @@ moer_status moer_block_plan(const moer_block_plan_args* a, void* ws, size_t ws_b
 }
 
 size_t moer_expert_order_workspace_bytes(const moer_dims* d, int64_t T) {
-  if (d == nullptr || d->L < 1 || d->E < 1 || d->k < 1 || T < 1 || T >= (int64_t(1) << 31)) return WS_HEADER;
+  if (check_dims(d, false) != MOER_OK || T < 1 || T >= (int64_t(1) << 31)) return WS_HEADER;
   return WS_HEADER + moer::expert_order_scratch_bytes(d, T);
 }
 

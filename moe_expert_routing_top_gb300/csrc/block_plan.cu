@@ -13,33 +13,44 @@
 // held it and from free_pages otherwise, so nothing waits for the table's new
 // entries to be written.
 //
-// Two kernels.  The sums: a block scans 4,096 requests, four to a thread, after
-// adding up the lengths of all requests before them by itself (a few
-// thousand requests are a few reads of L2; a chain of blocks would cost more).
-// The fill: a block takes 2,048 neighbouring tokens (then blocks, then cached
-// blocks); two warps find the first and the last one's request by a 32-way
-// search, and a thread searches between them only, once for the four tokens
-// that it writes with vector stores.  It is bound by the stores (16 bytes a token).
+// The sums: blocks of 1,024 requests (four to a thread) add up their own, then,
+// in a second launch, add the sums before them and scan.
+// The fill: a block of 256 threads takes 256 KV blocks.  A thread to a KV block
+// finds its request (two warps bracket the block's requests by a 32-way search,
+// the thread searches between them), its page and its first token; then the
+// tokens are written by as many lanes to a KV block as it has tokens (a power of
+// two, 32 at most), from what was found once.  Finding request and page for
+// every four tokens instead took five times the instructions.
+// It is bound by the stores (16 bytes a token).
+// Small batches take one launch: one block does it all, in shared memory.
 #include "common.cuh"
 #include "pdl.cuh"
 
 namespace moer {
 
 namespace {
-constexpr int BP_SCAN = 1024;
-constexpr int BP_EACH = 4;                     // requests of a thread in the scan
-constexpr int BP_CHUNK = BP_SCAN * BP_EACH;
-constexpr int BP_FILL = 256;
-constexpr int BP_ITEMS = 2048;                 // tokens or blocks of a fill block
-constexpr int BP_SMALL = 4;                    // fill blocks that one block does by itself
+constexpr int BP_THREADS = 256;
+constexpr int BP_EACH = 4;                       // requests of a thread in the scan
+constexpr int BP_CHUNK = BP_THREADS * BP_EACH;   // of a block
+constexpr int SMALL_R = BP_CHUNK;                // requests of a small batch,
+constexpr int64_t SMALL_ITEMS = 8192;            // its tokens and blocks
+
+// What the fill reads of the requests: the caller's arrays and the sums, or a
+// small batch's copies in shared memory.
+struct Tables {
+  const int32_t *new_len, *ctx_len;  // ctx_len may be NULL
+  const int32_t *req, *blk, *cac, *taken;  // [R+1]
+};
 
 struct PlanParams {
   moer_block_plan_args a;
   uint32_t mul, shift;     // x / B = (x mul) >> (32 + shift) for x < 2^31; shift 32: B = 1
   int32_t* taken_off;      // [R+1]
   uint32_t* status;
-  int vec;                 // 1: the token maps take vector stores
-  int tok_blocks, blk_blocks;  // fill blocks of tokens, of blocks
+  int64_t* partial;        // [chunks][4] sums of each chunk of requests
+  int vec_len;             // 1: the lengths take vector loads
+  int vec_tab;             // 1: blk_tab's pairs are on 8 bytes
+  int lanes;               // to a KV block when tokens are written: a power of two
 };
 
 // x / B for x < 2^31: with s = ceil(log2 B) the multiplier is floor(2^(31 + s) / B) + 1,
@@ -52,11 +63,23 @@ struct Request {
   uint32_t c, n;  // tokens held, tokens computed: their sum is below 2^31
 };
 
-__device__ __forceinline__ Request request(const PlanParams& p, int r, bool& bad) {
-  const int n = p.a.new_len[r], c = p.a.ctx_len != nullptr ? p.a.ctx_len[r] : 0;
+__device__ __forceinline__ Request request(int n, int c, bool& bad) {
   if (n < 0 || c < 0 || max(n, 0) > 0x7FFFFFFF - max(c, 0)) bad = true;
   const uint32_t held = (uint32_t)max(c, 0);
   return {held, min((uint32_t)max(n, 0), 0x7FFFFFFFu - held)};  // positions are int32
+}
+
+__device__ __forceinline__ Request request(const Tables& t, int r) {
+  bool bad;
+  return request(t.new_len[r], t.ctx_len != nullptr ? t.ctx_len[r] : 0, bad);
+}
+
+// Four neighbouring lengths from r on, 0 past the end or where there are none.
+__device__ __forceinline__ int4 four(const int32_t* len, int R, int r, int vec) {
+  if (len == nullptr) return make_int4(0, 0, 0, 0);
+  if (vec != 0 && r + 4 <= R) return *reinterpret_cast<const int4*>(len + r);
+  return make_int4(r < R ? len[r] : 0, r + 1 < R ? len[r + 1] : 0, r + 2 < R ? len[r + 2] : 0,
+                   r + 3 < R ? len[r + 3] : 0);
 }
 
 // Pages that x tokens touch, x < 2^31.
@@ -75,93 +98,136 @@ __device__ __forceinline__ void sums_of(const PlanParams& p, const Request& q, u
 
 __device__ __forceinline__ int32_t clamp32(int64_t v) { return (int32_t)min64(v, 0x7FFFFFFF); }
 
-// The sums, by gridDim.x blocks of 1,024 threads.
-__device__ __forceinline__ void scan_requests(const PlanParams& p) {
-  __shared__ int64_t wsum[2][4][BP_SCAN / 32];
+// Sums of four values over the block; every thread returns them.
+__device__ __forceinline__ void block_sums(int64_t (&x)[4], int64_t (*wsum)[BP_THREADS / 32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x[k] += __shfl_xor_sync(FULL, x[k], o);
+    if (lane == 0) wsum[k][warp] = x[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[k] = 0;
+#pragma unroll
+    for (int w = 0; w < BP_THREADS / 32; ++w) x[k] += wsum[k][w];
+  }
+  __syncthreads();
+}
+
+// The four requests of a thread, and whether their lengths or tables are bad.
+struct Four {
+  uint32_t s[BP_EACH][4];
+  int n[BP_EACH], c[BP_EACH];
+  bool bad;
+};
+__device__ __forceinline__ Four four_requests(const PlanParams& p, int r0) {
+  const moer_block_plan_args& a = p.a;
+  const int4 n4 = four(a.new_len, a.R, r0, p.vec_len), c4 = four(a.ctx_len, a.R, r0, p.vec_len);
+  Four f = {{}, {n4.x, n4.y, n4.z, n4.w}, {c4.x, c4.y, c4.z, c4.w}, false};
+#pragma unroll
+  for (int i = 0; i < BP_EACH; ++i) {
+    const Request q = request(f.n[i], f.c[i], f.bad);
+    if (a.pages != nullptr && pages_of(p, q.c + q.n) > (uint32_t)a.ld_pages) f.bad = true;
+    sums_of(p, q, f.s[i]);
+  }
+  return f;
+}
+
+__global__ void __launch_bounds__(BP_THREADS) plan_sum_kernel(const PlanParams p) {
+  __shared__ int64_t wsum[4][BP_THREADS / 32];
+  pdl_wait();
+  const Four f = four_requests(p, (int)blockIdx.x * BP_CHUNK + (int)threadIdx.x * BP_EACH);
+  int64_t x[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < BP_EACH; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] += f.s[i][k];
+  block_sums(x, wsum);
+  if (threadIdx.x == 0)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) p.partial[(int64_t)blockIdx.x * 4 + k] = x[k];
+  pdl_release();
+}
+
+// The offsets of the block's requests; `keep` (a small batch): copies of the lengths
+// and offsets in shared memory, SMALL_R + 1 of each.
+__device__ __forceinline__ void scan_requests(const PlanParams& p, int32_t* keep) {
+  __shared__ int64_t wsum[4][BP_THREADS / 32];
   const moer_block_plan_args& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r0 = (int)blockIdx.x * BP_CHUNK + (int)threadIdx.x * BP_EACH;
-  bool bad = false;
-  // the thread's requests, and its share of those before the block's
-  uint32_t s[BP_EACH][4];
-  int64_t x[4] = {0, 0, 0, 0}, before[4] = {0, 0, 0, 0};
+  int64_t base[4] = {0, 0, 0, 0};
+  if (blockIdx.x > 0) {
+    for (int c = threadIdx.x; c < (int)blockIdx.x; c += BP_THREADS)
 #pragma unroll
-  for (int i = 0; i < BP_EACH; ++i) {
-    Request q = {0u, 0u};
-    if (r0 + i < a.R) {
-      q = request(p, r0 + i, bad);
-      if (a.pages != nullptr && pages_of(p, q.c + q.n) > (uint32_t)a.ld_pages) bad = true;
-    }
-    sums_of(p, q, s[i]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] += s[i][k];
+      for (int k = 0; k < 4; ++k) base[k] += p.partial[(int64_t)c * 4 + k];
+    block_sums(base, wsum);
   }
-  for (int r = threadIdx.x; r < (int)blockIdx.x * BP_CHUNK; r += BP_SCAN) {
-    uint32_t v[4];
-    sums_of(p, request(p, r, bad), v);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) before[k] += v[k];
-  }
+  const Four f = four_requests(p, r0);
+  bool bad = f.bad;
+  int64_t x[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    int64_t y = x[k], b = before[k];
+    const int64_t own = (int64_t)f.s[0][k] + f.s[1][k] + f.s[2][k] + f.s[3][k];
+    int64_t y = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t z = __shfl_up_sync(FULL, y, o);
       if (lane >= o) y += z;
     }
-    if (blockIdx.x > 0)
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(FULL, b, o);
-    if (lane == 31) wsum[0][k][warp] = y, wsum[1][k][warp] = b;
-    x[k] = y - x[k];  // of the warp's earlier threads
+    if (lane == 31) wsum[k][warp] = y;
+    x[k] = y - own;
   }
   __syncthreads();
-  // one warp for each of the four: the warps' sums, scanned from the sum before the block
-  if (warp < 4) {
-    const int64_t y = wsum[0][warp][lane];
-    int64_t z = y, b = wsum[1][warp][lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(FULL, z, o);
-      if (lane >= o) z += u;
+  for (int k = 0; k < 4; ++k) {
+    x[k] += base[k];
+#pragma unroll
+    for (int w = 0; w < BP_THREADS / 32; ++w) {
+      if (w < warp) x[k] += wsum[k][w];
+      base[k] += wsum[k][w];
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(FULL, b, o);
-    wsum[0][warp][lane] = b + z - y;
-    if (lane == 31) wsum[1][warp][0] = b + z;  // up to the block's end
   }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] += wsum[0][k][warp];
 #pragma unroll
   for (int i = 0; i < BP_EACH; ++i)
     if (r0 + i < a.R) {
-      a.req_off[r0 + i] = clamp32(x[0]);
-      a.req_blk_off[r0 + i] = clamp32(x[1]);
-      if (a.req_cache_off != nullptr) a.req_cache_off[r0 + i] = clamp32(x[2]);
-      p.taken_off[r0 + i] = clamp32(x[3]);
+      const int r = r0 + i;
+      a.req_off[r] = clamp32(x[0]);
+      a.req_blk_off[r] = clamp32(x[1]);
+      if (a.req_cache_off != nullptr) a.req_cache_off[r] = clamp32(x[2]);
+      if (keep != nullptr) {
+        keep[r] = f.n[i];
+        keep[SMALL_R + 1 + r] = f.c[i];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] += s[i][k];
+        for (int k = 0; k < 4; ++k) keep[(2 + k) * (SMALL_R + 1) + r] = clamp32(x[k]);
+      } else {
+        p.taken_off[r] = clamp32(x[3]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] += f.s[i][k];
     }
   if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
-    const int64_t t[4] = {wsum[1][0][0], wsum[1][1][0], wsum[1][2][0], wsum[1][3][0]};
-    a.req_off[a.R] = clamp32(t[0]);
-    a.req_blk_off[a.R] = clamp32(t[1]);
-    if (a.req_cache_off != nullptr) a.req_cache_off[a.R] = clamp32(t[2]);
-    p.taken_off[a.R] = clamp32(t[3]);
+    a.req_off[a.R] = clamp32(base[0]);
+    a.req_blk_off[a.R] = clamp32(base[1]);
+    if (a.req_cache_off != nullptr) a.req_cache_off[a.R] = clamp32(base[2]);
+    p.taken_off[a.R] = clamp32(base[3]);
+    if (keep != nullptr)
+      for (int k = 0; k < 4; ++k) keep[(2 + k) * (SMALL_R + 1) + a.R] = clamp32(base[k]);
     if (a.totals != nullptr)
-      for (int k = 0; k < 4; ++k) a.totals[k] = clamp32(t[k]);
-    if (t[0] > a.T || t[1] > a.nblk || (a.cache_idx != nullptr && t[2] > a.ncached) ||
-        (a.free_pages != nullptr && t[3] > a.n_free))
+      for (int k = 0; k < 4; ++k) a.totals[k] = clamp32(base[k]);
+    if (base[0] > a.T || base[1] > a.nblk || (a.cache_idx != nullptr && base[2] > a.ncached) ||
+        (a.free_pages != nullptr && base[3] > a.n_free))
       bad = true;
   }
   if (bad) atomicOr(p.status, WS_BIT_EDATA);
 }
 
-__global__ void __launch_bounds__(BP_SCAN) plan_scan_kernel(const PlanParams p) {
+__global__ void __launch_bounds__(BP_THREADS) plan_scan_kernel(const PlanParams p) {
   pdl_wait();
-  scan_requests(p);
+  scan_requests(p, nullptr);
   pdl_release();
 }
 
@@ -195,201 +261,149 @@ __device__ __forceinline__ int find_warp(const int32_t* off, int R, int i) {
 
 // The page of a request's page number: held pages from the table, new ones
 // from free_pages (or from the table where that is complete); -1 if there is none.
-__device__ __forceinline__ int page_of(const PlanParams& p, int r, uint32_t held, uint32_t i) {
+__device__ __forceinline__ int page_of(const PlanParams& p, const Tables& tb, int r, uint32_t held, uint32_t i) {
   const moer_block_plan_args& a = p.a;
   if (i >= (uint32_t)a.ld_pages) return -1;
   if (a.free_pages != nullptr && i >= held) {
-    const int64_t f = (int64_t)p.taken_off[r] + (i - held);
+    const int64_t f = (int64_t)tb.taken[r] + (i - held);
     return f < a.n_free ? a.free_pages[f] : -1;
   }
   return a.pages[(int64_t)r * a.ld_pages + i];
 }
 
-// Walks over neighbouring tokens: the request, and the slot on its page.
-struct Walk {
-  int r;
-  int64_t end;             // first token past the request
-  uint32_t pos, page_no, held, rest;
-  int page;
-  __device__ __forceinline__ void enter(const PlanParams& p, int request_no, int t) {
-    bool bad;
-    r = request_no;
-    const Request q = request(p, r, bad);
-    const int at = p.a.req_off[r];
-    end = (int64_t)at + q.n;
-    pos = q.c + (uint32_t)(t - at);
-    held = pages_of(p, q.c);
-    page_no = div_b(p, pos);
-    rest = pos - page_no * (uint32_t)p.a.block;
-    page = p.a.slot_map != nullptr ? page_of(p, r, held, page_no) : -1;
-  }
-  // to token t, the one after the last
-  __device__ __forceinline__ void next(const PlanParams& p, int t) {
-    ++pos;
-    if (t >= end) {
-      int q = r + 1;
-      while (p.a.req_off[q + 1] <= t) ++q;  // requests without tokens
-      enter(p, q, t);
-    } else if (++rest == (uint32_t)p.a.block) {
-      rest = 0u;
-      ++page_no;
-      if (p.a.slot_map != nullptr) page = page_of(p, r, held, page_no);
-    }
-  }
-};
-
-__device__ void fill_tokens(const PlanParams& p, int64_t i0, int* range) {
-  const moer_block_plan_args& a = p.a;
-  const int T = a.req_off[a.R];
-  const int n_in = (int)max64(0, min64(BP_ITEMS, T - i0));  // of the block's tokens
-  if (threadIdx.x < 64 && n_in > 0) {
+// The requests of items i0 and i0 + n - 1, by two warps; every thread calls it.
+__device__ __forceinline__ void find_range(const int32_t* off, int R, int i0, int n, int* range) {
+  if (threadIdx.x < 64) {
     const int w = threadIdx.x >> 5;
-    const int r = find_warp(a.req_off, a.R, (int)i0 + (w == 0 ? 0 : n_in - 1));
+    const int r = find_warp(off, R, i0 + (w == 0 ? 0 : n - 1));
     if ((threadIdx.x & 31) == 0) range[w] = r;
   }
   __syncthreads();
-  for (int k = (int)threadIdx.x * 4; k < BP_ITEMS; k += (int)blockDim.x * 4) {
-    const int64_t t0 = i0 + k;
-    if (t0 >= a.T) break;
-    int64_t slot[4] = {-1, -1, -1, -1};
-    int req[4] = {-1, -1, -1, -1}, pos[4] = {-1, -1, -1, -1};
-    if (k < n_in) {
-      Walk w;
-      w.enter(p, find(a.req_off, range[0], range[1] + 1, (int)t0), (int)t0);
-      if (t0 + 4 <= w.end && w.rest + 4u <= (uint32_t)a.block) {
-        // all four on one page of one request
-        const int64_t s0 = w.page >= 0 ? (int64_t)w.page * a.block + w.rest : -1;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          req[j] = w.r;
-          pos[j] = (int)w.pos + j;
-          slot[j] = s0 >= 0 ? s0 + j : -1;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (k + j < n_in) {
-            if (j > 0) w.next(p, (int)t0 + j);
-            req[j] = w.r;
-            pos[j] = (int)w.pos;
-            if (w.page >= 0) slot[j] = (int64_t)w.page * a.block + w.rest;
-          }
-      }
-    }
-    if (p.vec != 0 && t0 + 4 <= a.T) {
-      if (a.slot_map != nullptr) {
-        *reinterpret_cast<longlong2*>(a.slot_map + t0) = make_longlong2(slot[0], slot[1]);
-        *reinterpret_cast<longlong2*>(a.slot_map + t0 + 2) = make_longlong2(slot[2], slot[3]);
-      }
-      if (a.tok_req != nullptr) *reinterpret_cast<int4*>(a.tok_req + t0) = make_int4(req[0], req[1], req[2], req[3]);
-      if (a.tok_pos != nullptr) *reinterpret_cast<int4*>(a.tok_pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (t0 + j < a.T) {
-          if (a.slot_map != nullptr) a.slot_map[t0 + j] = slot[j];
-          if (a.tok_req != nullptr) a.tok_req[t0 + j] = req[j];
-          if (a.tok_pos != nullptr) a.tok_pos[t0 + j] = pos[j];
-        }
-    }
-  }
 }
 
-__device__ void fill_blocks(const PlanParams& p, int64_t i0, int* range) {
+// A KV block's tokens: the first one's slot (-1: no page), number and position, how
+// many there is room for, and their request.
+struct Run {
+  int64_t slot;
+  int tok0, len, pos, req;
+};
+
+// The batch's KV blocks, and with each its tokens.
+__device__ void fill_blocks(const PlanParams& p, const Tables& tb) {
+  __shared__ Run runs[BP_THREADS];
+  __shared__ int range[2];
   const moer_block_plan_args& a = p.a;
-  const int T = a.req_off[a.R], nblk = a.req_blk_off[a.R];
-  const int n_in = (int)max64(0, min64(BP_ITEMS, nblk - i0));
-  if (threadIdx.x < 64 && n_in > 0) {
-    const int w = threadIdx.x >> 5;
-    const int r = find_warp(a.req_blk_off, a.R, (int)i0 + (w == 0 ? 0 : n_in - 1));
-    if ((threadIdx.x & 31) == 0) range[w] = r;
-  }
-  __syncthreads();
-  for (int k = threadIdx.x; k < BP_ITEMS && i0 + k < a.nblk; k += (int)blockDim.x) {
-    const int64_t b = i0 + k;
-    int tok0 = T, len = 0, slot = -1;
-    if (k < n_in) {
-      bool bad;
-      const int r = find(a.req_blk_off, range[0], range[1] + 1, (int)b);
-      const Request q = request(p, r, bad);
-      const uint32_t B = (uint32_t)a.block, i = div_b(p, q.c) + (uint32_t)(b - a.req_blk_off[r]);
+  const int nblk = tb.blk[a.R];
+  const bool tokens = a.slot_map != nullptr || a.tok_req != nullptr || a.tok_pos != nullptr;
+  const uint32_t B = (uint32_t)a.block;
+  const int room = (int)min64(a.T, 0x7FFFFFFF);
+  for (int64_t b0 = (int64_t)blockIdx.x * BP_THREADS; b0 < nblk; b0 += (int64_t)gridDim.x * BP_THREADS) {
+    const int n = (int)min64(BP_THREADS, nblk - b0);
+    find_range(tb.blk, a.R, (int)b0, n, range);
+    if ((int)threadIdx.x < n) {
+      const int b = (int)b0 + (int)threadIdx.x;
+      const int r = find(tb.blk, range[0], range[1] + 1, b);
+      const Request q = request(tb, r);
+      const uint32_t i = div_b(p, q.c) + (uint32_t)(b - tb.blk[r]);
       const uint32_t lo = max(i * B, q.c), hi = min(i * B + B, q.c + q.n);
-      tok0 = clamp32((int64_t)a.req_off[r] + (lo - q.c));
-      len = (int)(hi - lo);
+      const int tok0 = clamp32((int64_t)tb.req[r] + (lo - q.c)), len = (int)(hi - lo);
+      int page = -1;
       if (a.pages != nullptr) {
         const uint32_t held = pages_of(p, q.c);
-        const int page = page_of(p, r, held, i);
-        if (len == a.block) slot = page;
+        page = page_of(p, tb, r, held, i);
         if (a.free_pages != nullptr && i >= held && i < (uint32_t)a.ld_pages)
           a.pages[(int64_t)r * a.ld_pages + i] = page;
       }
+      if (b < a.nblk) {
+        if (p.vec_tab != 0) {
+          *reinterpret_cast<int2*>(a.blk_tab + 2 * (int64_t)b) = make_int2(tok0, len);
+        } else {
+          a.blk_tab[2 * (int64_t)b] = tok0;
+          a.blk_tab[2 * (int64_t)b + 1] = len;
+        }
+        if (a.insert_slot != nullptr) a.insert_slot[b] = len == a.block ? page : -1;
+      }
+      runs[threadIdx.x] = {page >= 0 ? (int64_t)page * a.block + (lo - i * B) : -1, tok0,
+                           min(len, max(room - tok0, 0)), (int)lo, r};
     }
-    a.blk_tab[2 * b] = tok0;
-    a.blk_tab[2 * b + 1] = len;
-    if (a.insert_slot != nullptr) a.insert_slot[b] = slot;
+    __syncthreads();
+    if (tokens) {
+      const int W = p.lanes, o0 = (int)threadIdx.x & (W - 1);
+      for (int k = (int)threadIdx.x / W; k < n; k += BP_THREADS / W) {
+        const Run u = runs[k];
+        for (int o = o0; o < u.len; o += W) {
+          const int64_t t = (int64_t)u.tok0 + o;
+          if (a.slot_map != nullptr) a.slot_map[t] = u.slot >= 0 ? u.slot + o : -1;
+          if (a.tok_req != nullptr) a.tok_req[t] = u.req;
+          if (a.tok_pos != nullptr) a.tok_pos[t] = u.pos + o;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  // room that the batch leaves
+  const int64_t step = (int64_t)gridDim.x * BP_THREADS, first = (int64_t)blockIdx.x * BP_THREADS + threadIdx.x;
+  for (int64_t t = tb.req[a.R] + first; t < a.T; t += step) {
+    if (a.slot_map != nullptr) a.slot_map[t] = -1;
+    if (a.tok_req != nullptr) a.tok_req[t] = -1;
+    if (a.tok_pos != nullptr) a.tok_pos[t] = -1;
+  }
+  for (int64_t b = nblk + first; b < a.nblk; b += step) {
+    a.blk_tab[2 * b] = tb.req[a.R];
+    a.blk_tab[2 * b + 1] = 0;
+    if (a.insert_slot != nullptr) a.insert_slot[b] = -1;
   }
 }
 
-__device__ void fill_cached(const PlanParams& p, int64_t i0, int* range) {
+__device__ void fill_cached(const PlanParams& p, const Tables& tb) {
+  __shared__ int range[2];
   const moer_block_plan_args& a = p.a;
-  const int nc = a.req_cache_off[a.R];
-  const int n_in = (int)max64(0, min64(BP_ITEMS, nc - i0));
-  if (threadIdx.x < 64 && n_in > 0) {
-    const int w = threadIdx.x >> 5;
-    const int r = find_warp(a.req_cache_off, a.R, (int)i0 + (w == 0 ? 0 : n_in - 1));
-    if ((threadIdx.x & 31) == 0) range[w] = r;
-  }
-  __syncthreads();
-  for (int k = threadIdx.x; k < BP_ITEMS && i0 + k < a.ncached; k += (int)blockDim.x) {
-    int page = -1;
-    if (k < n_in) {
-      const int r = find(a.req_cache_off, range[0], range[1] + 1, (int)i0 + k);
-      const int i = (int)i0 + k - a.req_cache_off[r];
-      if (i < a.ld_pages) page = a.pages[(int64_t)r * a.ld_pages + i];
+  const int nc = tb.cac[a.R];
+  constexpr int ITEMS = BP_THREADS * 4;
+  for (int64_t i0 = (int64_t)blockIdx.x * ITEMS; i0 < a.ncached; i0 += (int64_t)gridDim.x * ITEMS) {
+    const int n = (int)max64(0, min64(ITEMS, nc - i0));
+    if (n > 0) find_range(tb.cac, a.R, (int)i0, n, range);
+    for (int k = threadIdx.x; k < ITEMS && i0 + k < a.ncached; k += BP_THREADS) {
+      int page = -1;
+      if (k < n) {
+        const int r = find(tb.cac, range[0], range[1] + 1, (int)i0 + k);
+        const int i = (int)i0 + k - tb.cac[r];
+        if (i < a.ld_pages) page = a.pages[(int64_t)r * a.ld_pages + i];
+      }
+      a.cache_idx[i0 + k] = page;
     }
-    a.cache_idx[i0 + k] = page;
+    __syncthreads();
   }
 }
 
-__global__ void __launch_bounds__(BP_FILL) plan_fill_kernel(const PlanParams p) {
-  __shared__ int range[2];  // requests of the block's first and last item
+__global__ void __launch_bounds__(BP_THREADS) plan_fill_kernel(const PlanParams p) {
   pdl_wait();
-  const int b = (int)blockIdx.x;
-  if (b < p.tok_blocks)
-    fill_tokens(p, (int64_t)b * BP_ITEMS, range);
-  else if (b < p.tok_blocks + p.blk_blocks)
-    fill_blocks(p, (int64_t)(b - p.tok_blocks) * BP_ITEMS, range);
-  else
-    fill_cached(p, (int64_t)(b - p.tok_blocks - p.blk_blocks) * BP_ITEMS, range);
+  const Tables tb = {p.a.new_len, p.a.ctx_len, p.a.req_off, p.a.req_blk_off, p.a.req_cache_off, p.taken_off};
+  fill_blocks(p, tb);
+  if (p.a.cache_idx != nullptr) fill_cached(p, tb);
   pdl_release();
 }
 
-// Small batches: one block makes the sums and then fills the tables itself.
-__global__ void __launch_bounds__(BP_SCAN) plan_small_kernel(const PlanParams p) {
-  __shared__ int range[2];
+__global__ void __launch_bounds__(BP_THREADS) plan_small_kernel(const PlanParams p) {
+  __shared__ int32_t keep[6 * (SMALL_R + 1)];
   pdl_wait();
-  scan_requests(p);
-  __syncthreads();  // the sums in global memory are this block's own
-  for (int b = 0; b < p.tok_blocks; ++b) {
-    fill_tokens(p, (int64_t)b * BP_ITEMS, range);
-    __syncthreads();
-  }
-  for (int b = 0; b < p.blk_blocks; ++b) {
-    fill_blocks(p, (int64_t)b * BP_ITEMS, range);
-    __syncthreads();
-  }
-  if (p.a.cache_idx != nullptr)
-    for (int64_t i = 0; i < p.a.ncached; i += BP_ITEMS) {
-      fill_cached(p, i, range);
-      __syncthreads();
-    }
+  scan_requests(p, keep);
+  __syncthreads();
+  constexpr int S = SMALL_R + 1;
+  const Tables tb = {keep, keep + S, keep + 2 * S, keep + 3 * S, keep + 4 * S, keep + 5 * S};
+  fill_blocks(p, tb);
+  if (p.a.cache_idx != nullptr) fill_cached(p, tb);
   pdl_release();
 }
 
 bool on16(const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
 }  // namespace
 
-size_t block_plan_scratch_bytes(int32_t R) { return ((size_t)R + 1) * 4; }
+// The pages taken before each request, then the chunks' sums.
+size_t block_plan_scratch_bytes(int32_t R) {
+  const size_t chunks = ((size_t)R + BP_CHUNK - 1) / BP_CHUNK;
+  return (((size_t)R + 1) * 4 + 15) / 16 * 16 + chunks * 4 * sizeof(int64_t);
+}
 
 moer_status block_plan_launch(const moer_block_plan_args* a, void* ws, cudaStream_t st) {
   PlanParams p;
@@ -399,19 +413,22 @@ moer_status block_plan_launch(const moer_block_plan_args* a, void* ws, cudaStrea
   while ((1ull << log) < B) ++log;
   p.mul = B == 1 ? 0u : (uint32_t)((1ull << (31u + log)) / B + 1ull);
   p.shift = B == 1 ? 32u : log - 1u;
+  p.lanes = 1 << (log < 5u ? log : 5u);
   p.status = static_cast<uint32_t*>(ws);
-  p.taken_off = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + WS_HEADER);
-  p.vec = on16(a->slot_map) && on16(a->tok_req) && on16(a->tok_pos);
-  const bool tokens = a->slot_map != nullptr || a->tok_req != nullptr || a->tok_pos != nullptr;
-  auto blocks = [](int64_t n) { return (n + BP_ITEMS - 1) / BP_ITEMS; };
-  p.tok_blocks = tokens ? (int)blocks(a->T) : 0;
-  p.blk_blocks = (int)blocks(a->nblk);
-  const int64_t fill = (int64_t)p.tok_blocks + p.blk_blocks + (a->cache_idx != nullptr ? blocks(a->ncached) : 0);
-  if (a->R <= BP_CHUNK && fill <= BP_SMALL)
-    return launch_pdl(plan_small_kernel, dim3(1), dim3(BP_SCAN), 0, st, p) == cudaSuccess ? MOER_OK : MOER_ECUDA;
-  const int scan = a->R > BP_CHUNK ? (a->R + BP_CHUNK - 1) / BP_CHUNK : 1;
-  cudaError_t e = launch_pdl(plan_scan_kernel, dim3(scan), dim3(BP_SCAN), 0, st, p);
-  if (e == cudaSuccess && fill > 0) e = launch_pdl(plan_fill_kernel, dim3((unsigned)fill), dim3(BP_FILL), 0, st, p);
+  char* scratch = static_cast<char*>(ws) + WS_HEADER;
+  p.taken_off = reinterpret_cast<int32_t*>(scratch);
+  p.partial = reinterpret_cast<int64_t*>(scratch + (((size_t)a->R + 1) * 4 + 15) / 16 * 16);
+  p.vec_len = on16(a->new_len) && on16(a->ctx_len);
+  p.vec_tab = reinterpret_cast<uintptr_t>(a->blk_tab) % 8 == 0;
+  const dim3 block(BP_THREADS);
+  if (a->R <= SMALL_R && a->T + a->nblk + a->ncached <= SMALL_ITEMS)
+    return launch_pdl(plan_small_kernel, dim3(1), block, 0, st, p) == cudaSuccess ? MOER_OK : MOER_ECUDA;
+  const int chunks = a->R > BP_CHUNK ? (a->R + BP_CHUNK - 1) / BP_CHUNK : 1;
+  cudaError_t e = chunks > 1 ? launch_pdl(plan_sum_kernel, dim3(chunks), block, 0, st, p) : cudaSuccess;
+  if (e == cudaSuccess) e = launch_pdl(plan_scan_kernel, dim3(chunks), block, 0, st, p);
+  // a block to 256 KV blocks (their number is at most nblk where the batch fits)
+  const int64_t fill = max64(1, (max64(a->nblk, a->ncached / 4) + BP_THREADS - 1) / BP_THREADS);
+  if (e == cudaSuccess) e = launch_pdl(plan_fill_kernel, dim3((unsigned)fill), block, 0, st, p);
   return e == cudaSuccess ? MOER_OK : MOER_ECUDA;
 }
 
