@@ -2,18 +2,22 @@
 // the order of their experts (a stable counting sort by the expert id), each
 // expert's segment padded to a multiple of `align`.
 //
-// Over chunks of 8,192 consecutive pairs of a layer:
+// Over chunks of up to 32 tiles of 32 tokens (8,192 pairs):
 //   count    a chunk's histogram of experts (16 ids to a thread, one load);
 //   offsets  per layer, the experts' totals, their padded offsets and, in place
 //            of each histogram, the row at which the chunk's pairs of an
-//            expert start; the padding is set to -1;
-//   place    a chunk is sorted in shared memory and written out from there: every
-//            warp takes its pairs 32 at a time in order, finds the lanes with
-//            the same expert by a vote on each bit of the id, and adds their
-//            number below to the warp's running count; the warps' counts are
-//            then scanned, and rows follow.
+//            expert start;
+//   place    a chunk is sorted in shared memory and written out from there.  For
+//            every tile and expert a word holds which of the tile's 32 tokens
+//            chose the expert, one bit each, set by an atomic or: a pair's rank
+//            in its tile is the number of lower bits, whatever the order in which
+//            the bits came.  The words' counts are summed over the tiles, and
+//            rows follow.  (Ranking by votes on the ids' bits took 124
+//            instructions for 32 pairs; this takes about a third.)
 // Sorting in shared memory first turns the scattered 4-byte writes of `order`
 // into runs (a chunk holds 64 pairs of each of 128 experts: 256 bytes).
+// A token that names an expert twice has one bit for two pairs: the chunk is
+// then placed by a thread to an expert that reads the pairs in order.
 // A layer that fits one chunk takes one launch, which does all three.
 #include "common.cuh"
 #include "pdl.cuh"
@@ -23,15 +27,17 @@ namespace moer {
 namespace {
 constexpr int EO_WARPS = 16;
 constexpr int EO_THREADS = EO_WARPS * 32;
-constexpr int EO_PAIRS = 8192;                  // of a chunk
-constexpr int EO_IT = EO_PAIRS / EO_THREADS;    // rounds of 32 pairs of a warp
+constexpr int EO_PAIRS = 8192;                  // of a chunk, at most
+constexpr int EO_TILES = 32;                    // of a chunk, at most (16 for E > 128)
 constexpr int EO_SCAN = 1024;
 
 struct OrderParams {
   const uint8_t* ids;  // [L][N]
   int N, E, L, align;  // pairs and experts of a layer
+  int k, T, ctok;      // ids of a token, tokens of a layer and of a chunk
   int nchunk;
-  int vec;             // 1: every layer's ids start on 16 bytes
+  int vec;             // 1: every layer's ids and inv start on 16 bytes
+  int pairs;           // 1: k is even and inv takes pairs
   uint32_t* hist;      // [L][nchunk][E]
   int32_t* off;        // [L][E+1]
   int32_t* order;      // [L][ld] or NULL
@@ -55,30 +61,33 @@ __device__ __forceinline__ void load_ids(const OrderParams& p, const uint8_t* id
 
 __global__ void __launch_bounds__(EO_THREADS) order_count_kernel(const OrderParams p) {
   __shared__ uint32_t h[256];
-  __shared__ __align__(16) uint8_t sid[EO_PAIRS];
   pdl_wait();
   const int l = blockIdx.x / p.nchunk, c = blockIdx.x - l * p.nchunk;
-  const int64_t i0 = (int64_t)c * EO_PAIRS;
-  const int n = (int)min64(EO_PAIRS, p.N - i0);
+  const int64_t i0 = (int64_t)c * p.ctok * p.k;
+  const int n = (int)min64((int64_t)p.ctok * p.k, p.N - i0);
+  const uint8_t* ids = p.ids + (size_t)l * p.N + i0;
+  const int i = (int)threadIdx.x * 16;
+  uint4 q = make_uint4(0u, 0u, 0u, 0u);
+  const bool whole = p.vec != 0 && i + 16 <= n;
+  if (whole) q = *reinterpret_cast<const uint4*>(ids + i);
   if (threadIdx.x < 256) h[threadIdx.x] = 0u;
-  load_ids(p, p.ids + (size_t)l * p.N + i0, n, sid);
   __syncthreads();
-  bool bad = false;
-  // a warp's lanes read neighbouring words; each holds four ids
-  for (int w = threadIdx.x; 4 * w < n; w += EO_THREADS) {
-    const uint32_t q = *reinterpret_cast<const uint32_t*>(sid + 4 * w);
+  if (whole) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = (q >> (8 * j)) & 255;
-      if (4 * w + j < n) {
-        atomicAdd(&h[e], 1u);
-        bad = bad || e >= p.E;
-      }
-    }
+    for (int j = 0; j < 16; ++j) atomicAdd(&h[w[j / 4] >> (8 * (j % 4)) & 255u], 1u);
+  } else if (p.vec != 0) {
+    for (int j = i; j < n; ++j) atomicAdd(&h[ids[j]], 1u);
+  } else {
+    for (int j = threadIdx.x; j < n; j += EO_THREADS) atomicAdd(&h[ids[j]], 1u);
   }
-  if (bad) atomicOr(p.status, WS_BIT_EDATA);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += EO_THREADS) p.hist[(size_t)blockIdx.x * p.E + e] = h[e];
+  for (int e = threadIdx.x; e < 256; e += EO_THREADS) {
+    if (e < p.E)
+      p.hist[(size_t)blockIdx.x * p.E + e] = h[e];
+    else if (h[e] != 0u)
+      atomicOr(p.status, WS_BIT_EDATA);
+  }
   pdl_release();
 }
 
@@ -105,19 +114,20 @@ __device__ __forceinline__ uint32_t scan256(uint32_t v, uint32_t* wsum, uint32_t
   return before + x - v;
 }
 
-// -1 in the rows of a layer's `order` that hold no pair, by `nwarps` warps.
-__device__ __forceinline__ void fill_padding(const OrderParams& p, int l, const uint32_t* off, const uint32_t* tot,
-                                             int nwarps) {
+// -1 in the rows of a layer's `order` that hold no pair, by the layer's last
+// chunk: `end` [E] the rows after the experts' last pairs, `off` [E+1].
+template <typename Off>
+__device__ __forceinline__ void fill_padding(const OrderParams& p, int l, const Off* off, const uint32_t* end) {
   int32_t* order = p.order + (size_t)l * p.ld;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = warp; e < p.E; e += nwarps)
-    for (uint32_t r = off[e] + tot[e] + lane; r < off[e + 1]; r += 32) order[r] = -1;
-  for (int64_t r = (int64_t)off[p.E] + threadIdx.x; r < p.ld; r += nwarps * 32) order[r] = -1;
+  for (int e = warp; e < p.E; e += EO_WARPS)
+    for (uint32_t r = end[e] + lane; r < (uint32_t)off[e + 1]; r += 32) order[r] = -1;
+  for (int64_t r = (int64_t)(uint32_t)off[p.E] + threadIdx.x; r < p.ld; r += EO_THREADS) order[r] = -1;
 }
 
 // One block per layer: four threads to an expert, each with a quarter of the chunks.
 __global__ void __launch_bounds__(EO_SCAN) order_offsets_kernel(const OrderParams p) {
-  __shared__ uint32_t off[257], tot[256], wsum[8], quarter[4][256];
+  __shared__ uint32_t off[257], wsum[8], quarter[4][256];
   pdl_wait();
   const int l = blockIdx.x, e = threadIdx.x & 255, q = threadIdx.x >> 8;
   uint32_t* h = p.hist + (size_t)l * p.nchunk * p.E;
@@ -135,7 +145,6 @@ __global__ void __launch_bounds__(EO_SCAN) order_offsets_kernel(const OrderParam
   const uint32_t at = scan256(q == 0 ? padded : 0u, wsum, total);
   if (q == 0) {
     off[e] = at;
-    tot[e] = all;
     if (e == 0) off[256] = total;  // E = 256; a smaller E's end is its next, empty expert's start
   }
   __syncthreads();
@@ -150,107 +159,207 @@ __global__ void __launch_bounds__(EO_SCAN) order_offsets_kernel(const OrderParam
       r += n;
     }
   }
-  if (p.order != nullptr) fill_padding(p, l, off, tot, EO_SCAN / 32);
   pdl_release();
 }
 
-// BITS: of an expert id (E <= 2^BITS).  ALONE: the layer is one chunk, and this
-// launch also makes the offsets and the padding.
-template <int BITS, bool ALONE>
+// EM: room for the experts, 64, 128 or 256.  ALONE: the layer is one chunk, and this
+// launch also makes the offsets.
+template <int EM>
+struct PlaceGeo {
+  static constexpr int TILES = EM > 128 ? 16 : EO_TILES;
+  static constexpr int PAIRS = EM > 128 ? EO_PAIRS / 2 : EO_PAIRS;
+  static constexpr size_t OFF_SORTED = (size_t)TILES * EM * 8;
+  static constexpr size_t OFF_IDS = OFF_SORTED + (size_t)PAIRS * 4;
+  static constexpr size_t SMEM8 = OFF_IDS, SMEM = OFF_IDS + PAIRS;  // k = 8, any k
+};
+
+// The word of a tile that holds expert e's tokens, and the one that holds the place
+// of its first pair: neighbours, in turns, so that either spreads over all banks.
+__device__ __forceinline__ int bits_at(int e) { return 2 * e + (e >> 4 & 1); }
+__device__ __forceinline__ int place_at(int e) { return 2 * e + 1 - (e >> 4 & 1); }
+
+template <int EM, bool ALONE, bool K8>
 __global__ void __launch_bounds__(EO_THREADS) order_place_kernel(const OrderParams p) {
-  constexpr int EM = 1 << BITS;
-  __shared__ uint32_t count[EO_WARPS][EM];  // pairs of each expert: the warp's, then those before it in the chunk
-  __shared__ uint32_t shift[256];           // row of an expert's first pair, less its place in the sorted chunk
+  constexpr int SEG = EO_THREADS / EM;  // threads to an expert in the sums
+  constexpr int MINE = 2;               // tiles of a warp
+  extern __shared__ __align__(16) char smem[];
+  uint32_t(*tiles)[2 * EM] = reinterpret_cast<uint32_t(*)[2 * EM]>(smem);
+  uint32_t* sorted = reinterpret_cast<uint32_t*>(smem + PlaceGeo<EM>::OFF_SORTED);  // expert, pair
+  uint8_t* sid = reinterpret_cast<uint8_t*>(smem + PlaceGeo<EM>::OFF_IDS);          // the ids, where k is not 8
+  __shared__ uint32_t shift[256];       // row of an expert's first pair, less its place in the sorted chunk
+  __shared__ uint32_t end[256];         // row after its last pair
+  __shared__ uint32_t part[SEG][EM];
   __shared__ uint32_t wsum[8];
-  __shared__ __align__(16) uint8_t sid[EO_PAIRS];
-  __shared__ uint16_t sorted[EO_PAIRS];
+  __shared__ uint32_t off[257];
+  __shared__ uint32_t strangers;        // ids of no expert
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = blockIdx.x / p.nchunk, c = blockIdx.x - l * p.nchunk;
-  const int64_t i0 = (int64_t)c * EO_PAIRS;
-  const int n = (int)min64(EO_PAIRS, p.N - i0);
-  load_ids(p, p.ids + (size_t)l * p.N + i0, n, sid);
-  for (int e = lane; e < EM; e += 32) count[warp][e] = 0u;
-  __syncthreads();
-  uint32_t rank[EO_IT];
-  // a warp's pairs: whole rounds of 32, spread over the warps where the chunk is short
-  const int span = (n + EO_THREADS - 1) / EO_THREADS * 32;
-  const int w0 = warp * span;
-  bool bad = false;
+  const int k = K8 ? 8 : p.k;
+  const int64_t t0 = (int64_t)c * p.ctok;
+  const int ntok = (int)min64(p.ctok, p.T - t0), ntile = (ntok + 31) >> 5, n = ntok * k;
+  const int64_t i0 = t0 * k;
+  const uint8_t* ids = p.ids + (size_t)l * p.N + i0;
+  const unsigned below = (1u << lane) - 1u;
+  if (threadIdx.x == 0) strangers = 0u;
+  uint2 eight[MINE];
 #pragma unroll
-  for (int it = 0; it < EO_IT; ++it) {
-    if (it * 32 >= span) break;
-    const int i = w0 + it * 32 + lane;
-    const int e = i < n ? sid[i] : 256;
-    const bool ok = e < p.E;
-    bad = bad || (i < n && !ok);
-    unsigned same = __ballot_sync(FULL, ok);
-#pragma unroll
-    for (int b = 0; b < BITS; ++b) {
-      const unsigned v = __ballot_sync(FULL, (e >> b) & 1);
-      same &= ((e >> b) & 1) ? v : ~v;
-    }
-    const unsigned below = same & ((1u << lane) - 1u);
-    const uint32_t before = ok ? count[warp][e & (EM - 1)] : 0u;
-    __syncwarp();
-    if (ok && below == 0u) count[warp][e & (EM - 1)] = before + __popc(same);
-    __syncwarp();
-    rank[it] = before + __popc(below);
+  for (int q = 0; q < MINE; ++q) {
+    const int tile = warp + q * EO_WARPS, t = tile * 32 + lane;
+    eight[q] = make_uint2(0u, 0u);
+    if (K8 && t < ntok) eight[q] = *reinterpret_cast<const uint2*>(ids + t * 8);
+    if (tile < ntile)
+      for (int e = lane; e < EM; e += 32) reinterpret_cast<uint2*>(tiles[tile])[e] = make_uint2(0u, 0u);
   }
-  if (ALONE && bad) atomicOr(p.status, WS_BIT_EDATA);
+  if (!K8) load_ids(p, ids, n, sid);
   __syncthreads();
-  // the warps' counts become the pairs of earlier warps; the experts' totals are scanned
-  uint32_t mine = 0u;
-  const int e = threadIdx.x;
-  if (e < EM) {
+  auto id_of = [&](int q, int t, int j) {
+    if (K8) return (int)(__byte_perm(eight[q].x, eight[q].y, j) & 255u);
+    return (int)sid[t * k + j];
+  };
+  // each lane begins with another choice: tokens often rank the same expert first
+  const int turn = K8 ? lane & 7 : lane % k;
+  uint32_t none = 0u;
 #pragma unroll
-    for (int w = 0; w < EO_WARPS; ++w) {
-      const uint32_t v = count[w][e];
-      count[w][e] = mine;
-      mine += v;
+  for (int q = 0; q < MINE; ++q) {
+    const int tile = warp + q * EO_WARPS, t = tile * 32 + lane;
+    if (t < ntok) {
+      int j = turn;
+#pragma unroll 8
+      for (int i = 0; i < k; ++i) {
+        const int e = id_of(q, t, j);
+        if (e < p.E)
+          atomicOr(&tiles[tile][bits_at(e)], 1u << lane);
+        else
+          ++none;
+        j = K8 ? (j + 1) & 7 : j + 1 < k ? j + 1 : 0;
+      }
     }
   }
-  uint32_t total;
-  const uint32_t start = scan256(e < 256 ? mine : 0u, wsum, total);
+  if (none != 0u) {
+    atomicAdd(&strangers, none);
+    if (ALONE) atomicOr(p.status, WS_BIT_EDATA);
+  }
+  __syncthreads();
+  // the pairs of each expert: in earlier tiles, and in all
+  const int e = threadIdx.x % EM, seg = threadIdx.x / EM;
+  const int s0 = ntile * seg / SEG, s1 = ntile * (seg + 1) / SEG;
+  uint32_t count = 0u;
+  for (int tile = s0; tile < s1; ++tile) count += __popc(tiles[tile][bits_at(e)]);
+  uint32_t mine, before, total, start;
+  auto sum = [&]() {
+    part[seg][e] = count;
+    __syncthreads();
+    mine = before = 0u;
+#pragma unroll
+    for (int i = 0; i < SEG; ++i) {
+      if (i < seg) before += part[i][e];
+      mine += part[i][e];
+    }
+    start = scan256((int)threadIdx.x < EM ? mine : 0u, wsum, total);
+  };
+  sum();
+  const bool serial = total + strangers != (uint32_t)n;  // some token names an expert twice
+  if (serial) {
+    count = 0u;
+    if (seg == 0 && e < p.E)
+      for (int i = 0; i < n; ++i) count += ids[i] == e ? 1u : 0u;
+    sum();
+  }
   uint32_t row = 0u;
   if constexpr (ALONE) {
-    __shared__ uint32_t off[257], tot[256];
     const uint32_t padded = (mine + p.align - 1) / p.align * p.align;
-    uint32_t end;
-    row = scan256(e < 256 ? padded : 0u, wsum, end);
-    if (e < 256) off[e] = row, tot[e] = mine;
-    if (e == 0) off[256] = end;
+    uint32_t last;
+    row = scan256((int)threadIdx.x < EM ? padded : 0u, wsum, last);
+    if (threadIdx.x < 256) off[threadIdx.x] = row;
+    if (threadIdx.x == 0) off[256] = last;
     __syncthreads();
-    if (e <= p.E) p.off[(size_t)l * (p.E + 1) + e] = (int32_t)off[e];
-    if (p.order != nullptr) fill_padding(p, l, off, tot, EO_WARPS);
-  } else if (e < p.E) {
-    row = p.hist[(size_t)blockIdx.x * p.E + e];
+    if ((int)threadIdx.x <= p.E) p.off[(size_t)l * (p.E + 1) + threadIdx.x] = (int32_t)off[threadIdx.x];
+  } else if ((int)threadIdx.x < p.E) {
+    row = p.hist[(size_t)blockIdx.x * p.E + threadIdx.x];
   }
-  if (e < EM) {
-    shift[e] = row - start;
-#pragma unroll
-    for (int w = 0; w < EO_WARPS; ++w) count[w][e] += start;
+  if ((int)threadIdx.x < EM) {
+    shift[threadIdx.x] = row - start;
+    end[threadIdx.x] = row + mine;
+    part[0][threadIdx.x] = start;
   }
   __syncthreads();
+  start = part[0][e];
   int32_t* inv = p.inv != nullptr ? p.inv + (size_t)l * p.N + i0 : nullptr;
-#pragma unroll
-  for (int it = 0; it < EO_IT; ++it) {
-    if (it * 32 >= span) break;
-    const int i = w0 + it * 32 + lane;
-    if (i < n) {
-      const int x = sid[i];
-      const bool ok = x < p.E;
-      const uint32_t place = ok ? rank[it] + count[warp][x & (EM - 1)] : 0u;
-      if (ok) sorted[place] = (uint16_t)i;
-      if (inv != nullptr) inv[i] = ok ? (int32_t)(place + shift[x & (EM - 1)]) : -1;
+  if (!serial) {
+    uint32_t at = start + before;
+    for (int tile = s0; tile < s1; ++tile) {
+      tiles[tile][place_at(e)] = at;
+      at += __popc(tiles[tile][bits_at(e)]);
     }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < MINE; ++q) {
+      const int tile = warp + q * EO_WARPS, t = tile * 32 + lane;
+      if (t < ntok) {
+        auto row_of = [&](int j) {
+          const int x = id_of(q, t, j);
+          int32_t r = -1;
+          if (x < p.E) {
+            const uint2 w = reinterpret_cast<const uint2*>(tiles[tile])[x];
+            const bool odd = (x >> 4 & 1) != 0;
+            const uint32_t place = (odd ? w.x : w.y) + __popc((odd ? w.y : w.x) & below);
+            sorted[place] = (uint32_t)x << 16 | (uint32_t)(t * k + j);
+            r = (int32_t)(place + shift[x]);
+          }
+          return r;
+        };
+        if constexpr (K8) {
+          int32_t rows[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) rows[j] = row_of(j);
+          if (inv != nullptr) {
+            if (p.vec != 0) {
+              *reinterpret_cast<int4*>(inv + t * 8) = make_int4(rows[0], rows[1], rows[2], rows[3]);
+              *reinterpret_cast<int4*>(inv + t * 8 + 4) = make_int4(rows[4], rows[5], rows[6], rows[7]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) inv[t * 8 + j] = rows[j];
+            }
+          }
+        } else if (p.pairs != 0) {
+          for (int j = 0; j < k; j += 2) {
+            const int32_t a = row_of(j), b = row_of(j + 1);
+            if (inv != nullptr) *reinterpret_cast<int2*>(inv + t * k + j) = make_int2(a, b);
+          }
+        } else {
+          for (int j = 0; j < k; ++j) {
+            const int32_t a = row_of(j);
+            if (inv != nullptr) inv[t * k + j] = a;
+          }
+        }
+      }
+    }
+  } else {
+    if (seg == 0 && e < p.E) {
+      uint32_t at = start;
+      for (int i = 0; i < n; ++i)
+        if (ids[i] == e) {
+          if (inv != nullptr) inv[i] = (int32_t)(at + shift[e]);
+          sorted[at++] = (uint32_t)e << 16 | (uint32_t)i;
+        }
+    }
+    if (inv != nullptr)
+      for (int i = threadIdx.x; i < n; i += EO_THREADS)
+        if (ids[i] >= p.E) inv[i] = -1;
   }
   if (p.order != nullptr) {
     __syncthreads();
     int32_t* order = p.order + (size_t)l * p.ld;
     for (int s = threadIdx.x; s < (int)total; s += EO_THREADS) {
-      const int i = sorted[s];
-      order[(uint32_t)s + shift[sid[i]]] = (int32_t)(i0 + i);
+      const uint32_t w = sorted[s];
+      order[(uint32_t)s + shift[w >> 16]] = (int32_t)(i0 + (w & 0xFFFFu));
+    }
+    if (c == p.nchunk - 1) {
+      if constexpr (ALONE)
+        fill_padding(p, l, off, end);
+      else
+        fill_padding(p, l, p.off + (size_t)l * (p.E + 1), end);
     }
   }
   pdl_release();
@@ -263,19 +372,39 @@ __global__ void order_empty_kernel(const OrderParams p) {
     for (int64_t r = threadIdx.x; r < p.ld; r += blockDim.x) p.order[(size_t)l * p.ld + r] = -1;
 }
 
-int64_t order_chunks(int64_t N) { return (N + EO_PAIRS - 1) / EO_PAIRS; }
+// Tokens of a chunk: as many tiles of 32 as the pairs and the tiles allow.
+int order_ctok(int E, int k) {
+  const int tiles = E > 128 ? 16 : EO_TILES, pairs = E > 128 ? EO_PAIRS / 2 : EO_PAIRS;
+  const int fit = pairs / (32 * k);
+  return 32 * (fit < tiles ? fit : tiles);
+}
+int64_t order_chunks(int E, int k, int64_t T) {
+  const int ctok = order_ctok(E, k);
+  return (T + ctok - 1) / ctok;
+}
 
+template <int EM, bool ALONE, bool K8>
+cudaError_t place_run(const OrderParams& p, cudaStream_t st) {
+  static std::atomic<unsigned long long> set{0};
+  constexpr size_t smem = K8 ? PlaceGeo<EM>::SMEM8 : PlaceGeo<EM>::SMEM;
+  const cudaError_t e = smem_optin(order_place_kernel<EM, ALONE, K8>, (int)smem, set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(order_place_kernel<EM, ALONE, K8>, dim3(p.L * p.nchunk), dim3(EO_THREADS), smem, st, p);
+}
 template <bool ALONE>
 cudaError_t place(const OrderParams& p, cudaStream_t st) {
-  const dim3 grid(p.L * p.nchunk), block(EO_THREADS);
-  return p.E <= 64    ? launch_pdl(order_place_kernel<6, ALONE>, grid, block, 0, st, p)
-         : p.E <= 128 ? launch_pdl(order_place_kernel<7, ALONE>, grid, block, 0, st, p)
-                      : launch_pdl(order_place_kernel<8, ALONE>, grid, block, 0, st, p);
+  if (p.k == 8)
+    return p.E <= 64    ? place_run<64, ALONE, true>(p, st)
+           : p.E <= 128 ? place_run<128, ALONE, true>(p, st)
+                        : place_run<256, ALONE, true>(p, st);
+  return p.E <= 64    ? place_run<64, ALONE, false>(p, st)
+         : p.E <= 128 ? place_run<128, ALONE, false>(p, st)
+                      : place_run<256, ALONE, false>(p, st);
 }
 }  // namespace
 
 size_t expert_order_scratch_bytes(const moer_dims* d, int64_t T) {
-  return (size_t)d->L * (size_t)order_chunks(T * d->k) * (size_t)d->E * 4;
+  return (size_t)d->L * (size_t)order_chunks(d->E, d->k, T) * (size_t)d->E * 4;
 }
 
 moer_status expert_order_launch(const moer_dims* d, const uint8_t* topk, int64_t T, int32_t align, int32_t* off,
@@ -285,9 +414,14 @@ moer_status expert_order_launch(const moer_dims* d, const uint8_t* topk, int64_t
   p.N = (int)(T * d->k);
   p.E = d->E;
   p.L = d->L;
+  p.k = d->k;
+  p.T = (int)T;
+  p.ctok = order_ctok(d->E, d->k);
   p.align = align;
-  p.nchunk = (int)order_chunks(p.N);
-  p.vec = reinterpret_cast<uintptr_t>(topk) % 16 == 0 && (p.L == 1 || p.N % 16 == 0);
+  p.nchunk = (int)order_chunks(d->E, d->k, T);
+  p.vec = reinterpret_cast<uintptr_t>(topk) % 16 == 0 && reinterpret_cast<uintptr_t>(inv) % 16 == 0 &&
+          (p.L == 1 || p.N % 16 == 0);
+  p.pairs = p.k % 2 == 0 && reinterpret_cast<uintptr_t>(inv) % 8 == 0;
   p.hist = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + WS_HEADER);
   p.off = off;
   p.order = order;
