@@ -39,6 +39,7 @@ struct ScoreParams {
 };
 
 constexpr float NEG_INF = -__builtin_huge_valf();
+constexpr float LOWEST = -3.402823466e38f;  // the lowest finite number
 
 // ------------------------------------------------------- four logits at once
 // Logits are held as fp32 whatever their type (an exact conversion); a

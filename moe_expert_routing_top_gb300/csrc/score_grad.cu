@@ -158,12 +158,17 @@ __device__ __forceinline__ void store8(X* p, int room, bool wide, const float (&
   if (room >= 8) store4<X>(p + 4, true, b);
 }
 
+// The loads of a warp's next rows are in flight while it works on the present ones:
+// ids and weights' gradients two tiles ahead, the chosen logits (which need the
+// ids) and the rows one tile ahead.  Rows are read before their own are written,
+// so that d_logits may be the logits.
 template <typename X, int LR, bool DENSE>
 __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const ScoreParams p) {
   constexpr int EB = sizeof(X);
   constexpr int RS = 32 / LR;               // rows of a step of the dense part
   constexpr int STEPS = SGT_ROWS / RS;
   constexpr int PITCH = 8 * LR;
+  constexpr int AHEAD = SGT_WARPS * SGT_ROWS;  // tokens from a warp's tile to its next
   // expert e of a row lies at (e / 8) * 4 + e % 4, the upper half of its block 4 LR further on:
   // a lane's two vector accesses are then free of bank conflicts
   __shared__ __align__(16) float chosen[SGT_WARPS][SGT_ROWS][PITCH];
@@ -173,38 +178,68 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = blockIdx.x / p.nspan, unit = blockIdx.x - l * p.nspan;
   const bool soft = p.score == MOER_SCORE_SOFTMAX;
-  const X* base = static_cast<const X*>(p.logits) + l * p.ld_layer;
-  X* obase = static_cast<X*>(p.d_logits) + l * p.ldg_layer;
+  const bool has_a = DENSE && p.d_score_sum != nullptr;
   const int rc = lane >> 3, j = lane & 7;    // the lane's choice
   const int rd = lane / LR, blk = lane % LR; // its block
   const int room = p.E - 8 * blk;
   float a[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    a[i] = DENSE && p.d_score_sum != nullptr && 8 * blk + i < p.E ? p.d_score_sum[(size_t)l * p.E + 8 * blk + i] : 0.f;
-  const int64_t t1 = min64(p.T, (int64_t)(unit + 1) * p.span);
-  for (int64_t t0 = (int64_t)unit * p.span + warp * SGT_ROWS; t0 < t1; t0 += SGT_WARPS * SGT_ROWS) {
-    Raw<EB> raw[STEPS];
-    if (DENSE)
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const int64_t t = min64(t0 + s * RS + rd, t1 - 1);
-        raw[s].template load<X>(base + t * p.ld_token + 8 * blk, room, p.wide != 0);
-      }
-    const int64_t tc = t0 + rc;
-    int id = 0;
-    float g = 0.f, xj = NEG_INF;
-    bool ok = tc < t1 && j < p.k;
-    if (ok) {
-      const int64_t at = ((int64_t)l * p.T + tc) * p.k + j;
-      id = p.ids[at];
-      g = p.scale * p.d_weights[at];
-      ok = id < p.E;
-      if (ok)
-        xj = live_logit(Quad<X>::one(base[tc * p.ld_token + id]));
-      else
-        atomicOr(p.status, WS_BIT_EDATA), g = 0.f, id = 0;
+  for (int i = 0; i < 8; ++i) a[i] = has_a && 8 * blk + i < p.E ? p.d_score_sum[(size_t)l * p.E + 8 * blk + i] : 0.f;
+  // positions within the unit, in 32 bits: first tile, end
+  const int64_t u0 = (int64_t)unit * p.span;
+  const int t1 = (int)min64(p.span, p.T - u0);
+  const X* rows = static_cast<const X*>(p.logits) + l * p.ld_layer + u0 * p.ld_token;
+  X* outs = static_cast<X*>(p.d_logits) + l * p.ldg_layer + u0 * p.ldg_token + 8 * blk;
+  const uint8_t* ids = p.ids + ((int64_t)l * p.T + u0) * p.k + j;
+  const float* dw = p.d_weights + ((int64_t)l * p.T + u0) * p.k + j;
+  struct Pick {
+    int id;   // E and more: no such expert
+    float g;
+  };
+  auto pick = [&](int t0) {
+    Pick c = {0xFFFF, 0.f};  // no choice at all
+    const int t = t0 + rc;
+    if (t < t1 && j < p.k) {
+      c.id = ids[(int64_t)t * p.k];
+      c.g = dw[(int64_t)t * p.k];
     }
+    return c;
+  };
+  auto gather = [&](int t0, const Pick& c) {
+    X x = Quad<X>::back(NEG_INF);
+    if (c.id < p.E) x = rows[(int64_t)(t0 + rc) * p.ld_token + c.id];
+    return x;
+  };
+  auto fetch = [&](Raw<EB>(&to)[STEPS], int t0) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int t = t0 + s * RS + rd;
+      to[s].template load<X>(rows + (int64_t)t * p.ld_token + 8 * blk, t < t1 ? room : 0, p.wide != 0);
+    }
+  };
+  int t0 = warp * SGT_ROWS;
+  if (t0 >= t1) {
+    pdl_release();
+    return;
+  }
+  Pick now = pick(t0), then = pick(t0 + AHEAD);
+  Raw<EB> raw[DENSE ? STEPS : 1];
+  if constexpr (DENSE) fetch(raw, t0);
+  X xnow = gather(t0, now);
+  for (; t0 < t1; t0 += AHEAD) {
+    float v[STEPS][8], rz[STEPS], dot[STEPS];
+    if constexpr (DENSE) {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) raw[s].template get<X>(v[s]);
+      fetch(raw, t0 + AHEAD);
+    }
+    const X xthen = gather(t0 + AHEAD, then);
+    const Pick after = pick(t0 + 2 * AHEAD);
+    bool ok = now.id < p.E;
+    if (now.id >= p.E && now.id != 0xFFFF) atomicOr(p.status, WS_BIT_EDATA);
+    const int id = ok ? now.id : 0;
+    const float g = ok ? p.scale * now.g : 0.f;
+    const float xj = live_logit(Quad<X>::one(xnow));
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       float4* z = reinterpret_cast<float4*>(chosen[warp][s * RS + rd]);
@@ -213,31 +248,42 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
     }
     const int slot = (id >> 3) * 4 + (id & 3) + ((id & 4) != 0 ? 4 * LR : 0);
     if (ok) owner[warp][rc][slot] = (uint8_t)j;
-    float v[STEPS][8], rz[STEPS], dot[STEPS];
     if constexpr (DENSE) {
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
-        raw[s].template get<X>(v[s]);
         if (soft) {
-          float m = NEG_INF;
+          float m = LOWEST;  // under every number lies only -inf, whose exponential is 0
 #pragma unroll
           for (int i = 0; i < 8; ++i) m = fmaxf(m, v[s][i]);
           m = part_max<LR>(m);
-          // no expert, or one at +inf: with exact comparisons
-          const bool edge = __any_sync(FULL, !(fabsf(m) < 3e38f));
-          float z = 0.f, d = 0.f;
+          float z = 0.f, e[8];
           const float mm = m * LOG2E;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float x = fmaxf(v[s][i], NEG_INF);  // NaN -> -inf
-            v[s][i] = edge ? exp_below(x, m) : ex2_approx(fmaf(x, LOG2E, -mm));
-            z += v[s][i];
-            d = fmaf(a[i], v[s][i], d);
+            e[i] = ex2_approx(fmaf(v[s][i], LOG2E, -mm));
+            z += e[i];
           }
           z = part_sum<LR>(z);
-          rz[s] = z > 0.f ? 1.f / z : 0.f;
-          dot[s] = part_sum<LR>(d) * rz[s];
-          if (blk == 0) scalar[warp][s * RS + rd] = make_float4(m, rz[s], 0.f, 0.f);
+          if (__any_sync(FULL, !(z < 3e38f))) {  // a NaN or +inf among the logits, or nothing but masks
+            z = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              e[i] = exp_below(live_logit(v[s][i]), m);
+              z += e[i];
+            }
+            z = part_sum<LR>(z);
+          }
+          rz[s] = z > 0.f ? rcp_approx(z) : 0.f;
+          dot[s] = 0.f;
+          if (has_a) {
+            float d = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d = fmaf(a[i], e[i], d);
+            dot[s] = part_sum<LR>(d) * rz[s];
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[s][i] = e[i];
+          if (!p.renorm && blk == 0) scalar[warp][s * RS + rd] = make_float4(m, rz[s], 0.f, 0.f);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[s][i] = a[i] * sigmoid_slope(live_logit(v[s][i]));
@@ -248,25 +294,29 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
     // the part at the chosen expert
     float dj;
     if (soft) {
+      const float4 mr = DENSE && !p.renorm ? scalar[warp][rc] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float m = p.renorm ? fmaxf(part_max<8>(xj), LOWEST) : mr.x;
+      const float e = xj == m ? 1.f : ex2_approx(LOG2E * (xj - m));
       if (p.renorm) {
-        const float q0 = exp_below(xj, part_max<8>(xj)), z = part_sum<8>(q0);
-        const float q = z > 0.f ? q0 / z : 0.f;
+        const float z = part_sum<8>(e);
+        const float q = z > 0.f ? e * rcp_approx(z) : 0.f;
         dj = q * (g - part_sum<8>(g * q));
       } else {
-        const float4 mr = scalar[warp][rc];
-        dj = g * exp_below(xj, mr.x) * mr.y;
+        dj = g * e * mr.y;
         const float dg = part_sum<8>(dj);
         __syncwarp();
         if (j == 0) scalar[warp][rc].z = dg;
       }
     } else {
+      // s and s (1 - s) from one exponential of -|x|
+      const float t = expf(-fabsf(xj)), r = rcp_approx(1.f + t);
       dj = g;
       if (p.renorm) {
-        const float s = ok ? sigmoid(xj) : 0.f;
+        const float s = ok ? (xj >= 0.f ? r : t * r) : 0.f;
         const float z = part_sum<8>(s), rs = z > 0.f ? 1.f / z : 0.f;
         dj = (g - part_sum<8>(g * s) * rs) * rs;
       }
-      dj *= sigmoid_slope(xj);
+      dj *= t * r * r;
     }
     float* at = &chosen[warp][rc][slot];
     const bool lost = ok && owner[warp][rc][slot] != j;  // an id that is repeated in its row
@@ -288,17 +338,25 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
       float dx[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
       if constexpr (DENSE) {
         if (soft) {
-          const float d = dot[s] + (p.renorm ? 0.f : scalar[warp][r].z);
+          const float d = rz[s] * (dot[s] + (p.renorm ? 0.f : scalar[warp][r].z));
+          if (has_a) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dx[i] += v[s][i] * rz[s] * (a[i] - d);
+            for (int i = 0; i < 8; ++i) dx[i] = fmaf(v[s][i], fmaf(a[i], rz[s], -d), dx[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dx[i] = fmaf(v[s][i], -d, dx[i]);
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) dx[i] += v[s][i];
         }
       }
-      if (t0 + r < t1) store8<X>(obase + (t0 + r) * p.ldg_token + 8 * blk, room, p.wide != 0, dx);
+      if (t0 + r < t1) store8<X>(outs + (int64_t)(t0 + r) * p.ldg_token, room, p.wide != 0, dx);
     }
     __syncwarp();
+    now = then;
+    then = after;
+    xnow = xthen;
   }
   pdl_release();
 }
