@@ -168,6 +168,11 @@ __device__ __forceinline__ float ex2_approx(float x) {  // 2 units in the last p
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float fma_sat(float a, float b, float c) {  // NaN -> 0
+  float r;
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // A logit that counts: -inf for a masked expert, NaN included.
 __device__ __forceinline__ float live_logit(float x) { return x == x ? x : NEG_INF; }
 // 1 / (1 + exp(-x)): 0 at -inf, 1 at +inf; below x = -87 the result is under
@@ -194,6 +199,14 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
   return v;
+}
+
+// Whether n holds a logit exactly: 16-bit logits of size 2^-5 to 128 are
+// multiples of 2^-15, a step of n, so that equal n mean equal logits there and
+// the id in the key orders them.
+template <int EB>
+__device__ __forceinline__ bool exact_n(int n) {
+  return EB == 2 && abs(n - 4194304) > 1024 && n > 0;
 }
 
 // Inverse of rank_key for keys of numbers (NaN's key 1 gives -inf: it adds

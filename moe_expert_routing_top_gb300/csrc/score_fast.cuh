@@ -38,19 +38,6 @@ namespace moer {
 
 constexpr int SF_WARPS = 4;
 
-__device__ __forceinline__ float fma_sat(float a, float b, float c) {  // NaN -> 0
-  float r;
-  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-// Whether n holds a logit exactly: 16-bit logits of size 2^-5 to 128 are
-// multiples of 2^-15, a step of n, so that equal n mean equal logits there and
-// the id in the key orders them.
-template <int EB>
-__device__ __forceinline__ bool exact_n(int n) {
-  return EB == 2 && abs(n - 4194304) > 1024 && n > 0;
-}
-
 // Keys of a block: t holds n in the low 23 bits of a number in [2^23, 2^24); 255 - id goes below n.
 __device__ __forceinline__ void block_ids(const float (&t)[8], uint32_t key_mul, int pos, int (&c)[8]) {
 #pragma unroll

@@ -12,12 +12,13 @@
 // part at the k chosen experts, so a renormalised gate without score sums
 // reads its chosen logits alone.
 //
-// score_grad_tile_kernel (k <= 8, aligned rows): a warp takes four rows of a layer.
-// The choices go to 8 lanes a row, the dense part to LR lanes a row, each with a
-// block of 8 neighbouring experts, so that both are coalesced and full; the
-// chosen experts' parts reach their blocks through a row of shared memory.
+// score_grad_tile_kernel (aligned rows): a warp takes four rows of a layer (two where
+// k > 8, one where k > 16).  The choices go to 8 (16, 32) lanes a row, the dense
+// part to LR lanes a row, each with a block of 8 neighbouring experts, so that both
+// are coalesced and full; the chosen experts' parts reach their blocks through a
+// row of shared memory.
 //
-// score_grad_kernel (any k and alignment): one warp per row; a lane holds the
+// score_grad_kernel (rows off their vectors' boundaries): one warp per row; a lane holds the
 // quads 4 (lane + 32 i) and lane j < k the j-th choice.
 #include "pdl.cuh"
 #include "score.cuh"
@@ -129,7 +130,6 @@ __global__ void __launch_bounds__(SG_WARPS * 32) score_grad_kernel(const ScorePa
 }
 
 constexpr int SGT_WARPS = 8;
-constexpr int SGT_ROWS = 4;  // of a warp at a time
 
 template <int N>
 __device__ __forceinline__ float part_sum(float v) {
@@ -162,24 +162,27 @@ __device__ __forceinline__ void store8(X* p, int room, bool wide, const float (&
 // ids and weights' gradients two tiles ahead, the chosen logits (which need the
 // ids) and the rows one tile ahead.  Rows are read before their own are written,
 // so that d_logits may be the logits.
-template <typename X, int LR, bool DENSE>
+// LR: lanes of a row in the dense part (E <= 8 LR).  KL: lanes of a row for the
+// choices (k <= KL <= LR).
+template <typename X, int LR, int KL, bool DENSE>
 __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const ScoreParams p) {
   constexpr int EB = sizeof(X);
+  constexpr int ROWS = 32 / KL;             // of a warp at a time
   constexpr int RS = 32 / LR;               // rows of a step of the dense part
-  constexpr int STEPS = SGT_ROWS / RS;
+  constexpr int STEPS = ROWS / RS;
   constexpr int PITCH = 8 * LR;
-  constexpr int AHEAD = SGT_WARPS * SGT_ROWS;  // tokens from a warp's tile to its next
+  constexpr int AHEAD = SGT_WARPS * ROWS;  // tokens from a warp's tile to its next
   // expert e of a row lies at (e / 8) * 4 + e % 4, the upper half of its block 4 LR further on:
   // a lane's two vector accesses are then free of bank conflicts
-  __shared__ __align__(16) float chosen[SGT_WARPS][SGT_ROWS][PITCH];
-  __shared__ uint8_t owner[SGT_WARPS][SGT_ROWS][PITCH];
-  __shared__ float4 scalar[SGT_WARPS][SGT_ROWS];
+  __shared__ __align__(16) float chosen[SGT_WARPS][ROWS][PITCH];
+  __shared__ uint8_t owner[SGT_WARPS][ROWS][PITCH];
+  __shared__ float4 scalar[SGT_WARPS][ROWS];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = blockIdx.x / p.nspan, unit = blockIdx.x - l * p.nspan;
   const bool soft = p.score == MOER_SCORE_SOFTMAX;
   const bool has_a = DENSE && p.d_score_sum != nullptr;
-  const int rc = lane >> 3, j = lane & 7;    // the lane's choice
+  const int rc = lane / KL, j = lane % KL;    // the lane's choice
   const int rd = lane / LR, blk = lane % LR; // its block
   const int room = p.E - 8 * blk;
   float a[8];
@@ -217,7 +220,7 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
       to[s].template load<X>(rows + (int64_t)t * p.ld_token + 8 * blk, t < t1 ? room : 0, p.wide != 0);
     }
   };
-  int t0 = warp * SGT_ROWS;
+  int t0 = warp * ROWS;
   if (t0 >= t1) {
     pdl_release();
     return;
@@ -295,15 +298,15 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
     float dj;
     if (soft) {
       const float4 mr = DENSE && !p.renorm ? scalar[warp][rc] : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float m = p.renorm ? fmaxf(part_max<8>(xj), LOWEST) : mr.x;
+      const float m = p.renorm ? fmaxf(part_max<KL>(xj), LOWEST) : mr.x;
       const float e = xj == m ? 1.f : ex2_approx(LOG2E * (xj - m));
       if (p.renorm) {
-        const float z = part_sum<8>(e);
+        const float z = part_sum<KL>(e);
         const float q = z > 0.f ? e * rcp_approx(z) : 0.f;
-        dj = q * (g - part_sum<8>(g * q));
+        dj = q * (g - part_sum<KL>(g * q));
       } else {
         dj = g * e * mr.y;
-        const float dg = part_sum<8>(dj);
+        const float dg = part_sum<KL>(dj);
         __syncwarp();
         if (j == 0) scalar[warp][rc].z = dg;
       }
@@ -313,8 +316,8 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
       dj = g;
       if (p.renorm) {
         const float s = ok ? (xj >= 0.f ? r : t * r) : 0.f;
-        const float z = part_sum<8>(s), rs = z > 0.f ? 1.f / z : 0.f;
-        dj = (g - part_sum<8>(g * s) * rs) * rs;
+        const float z = part_sum<KL>(s), rs = z > 0.f ? 1.f / z : 0.f;
+        dj = (g - part_sum<KL>(g * s) * rs) * rs;
       }
       dj *= t * r * r;
     }
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
     if (__any_sync(FULL, lost)) {
       if (ok) *at = 0.f;
       __syncwarp();
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < KL; ++i) {
         if (ok && j == i) *at += dj;
         __syncwarp();
       }
@@ -361,20 +364,23 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
   pdl_release();
 }
 
-template <typename X, int LR>
+template <typename X, int LR, int KL>
 cudaError_t grad_tile_run(const ScoreParams& p, cudaStream_t st) {
   const bool dense = p.d_score_sum != nullptr || (p.score == MOER_SCORE_SOFTMAX && !p.renorm);
   const dim3 grid((unsigned)(p.L * p.nspan)), block(SGT_WARPS * 32);
-  return dense ? launch_pdl(score_grad_tile_kernel<X, LR, true>, grid, block, 0, st, p)
-               : launch_pdl(score_grad_tile_kernel<X, LR, false>, grid, block, 0, st, p);
+  return dense ? launch_pdl(score_grad_tile_kernel<X, LR, KL, true>, grid, block, 0, st, p)
+               : launch_pdl(score_grad_tile_kernel<X, LR, KL, false>, grid, block, 0, st, p);
 }
 
 template <typename X>
 cudaError_t grad_run(const ScoreParams& p, cudaStream_t st) {
-  if (p.k <= 8 && p.vec != 0)
-    return p.E <= 64    ? grad_tile_run<X, 8>(p, st)
-           : p.E <= 128 ? grad_tile_run<X, 16>(p, st)
-                        : grad_tile_run<X, 32>(p, st);
+  if (p.vec != 0) {
+    if (p.k > 16) return grad_tile_run<X, 32, 32>(p, st);
+    if (p.k > 8) return p.E <= 128 ? grad_tile_run<X, 16, 16>(p, st) : grad_tile_run<X, 32, 16>(p, st);
+    return p.E <= 64    ? grad_tile_run<X, 8, 8>(p, st)
+           : p.E <= 128 ? grad_tile_run<X, 16, 8>(p, st)
+                        : grad_tile_run<X, 32, 8>(p, st);
+  }
   const int64_t rows = (int64_t)p.L * p.T;
   const int64_t want = (rows + SG_WARPS - 1) / SG_WARPS;
   const int sms = device_sm_count();
@@ -387,7 +393,7 @@ cudaError_t grad_run(const ScoreParams& p, cudaStream_t st) {
 
 moer_status score_grad_launch(ScoreParams p, int dtype, cudaStream_t st) {
   // units of a layer's tokens, a multiple of the rows that a block takes at a time
-  constexpr int STEP = SGT_WARPS * SGT_ROWS, UNITS = 152 * 32;
+  const int STEP = SGT_WARPS * (p.k <= 8 ? 4 : p.k <= 16 ? 2 : 1), UNITS = 152 * 32;
   const int64_t span = ((p.T * p.L + UNITS - 1) / UNITS + STEP - 1) / STEP * STEP;
   p.span = (int)span;
   p.nspan = (int)((p.T + span - 1) / span);

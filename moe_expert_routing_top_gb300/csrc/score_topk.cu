@@ -1,9 +1,13 @@
 // score_topk.cu -- moer_score_topk: scores, choice and weights of the router.
 //
-// General kernel (any E <= 256 with E % 4 == 0, any k <= 32, any options): one
-// warp per row.  A lane holds the quads of neighbouring experts 4 (lane + 32 i),
-// as fp32 logits, scores and order-preserving keys of the choice; k rounds of
-// a warp maximum over the keys pick the experts, ties to the lower id.
+// Batches of some thousand rows with k <= 8 go to the fast kernel
+// (score_fast.cuh).  The kernel here takes any E <= 256 with E % 4 == 0, any
+// k <= 32, options and alignment, and is the faster one for few rows: one warp
+// per row, a lane with the quads of neighbouring experts 4 (lane + 32 i).  The
+// choice goes by the fast kernel's keys, a fixed-point number above 255 - id:
+// a lane sorts its own, and k + 1 rounds of a warp maximum over the lanes' first
+// keys take them in order.  Rows that the keys do not settle (see score_fast.cuh)
+// are redone with exact keys (score_row.cuh).
 // A unit of work is a span of tokens of one layer; its eight warps take the
 // rows in turn, and where score sums are wanted each lane adds up its own
 // experts' scores, the warps' sums are joined in warp order and the units' in
@@ -58,24 +62,185 @@ bool fast_supported(const ScoreParams& p) {
   return gs % (8 * lanes) == 0 && (mb & (mb - 1)) == 0 && p.n_group <= 8;
 }
 
+// Sorts four keys in descending order.
+__device__ __forceinline__ void sort4_desc(int (&c)[4]) {
+  cas(c[0], c[2]); cas(c[1], c[3]);
+  cas(c[0], c[1]); cas(c[2], c[3]);
+  cas(c[1], c[2]);
+}
+
+// One row by one warp.  group: the lane's experts' groups; best, second: room for
+// 32 keys each in shared memory (with groups).
+// x: the lane's logits, -inf past the row's end.
 template <typename X, int NQ>
-__global__ void __launch_bounds__(SC_WARPS * 32) score_topk_kernel(const ScoreParams p) {
+__device__ void row_by_keys(const ScoreParams& p, const X* row, float (&x)[4 * NQ], const float (&bias)[4 * NQ],
+                            const int (&group)[4 * NQ], int* best, int* second, int64_t out, int l, int lane,
+                            float (&sum)[4 * NQ]) {
+  constexpr int EB = sizeof(X);
+  const bool soft = p.score == MOER_SCORE_SOFTMAX;
+  const bool use_s = p.bias != nullptr || (p.n_group > 1 && p.group_best == 2);  // the choice takes scores
+  const bool dense = p.partial != nullptr || use_s || (soft && !p.renorm);
+  const int near = use_s ? 2 : 0;
+  int key[4 * NQ];
+#pragma unroll
+  for (int i = 0; i < 4 * NQ; ++i) x[i] = live_logit(x[i]);
+  float m = NEG_INF, rz = 0.f;
+  if (dense) {
+    float s[4 * NQ];
+    if (soft) {
+#pragma unroll
+      for (int i = 0; i < 4 * NQ; ++i) m = fmaxf(m, x[i]);
+      m = warp_max(m);
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * NQ; ++i) {
+        s[i] = x[i] == m ? 1.f : ex2_approx(LOG2E * (x[i] - m));  // equal infinities share
+        if (x[i] == NEG_INF) s[i] = 0.f;
+        z += s[i];
+      }
+      z = warp_sum(z);
+      rz = z > 0.f ? 1.f / z : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * NQ; ++i) s[i] *= rz;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4 * NQ; ++i) s[i] = rcp_approx(1.f + ex2_approx(-LOG2E * x[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * NQ; ++i) {
+      sum[i] += s[i];
+      if (use_s) key[i] = (int)(__float_as_uint(fmaf(fma_sat(s[i] + bias[i], 0.25f, 0.25f), 8388607.f, 8388608.f)) << 8);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4 * NQ; ++i) {
+    const int e = 4 * (lane + 32 * (i / 4)) + i % 4;
+    if (!use_s) key[i] = (int)(__float_as_uint(fmaf(fma_sat(x[i], 1.f / 256.f, 0.5f), 8388607.f, 8388608.f)) << 8);
+    if (x[i] == NEG_INF) key[i] = 0;  // masked experts stay out whatever their bias
+    key[i] = e < p.E ? key[i] | (255 - e) : -1;
+  }
+  bool bad = false;
+  if (p.n_group > 1) {
+    best[lane] = second[lane] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4 * NQ; ++i)
+      if (key[i] >= 0) atomicMax(&best[group[i]], key[i]);
+    __syncwarp();
+    if (p.group_best == 2) {
+#pragma unroll
+      for (int i = 0; i < 4 * NQ; ++i)
+        if (key[i] >= 0 && key[i] != best[group[i]]) atomicMax(&second[group[i]], key[i]);
+      __syncwarp();
+    }
+    const int n2 = second[lane] >> 8;
+    const bool real = lane < p.n_group;
+    // the second best counts only where there are two numbers to add
+    if (real && p.group_best == 2 && n2 <= 0) bad = true;
+    const int gk = real ? ((best[lane] >> 8) + (p.group_best == 2 ? n2 : 0)) * 32 + (31 - lane) : -1;
+    int above = 0;
+    for (int g = 0; g < p.n_group; ++g) above += __shfl_sync(FULL, gk, g) > gk ? 1 : 0;
+    const bool kept = real && above < p.top_group;
+    const unsigned keep = __ballot_sync(FULL, kept);
+    const int thr = __reduce_min_sync(FULL, kept ? gk : INT_MAX) >> 5;
+    const int nxt = __reduce_max_sync(FULL, kept ? -1 : gk) >> 5;
+    if (thr - nxt <= 3 * near && (use_s || !exact_n<EB>(thr))) bad = true;
+#pragma unroll
+    for (int i = 0; i < 4 * NQ; ++i)
+      if (!((keep >> group[i]) & 1u)) key[i] = -1;
+    __syncwarp();
+  }
+  if constexpr (NQ == 1)
+    sort4_desc(key);
+  else
+    sort8_desc(key);
+  // lane r < k holds the r-th key, lane k (or all, if k is 32) the one after
+  int mine = INT_MIN, after = INT_MIN;
+  for (int r = 0; r <= p.k; ++r) {
+    const int top = __reduce_max_sync(FULL, key[0]);
+    if (r == p.k) after = top;
+    if (lane == r) mine = top;
+    if (key[0] == top) {  // keys differ: one lane (or only empty ones are left)
+#pragma unroll
+      for (int i = 0; i + 1 < 4 * NQ; ++i) key[i] = key[i + 1];
+      key[4 * NQ - 1] = -1;
+    }
+  }
+  const bool on = lane < p.k;
+  const int id = 255 - (mine & 255);
+  const float xj = on && mine >= 0 && id < p.E ? live_logit(Quad<X>::one(row[id])) : NEG_INF;
+  const float bj = on && p.bias != nullptr && mine >= 0 ? p.bias[(size_t)l * p.E + id] : 0.f;
+  int next = __shfl_down_sync(FULL, mine, 1);
+  if (lane == p.k - 1) next = after;
+  const float xn = __shfl_down_sync(FULL, xj, 1), bn = __shfl_down_sync(FULL, bj, 1);
+  if (on) {
+    const bool open = (mine >> 8) - (next >> 8) <= near && (use_s || !exact_n<EB>(mine >> 8));
+    bad = bad || mine < 256 || (mine >> 8) >= 8388607;
+    bad = bad || (open && (lane == p.k - 1 ? next >= 0 : !(xj == xn && bj == bn)));
+  }
+  if (__any_sync(FULL, bad)) {
+    float none[4 * NQ];
+#pragma unroll
+    for (int i = 0; i < 4 * NQ; ++i) none[i] = 0.f;
+    score_row<X, NQ>(p, row, bias, p.topk + out * p.k, p.weights != nullptr ? p.weights + out * p.k : nullptr, lane, none);
+    return;
+  }
+  if (on) p.topk[out * p.k + lane] = (uint8_t)id;
+  if (p.weights != nullptr) {
+    float w = 0.f;
+    if (soft)
+      w = exp_below(xj, p.renorm ? warp_max(xj) : m) * (p.renorm ? 1.f : rz);
+    else if (on)
+      w = sigmoid(xj);
+    if (p.renorm) {
+      const float z = warp_sum(w);
+      w = z > 0.f ? w / z : 0.f;
+    }
+    if (on) p.weights[out * p.k + lane] = p.scale * w;
+  }
+}
+
+template <typename X, int NQ>
+__global__ void __launch_bounds__(SC_WARPS * 32, 3) score_topk_kernel(const ScoreParams p) {
   __shared__ float part[SC_WARPS][128 * NQ];
+  __shared__ int group_key[SC_WARPS][2][32];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = blockIdx.x / p.nspan, u = blockIdx.x - l * p.nspan;
   float bias[4 * NQ], sum[4 * NQ];
+  int group[4 * NQ];
+  const int gs = p.E / p.n_group;
 #pragma unroll
   for (int i = 0; i < 4 * NQ; ++i) {
     const int e = 4 * (lane + 32 * (i / 4)) + i % 4;
+    group[i] = p.n_group > 1 ? min(e / gs, 31) : 0;
     bias[i] = p.bias != nullptr && e < p.E ? p.bias[(size_t)l * p.E + e] : 0.f;
     sum[i] = 0.f;
   }
   const int64_t t1 = min64(p.T, (int64_t)(u + 1) * p.span);
-  for (int64_t t = (int64_t)u * p.span + warp; t < t1; t += SC_WARPS)
-    score_row<X, NQ>(p, static_cast<const X*>(p.logits) + l * p.ld_layer + t * p.ld_token, bias,
-                     p.topk + ((int64_t)l * p.T + t) * p.k,
-                     p.weights != nullptr ? p.weights + ((int64_t)l * p.T + t) * p.k : nullptr, lane, sum);
+  int64_t t = (int64_t)u * p.span + warp;
+  const X* row = static_cast<const X*>(p.logits) + l * p.ld_layer + t * p.ld_token;
+  float x[4 * NQ], ahead[4 * NQ];  // the row's logits, and those of the warp's next one
+  auto fetch = [&](const X* of, float (&to)[4 * NQ]) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int e = 4 * (lane + 32 * q);
+      float v[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+      if (e < p.E) load4<X>(of + e, p.vec != 0, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) to[4 * q + j] = v[j];
+    }
+  };
+  if (t < t1) fetch(row, x);
+  for (; t < t1; t += SC_WARPS) {
+    const X* next = row + SC_WARPS * p.ld_token;
+    if (t + SC_WARPS < t1) fetch(next, ahead);
+    row_by_keys<X, NQ>(p, row, x, bias, group, group_key[warp][0], group_key[warp][1], (int64_t)l * p.T + t, l, lane,
+                       sum);
+#pragma unroll
+    for (int i = 0; i < 4 * NQ; ++i) x[i] = ahead[i];
+    row = next;
+  }
   if (p.partial != nullptr) {
 #pragma unroll
     for (int i = 0; i < 4 * NQ; ++i) part[warp][4 * (lane + 32 * (i / 4)) + i % 4] = sum[i];
