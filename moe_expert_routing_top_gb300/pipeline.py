@@ -15,6 +15,13 @@ place of the first call.  `moer_ids_signature` derives the block counts and
 co-activation from top-k ids already produced (the bench uses it to time the
 dominant kernel's call alone).
 
+With a scored gate (`set_gate`: softmax or sigmoid scores, a balance bias, expert
+groups, renormalised weights) the step runs on the ids of `moer_score_topk`
+instead and also gives the experts' weights and token lists (`score_step`;
+`moer_expert_order`); `score_grad` is the gate's gradient for training.
+`BatchDev.from_lengths` makes a batch's tables on the GPU from its requests'
+lengths (`moer_block_plan`).
+
 `calibrate` runs the offline half (idf, greedy layer mask, balanced K-means
 centroids, spectral expert groups) call by call on the GPU, and
 `save_calibration` / `load_calibration` carry its result to the serving side.
@@ -45,6 +52,47 @@ class BatchDev:
     req_cache_off: Optional[torch.Tensor]
     insert_slot: Optional[torch.Tensor]
     ncached: int = 0
+    req_off: Optional[torch.Tensor] = None   # with from_lengths: [R+1] CSR of the computed tokens,
+    slot_map: Optional[torch.Tensor] = None  # [T] int64 KV cache slot of each,
+    tok_req: Optional[torch.Tensor] = None   # [T] its request
+    tok_pos: Optional[torch.Tensor] = None   # [T] and its position there
+
+    @staticmethod
+    def from_lengths(new_len, ctx_len, block, pages=None, free_pages=None, device="cuda", stream=None) -> "BatchDev":
+        """A batch's tables made on the GPU from the requests' lengths (host arrays: tokens to
+        compute, tokens held in the KV cache).  `pages` [R][width] int32 (device) is the KV
+        cache's block table, with the held tokens' pages in it; the pages newly needed come
+        from `free_pages` (device) in request order and are written into it.  Without `pages`
+        the batch has no slots and no signature cache."""
+        new = np.ascontiguousarray(new_len, dtype=np.int32)
+        ctx = np.ascontiguousarray(ctx_len, dtype=np.int32)
+        B, R = int(block), len(new)
+        n, c = new.astype(np.int64), ctx.astype(np.int64)
+        T, nblk = int(n.sum()), int(np.where(n > 0, -(-(c % B + n) // B), 0).sum())
+        ncached = int((c // B).sum()) if pages is not None else 0
+        i32 = torch.int32
+
+        def empty(*shape, dtype=i32):
+            return torch.empty(shape, dtype=dtype, device=device)
+        b = {"new_len": torch.from_numpy(new).to(device), "ctx_len": torch.from_numpy(ctx).to(device),
+             "req_off": empty(R + 1), "req_blk_off": empty(R + 1), "blk_tab": empty(max(nblk, 1), 2),
+             "tok_req": empty(T), "tok_pos": empty(T)}
+        if pages is not None:
+            b.update(pages=pages, free_pages=free_pages, insert_slot=empty(max(nblk, 1)), req_cache_off=empty(R + 1),
+                     cache_idx=empty(max(ncached, 1)), slot_map=empty(T, dtype=torch.int64))
+        args = nat.make_block_plan(R=R, block=B, T=T, nblk=nblk, ncached=ncached,
+                                   ld_pages=0 if pages is None else pages.shape[1],
+                                   n_free=0 if free_pages is None else free_pages.numel(), **b)
+        wsb = nat.moer_block_plan_workspace_bytes(R)
+        ws = torch.zeros(wsb, dtype=torch.uint8, device=device)
+        nat.moer_block_plan(args, ws, wsb, stream)
+        code = nat.moer_ws_status(ws, stream)
+        if code != 0:
+            raise nat.MoerError("moer_block_plan", code, nat.moer_status_str(code))
+        return BatchDev(T=T, R=R, nblk=nblk, blk_tab=b["blk_tab"], req_blk_off=b["req_blk_off"],
+                        cache_idx=b.get("cache_idx"), req_cache_off=b.get("req_cache_off"),
+                        insert_slot=b.get("insert_slot"), ncached=ncached, req_off=b["req_off"],
+                        slot_map=b.get("slot_map"), tok_req=b["tok_req"], tok_pos=b["tok_pos"])
 
     @staticmethod
     def from_host(b, device="cuda", with_cache=True, pin=False) -> "BatchDev":
@@ -92,6 +140,7 @@ class RoutingStats:
                       if nslots > 0 else None)
         self.nslots = nslots
         self.gate_H = 0
+        self.score_opts = self.bias = None
         self._alloc(max_T, max_nblk, max_R)
 
     def _alloc(self, T, nblk, R):
@@ -106,6 +155,10 @@ class RoutingStats:
         self.ws_bytes = nat.moer_workspace_bytes(self.dims, T, nblk, R, D)
         if self.gate_H:
             self.ws_bytes = max(self.ws_bytes, nat.moer_gate_workspace_bytes(self.dims, self.gate_H))
+        if self.score_opts is not None:
+            self.weights = torch.empty(L * max(T, 1) * k, dtype=torch.float32, device=dev)
+            self.ws_bytes = max(self.ws_bytes, nat.moer_score_workspace_bytes(self.dims, T),
+                                nat.moer_expert_order_workspace_bytes(self.dims, T))
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
 
     def ensure(self, T, nblk, R, H=0):
@@ -118,6 +171,61 @@ class RoutingStats:
     def topk_for(self, T: int) -> torch.Tensor:
         """The top-k ids of the last batch of T tokens, as [L][T][k]."""
         return self.topk[:self.L * T * self.k].view(self.L, T, self.k)
+
+    # ------------------------------------------------------ scored gates
+    def set_gate(self, opts: "nat.moer_score_opts", bias=None):
+        """The scored gate of `score_step` (options from make_score_opts) and its balance bias
+        ([L][E] fp32, or None), which the caller may go on changing in place."""
+        self.score_opts = opts
+        self.bias = None if bias is None else torch.as_tensor(bias, dtype=torch.float32).to(self.device).contiguous()
+        self._alloc(*self.cap)
+
+    def weights_for(self, T: int) -> torch.Tensor:
+        """The weights of the last batch of T tokens, as [L][T][k]."""
+        return self.weights[:self.L * T * self.k].view(self.L, T, self.k)
+
+    def score_topk(self, logits, score_sum=None):
+        """Top-k ids and weights of the scored gate; logits [L][T][E] with any strides between
+        rows; score_sum [L][E] fp32, if given, receives the scores' sums."""
+        T = logits.shape[1]
+        nat.moer_score_topk(self.dims, self.score_opts, logits, T, logits.stride(1), logits.stride(0), self.bias,
+                            self.topk, self.weights, score_sum, self.ws, self.ws_bytes, self.stream)
+
+    def score_grad(self, logits, d_weights, d_score_sum=None, out=None) -> torch.Tensor:
+        """The logits' gradient from that of the weights ([L][T][k] fp32) and, if given, of the
+        score sums ([L][E]), for the ids of the last score_topk call on these logits."""
+        T = logits.shape[1]
+        out = torch.empty_like(logits) if out is None else out
+        nat.moer_score_topk_grad(self.dims, self.score_opts, logits, T, logits.stride(1), logits.stride(0), self.topk,
+                                 d_weights, d_score_sum, out, out.stride(1), out.stride(0), self.ws, self.ws_bytes,
+                                 self.stream)
+        return out
+
+    def expert_order(self, T: int, align: int = 1):
+        """The experts' token lists of the last batch: offsets [L][E+1], pairs in expert order
+        [L][rows] (segments padded to `align`) and each pair's row [L][T][k]."""
+        n = T * self.k
+        ld = n + min(self.E, n) * (align - 1)
+        i32, dev = torch.int32, self.device
+        off = torch.empty((self.L, self.E + 1), dtype=i32, device=dev)
+        order = torch.empty((self.L, ld), dtype=i32, device=dev)
+        inv = torch.empty((self.L, T, self.k), dtype=i32, device=dev)
+        nat.moer_expert_order(self.dims, self.topk, T, align, off, order, ld, inv, self.ws, self.ws_bytes, self.stream)
+        return off, order, inv
+
+    def score_step(self, logits, bd: BatchDev, align=1, score_sum=None, write_sig=True):
+        """All rows of the path over one batch through the scored gate, and the experts' token
+        lists (returned).  Co-activation and loads need E <= 128 and k in {6, 8}
+        (moer_ids_signature's limit) and are left as they are otherwise."""
+        self.ensure(bd.T, bd.nblk, bd.R)
+        self.score_topk(logits, score_sum)
+        counted = self.E <= 128 and self.k in (6, 8)
+        self.ids_signature(bd, blk_counts=True, affinity=counted)
+        self.block_stitch(bd)
+        if counted:
+            self.affinity_load()
+        self.route(bd.R, write_sig)
+        return self.expert_order(bd.T, align)
 
     def reset_stats(self):
         self.affinity.zero_()
