@@ -129,6 +129,7 @@ __device__ __forceinline__ void fill_padding(const OrderParams& p, int l, const 
 __global__ void __launch_bounds__(EO_SCAN) order_offsets_kernel(const OrderParams p) {
   __shared__ uint32_t off[257], wsum[8], quarter[4][256];
   pdl_wait();
+  pdl_release();  // the place kernel's blocks rank their pairs meanwhile, and wait before they read what this one writes
   const int l = blockIdx.x, e = threadIdx.x & 255, q = threadIdx.x >> 8;
   uint32_t* h = p.hist + (size_t)l * p.nchunk * p.E;
   const int c0 = (int)((int64_t)p.nchunk * q / 4), c1 = (int)((int64_t)p.nchunk * (q + 1) / 4);
@@ -159,7 +160,6 @@ __global__ void __launch_bounds__(EO_SCAN) order_offsets_kernel(const OrderParam
       r += n;
     }
   }
-  pdl_release();
 }
 
 // EM: room for the experts, 64, 128 or 256.  ALONE: the layer is one chunk, and this
@@ -192,7 +192,9 @@ __global__ void __launch_bounds__(EO_THREADS) order_place_kernel(const OrderPara
   __shared__ uint32_t wsum[8];
   __shared__ uint32_t off[257];
   __shared__ uint32_t strangers;        // ids of no expert
-  pdl_wait();
+  // Not ALONE, the ids are final already: the offsets kernel releases this one only
+  // after the kernels before it have ended, and only its offsets are waited for, below.
+  if (ALONE) pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = blockIdx.x / p.nchunk, c = blockIdx.x - l * p.nchunk;
   const int k = K8 ? 8 : p.k;
@@ -266,6 +268,7 @@ __global__ void __launch_bounds__(EO_THREADS) order_place_kernel(const OrderPara
       for (int i = 0; i < n; ++i) count += ids[i] == e ? 1u : 0u;
     sum();
   }
+  if (!ALONE) pdl_wait();
   uint32_t row = 0u;
   if constexpr (ALONE) {
     const uint32_t padded = (mine + p.align - 1) / p.align * p.align;

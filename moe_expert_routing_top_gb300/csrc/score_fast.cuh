@@ -135,15 +135,8 @@ __device__ __forceinline__ void put_ids(uint8_t* to, int own, int even, const in
   }
 }
 
-// What the choice goes by.
-enum ScoreKind {
-  BY_LOGIT = 0,        // the logits alone; weights from the chosen ones
-  BY_LOGIT_DENSE = 1,  // the logits; with the column pass
-  BY_SCORE = 2         // scores (a bias, or groups ranked by two scores), or groups
-};
-
 template <typename X, int G, int NB, int KIND>
-__global__ void __launch_bounds__(SF_WARPS * 32, 5) score_fast_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)) score_fast_kernel(const ScoreParams p) {
   constexpr int RW = 32 / G;            // rows of a warp at a time
   constexpr int EB = sizeof(X);
   constexpr int NQ = G > 2 ? 2 : 1;     // quads of a lane on the exact path
@@ -553,10 +546,11 @@ __global__ void __launch_bounds__(SF_WARPS * 32, 5) score_fast_kernel(const Scor
 template <typename X, int G, int NB>
 cudaError_t score_fast_shape(const ScoreParams& p, cudaStream_t st) {
   const dim3 grid(p.L * p.nspan), block(SF_WARPS * 32);
-  if (p.bias != nullptr || p.n_group > 1) return launch_pdl(score_fast_kernel<X, G, NB, BY_SCORE>, grid, block, 0, st, p);
-  if (p.partial != nullptr || (p.score == MOER_SCORE_SOFTMAX && !p.renorm))
-    return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT_DENSE>, grid, block, 0, st, p);
-  return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT>, grid, block, 0, st, p);
+  switch (score_kind(p.bias != nullptr, p.n_group, p.partial != nullptr, p.score == MOER_SCORE_SOFTMAX, p.renorm != 0)) {
+    case BY_LOGIT: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT>, grid, block, 0, st, p);
+    case BY_LOGIT_DENSE: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT_DENSE>, grid, block, 0, st, p);
+    default: return launch_pdl(score_fast_kernel<X, G, NB, BY_SCORE>, grid, block, 0, st, p);
+  }
 }
 
 template <typename X>

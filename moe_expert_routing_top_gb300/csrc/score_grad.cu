@@ -191,36 +191,44 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
   // positions within the unit, in 32 bits: first tile, end
   const int64_t u0 = (int64_t)unit * p.span;
   const int t1 = (int)min64(p.span, p.T - u0);
-  const X* rows = static_cast<const X*>(p.logits) + l * p.ld_layer + u0 * p.ld_token;
-  X* outs = static_cast<X*>(p.d_logits) + l * p.ldg_layer + u0 * p.ldg_token + 8 * blk;
-  const uint8_t* ids = p.ids + ((int64_t)l * p.T + u0) * p.k + j;
-  const float* dw = p.d_weights + ((int64_t)l * p.T + u0) * p.k + j;
   struct Pick {
     int id;   // E and more: no such expert
     float g;
   };
-  auto pick = [&](int t0) {
+  // addresses of the lane's choice and block in the warp's first tile; `tile` counts tiles from it
+  const int t00 = warp * ROWS;
+  const uint8_t* ids = p.ids + ((int64_t)l * p.T + u0 + t00 + rc) * p.k + j;
+  const float* dw = p.d_weights + ((int64_t)l * p.T + u0 + t00 + rc) * p.k + j;
+  const X* crow = static_cast<const X*>(p.logits) + l * p.ld_layer + (u0 + t00 + rc) * p.ld_token;
+  const X* brow = static_cast<const X*>(p.logits) + l * p.ld_layer + (u0 + t00 + rd) * p.ld_token + 8 * blk;
+  X* orow = static_cast<X*>(p.d_logits) + l * p.ldg_layer + (u0 + t00 + rd) * p.ldg_token + 8 * blk;
+  const int kstep = AHEAD * p.k;
+  const int64_t cstep = AHEAD * p.ld_token, ostep = AHEAD * p.ldg_token;
+  const int64_t rs_in = RS * p.ld_token, rs_out = RS * p.ldg_token;
+  const bool chooses = j < p.k;
+  auto pick = [&](int t0) {  // at the tile that ids and dw point to, whose first token is t0
     Pick c = {0xFFFF, 0.f};  // no choice at all
-    const int t = t0 + rc;
-    if (t < t1 && j < p.k) {
-      c.id = ids[(int64_t)t * p.k];
-      c.g = dw[(int64_t)t * p.k];
+    if (chooses && t0 + rc < t1) {
+      c.id = *ids;
+      c.g = *dw;
     }
+    ids += kstep;
+    dw += kstep;
     return c;
   };
-  auto gather = [&](int t0, const Pick& c) {
+  auto gather = [&](const Pick& c) {
     X x = Quad<X>::back(NEG_INF);
-    if (c.id < p.E) x = rows[(int64_t)(t0 + rc) * p.ld_token + c.id];
+    if (c.id < p.E) x = crow[c.id];
+    crow += cstep;
     return x;
   };
   auto fetch = [&](Raw<EB>(&to)[STEPS], int t0) {
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int t = t0 + s * RS + rd;
-      to[s].template load<X>(rows + (int64_t)t * p.ld_token + 8 * blk, t < t1 ? room : 0, p.wide != 0);
-    }
+    for (int s = 0; s < STEPS; ++s)
+      to[s].template load<X>(brow + s * rs_in, t0 + s * RS + rd < t1 ? room : 0, p.wide != 0);
+    brow += cstep;
   };
-  int t0 = warp * ROWS;
+  int t0 = t00;
   if (t0 >= t1) {
     pdl_release();
     return;
@@ -228,7 +236,7 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
   Pick now = pick(t0), then = pick(t0 + AHEAD);
   Raw<EB> raw[DENSE ? STEPS : 1];
   if constexpr (DENSE) fetch(raw, t0);
-  X xnow = gather(t0, now);
+  X xnow = gather(now);
   for (; t0 < t1; t0 += AHEAD) {
     float v[STEPS][8], rz[STEPS], dot[STEPS];
     if constexpr (DENSE) {
@@ -236,7 +244,7 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
       for (int s = 0; s < STEPS; ++s) raw[s].template get<X>(v[s]);
       fetch(raw, t0 + AHEAD);
     }
-    const X xthen = gather(t0 + AHEAD, then);
+    const X xthen = gather(then);
     const Pick after = pick(t0 + 2 * AHEAD);
     bool ok = now.id < p.E;
     if (now.id >= p.E && now.id != 0xFFFF) atomicOr(p.status, WS_BIT_EDATA);
@@ -354,8 +362,9 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
           for (int i = 0; i < 8; ++i) dx[i] += v[s][i];
         }
       }
-      if (t0 + r < t1) store8<X>(outs + (int64_t)(t0 + r) * p.ldg_token, room, p.wide != 0, dx);
+      if (t0 + r < t1) store8<X>(orow + s * rs_out, room, p.wide != 0, dx);
     }
+    orow += ostep;
     __syncwarp();
     now = then;
     then = after;

@@ -27,7 +27,6 @@ constexpr int SC_WARPS = 8;
 constexpr int SC_UNITS = 4864;  // units asked for: 152 SMs x 32
 
 constexpr int64_t SC_FAST_ROWS = 4096;  // rows from which the fast kernel is taken
-constexpr int SC_FAST_RESIDENT = 5;     // its blocks on an SM
 
 // Tokens of a unit: a multiple of `step`, the rows that a block takes at a time.
 int score_span(int64_t T, int L, int step) {
@@ -297,7 +296,10 @@ moer_status score_topk_launch(ScoreParams p, int dtype, float* score_sum, void* 
   if (fast) {
     const int sms = device_sm_count();
     if (sms <= 0) return MOER_ECUDA;
-    p.span = fast_span(p.T, p.L, p.E <= 64 ? 128 : p.E <= 128 ? 64 : 32, (int64_t)sms * SC_FAST_RESIDENT);
+    const int kind = score_kind(p.bias != nullptr, p.n_group, score_sum != nullptr, p.score == MOER_SCORE_SOFTMAX,
+                                p.renorm != 0);
+    p.span = fast_span(p.T, p.L, p.E <= 64 ? 128 : p.E <= 128 ? 64 : 32,
+                       (int64_t)sms * score_resident(dtype == MOER_F32 ? 4 : 2, kind));
   } else {
     p.span = score_span(p.T, p.L, SC_WARPS);
   }
