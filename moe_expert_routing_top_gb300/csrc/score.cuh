@@ -38,19 +38,25 @@ struct ScoreParams {
   uint32_t* status;
 };
 
-// What the fast kernel's choice goes by.
+// What the fast kernel's choice goes by.  A kernel for each keeps its code short:
+// one for all of the last three took as long with a fifth fewer instructions
+// an expert, for it left the instruction cache between its branches.
 enum ScoreKind {
   BY_LOGIT = 0,        // the logits alone; weights from the chosen ones
   BY_LOGIT_DENSE = 1,  // the logits; with the column pass
-  BY_SCORE = 2         // scores (a bias, or groups ranked by two scores), or groups
+  BY_GROUP = 2,        // groups ranked by their best logit
+  BY_SIGMOID = 3,      // scores: a bias, or groups ranked by two scores
+  BY_SOFTMAX = 4
 };
-constexpr ScoreKind score_kind(bool bias, int n_group, bool sums, bool soft, bool renorm) {
-  return bias || n_group > 1 ? BY_SCORE : sums || (soft && !renorm) ? BY_LOGIT_DENSE : BY_LOGIT;
+inline ScoreKind score_kind(bool bias, int n_group, int group_best, bool sums, bool soft, bool renorm) {
+  if (bias || (n_group > 1 && group_best == 2)) return soft ? BY_SOFTMAX : BY_SIGMOID;
+  if (n_group > 1) return BY_GROUP;
+  return sums || (soft && !renorm) ? BY_LOGIT_DENSE : BY_LOGIT;
 }
 // Blocks of 128 threads of the fast kernel on an SM, which sets its registers.  Cases
 // of 3.1 M rows x 128 fp32 / 213 k x 256 bf16 by score / 780 k x 64 bf16 with column
 // pass: 4 blocks 341 / 87 / 72 us, 5 blocks 291 / 91 / 70 us, 6 blocks 334 / 142 / 67 us.
-constexpr int score_resident(int elem, int kind) { return kind == BY_SCORE ? 4 : elem == 2 ? 6 : 5; }
+constexpr int score_resident(int elem, int kind) { return kind >= BY_GROUP ? 5 : elem == 2 ? 6 : 5; }
 
 constexpr float NEG_INF = -__builtin_huge_valf();
 constexpr float LOWEST = -3.402823466e38f;  // the lowest finite number
@@ -123,9 +129,10 @@ struct Raw;
 template <>
 struct Raw<4> {
   float v[8];
+  // room: experts left in the row; the block's others are `fill` (-inf or 0)
   template <typename X>
-  __device__ __forceinline__ void load(const float* p, int room, bool) {
-    float4 a = make_float4(NEG_INF, NEG_INF, NEG_INF, NEG_INF), b = a;
+  __device__ __forceinline__ void load(const float* p, int room, bool, float fill = NEG_INF) {
+    float4 a = make_float4(fill, fill, fill, fill), b = a;
     if (room >= 4) a = *reinterpret_cast<const float4*>(p);
     if (room >= 8) b = *reinterpret_cast<const float4*>(p + 4);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
@@ -140,9 +147,9 @@ template <>
 struct Raw<2> {
   uint4 v;
   template <typename X>
-  __device__ __forceinline__ void load(const X* p, int room, bool wide) {
-    constexpr uint32_t LOW = sizeof(X) == 2 && std::is_same<X, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
-    v = make_uint4(LOW, LOW, LOW, LOW);
+  __device__ __forceinline__ void load(const X* p, int room, bool wide, float fill = NEG_INF) {
+    const uint32_t low = fill == 0.f ? 0u : std::is_same<X, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+    v = make_uint4(low, low, low, low);
     if (wide) {
       if (room >= 8) v = *reinterpret_cast<const uint4*>(p);
       else if (room >= 4) {

@@ -11,8 +11,8 @@
 // the binade [2^23, 2^24), whose mantissa bits are n; a multiply-add puts
 // 255 - id below it.  The three steps run on the FMA pipe, while the networks'
 // minima and maxima fill the ALU pipe, which is the kernel's bound.  The range is
-// +-128 for logits (steps of 2^-15) and [-1, 3) for choice scores (5e-7; with
-// biases of at most 1 the first two steps and the bias are one multiply-add).
+// +-128 for logits (steps of 2^-15) and [-1, 3) for choice scores (5e-7; the bias
+// comes in with the first step).
 //
 // A row's answer is kept only where it is certain: the k-th key above 0, the
 // first below the top of the range, no two neighbours among the k + 1 leading keys
@@ -135,6 +135,32 @@ __device__ __forceinline__ void put_ids(uint8_t* to, int own, int even, const in
   }
 }
 
+struct Eight {
+  float v[8];
+};
+// u = (c + 1) / 4 of a block's choice scores c = s + b, saturated onto [0, 1].
+template <int KIND>
+__device__ __forceinline__ Eight choice(Eight x, const Eight& bias, float mm, float rs) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float s = KIND == BY_SOFTMAX ? ex2_approx(fmaf(x.v[j], LOG2E, -mm)) * rs
+                                       : rcp_approx(1.f + ex2_approx(-LOG2E * x.v[j]));
+    x.v[j] = fma_sat(s, 0.25f, bias.v[j]);
+  }
+  return x;
+}
+// The same where logits are infinite or NaN: masked experts stay out whatever their bias.
+template <int KIND>
+__device__ __noinline__ Eight far_choice(Eight x, Eight bias, float mm, float rs) {
+  Eight y = x;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y.v[j] = fmaxf(x.v[j], NEG_INF);  // NaN -> -inf
+  const Eight u = choice<KIND>(y, bias, mm, rs);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y.v[j] = y.v[j] == NEG_INF ? 0.f : u.v[j];
+  return y;
+}
+
 template <typename X, int G, int NB, int KIND>
 __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)) score_fast_kernel(const ScoreParams p) {
   constexpr int RW = 32 / G;            // rows of a warp at a time
@@ -144,35 +170,27 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
   constexpr int CL = 8 * G;             // lanes of a row in the column pass
   constexpr int PF = NB % 4 == 0 ? 4 : NB % 3 == 0 ? 3 : 2;  // blocks in flight: a block's registers take the one PF ahead
   static_assert(NB % PF == 0, "whole rounds of the block buffers");
-  constexpr int ROUNDS = KIND == BY_SCORE ? 1 : NB / PF;  // unrolled (the longer body: rolled, for the instruction cache)
-  __shared__ __align__(16) float sbias[KIND == BY_SCORE ? 256 : 1];
+  constexpr bool LISTS = KIND >= BY_GROUP;     // there may be groups
+  constexpr bool SCORES = KIND >= BY_SIGMOID;  // the choice takes scores
+  constexpr int ROUNDS = SCORES ? 1 : NB / PF; // unrolled (the longer bodies: rolled, for the instruction cache)
+  __shared__ __align__(16) float sbias[SCORES ? 256 : 1];
   __shared__ float part[SF_WARPS][KIND != BY_LOGIT ? 8 * CL : 1];
-  __shared__ int4 lists[KIND == BY_SCORE ? SF_WARPS : 1][KIND == BY_SCORE ? NB : 1][2][32];  // sorted blocks
+  __shared__ int4 lists[LISTS ? SF_WARPS : 1][LISTS ? NB : 1][2][32];  // sorted blocks
   __shared__ float2 row_mr[SF_WARPS][RW];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane % G, rl = lane / G;
   const int l = blockIdx.x / p.nspan, unit = blockIdx.x - l * p.nspan;
   const bool soft = p.score == MOER_SCORE_SOFTMAX;
-  const bool has_bias = KIND == BY_SCORE && p.bias != nullptr;
-  const bool use_s = KIND == BY_SCORE && (has_bias || (p.n_group > 1 && p.group_best == 2));
+  const bool has_bias = SCORES && p.bias != nullptr;
   const bool sums = KIND != BY_LOGIT && p.partial != nullptr;
   const bool columns = KIND != BY_LOGIT && (sums || (soft && !p.renorm));
-  // biases of at most 1 in size: n = s 2^21 + (b + 1) 2^21 in one multiply-add, at most one step off
-  bool tight = true;
-  if (use_s) {
-    bool in = true;
-    for (int e = threadIdx.x; e < 256; e += SF_WARPS * 32) {
-      sbias[e] = has_bias && e < p.E ? p.bias[(size_t)l * p.E + e] : 0.f;
-      in = in && fabsf(sbias[e]) <= 1.f;
-    }
-    tight = __syncthreads_and(in) != 0;
-    if (tight)
-      for (int e = threadIdx.x; e < 256; e += SF_WARPS * 32) sbias[e] = fmaf(sbias[e], 2097152.f, 10485760.f);
+  if constexpr (SCORES) {
+    for (int e = threadIdx.x; e < 256; e += SF_WARPS * 32)  // u = s / 4 + (b + 1) / 4
+      sbias[e] = has_bias && e < p.E ? fmaf(p.bias[(size_t)l * p.E + e], 0.25f, 0.25f) : 0.25f;
     __syncthreads();
   }
-  // steps of n that do not settle an order: a score is rounded before its key is
-  const int near = use_s ? 2 : 0;
+  constexpr int near = SCORES ? 2 : 0;  // steps of n that do not settle an order: a score is rounded before its key is
   float acc[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) acc[q] = 0.f;
@@ -188,7 +206,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
     if (full)
       to.template load<X>(of + e, 8, true);
     else
-      to.template load<X>(of + e, p.E - e, p.wide != 0);
+      to.template load<X>(of + e, p.E - e, p.wide != 0, SCORES ? 0.f : NEG_INF);
   };
   const X* row = t0 < t1 ? row_at(t0) : base;
   if (t0 < t1)
@@ -201,12 +219,13 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
     int top[8], ninth = INT_MIN;
     bool bad = false;
     float mm = 0.f, rs = 1.f;
-    if (KIND == BY_SCORE && use_s && soft) {
+    if constexpr (KIND == BY_SOFTMAX) {
       // the softmax first: the row from L1 twice, its largest logit and the sum
       float m = NEG_INF, z = 0.f;
       for (int b = 0; b < NB; ++b) {
         Raw<EB> again;
-        fetch(again, b, row);
+        const int e = 8 * (i + G * b);
+        again.template load<X>(row + e, p.E - e, p.wide != 0);
         float x[8];
         again.template get<X>(x);
 #pragma unroll
@@ -217,7 +236,8 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
       mm = bad ? 0.f : m * LOG2E;
       for (int b = 0; b < NB; ++b) {
         Raw<EB> again;
-        fetch(again, b, row);
+        const int e = 8 * (i + G * b);
+        again.template load<X>(row + e, p.E - e, p.wide != 0);
         float x[8];
         again.template get<X>(x);
 #pragma unroll
@@ -228,57 +248,39 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
 #pragma unroll ROUNDS
     for (int g = 0; g < NB; g += PF) {
       const bool last_round = g + PF == NB;
-      bool far = false;  // some logit of the round is infinite or NaN (experts past the row's end are -inf)
-      if (use_s) far = __any_sync(FULL, !finite_blocks<X, PF>(raw));
+      bool far = false;  // some logit of the round is infinite or NaN
+      if constexpr (SCORES) far = __any_sync(FULL, !finite_blocks<X, PF>(raw));
 #pragma unroll
       for (int j0 = 0; j0 < PF; ++j0) {
-        const int b = g + j0;
-        float x[8];
-        raw[j0].template get<X>(x);
+        const int b = g + j0, e = 8 * (i + G * b);
+        Eight x;
+        raw[j0].template get<X>(x.v);
         if (!last_round)
           fetch(raw[j0], b + PF, row);
         else if (more)
           fetch(raw[j0], j0, next);
         int c[8];
-        if (use_s) {
-          uint32_t masked = 0u;
-          if (far) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              x[j] = fmaxf(x[j], NEG_INF);  // NaN -> -inf
-              if (x[j] == NEG_INF) masked |= 1u << j;
-            }
-          }
-          const int e = 8 * (i + G * b);
+        if constexpr (SCORES) {
           const float4 b0 = *reinterpret_cast<const float4*>(&sbias[e]), b1 = *reinterpret_cast<const float4*>(&sbias[e + 4]);
-          const float bias[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-          if (soft) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = ex2_approx(fmaf(x[j], LOG2E, -mm)) * rs;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = rcp_approx(1.f + ex2_approx(-LOG2E * x[j]));
-          }
-          if (tight) {  // n in one step, the bias holding the rest
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], 2097152.f, bias[j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = fmaf(fma_sat(x[j] + bias[j], 0.25f, 0.25f), 8388607.f, 8388608.f);
-          }
-          block_ids(x, p.key_mul, 8 * G * b, c);
-          if (far) {  // masked experts stay out whatever their bias
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if ((masked >> j) & 1u) c[j] &= 255;
-          }
+          const Eight bias = {{b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w}};
+          if (far)
+            x = far_choice<KIND>(x, bias, mm, rs);
+          else
+            x = choice<KIND>(x, bias, mm, rs);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = fmaf(fma_sat(x[j], 1.f / 256.f, 0.5f), 8388607.f, 8388608.f);
-          block_ids(x, p.key_mul, 8 * G * b, c);
+          for (int j = 0; j < 8; ++j) x.v[j] = fma_sat(x.v[j], 1.f / 256.f, 0.5f);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x.v[j] = fmaf(x.v[j], 8388607.f, 8388608.f);
+        block_ids(x.v, p.key_mul, 8 * G * b, c);
+        if (SCORES && !full) {  // experts past the row's end
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (e + (j & 4) >= p.E) c[j] &= 255;
         }
         sort8_desc(c);
-        if (KIND == BY_SCORE && p.n_group > 1) {
+        if (LISTS && p.n_group > 1) {
           lists[warp][b][0][lane] = make_int4(c[0], c[1], c[2], c[3]);
           lists[warp][b][1][lane] = make_int4(c[4], c[5], c[6], c[7]);
         } else if (j0 == 0 && g == 0) {
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
         }
       }
     }
-    if (KIND == BY_SCORE && p.n_group > 1) {
+    if (LISTS && p.n_group > 1) {
       // a group is mb blocks of every lane of the row
       const int sh = 31 - __clz(p.E / p.n_group / (8 * G)), mb = 1 << sh;
       int g1[8], g2[8], gk[8];
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
         if (r < p.top_group) thr = gk[r], nxt = gk[r + 1];
       // the sum of two scores' keys can be three steps off either way; equal keys of
       // logits may stand in either order, unless they hold their logits exactly
-      if ((thr >> 3) - (nxt >> 3) <= 3 * near && (use_s || !exact_n<EB>(thr >> 3))) bad = true;
+      if ((thr >> 3) - (nxt >> 3) <= 3 * near && (SCORES || !exact_n<EB>(thr >> 3))) bad = true;
       unsigned keep = 0u;  // the first blocks of the kept groups
 #pragma unroll
       for (int b = 0; b < 8; ++b)
@@ -391,10 +393,10 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
     least = min(least, last - after);
     bad = bad || last < 256 || (top[0] >> 8) >= 8388607;
     // all leading keys positive logits that their n hold exactly: the ids order equal ones
-    const bool sure = EB == 2 && !use_s && after > (4194304 + 1024) * 256 + 255;
+    const bool sure = EB == 2 && !SCORES && after > (4194304 + 1024) * 256 + 255;
     if (__any_sync(FULL, !sure && least < 256 * (near + 1))) {
       // neighbours that the keys do not settle have to be a true tie
-      auto open = [&](int hi, int lo) { return (hi >> 8) - (lo >> 8) <= near && (use_s || !exact_n<EB>(lo >> 8)); };
+      auto open = [&](int hi, int lo) { return (hi >> 8) - (lo >> 8) <= near && (SCORES || !exact_n<EB>(lo >> 8)); };
       if (open(last, after)) bad = true;
 #pragma unroll
       for (int j = 1; j < 8; ++j) {
@@ -406,8 +408,8 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
       }
     }
     // rows that are not settled, one by one
-    float m = KIND != BY_SCORE ? __shfl_sync(FULL, xj[0], rl * G) : 0.f;  // the first choice is the largest logit
-    if (KIND == BY_SCORE && columns) {
+    float m = KIND <= BY_LOGIT_DENSE ? __shfl_sync(FULL, xj[0], rl * G) : 0.f;  // the first choice is the largest logit
+    if (LISTS && columns) {
       if (soft) {  // the largest logit may lie in a group that is dropped
         m = NEG_INF;
 #pragma unroll
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
     if (p.weights != nullptr) {
       if (soft) {
         float mk = m;  // without groups and biases the row's largest logit is the first choice
-        if (KIND == BY_SCORE && p.renorm) {
+        if (LISTS && p.renorm) {
           mk = xj[0];
 #pragma unroll
           for (int jj = 1; jj < OUT; ++jj) mk = fmaxf(mk, xj[jj]);
@@ -546,10 +548,13 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
 template <typename X, int G, int NB>
 cudaError_t score_fast_shape(const ScoreParams& p, cudaStream_t st) {
   const dim3 grid(p.L * p.nspan), block(SF_WARPS * 32);
-  switch (score_kind(p.bias != nullptr, p.n_group, p.partial != nullptr, p.score == MOER_SCORE_SOFTMAX, p.renorm != 0)) {
+  switch (score_kind(p.bias != nullptr, p.n_group, p.group_best, p.partial != nullptr, p.score == MOER_SCORE_SOFTMAX,
+                     p.renorm != 0)) {
     case BY_LOGIT: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT>, grid, block, 0, st, p);
     case BY_LOGIT_DENSE: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT_DENSE>, grid, block, 0, st, p);
-    default: return launch_pdl(score_fast_kernel<X, G, NB, BY_SCORE>, grid, block, 0, st, p);
+    case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, NB, BY_GROUP>, grid, block, 0, st, p);
+    case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, NB, BY_SIGMOID>, grid, block, 0, st, p);
+    default: return launch_pdl(score_fast_kernel<X, G, NB, BY_SOFTMAX>, grid, block, 0, st, p);
   }
 }
 
