@@ -161,7 +161,8 @@ __device__ __noinline__ Eight far_choice(Eight x, Eight bias, float mm, float rs
   return y;
 }
 
-template <typename X, int G, int NB, int KIND>
+// WHOLE: E = 8 G NB and rows on 16 bytes, every block whole.
+template <typename X, int G, int NB, int KIND, bool WHOLE>
 __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)) score_fast_kernel(const ScoreParams p) {
   constexpr int RW = 32 / G;            // rows of a warp at a time
   constexpr int EB = sizeof(X);
@@ -200,13 +201,12 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
   // rows past the unit's end read its last row again
   auto row_at = [&](int64_t t) { return base + min64(t + rl, t1 - 1) * p.ld_token; };
   Raw<EB> raw[PF];
-  const bool full = p.E == 8 * G * NB && p.wide != 0;  // every block whole, on 16 bytes
-  auto fetch = [&](Raw<EB>& to, int b, const X* of) {
+  auto fetch = [&](Raw<EB>& to, int b, const X* of, float fill = KIND >= BY_SIGMOID ? 0.f : NEG_INF) {
     const int e = 8 * (i + G * b);
-    if (full)
+    if constexpr (WHOLE)
       to.template load<X>(of + e, 8, true);
     else
-      to.template load<X>(of + e, p.E - e, p.wide != 0, SCORES ? 0.f : NEG_INF);
+      to.template load<X>(of + e, p.E - e, p.wide != 0, fill);
   };
   const X* row = t0 < t1 ? row_at(t0) : base;
   if (t0 < t1)
@@ -224,8 +224,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
       float m = NEG_INF, z = 0.f;
       for (int b = 0; b < NB; ++b) {
         Raw<EB> again;
-        const int e = 8 * (i + G * b);
-        again.template load<X>(row + e, p.E - e, p.wide != 0);
+        fetch(again, b, row, NEG_INF);
         float x[8];
         again.template get<X>(x);
 #pragma unroll
@@ -236,8 +235,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
       mm = bad ? 0.f : m * LOG2E;
       for (int b = 0; b < NB; ++b) {
         Raw<EB> again;
-        const int e = 8 * (i + G * b);
-        again.template load<X>(row + e, p.E - e, p.wide != 0);
+        fetch(again, b, row, NEG_INF);
         float x[8];
         again.template get<X>(x);
 #pragma unroll
@@ -274,7 +272,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
 #pragma unroll
         for (int j = 0; j < 8; ++j) x.v[j] = fmaf(x.v[j], 8388607.f, 8388608.f);
         block_ids(x.v, p.key_mul, 8 * G * b, c);
-        if (SCORES && !full) {  // experts past the row's end
+        if (SCORES && !WHOLE) {  // experts past the row's end
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             if (e + (j & 4) >= p.E) c[j] &= 255;
@@ -414,9 +412,8 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
         m = NEG_INF;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const int e = 8 * (i + G * b);
           Raw<EB> again;
-          again.template load<X>(row + e, p.E - e, p.wide != 0);
+          fetch(again, b, row, NEG_INF);
           float x[8];
           again.template get<X>(x);
 #pragma unroll
@@ -456,7 +453,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
         const int r = s * (4 / G) + lane / CL;
         float x[8];
         Raw<EB> line;
-        if (full && e < p.E)  // the row may have fewer columns than its lanes own
+        if constexpr (WHOLE && CL == NB * G)
           line.template load<X>(at + (int64_t)min(r, rows - 1) * p.ld_token, 8, true);
         else
           line.template load<X>(at + (int64_t)min(r, rows - 1) * p.ld_token, p.E - e, p.wide != 0);
@@ -545,29 +542,35 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
   pdl_release();
 }
 
-template <typename X, int G, int NB>
+template <typename X, int G, int NB, bool WHOLE>
 cudaError_t score_fast_shape(const ScoreParams& p, cudaStream_t st) {
   const dim3 grid(p.L * p.nspan), block(SF_WARPS * 32);
   switch (score_kind(p.bias != nullptr, p.n_group, p.group_best, p.partial != nullptr, p.score == MOER_SCORE_SOFTMAX,
                      p.renorm != 0)) {
-    case BY_LOGIT: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT>, grid, block, 0, st, p);
-    case BY_LOGIT_DENSE: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT_DENSE>, grid, block, 0, st, p);
-    case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, NB, BY_GROUP>, grid, block, 0, st, p);
-    case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, NB, BY_SIGMOID>, grid, block, 0, st, p);
-    default: return launch_pdl(score_fast_kernel<X, G, NB, BY_SOFTMAX>, grid, block, 0, st, p);
+    case BY_LOGIT: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT, WHOLE>, grid, block, 0, st, p);
+    case BY_LOGIT_DENSE: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT_DENSE, WHOLE>, grid, block, 0, st, p);
+    case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, NB, BY_GROUP, WHOLE>, grid, block, 0, st, p);
+    case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, NB, BY_SIGMOID, WHOLE>, grid, block, 0, st, p);
+    default: return launch_pdl(score_fast_kernel<X, G, NB, BY_SOFTMAX, WHOLE>, grid, block, 0, st, p);
   }
 }
 
+// The lanes of a row and the blocks of a lane by the experts alone.
 template <typename X>
 cudaError_t score_fast_run(const ScoreParams& p, cudaStream_t st) {
   const int nb = (p.E + 7) / 8;
-  if (p.E <= 16) return score_fast_shape<X, 1, 2>(p, st);
-  if (p.E <= 32) return score_fast_shape<X, 1, 4>(p, st);
-  if (p.E <= 64) return score_fast_shape<X, 1, 8>(p, st);
-  if (nb <= 12) return score_fast_shape<X, 2, 6>(p, st);
-  if (nb <= 16) return score_fast_shape<X, 2, 8>(p, st);
-  if (nb <= 24) return score_fast_shape<X, 4, 6>(p, st);
-  return score_fast_shape<X, 4, 8>(p, st);
+  if (p.wide != 0) {
+    if (p.E == 64) return score_fast_shape<X, 1, 8, true>(p, st);
+    if (p.E == 128) return score_fast_shape<X, 2, 8, true>(p, st);
+    if (p.E == 256) return score_fast_shape<X, 4, 8, true>(p, st);
+  }
+  if (p.E <= 16) return score_fast_shape<X, 1, 2, false>(p, st);
+  if (p.E <= 32) return score_fast_shape<X, 1, 4, false>(p, st);
+  if (p.E <= 64) return score_fast_shape<X, 1, 8, false>(p, st);
+  if (nb <= 12) return score_fast_shape<X, 2, 6, false>(p, st);
+  if (nb <= 16) return score_fast_shape<X, 2, 8, false>(p, st);
+  if (nb <= 24) return score_fast_shape<X, 4, 6, false>(p, st);
+  return score_fast_shape<X, 4, 8, false>(p, st);
 }
 
 }  // namespace moer
