@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
       __syncwarp();
       const int col = lane % CL, e = 8 * col;
       const X* at = base + t0 * p.ld_token + e;
-#pragma unroll 2
+#pragma unroll 1
       for (int s = 0; s < 8; ++s) {
         const int r = s * (4 / G) + lane / CL;
         float x[8];
