@@ -39,19 +39,21 @@ struct ScoreParams {
 };
 
 // What the fast kernel's choice goes by.  A kernel for each keeps its code short:
-// one for all of the last three took as long with a fifth fewer instructions
+// one for all that take scores or groups took as long with a fifth fewer instructions
 // an expert, for it left the instruction cache between its branches.
 enum ScoreKind {
   BY_LOGIT = 0,        // the logits alone; weights from the chosen ones
-  BY_LOGIT_DENSE = 1,  // the logits; with the column pass
-  BY_GROUP = 2,        // groups ranked by their best logit
-  BY_SIGMOID = 3,      // scores: a bias, or groups ranked by two scores
-  BY_SOFTMAX = 4
+  SOFTMAX_SUMS = 1,    // the logits; with the column pass of a softmax
+  SIGMOID_SUMS = 2,    // the logits; with the column pass of a sigmoid
+  BY_GROUP = 3,        // groups ranked by their best logit
+  BY_SIGMOID = 4,      // scores: a bias, or groups ranked by two scores
+  BY_SOFTMAX = 5
 };
 inline ScoreKind score_kind(bool bias, int n_group, int group_best, bool sums, bool soft, bool renorm) {
   if (bias || (n_group > 1 && group_best == 2)) return soft ? BY_SOFTMAX : BY_SIGMOID;
   if (n_group > 1) return BY_GROUP;
-  return sums || (soft && !renorm) ? BY_LOGIT_DENSE : BY_LOGIT;
+  if (soft) return sums || !renorm ? SOFTMAX_SUMS : BY_LOGIT;
+  return sums ? SIGMOID_SUMS : BY_LOGIT;
 }
 // Blocks of 128 threads of the fast kernel on an SM, which sets its registers.  Cases
 // of 3.1 M rows x 128 fp32 / 213 k x 256 bf16 by score / 780 k x 64 bf16 with column

@@ -182,10 +182,11 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane % G, rl = lane / G;
   const int l = blockIdx.x / p.nspan, unit = blockIdx.x - l * p.nspan;
-  const bool soft = p.score == MOER_SCORE_SOFTMAX;
+  const bool soft = KIND == SOFTMAX_SUMS || KIND == BY_SOFTMAX ||
+                    (KIND != SIGMOID_SUMS && KIND != BY_SIGMOID && p.score == MOER_SCORE_SOFTMAX);
   const bool has_bias = SCORES && p.bias != nullptr;
   const bool sums = KIND != BY_LOGIT && p.partial != nullptr;
-  const bool columns = KIND != BY_LOGIT && (sums || (soft && !p.renorm));
+  const bool columns = KIND == SOFTMAX_SUMS || KIND == SIGMOID_SUMS || (KIND != BY_LOGIT && (sums || (soft && !p.renorm)));
   if constexpr (SCORES) {
     for (int e = threadIdx.x; e < 256; e += SF_WARPS * 32)  // u = s / 4 + (b + 1) / 4
       sbias[e] = has_bias && e < p.E ? fmaf(p.bias[(size_t)l * p.E + e], 0.25f, 0.25f) : 0.25f;
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
       }
     }
     // rows that are not settled, one by one
-    float m = KIND <= BY_LOGIT_DENSE ? __shfl_sync(FULL, xj[0], rl * G) : 0.f;  // the first choice is the largest logit
+    float m = KIND < BY_GROUP ? __shfl_sync(FULL, xj[0], rl * G) : 0.f;  // the first choice is the largest logit
     if (LISTS && columns) {
       if (soft) {  // the largest logit may lie in a group that is dropped
         m = NEG_INF;
@@ -548,7 +549,8 @@ cudaError_t score_fast_shape(const ScoreParams& p, cudaStream_t st) {
   switch (score_kind(p.bias != nullptr, p.n_group, p.group_best, p.partial != nullptr, p.score == MOER_SCORE_SOFTMAX,
                      p.renorm != 0)) {
     case BY_LOGIT: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT, WHOLE>, grid, block, 0, st, p);
-    case BY_LOGIT_DENSE: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT_DENSE, WHOLE>, grid, block, 0, st, p);
+    case SOFTMAX_SUMS: return launch_pdl(score_fast_kernel<X, G, NB, SOFTMAX_SUMS, WHOLE>, grid, block, 0, st, p);
+    case SIGMOID_SUMS: return launch_pdl(score_fast_kernel<X, G, NB, SIGMOID_SUMS, WHOLE>, grid, block, 0, st, p);
     case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, NB, BY_GROUP, WHOLE>, grid, block, 0, st, p);
     case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, NB, BY_SIGMOID, WHOLE>, grid, block, 0, st, p);
     default: return launch_pdl(score_fast_kernel<X, G, NB, BY_SOFTMAX, WHOLE>, grid, block, 0, st, p);
@@ -564,7 +566,6 @@ cudaError_t score_fast_run(const ScoreParams& p, cudaStream_t st) {
     if (p.E == 128) return score_fast_shape<X, 2, 8, true>(p, st);
     if (p.E == 256) return score_fast_shape<X, 4, 8, true>(p, st);
   }
-  if (p.E <= 16) return score_fast_shape<X, 1, 2, false>(p, st);
   if (p.E <= 32) return score_fast_shape<X, 1, 4, false>(p, st);
   if (p.E <= 64) return score_fast_shape<X, 1, 8, false>(p, st);
   if (nb <= 12) return score_fast_shape<X, 2, 6, false>(p, st);
