@@ -15,13 +15,12 @@
 // comes in with the first step).
 //
 // A row's answer is kept only where it is certain: the k-th key above 0, the
-// first below the top of the range, no two neighbours among the k + 1 leading keys
-// of equal n (of scores: within two steps) -- but for neighbours within the k whose
-// logits and biases are equal too, a true tie that the id in the key orders
-// (16-bit logits of size 2^-5 and more have exact keys, and need no check) --
-// and, with groups, the last kept group more
-// than the rounding of its keys above the first dropped one.  The warp redoes
-// the other rows one by one with the exact keys of score_row.cuh.
+// first below the top of the range, no three neighbours among the leading keys of
+// equal n (of scores: within two steps; two are ordered by their values; 16-bit
+// logits of size 2^-5 and more have exact keys, which their ids order), and, with
+// groups, the last kept group more than the rounding of its keys above the first
+// dropped one.  The warp redoes the other rows one by one with the exact keys of
+// score_row.cuh.
 //
 // The weights are computed from the chosen logits, read again (they are in L1).
 // A softmax over the row without a renormalisation, and score sums, take a pass
@@ -368,16 +367,19 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
     // the lane's choices: i OUT .. i OUT + OUT - 1
     float xj[OUT];
     int mine[OUT];
+    auto take = [&]() {
 #pragma unroll
-    for (int jj = 0; jj < OUT; ++jj) {
-      int c = top[jj];
+      for (int jj = 0; jj < OUT; ++jj) {
+        int c = top[jj];
 #pragma unroll
-      for (int g = 1; g < G; ++g)
-        if (i == g) c = top[g * OUT + jj];
-      mine[jj] = 255 - (c & 255);
-      xj[jj] = NEG_INF;
-      if (i * OUT + jj < p.k && mine[jj] < p.E) xj[jj] = Quad<X>::one(row[mine[jj]]);
-    }
+        for (int g = 1; g < G; ++g)
+          if (i == g) c = top[g * OUT + jj];
+        mine[jj] = 255 - (c & 255);
+        xj[jj] = NEG_INF;
+        if (i * OUT + jj < p.k && mine[jj] < p.E) xj[jj] = Quad<X>::one(row[mine[jj]]);
+      }
+    };
+    take();
     int after = ninth, least = INT_MAX;  // the key after the k-th, the closest two of the k + 1
 #pragma unroll
     for (int j = 7; j >= 1; --j)
@@ -394,17 +396,29 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
     // all leading keys positive logits that their n hold exactly: the ids order equal ones
     const bool sure = EB == 2 && !SCORES && after > (4194304 + 1024) * 256 + 255;
     if (__any_sync(FULL, !sure && least < 256 * (near + 1))) {
-      // neighbours that the keys do not settle have to be a true tie
-      auto open = [&](int hi, int lo) { return (hi >> 8) - (lo >> 8) <= near && (SCORES || !exact_n<EB>(lo >> 8)); };
-      if (open(last, after)) bad = true;
+      // two neighbours that their keys do not settle stand by their own values; three,
+      // or the eighth and the ninth (a tenth may be as near), are left to the exact path
+      auto value = [&](int e) {
+        const float x = live_logit(Quad<X>::one(row[e]));
+        if (!has_bias || x == NEG_INF) return x;  // without a bias the logits order the experts
+        return (KIND == BY_SOFTMAX ? ex2_approx(fmaf(x, LOG2E, -mm)) * rs : sigmoid(x)) + p.bias[(size_t)l * p.E + e];
+      };
+      bool before = false;  // the pair before was open
 #pragma unroll
-      for (int j = 1; j < 8; ++j) {
-        const float a = __shfl_sync(FULL, xj[j % OUT], rl * G + j / OUT);
-        const float b = __shfl_sync(FULL, xj[(j - 1) % OUT], rl * G + (j - 1) / OUT);
-        const int ea = 255 - (top[j] & 255), eb = 255 - (top[j - 1] & 255);
-        const bool same = a == b && (!has_bias || (max(ea, eb) < p.E && p.bias[(size_t)l * p.E + ea] == p.bias[(size_t)l * p.E + eb]));
-        if (j < p.k && open(top[j - 1], top[j]) && !same) bad = true;
+      for (int j = 1; j <= 8; ++j) {
+        const int hi = top[j - 1], lo = j < 8 ? top[j < 8 ? j : 0] : ninth;
+        const bool open = j <= p.k + 1 && (hi >> 8) - (lo >> 8) <= near && (SCORES || !exact_n<EB>(lo >> 8));
+        if (open && (before || (j == 8 && p.k == 8))) bad = true;
+        before = open;
+        if (j < 8 && open && j <= p.k) {
+          const int e = 255 - (hi & 255), f = 255 - (lo & 255);
+          if (max(e, f) < p.E) {
+            const float u = value(e), v = value(f);
+            if (v > u || (v == u && f < e)) top[j - 1] = lo, top[j < 8 ? j : 0] = hi;
+          }
+        }
       }
+      take();
     }
     // rows that are not settled, one by one
     float m = KIND < BY_GROUP ? __shfl_sync(FULL, xj[0], rl * G) : 0.f;  // the first choice is the largest logit
