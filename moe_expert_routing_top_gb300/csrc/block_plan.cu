@@ -328,14 +328,24 @@ __device__ void fill_blocks(const PlanParams& p, const Tables& tb) {
     }
     __syncthreads();
     if (tokens) {
-      const int W = p.lanes, o0 = (int)threadIdx.x & (W - 1);
-      for (int k = (int)threadIdx.x / W; k < n; k += BP_THREADS / W) {
-        const Run u = runs[k];
-        for (int o = o0; o < u.len; o += W) {
-          const int64_t t = (int64_t)u.tok0 + o;
-          if (a.slot_map != nullptr) a.slot_map[t] = u.slot >= 0 ? u.slot + o : -1;
-          if (a.tok_req != nullptr) a.tok_req[t] = u.req;
-          if (a.tok_pos != nullptr) a.tok_pos[t] = u.pos + o;
+      // W lanes to a KV block, and all its tokens in one go unless it has more than 32
+      const int W = p.lanes, o0 = (int)threadIdx.x & (W - 1), step = BP_THREADS / W;
+      auto write = [&](const Run& u, int o) {
+        const int t = u.tok0 + o;
+        if (a.slot_map != nullptr) a.slot_map[t] = u.slot >= 0 ? u.slot + o : -1;
+        if (a.tok_req != nullptr) a.tok_req[t] = u.req;
+        if (a.tok_pos != nullptr) a.tok_pos[t] = u.pos + o;
+      };
+      if (a.block <= 32) {
+#pragma unroll 4
+        for (int k = (int)threadIdx.x / W; k < n; k += step) {
+          const Run u = runs[k];
+          if (o0 < u.len) write(u, o0);
+        }
+      } else {
+        for (int k = (int)threadIdx.x / W; k < n; k += step) {
+          const Run u = runs[k];
+          for (int o = o0; o < u.len; o += W) write(u, o);
         }
       }
     }
