@@ -139,6 +139,14 @@ struct Raw<4> {
     if (room >= 8) b = *reinterpret_cast<const float4*>(p + 4);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
+  // two quads apart, either of which may be missing
+  template <typename X>
+  __device__ __forceinline__ void load2(const float* p, bool has, const float* q, bool has2, float fill) {
+    float4 a = make_float4(fill, fill, fill, fill), b = a;
+    if (has) a = *reinterpret_cast<const float4*>(p);
+    if (has2) b = *reinterpret_cast<const float4*>(q);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
   template <typename X>
   __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
@@ -167,6 +175,19 @@ struct Raw<2> {
         const uint2 a = *reinterpret_cast<const uint2*>(p + 4);
         v.z = a.x, v.w = a.y;
       }
+    }
+  }
+  template <typename X>
+  __device__ __forceinline__ void load2(const X* p, bool has, const X* q, bool has2, float fill) {
+    const uint32_t low = fill == 0.f ? 0u : std::is_same<X, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+    v = make_uint4(low, low, low, low);
+    if (has) {
+      const uint2 a = *reinterpret_cast<const uint2*>(p);
+      v.x = a.x, v.y = a.y;
+    }
+    if (has2) {
+      const uint2 a = *reinterpret_cast<const uint2*>(q);
+      v.z = a.x, v.w = a.y;
     }
   }
   template <typename X>

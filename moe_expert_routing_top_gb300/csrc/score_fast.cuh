@@ -50,10 +50,13 @@ namespace moer {
 constexpr int SF_WARPS = 4;
 
 // Keys of a block: t holds n in the low 23 bits of a number in [2^23, 2^24); 255 - id goes below n.
-__device__ __forceinline__ void block_ids(const float (&t)[8], uint32_t key_mul, int pos, int (&c)[8]) {
+// The upper quad's ids lie `gap` further on.
+__device__ __forceinline__ void block_ids(const float (&t)[8], uint32_t key_mul, int pos, int (&c)[8], int gap = 0) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(c[j]) : "r"(__float_as_uint(t[j])), "r"(key_mul), "r"(255 - pos - j));
+    asm("mad.lo.u32 %0, %1, %2, %3;"
+        : "=r"(c[j])
+        : "r"(__float_as_uint(t[j])), "r"(key_mul), "r"(255 - pos - j - (j < 4 ? 0 : gap)));
 }
 
 // Whether no logit of the blocks is infinite or NaN: the sum of their squares is
@@ -173,7 +176,10 @@ __device__ __noinline__ Eight far_choice(Eight x, Eight bias, float mm, float rs
 }
 
 // WHOLE: E = 8 G NB and rows on 16 bytes, every block whole.
-template <typename X, int G, int NB, int KIND, bool WHOLE>
+// SPLIT (groups of gs experts, gs a multiple of 4 but no power of two times 8 G): the
+// lane's blocks go group by group, mb to a group, and a block is the quads 2 m G + i
+// and (2 m + 1) G + i of its group, so that no block lies in two groups.
+template <typename X, int G, int NB, int KIND, bool WHOLE, bool SPLIT>
 __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)) score_fast_kernel(const ScoreParams p) {
   constexpr int RW = 32 / G;            // rows of a warp at a time
   constexpr int EB = sizeof(X);
@@ -213,12 +219,23 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
   // rows past the unit's end read its last row again
   auto row_at = [&](int64_t t) { return base + min64(t + rl, t1 - 1) * p.ld_token; };
   Raw<EB> raw[PF];
+  const int gs = LISTS ? p.E / p.n_group : 0, per = LISTS ? (gs + 8 * G - 1) / (8 * G) : 1;
+  const int sh = per > 1 ? 32 - __clz(per - 1) : 0, mb = 1 << sh;  // blocks of a lane to a group
+  // first expert of a block's first quad, less the lane's part, and whether its quads lie in the row
+  auto split_at = [&](int b) { return (b >> sh) * gs + 8 * G * (b & (mb - 1)); };
+  auto split_has = [&](int b, int h) {
+    return 8 * G * (b & (mb - 1)) + 4 * (G * h + i) < gs && (b >> sh) < p.n_group;
+  };
   auto fetch = [&](Raw<EB>& to, int b, const X* of, float fill = KIND >= BY_SIGMOID ? 0.f : NEG_INF) {
     const int e = 8 * (i + G * b);
-    if constexpr (WHOLE)
+    if constexpr (SPLIT) {
+      const X* at = of + split_at(b) + 4 * i;
+      to.template load2<X>(at, split_has(b, 0), at + 4 * G, split_has(b, 1), fill);
+    } else if constexpr (WHOLE) {
       to.template load<X>(of + e, 8, true);
-    else
+    } else {
       to.template load<X>(of + e, p.E - e, p.wide != 0, fill);
+    }
   };
   const X* row = t0 < t1 ? row_at(t0) : base;
   if (t0 < t1)
@@ -271,7 +288,9 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
           fetch(raw[j0], j0, next);
         int c[8];
         if constexpr (SCORES) {
-          const float4 b0 = *reinterpret_cast<const float4*>(&sbias[e]), b1 = *reinterpret_cast<const float4*>(&sbias[e + 4]);
+          const int f = SPLIT ? split_at(b) + 4 * i : e, f1 = SPLIT ? f + 4 * G : e + 4;  // past 252 is no expert
+          const float4 b0 = *reinterpret_cast<const float4*>(&sbias[SPLIT ? min(f, 252) : f]);
+          const float4 b1 = *reinterpret_cast<const float4*>(&sbias[SPLIT ? min(f1, 252) : f1]);
           const Eight bias = {{b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w}};
           if (far)
             x = far_choice<KIND>(x, bias, mm, rs);
@@ -283,11 +302,14 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) x.v[j] = fmaf(x.v[j], 8388607.f, 8388608.f);
-        block_ids(x.v, p.key_mul, 8 * G * b, c);
-        if (SCORES && !WHOLE) {  // experts past the row's end
+        if constexpr (SPLIT)
+          block_ids(x.v, p.key_mul, split_at(b), c, 4 * G - 4);
+        else
+          block_ids(x.v, p.key_mul, 8 * G * b, c);
+        if (SCORES && !WHOLE) {  // experts past the row's (or the group's) end
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (e + (j & 4) >= p.E) c[j] &= 255;
+            if (SPLIT ? !split_has(b, j / 4) : e + (j & 4) >= p.E) c[j] &= 255;
         }
         sort8_desc(c);
         if (LISTS && p.n_group > 1) {
@@ -303,7 +325,6 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
     }
     if (LISTS && p.n_group > 1) {
       // a group is mb blocks of every lane of the row
-      const int sh = 31 - __clz(p.E / p.n_group / (8 * G)), mb = 1 << sh;
       int g1[8], g2[8], gk[8];
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
@@ -365,8 +386,8 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
     }
     // ids of the row: the lane's own part comes off the inverted position
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top[j] -= 8 * i;
-    ninth -= 8 * i;
+    for (int j = 0; j < 8; ++j) top[j] -= (SPLIT ? 4 : 8) * i;
+    ninth -= (SPLIT ? 4 : 8) * i;
 #pragma unroll
     for (int o = 1; o < G; o *= 2) {
       int other[8];
@@ -573,19 +594,35 @@ cudaError_t score_fast_shape(const ScoreParams& p, cudaStream_t st) {
   const dim3 grid(p.L * p.nspan), block(SF_WARPS * 32);
   switch (score_kind(p.bias != nullptr, p.n_group, p.group_best, p.partial != nullptr, p.score == MOER_SCORE_SOFTMAX,
                      p.renorm != 0)) {
-    case BY_LOGIT: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT, WHOLE>, grid, block, 0, st, p);
-    case SOFTMAX_SUMS: return launch_pdl(score_fast_kernel<X, G, NB, SOFTMAX_SUMS, WHOLE>, grid, block, 0, st, p);
-    case SIGMOID_SUMS: return launch_pdl(score_fast_kernel<X, G, NB, SIGMOID_SUMS, WHOLE>, grid, block, 0, st, p);
-    case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, NB, BY_GROUP, WHOLE>, grid, block, 0, st, p);
-    case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, NB, BY_SIGMOID, WHOLE>, grid, block, 0, st, p);
-    default: return launch_pdl(score_fast_kernel<X, G, NB, BY_SOFTMAX, WHOLE>, grid, block, 0, st, p);
+    case BY_LOGIT: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT, WHOLE, false>, grid, block, 0, st, p);
+    case SOFTMAX_SUMS: return launch_pdl(score_fast_kernel<X, G, NB, SOFTMAX_SUMS, WHOLE, false>, grid, block, 0, st, p);
+    case SIGMOID_SUMS: return launch_pdl(score_fast_kernel<X, G, NB, SIGMOID_SUMS, WHOLE, false>, grid, block, 0, st, p);
+    case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, NB, BY_GROUP, WHOLE, false>, grid, block, 0, st, p);
+    case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, NB, BY_SIGMOID, WHOLE, false>, grid, block, 0, st, p);
+    default: return launch_pdl(score_fast_kernel<X, G, NB, BY_SOFTMAX, WHOLE, false>, grid, block, 0, st, p);
+  }
+}
+
+// Groups of quads that are no blocks of 8 on every lane.
+template <typename X, int G>
+cudaError_t score_fast_split(const ScoreParams& p, cudaStream_t st) {
+  const dim3 grid(p.L * p.nspan), block(SF_WARPS * 32);
+  switch (score_kind(p.bias != nullptr, p.n_group, p.group_best, false, p.score == MOER_SCORE_SOFTMAX, p.renorm != 0)) {
+    case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, 8, BY_GROUP, false, true>, grid, block, 0, st, p);
+    case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, 8, BY_SIGMOID, false, true>, grid, block, 0, st, p);
+    default: return launch_pdl(score_fast_kernel<X, G, 8, BY_SOFTMAX, false, true>, grid, block, 0, st, p);
   }
 }
 
 // The lanes of a row and the blocks of a lane by the experts alone.
 template <typename X>
 cudaError_t score_fast_run(const ScoreParams& p, cudaStream_t st) {
-  const int nb = (p.E + 7) / 8;
+  const int nb = (p.E + 7) / 8, lanes = p.E <= 64 ? 1 : p.E <= 128 ? 2 : 4;
+  const int gs = p.E / p.n_group, per = gs / (8 * lanes);
+  if (p.n_group > 1 && (gs % (8 * lanes) != 0 || (per & (per - 1)) != 0))
+    return lanes == 1   ? score_fast_split<X, 1>(p, st)
+           : lanes == 2 ? score_fast_split<X, 2>(p, st)
+                        : score_fast_split<X, 4>(p, st);
   if (p.wide != 0) {
     if (p.E == 64) return score_fast_shape<X, 1, 8, true>(p, st);
     if (p.E == 128) return score_fast_shape<X, 2, 8, true>(p, st);

@@ -247,6 +247,23 @@ def test_throughput_groups(env, E, k, n, keep, best, score, dtype):
         _check_forward(_forward(env, dev, E, k, dtype, bias=bias, sums=biased, **o), x, k, bias=bias, **o)
 
 
+# groups of quads that are no whole blocks of the throughput kernel's lanes
+@pytest.mark.parametrize("E,k,n,keep", [(160, 6, 8, 3), (96, 8, 8, 4), (96, 5, 4, 2), (192, 8, 8, 4), (192, 4, 2, 1), (192, 8, 4, 3), (32, 8, 8, 4),
+                                        (16, 2, 4, 2), (252, 8, 7, 3), (60, 4, 3, 2)])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_throughput_odd_groups(env, E, k, n, keep, best, score, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E + n + 1)
+    for special in (None, "masks"):
+        dev, x = _logits(torch, rs, 2, 1060, E, dtype, special=special)
+        for biased in (False, True):
+            bias = rs.normal(0, 0.05, size=(2, E)) if biased else None
+            o = dict(score=score, renorm=not biased, n_group=n, top_group=keep, best=best)
+            _check_forward(_forward(env, dev, E, k, dtype, bias=bias, sums=biased, **o), x, k, bias=bias, **o)
+
+
 @pytest.mark.parametrize("special", ["masks", "ties", "inf", "lowest"])
 @pytest.mark.parametrize("E,k,n", [(64, 6, 1), (128, 8, 8), (256, 8, 8), (60, 5, 1)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
@@ -270,6 +287,32 @@ def test_throughput_layouts(env, layout, dtype):
         dev, x = _logits(torch, rs, 3, 1500, E, dtype, layout=layout)
         bias = rs.normal(0, 0.05, size=(3, E))
         _check_forward(_forward(env, dev, E, k, dtype, bias=bias, score="sigmoid"), x, k, bias=bias, score="sigmoid")
+
+
+def test_offsets_past_32_bits(env):
+    """More than 2^31 logits: the first and the last rows' choices, weights and gradients."""
+    torch, nat = env
+    E, k, T = 128, 8, (1 << 24) + 4099
+    x = torch.zeros((1, T, E), dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    ends = torch.cat([torch.arange(2000), torch.arange(T - 2000, T)]).cuda()
+    x[0, ends] = torch.randn((4000, E), device="cuda", generator=gen).to(x.dtype)
+    d, o = nat.make_dims(E, k, 1, [], 16), nat.make_score_opts(dtype="bf16")
+    ids = torch.empty((1, T, k), dtype=torch.uint8, device="cuda")
+    w = torch.empty((1, T, k), device="cuda")
+    n = nat.moer_score_workspace_bytes(d, T)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    nat.moer_score_topk(d, o, x, T, E, T * E, None, ids, w, None, ws, n)
+    ref, rw, _, _ = router.score_topk(x[:, ends].double().cpu().numpy(), k)
+    assert np.array_equal(ids[:, ends].cpu().numpy(), ref)
+    assert (np.abs(w[:, ends].double().cpu().numpy() - rw) <= 4e-6 * rw).all()
+    assert (ids[0, T // 2] == torch.arange(k, device="cuda")).all()       # a row of ties
+    w.normal_(generator=gen)
+    dx = torch.empty_like(x)
+    nat.moer_score_topk_grad(d, o, x, T, E, T * E, ids, w, None, dx, E, T * E, ws, n)
+    assert nat.moer_ws_status(ws) == 0
+    _check_grad(dx[:, ends].double().cpu().numpy(), x[:, ends].double().cpu().numpy(), ref, w[:, ends].cpu().numpy(), None, "bf16")
 
 
 def test_same_bits_twice_and_on_another_stream(env):
@@ -450,6 +493,17 @@ def test_block_plan(env, R, B, most_new, most_ctx, room, aligned):
             assert (rest == (ref["totals"][0], 0)).all()
         else:
             assert (rest == -1).all(), name
+
+
+def test_block_plan_of_many_requests(env):
+    """More requests than one block's sums reach."""
+    rs = np.random.RandomState(7)
+    new, ctx, pages, free = _batch(rs, 70001, 4, 2, 9)
+    got, ref, ref_pages, status = _plan(env, new, ctx, 4, pages, free)
+    assert status == 0 and np.array_equal(got["pages"], ref_pages)
+    for name in ("req_off", "req_blk_off", "req_cache_off", "totals", "insert_slot", "cache_idx", "slot_map", "tok_req",
+                 "tok_pos", "blk_tab"):
+        assert np.array_equal(got[name], ref[name]), name
 
 
 def test_block_plan_without_pages(env):
