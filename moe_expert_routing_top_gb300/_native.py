@@ -144,11 +144,7 @@ EXPORTS = ("moer_workspace_bytes", "moer_topk_signature", "moer_topk_signature_n
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
 _current = None  # (current device, its current stream's handle), bound at the first call without a stream

@@ -13,8 +13,9 @@
 // held it and from free_pages otherwise, so nothing waits for the table's new
 // entries to be written.
 //
-// The sums: blocks of 1,024 requests (four to a thread) add up their own, then,
-// in a second launch, add the sums before them and scan.
+// The sums: a block scans 1,024 requests (four to a thread) from the sum of those
+// before them, which it makes by itself in batches of up to 4,096 requests; in
+// larger ones a launch before it has summed every block's own.
 // The fill: a block of 256 threads takes 256 KV blocks.  A thread to a KV block
 // finds its request (two warps bracket the block's requests by a 32-way search,
 // the thread searches between them), its page and its first token; then the
@@ -36,6 +37,7 @@ constexpr int BP_THREADS = 256;
 constexpr int BP_EACH = 4;                       // requests of a thread in the scan
 constexpr int BP_CHUNK = BP_THREADS * BP_EACH;   // of a block
 constexpr int SMALL_R = BP_CHUNK;                // requests of a small batch,
+constexpr int BP_ALONE = 4;                      // chunks up to which a block sums those before it by itself
 constexpr int64_t SMALL_ITEMS = 8192;            // its tokens and blocks
 
 // What the fill reads of the requests: the caller's arrays and the sums, or a
@@ -50,7 +52,8 @@ struct PlanParams {
   uint32_t mul, shift;     // x / B = (x mul) >> (32 + shift) for x < 2^31; shift 32: B = 1
   int32_t* taken_off;      // [R+1]
   uint32_t* status;
-  int64_t* partial;        // [chunks][4] sums of each chunk of requests
+  int64_t* partial;        // [chunks][4] sums of each chunk of requests, where
+  int summed;              // 1: a launch of its own has made them
   int vec_len;             // 1: the lengths take vector loads
   int vec_tab;             // 1: blk_tab's pairs are on 8 bytes
   int lanes;               // to a KV block when tokens are written: a power of two
@@ -164,9 +167,19 @@ __device__ __forceinline__ void scan_requests(const PlanParams& p, int32_t* keep
   const int r0 = (int)blockIdx.x * BP_CHUNK + (int)threadIdx.x * BP_EACH;
   int64_t base[4] = {0, 0, 0, 0};
   if (blockIdx.x > 0) {
-    for (int c = threadIdx.x; c < (int)blockIdx.x; c += BP_THREADS)
+    if (p.summed != 0) {
+      for (int c = threadIdx.x; c < (int)blockIdx.x; c += BP_THREADS)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) base[k] += p.partial[(int64_t)c * 4 + k];
+        for (int k = 0; k < 4; ++k) base[k] += p.partial[(int64_t)c * 4 + k];
+    } else {
+      for (int r = (int)threadIdx.x * BP_EACH; r < (int)blockIdx.x * BP_CHUNK; r += BP_CHUNK) {
+        const Four f = four_requests(p, r);
+#pragma unroll
+        for (int i = 0; i < BP_EACH; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) base[k] += f.s[i][k];
+      }
+    }
     block_sums(base, wsum);
   }
   const Four f = four_requests(p, r0);
@@ -437,7 +450,8 @@ moer_status block_plan_launch(const moer_block_plan_args* a, void* ws, cudaStrea
   if (a->R <= SMALL_R && a->T + a->nblk + a->ncached <= SMALL_ITEMS)
     return launch_pdl(plan_small_kernel, dim3(1), block, 0, st, p) == cudaSuccess ? MOER_OK : MOER_ECUDA;
   const int chunks = a->R > BP_CHUNK ? (a->R + BP_CHUNK - 1) / BP_CHUNK : 1;
-  cudaError_t e = chunks > 1 ? launch_pdl(plan_sum_kernel, dim3(chunks), block, 0, st, p) : cudaSuccess;
+  p.summed = chunks > BP_ALONE;
+  cudaError_t e = p.summed != 0 ? launch_pdl(plan_sum_kernel, dim3(chunks), block, 0, st, p) : cudaSuccess;
   if (e == cudaSuccess) e = launch_pdl(plan_scan_kernel, dim3(chunks), block, 0, st, p);
   // a block to 256 KV blocks (their number is at most nblk where the batch fits)
   const int64_t fill = max64(1, (max64(a->nblk, a->ncached / 4) + BP_THREADS - 1) / BP_THREADS);

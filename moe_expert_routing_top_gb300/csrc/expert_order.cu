@@ -250,8 +250,13 @@ __global__ void __launch_bounds__(EO_THREADS) order_place_kernel(const OrderPara
   // the pairs of each expert: in earlier tiles, and in all
   const int e = threadIdx.x % EM, seg = threadIdx.x / EM;
   const int s0 = ntile * seg / SEG, s1 = ntile * (seg + 1) / SEG;
-  uint32_t count = 0u;
-  for (int tile = s0; tile < s1; ++tile) count += __popc(tiles[tile][bits_at(e)]);
+  constexpr int EACH = PlaceGeo<EM>::TILES / SEG;  // tiles of a thread, at most
+  uint32_t count = 0u, in_tile[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    in_tile[i] = s0 + i < s1 ? __popc(tiles[s0 + i][bits_at(e)]) : 0u;
+    count += in_tile[i];
+  }
   uint32_t mine, before, total, start;
   auto sum = [&]() {
     part[seg][e] = count;
@@ -295,9 +300,10 @@ __global__ void __launch_bounds__(EO_THREADS) order_place_kernel(const OrderPara
   int32_t* inv = p.inv != nullptr ? p.inv + (size_t)l * p.N + i0 : nullptr;
   if (!serial) {
     uint32_t at = start + before;
-    for (int tile = s0; tile < s1; ++tile) {
-      tiles[tile][place_at(e)] = at;
-      at += __popc(tiles[tile][bits_at(e)]);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      if (s0 + i < s1) tiles[s0 + i][place_at(e)] = at;
+      at += in_tile[i];
     }
     __syncthreads();
 #pragma unroll
