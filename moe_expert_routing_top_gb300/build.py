@@ -19,6 +19,7 @@ SOURCES = ["api.cu", "topk_signature.cu", "topk_signature_tpr.cu", "block_counts
            "affinity_load.cu", "route.cu", "noalloc.cu", "gate_topk.cu", "kmeans.cu",
            "replicate.cu", "mask_select.cu", "spectral.cu", "selftest.cu",
            "score_topk.cu", "score_fast_f32.cu", "score_fast_bf16.cu", "score_fast_f16.cu",
+           "score_fast16_f32.cu", "score_fast16_bf16.cu", "score_fast16_f16.cu",
            "score_grad.cu", "score_grad_f32.cu", "score_grad_bf16.cu", "score_grad_f16.cu", "block_plan.cu", "expert_order.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -58,7 +58,10 @@ inline ScoreKind score_kind(bool bias, int n_group, int group_best, bool sums, b
 // Blocks of 128 threads of the fast kernel on an SM, which sets its registers.  Cases
 // of 3.1 M rows x 128 fp32 / 213 k x 256 bf16 by score / 780 k x 64 bf16 with column
 // pass: 4 blocks 341 / 87 / 72 us, 5 blocks 291 / 91 / 70 us, 6 blocks 334 / 142 / 67 us.
-constexpr int score_resident(int elem, int kind) { return kind >= BY_GROUP ? 5 : elem == 2 ? 6 : 5; }
+// A top 16 holds 8 keys more a lane, which spills with 5.
+constexpr int score_resident(int elem, int kind, int kt) {
+  return kt > 8 ? 4 : kind >= BY_GROUP ? 5 : elem == 2 ? 6 : 5;
+}
 
 constexpr float NEG_INF = -__builtin_huge_valf();
 constexpr float LOWEST = -3.402823466e38f;  // the lowest finite number

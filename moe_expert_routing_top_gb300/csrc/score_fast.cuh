@@ -1,10 +1,10 @@
 // score_fast.cuh -- the scored top-k gate at throughput sizes: G lanes per row
-// (E <= 64 G), k <= 8, 32 / G rows of a warp at a time.
+// (E <= 64 G), k <= KT = 8 or 16, 32 / G rows of a warp at a time.
 //
 // Lane i of a row holds the blocks of 8 neighbouring experts 8 (i + G b), b < NB.
 // Each block becomes 8 integer keys, sorted by a comparator network; the
-// blocks' lists are merged into the lane's top 8 with the 9th key, and the
-// lanes' lists across the row (rank.cuh).
+// blocks' lists are merged into the lane's top KT with the key after them, and the
+// lanes' lists across the row (rank.cuh; a top 16 is two lists of 8).
 //
 // Keys: what the choice goes by, v, is mapped to a 23-bit fixed-point number n by a
 // saturating multiply-add onto [0, 1] (NaN and -inf to 0) and a second one onto
@@ -149,6 +149,31 @@ __device__ __forceinline__ void put_ids(uint8_t* to, int own, int even, const in
   }
 }
 
+// Folds a sorted list of 8 into the running top KT: with KT = 16 the upper list takes
+// its 8 by Batcher's odd-even merge (25 comparators), whose lower half goes on into
+// the lower list.
+template <int KT, int N>
+__device__ __forceinline__ void fold(int (&top)[8], int (&low)[N], const int (&c)[8], int& next) {
+  if constexpr (KT == 8) {
+    merge8<true>(top, c, next);
+  } else {
+    int w[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = top[i], w[8 + i] = c[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cas(w[i], w[i + 8]);
+#pragma unroll
+    for (int i = 4; i < 8; ++i) cas(w[i], w[i + 4]);
+    cas(w[2], w[4]); cas(w[3], w[5]); cas(w[6], w[8]); cas(w[7], w[9]); cas(w[10], w[12]); cas(w[11], w[13]);
+#pragma unroll
+    for (int i = 1; i < 14; i += 2) cas(w[i], w[i + 1]);
+    int rest[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top[i] = w[i], rest[i] = w[8 + i];
+    merge8<true>(low, rest, next);
+  }
+}
+
 struct Eight {
   float v[8];
 };
@@ -179,12 +204,12 @@ __device__ __noinline__ Eight far_choice(Eight x, Eight bias, float mm, float rs
 // SPLIT (groups of gs experts, gs a multiple of 4 but no power of two times 8 G): the
 // lane's blocks go group by group, mb to a group, and a block is the quads 2 m G + i
 // and (2 m + 1) G + i of its group, so that no block lies in two groups.
-template <typename X, int G, int NB, int KIND, bool WHOLE, bool SPLIT>
-__global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)) score_fast_kernel(const ScoreParams p) {
+template <typename X, int G, int NB, int KT, int KIND, bool WHOLE, bool SPLIT>
+__global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND, KT)) score_fast_kernel(const ScoreParams p) {
   constexpr int RW = 32 / G;            // rows of a warp at a time
   constexpr int EB = sizeof(X);
   constexpr int NQ = G > 2 ? 2 : 1;     // quads of a lane on the exact path
-  constexpr int OUT = 8 / G;            // choices of a lane
+  constexpr int OUT = KT / G;           // choices of a lane
   constexpr int CL = 8 * G;             // lanes of a row in the column pass
   constexpr int PF = NB % 4 == 0 ? 4 : NB % 3 == 0 ? 3 : 2;  // blocks in flight: a block's registers take the one PF ahead
   static_assert(NB % PF == 0, "whole rounds of the block buffers");
@@ -245,11 +270,14 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
     const bool live = t0 + rl < t1;
     const bool more = t0 + SF_WARPS * RW < t1;
     const X* next = more ? row_at(t0 + SF_WARPS * RW) : row;
-    int top[8], ninth = INT_MIN;
+    // the running top KT, as sorted lists of 8, and the key after them
+    int top[8], low[KT > 8 ? 8 : 1], ninth = KT > 8 ? -1 : INT_MIN;
+#pragma unroll
+    for (int j = 0; j < (KT > 8 ? 8 : 1); ++j) low[j] = -1;
     bool bad = false;
     float mm = 0.f, rs = 1.f;
     if constexpr (KIND == BY_SOFTMAX) {
-      // the softmax first: the row from L1 twice, its largest logit and the sum
+      // the softmax first: its largest logit, and with a bias the sum, from L1
       float m = NEG_INF, z = 0.f;
       for (int b = 0; b < NB; ++b) {
         Raw<EB> again;
@@ -262,15 +290,17 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
       m = row_max<G>(m);
       bad = !(fabsf(m) < 128.f);  // nothing but masks, or infinities: left to the exact path
       mm = bad ? 0.f : m * LOG2E;
-      for (int b = 0; b < NB; ++b) {
-        Raw<EB> again;
-        fetch(again, b, row, NEG_INF);
-        float x[8];
-        again.template get<X>(x);
+      if (has_bias) {  // without one the exponentials order experts and groups as the scores do
+        for (int b = 0; b < NB; ++b) {
+          Raw<EB> again;
+          fetch(again, b, row, NEG_INF);
+          float x[8];
+          again.template get<X>(x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z += ex2_approx(fmaf(fmaxf(x[j], NEG_INF), LOG2E, -mm));
+          for (int j = 0; j < 8; ++j) z += ex2_approx(fmaf(fmaxf(x[j], NEG_INF), LOG2E, -mm));
+        }
+        rs = rcp_approx(row_sum<G>(z));
       }
-      rs = rcp_approx(row_sum<G>(z));
     }
 #pragma unroll ROUNDS
     for (int g = 0; g < NB; g += PF) {
@@ -319,7 +349,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
 #pragma unroll
           for (int j = 0; j < 8; ++j) top[j] = c[j];
         } else {
-          merge8<true>(top, c, ninth);
+          fold<KT>(top, low, c, ninth);
         }
       }
     }
@@ -368,7 +398,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
         if (g1[b] >= thr) keep |= 1u << b;
       for (int r = 1; r < mb; r *= 2) keep |= keep << r;  // and the others
       // their lists, each row's own; a single list's eight are all there is
-      ninth = 0;
+      ninth = KT > 8 ? -1 : 0;
       {
         const int b0 = __ffs(keep) - 1;
         keep &= keep - 1u;
@@ -381,32 +411,43 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
         keep &= keep - 1u;
         const int4 u = lists[warp][b0][0][lane], v = lists[warp][b0][1][lane];
         const int c[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-        merge8<true>(top, c, ninth);
+        fold<KT>(top, low, c, ninth);
       }
     }
     // ids of the row: the lane's own part comes off the inverted position
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top[j] -= (SPLIT ? 4 : 8) * i;
+    for (int j = 0; j < 8; ++j) {
+      top[j] -= (SPLIT ? 4 : 8) * i;
+      if (KT > 8) low[KT > 8 ? j : 0] -= (SPLIT ? 4 : 8) * i;
+    }
     ninth -= (SPLIT ? 4 : 8) * i;
 #pragma unroll
     for (int o = 1; o < G; o *= 2) {
       int other[8];
+      if constexpr (KT > 8) {  // the lower lists first: the upper ones' losers join them
+#pragma unroll
+        for (int j = 0; j < 8; ++j) other[j] = __shfl_xor_sync(FULL, low[j], o);
+        merge8<true>(low, other, ninth);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) other[j] = __shfl_xor_sync(FULL, top[j], o);
       const int n9 = __shfl_xor_sync(FULL, ninth, o);
-      merge8<true>(top, other, ninth);
+      fold<KT>(top, low, other, ninth);
       ninth = max(ninth, n9);
     }
+    int best[KT];
+#pragma unroll
+    for (int j = 0; j < KT; ++j) best[j] = j < 8 ? top[j & 7] : low[KT > 8 ? j & 7 : 0];
     // the lane's choices: i OUT .. i OUT + OUT - 1
     float xj[OUT];
     int mine[OUT];
     auto take = [&]() {
 #pragma unroll
       for (int jj = 0; jj < OUT; ++jj) {
-        int c = top[jj];
+        int c = best[jj];
 #pragma unroll
         for (int g = 1; g < G; ++g)
-          if (i == g) c = top[g * OUT + jj];
+          if (i == g) c = best[g * OUT + jj];
         mine[jj] = 255 - (c & 255);
         xj[jj] = NEG_INF;
         if (i * OUT + jj < p.k && mine[jj] < p.E) xj[jj] = Quad<X>::one(row[mine[jj]]);
@@ -415,22 +456,22 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
     take();
     int after = ninth, least = INT_MAX;  // the key after the k-th, the closest two of the k + 1
 #pragma unroll
-    for (int j = 7; j >= 1; --j)
-      if (j >= p.k) after = top[j];
+    for (int j = KT - 1; j >= 1; --j)
+      if (j >= p.k) after = best[j];
 #pragma unroll
-    for (int j = 1; j < 8; ++j)
-      if (j < p.k) least = min(least, top[j - 1] - top[j]);
-    int last = top[0];
+    for (int j = 1; j < KT; ++j)
+      if (j < p.k) least = min(least, best[j - 1] - best[j]);
+    int last = best[0];
 #pragma unroll
-    for (int j = 1; j < 8; ++j)
-      if (j < p.k) last = top[j];
+    for (int j = 1; j < KT; ++j)
+      if (j < p.k) last = best[j];
     least = min(least, last - after);
-    bad = bad || last < 256 || (top[0] >> 8) >= 8388607;
+    bad = bad || last < 256 || (best[0] >> 8) >= 8388607;
     // all leading keys positive logits that their n hold exactly: the ids order equal ones
     const bool sure = EB == 2 && !SCORES && after > (4194304 + 1024) * 256 + 255;
     if (__any_sync(FULL, !sure && least < 256 * (near + 1))) {
       // two neighbours that their keys do not settle stand by their own values; three,
-      // or the eighth and the ninth (a tenth may be as near), are left to the exact path
+      // or the last and the one after it (a further one may be as near), are left to the exact path
       auto value = [&](int e) {
         const float x = live_logit(Quad<X>::one(row[e]));
         if (!has_bias || x == NEG_INF) return x;  // without a bias the logits order the experts
@@ -438,16 +479,16 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
       };
       bool before = false;  // the pair before was open
 #pragma unroll
-      for (int j = 1; j <= 8; ++j) {
-        const int hi = top[j - 1], lo = j < 8 ? top[j < 8 ? j : 0] : ninth;
+      for (int j = 1; j <= KT; ++j) {
+        const int hi = best[j - 1], lo = j < KT ? best[j < KT ? j : 0] : ninth;
         const bool open = j <= p.k + 1 && (hi >> 8) - (lo >> 8) <= near && (SCORES || !exact_n<EB>(lo >> 8));
-        if (open && (before || (j == 8 && p.k == 8))) bad = true;
+        if (open && (before || (j == KT && p.k == KT))) bad = true;
         before = open;
-        if (j < 8 && open && j <= p.k) {
+        if (j < KT && open && j <= p.k) {
           const int e = 255 - (hi & 255), f = 255 - (lo & 255);
           if (max(e, f) < p.E) {
             const float u = value(e), v = value(f);
-            if (v > u || (v == u && f < e)) top[j - 1] = lo, top[j < 8 ? j : 0] = hi;
+            if (v > u || (v == u && f < e)) best[j - 1] = lo, best[j < KT ? j : 0] = hi;
           }
         }
       }
@@ -589,17 +630,17 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND)
   pdl_release();
 }
 
-template <typename X, int G, int NB, bool WHOLE>
+template <typename X, int G, int NB, int KT, bool WHOLE>
 cudaError_t score_fast_shape(const ScoreParams& p, cudaStream_t st) {
   const dim3 grid(p.L * p.nspan), block(SF_WARPS * 32);
   switch (score_kind(p.bias != nullptr, p.n_group, p.group_best, p.partial != nullptr, p.score == MOER_SCORE_SOFTMAX,
                      p.renorm != 0)) {
-    case BY_LOGIT: return launch_pdl(score_fast_kernel<X, G, NB, BY_LOGIT, WHOLE, false>, grid, block, 0, st, p);
-    case SOFTMAX_SUMS: return launch_pdl(score_fast_kernel<X, G, NB, SOFTMAX_SUMS, WHOLE, false>, grid, block, 0, st, p);
-    case SIGMOID_SUMS: return launch_pdl(score_fast_kernel<X, G, NB, SIGMOID_SUMS, WHOLE, false>, grid, block, 0, st, p);
-    case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, NB, BY_GROUP, WHOLE, false>, grid, block, 0, st, p);
-    case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, NB, BY_SIGMOID, WHOLE, false>, grid, block, 0, st, p);
-    default: return launch_pdl(score_fast_kernel<X, G, NB, BY_SOFTMAX, WHOLE, false>, grid, block, 0, st, p);
+    case BY_LOGIT: return launch_pdl(score_fast_kernel<X, G, NB, KT, BY_LOGIT, WHOLE, false>, grid, block, 0, st, p);
+    case SOFTMAX_SUMS: return launch_pdl(score_fast_kernel<X, G, NB, KT, SOFTMAX_SUMS, WHOLE, false>, grid, block, 0, st, p);
+    case SIGMOID_SUMS: return launch_pdl(score_fast_kernel<X, G, NB, KT, SIGMOID_SUMS, WHOLE, false>, grid, block, 0, st, p);
+    case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, NB, KT, BY_GROUP, WHOLE, false>, grid, block, 0, st, p);
+    case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, NB, KT, BY_SIGMOID, WHOLE, false>, grid, block, 0, st, p);
+    default: return launch_pdl(score_fast_kernel<X, G, NB, KT, BY_SOFTMAX, WHOLE, false>, grid, block, 0, st, p);
   }
 }
 
@@ -608,9 +649,9 @@ template <typename X, int G>
 cudaError_t score_fast_split(const ScoreParams& p, cudaStream_t st) {
   const dim3 grid(p.L * p.nspan), block(SF_WARPS * 32);
   switch (score_kind(p.bias != nullptr, p.n_group, p.group_best, false, p.score == MOER_SCORE_SOFTMAX, p.renorm != 0)) {
-    case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, 8, BY_GROUP, false, true>, grid, block, 0, st, p);
-    case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, 8, BY_SIGMOID, false, true>, grid, block, 0, st, p);
-    default: return launch_pdl(score_fast_kernel<X, G, 8, BY_SOFTMAX, false, true>, grid, block, 0, st, p);
+    case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, 8, 8, BY_GROUP, false, true>, grid, block, 0, st, p);
+    case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, 8, 8, BY_SIGMOID, false, true>, grid, block, 0, st, p);
+    default: return launch_pdl(score_fast_kernel<X, G, 8, 8, BY_SOFTMAX, false, true>, grid, block, 0, st, p);
   }
 }
 
@@ -624,16 +665,24 @@ cudaError_t score_fast_run(const ScoreParams& p, cudaStream_t st) {
            : lanes == 2 ? score_fast_split<X, 2>(p, st)
                         : score_fast_split<X, 4>(p, st);
   if (p.wide != 0) {
-    if (p.E == 64) return score_fast_shape<X, 1, 8, true>(p, st);
-    if (p.E == 128) return score_fast_shape<X, 2, 8, true>(p, st);
-    if (p.E == 256) return score_fast_shape<X, 4, 8, true>(p, st);
+    if (p.E == 64) return score_fast_shape<X, 1, 8, 8, true>(p, st);
+    if (p.E == 128) return score_fast_shape<X, 2, 8, 8, true>(p, st);
+    if (p.E == 256) return score_fast_shape<X, 4, 8, 8, true>(p, st);
   }
-  if (p.E <= 32) return score_fast_shape<X, 1, 4, false>(p, st);
-  if (p.E <= 64) return score_fast_shape<X, 1, 8, false>(p, st);
-  if (nb <= 12) return score_fast_shape<X, 2, 6, false>(p, st);
-  if (nb <= 16) return score_fast_shape<X, 2, 8, false>(p, st);
-  if (nb <= 24) return score_fast_shape<X, 4, 6, false>(p, st);
-  return score_fast_shape<X, 4, 8, false>(p, st);
+  if (p.E <= 32) return score_fast_shape<X, 1, 4, 8, false>(p, st);
+  if (p.E <= 64) return score_fast_shape<X, 1, 8, 8, false>(p, st);
+  if (nb <= 12) return score_fast_shape<X, 2, 6, 8, false>(p, st);
+  if (nb <= 16) return score_fast_shape<X, 2, 8, 8, false>(p, st);
+  if (nb <= 24) return score_fast_shape<X, 4, 6, 8, false>(p, st);
+  return score_fast_shape<X, 4, 8, 8, false>(p, st);
+}
+
+// k = 9 .. 16.
+template <typename X>
+cudaError_t score_fast16_run(const ScoreParams& p, cudaStream_t st) {
+  if (p.E <= 64) return score_fast_shape<X, 1, 8, 16, false>(p, st);
+  if (p.E <= 128) return score_fast_shape<X, 2, 8, 16, false>(p, st);
+  return score_fast_shape<X, 4, 8, 16, false>(p, st);
 }
 
 }  // namespace moer

@@ -1,6 +1,6 @@
 // score_topk.cu -- moer_score_topk: scores, choice and weights of the router.
 //
-// Batches of some thousand rows with k <= 8 go to the fast kernel
+// Batches of some thousand rows with k <= 16 go to the fast kernel
 // (score_fast.cuh).  The kernel here takes any E <= 256 with E % 4 == 0, any
 // k <= 32, options and alignment, and is the faster one for few rows: one warp
 // per row, a lane with the quads of neighbouring experts 4 (lane + 32 i).  The
@@ -25,6 +25,9 @@ namespace moer {
 cudaError_t score_fast_f32(const ScoreParams& p, cudaStream_t st);
 cudaError_t score_fast_bf16(const ScoreParams& p, cudaStream_t st);
 cudaError_t score_fast_f16(const ScoreParams& p, cudaStream_t st);
+cudaError_t score_fast16_f32(const ScoreParams& p, cudaStream_t st);  // k = 9 .. 16
+cudaError_t score_fast16_bf16(const ScoreParams& p, cudaStream_t st);
+cudaError_t score_fast16_f16(const ScoreParams& p, cudaStream_t st);
 
 namespace {
 constexpr int SC_WARPS = 8;
@@ -56,18 +59,21 @@ int fast_span(int64_t T, int L, int step, int64_t slots) {
   return (int)(best * step);
 }
 
-// The fast kernel's options (score_fast.cuh): k <= 8, aligned quads, and groups,
-// where there are any, of quads that make at most eight blocks of a lane.
+// The fast kernel's options (score_fast.cuh): k <= 16, aligned quads, and groups,
+// where there are any, of quads that make at most eight blocks of a lane (k > 8:
+// of whole blocks).
 // Few rows leave it idle lanes: at 1,024 / 2,048 / 4,096 rows it took 2.6 / 2.6 / 4.2 us
 // (a warp per row: 3.2 / 3.3 / 5.2) with E = 128 fp32, 4.3 / 4.3 / 4.3 (4.5 / 5.6 / 9.7)
 // with 256 bf16 experts in groups, 5.3 / 5.6 / 5.3 (4.1 / 5.3 / 8.9) with 64 bf16
-// experts and score sums.
+// experts and score sums.  With k = 10, 48 x 42,076 rows of 72 fp32 experts and score
+// sums took 1,072 us a warp per row, about 445 here (k = 9 and 16: 443 and 454).
 bool fast_supported(const ScoreParams& p) {
-  if (p.k > 8 || p.vec == 0 || p.E < 16 || p.L * p.T < SC_FAST_ROWS) return false;
+  if (p.k > 16 || p.vec == 0 || p.E < 16 || p.L * p.T < SC_FAST_ROWS) return false;
   if (p.n_group == 1) return true;
   const int lanes = p.E <= 64 ? 1 : p.E <= 128 ? 2 : 4, gs = p.E / p.n_group;
   int mb = 1;  // blocks of a lane to a group
   while (mb * 8 * lanes < gs) mb *= 2;
+  if (p.k > 8 && (gs % (8 * lanes) != 0 || mb * 8 * lanes != gs)) return false;
   return gs % 4 == 0 && p.n_group * mb <= 8;
 }
 
@@ -306,7 +312,7 @@ moer_status score_topk_launch(ScoreParams p, int dtype, float* score_sum, void* 
     const int kind = score_kind(p.bias != nullptr, p.n_group, p.group_best, score_sum != nullptr, p.score == MOER_SCORE_SOFTMAX,
                                 p.renorm != 0);
     p.span = fast_span(p.T, p.L, p.E <= 64 ? 128 : p.E <= 128 ? 64 : 32,
-                       (int64_t)sms * score_resident(dtype == MOER_F32 ? 4 : 2, kind));
+                       (int64_t)sms * score_resident(dtype == MOER_F32 ? 4 : 2, kind, p.k));
   } else {
     p.span = score_span(p.T, p.L, SC_WARPS);
   }
@@ -316,8 +322,12 @@ moer_status score_topk_launch(ScoreParams p, int dtype, float* score_sum, void* 
   const uintptr_t w = reinterpret_cast<uintptr_t>(p.weights);
   p.even = p.k == 8 && w % 16 == 0 ? 2 : p.k % 2 == 0 && w % 8 == 0 ? 1 : 0;
   cudaError_t e;
-  if (fast)
+  if (fast && p.k <= 8)
     e = dtype == MOER_F32 ? score_fast_f32(p, st) : dtype == MOER_BF16 ? score_fast_bf16(p, st) : score_fast_f16(p, st);
+  else if (fast)
+    e = dtype == MOER_F32    ? score_fast16_f32(p, st)
+        : dtype == MOER_BF16 ? score_fast16_bf16(p, st)
+                             : score_fast16_f16(p, st);
   else
     e = dtype == MOER_F32    ? score_run<float>(p, st)
         : dtype == MOER_BF16 ? score_run<__nv_bfloat16>(p, st)

@@ -592,3 +592,63 @@ def test_expert_order_odd_data(env):
     _order_case(env, ids, 64, 6, 16, extra=5, status=6)
     _order_case(env, np.full((1, 4000, 8), 3, dtype=np.uint8), 128, 8, 128)   # one expert takes all
     _order_case(env, np.zeros((2, 0, 8), dtype=np.uint8), 128, 8, 16, extra=9)
+
+
+# More than eight experts to a token at the sizes of the throughput kernel
+@pytest.mark.parametrize("E,k", [(16, 9), (16, 16), (24, 12), (32, 16), (60, 13), (64, 9), (64, 16), (72, 10), (100, 15), (128, 10), (128, 16),
+                                 (160, 12), (192, 11), (256, 9), (256, 16)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+def test_throughput_many_choices(env, E, k, dtype, score, renorm):
+    torch, _ = env
+    rs = np.random.RandomState(E + k)
+    dev, x = _logits(torch, rs, 2, 1031, E, dtype)
+    for biased in (False, True):
+        bias = rs.normal(0, 0.05, size=(2, E)) if biased else None
+        for sums in (False, True):
+            o = dict(score=score, renorm=renorm, scale=1.5)
+            _check_forward(_forward(env, dev, E, k, dtype, bias=bias, sums=sums, **o), x, k, bias=bias, **o)
+
+
+# groups of whole blocks and groups of quads; as many choices as the kept groups have experts
+@pytest.mark.parametrize("E,k,n,keep", [(256, 16, 8, 4), (256, 10, 8, 1), (128, 16, 8, 1), (128, 12, 4, 2), (64, 9, 8, 2), (64, 16, 2, 1),
+                                        (32, 16, 4, 2), (160, 12, 5, 2), (96, 10, 8, 4), (160, 16, 8, 3)])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_throughput_many_choices_in_groups(env, E, k, n, keep, best, score, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E + n + k)
+    dev, x = _logits(torch, rs, 1, 2100, E, dtype)
+    for biased in (False, True):
+        bias = rs.normal(0, 0.05, size=(1, E)) if biased else None
+        o = dict(score=score, renorm=not biased, n_group=n, top_group=keep, best=best)
+        _check_forward(_forward(env, dev, E, k, dtype, bias=bias, sums=biased, **o), x, k, bias=bias, **o)
+
+
+@pytest.mark.parametrize("special", ["masks", "ties", "inf", "lowest"])
+@pytest.mark.parametrize("E,k,n", [(64, 12, 1), (128, 16, 8), (256, 10, 8), (60, 9, 1)])
+@pytest.mark.parametrize("layout", ["token", "odd"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_throughput_many_choices_special_values(env, special, E, k, n, layout, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E + k + 1)
+    dev, x = _logits(torch, rs, 2, 1060, E, dtype, layout=layout, special=special)
+    for biased in (False, True):
+        bias = rs.normal(0, 0.5, size=(2, E)) if biased else None
+        o = dict(score="sigmoid" if biased else "softmax", renorm=biased, n_group=n, top_group=max(1, n // 2), best=1 + (n > 1))
+        ids, w, ss = _forward(env, dev, E, k, dtype, bias=bias, **o)
+        # Groups tie where their logits do, and the oracle leaves those rows open: every
+        # row's choice is that of the few rows' kernel, and the others are the oracle's
+        few = [_forward(env, dev[:, a:a + 530], E, k, dtype, bias=bias, sums=False, **o) for a in (0, 530)]
+        assert np.array_equal(ids, np.concatenate([f[0] for f in few], axis=1))
+        ws = np.concatenate([f[1] for f in few], axis=1)
+        assert (np.abs(w - ws) <= 8e-6 * np.abs(ws) + 4.8e-38).all()
+        b32 = None if bias is None else bias.astype(np.float32)
+        _, _, sums, gap = router.score_topk(x, k, bias=b32, **o)
+        assert (np.abs(ss - sums) <= 6e-6 * sums + 1e-30).all()
+        tol = 1e-5 * (1 + (0 if bias is None else np.abs(b32).max()))
+        for l in range(2):
+            at = gap[l] > tol
+            _check_forward((ids[l:l + 1, at], w[l:l + 1, at], None), x[l:l + 1, at], k,
+                           bias=None if bias is None else bias[l:l + 1], **o)
