@@ -45,12 +45,12 @@ enum ScoreKind {
   BY_LOGIT = 0,        // the logits alone; weights from the chosen ones
   SOFTMAX_SUMS = 1,    // the logits; with the column pass of a softmax
   SIGMOID_SUMS = 2,    // the logits; with the column pass of a sigmoid
-  BY_GROUP = 3,        // groups ranked by their best logit
-  BY_SIGMOID = 4,      // scores: a bias, or groups ranked by two scores
+  BY_GROUP = 3,        // the logits, in groups
+  BY_SIGMOID = 4,      // scores with a bias
   BY_SOFTMAX = 5
 };
-inline ScoreKind score_kind(bool bias, int n_group, int group_best, bool sums, bool soft, bool renorm) {
-  if (bias || (n_group > 1 && group_best == 2)) return soft ? BY_SOFTMAX : BY_SIGMOID;
+inline ScoreKind score_kind(bool bias, int n_group, bool sums, bool soft, bool renorm) {
+  if (bias) return soft ? BY_SOFTMAX : BY_SIGMOID;
   if (n_group > 1) return BY_GROUP;
   if (soft) return sums || !renorm ? SOFTMAX_SUMS : BY_LOGIT;
   return sums ? SIGMOID_SUMS : BY_LOGIT;

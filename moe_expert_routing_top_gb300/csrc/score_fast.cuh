@@ -226,12 +226,11 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
   const int l = blockIdx.x / p.nspan, unit = blockIdx.x - l * p.nspan;
   const bool soft = KIND == SOFTMAX_SUMS || KIND == BY_SOFTMAX ||
                     (KIND != SIGMOID_SUMS && KIND != BY_SIGMOID && p.score == MOER_SCORE_SOFTMAX);
-  const bool has_bias = SCORES && p.bias != nullptr;
   const bool sums = KIND != BY_LOGIT && p.partial != nullptr;
   const bool columns = KIND == SOFTMAX_SUMS || KIND == SIGMOID_SUMS || (KIND != BY_LOGIT && (sums || (soft && !p.renorm)));
   if constexpr (SCORES) {
     for (int e = threadIdx.x; e < 256; e += SF_WARPS * 32)  // u = s / 4 + (b + 1) / 4
-      sbias[e] = has_bias && e < p.E ? fmaf(p.bias[(size_t)l * p.E + e], 0.25f, 0.25f) : 0.25f;
+      sbias[e] = e < p.E ? fmaf(p.bias[(size_t)l * p.E + e], 0.25f, 0.25f) : 0.25f;
     __syncthreads();
   }
   constexpr int near = SCORES ? 2 : 0;  // steps of n that do not settle an order: a score is rounded before its key is
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
     bool bad = false;
     float mm = 0.f, rs = 1.f;
     if constexpr (KIND == BY_SOFTMAX) {
-      // the softmax first: its largest logit, and with a bias the sum, from L1
+      // the softmax first: its largest logit and the sum, from L1
       float m = NEG_INF, z = 0.f;
       for (int b = 0; b < NB; ++b) {
         Raw<EB> again;
@@ -290,17 +289,15 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
       m = row_max<G>(m);
       bad = !(fabsf(m) < 128.f);  // nothing but masks, or infinities: left to the exact path
       mm = bad ? 0.f : m * LOG2E;
-      if (has_bias) {  // without one the exponentials order experts and groups as the scores do
-        for (int b = 0; b < NB; ++b) {
-          Raw<EB> again;
-          fetch(again, b, row, NEG_INF);
-          float x[8];
-          again.template get<X>(x);
+      for (int b = 0; b < NB; ++b) {
+        Raw<EB> again;
+        fetch(again, b, row, NEG_INF);
+        float x[8];
+        again.template get<X>(x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) z += ex2_approx(fmaf(fmaxf(x[j], NEG_INF), LOG2E, -mm));
-        }
-        rs = rcp_approx(row_sum<G>(z));
+        for (int j = 0; j < 8; ++j) z += ex2_approx(fmaf(fmaxf(x[j], NEG_INF), LOG2E, -mm));
       }
+      rs = rcp_approx(row_sum<G>(z));
     }
 #pragma unroll ROUNDS
     for (int g = 0; g < NB; g += PF) {
@@ -354,7 +351,8 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
       }
     }
     if (LISTS && p.n_group > 1) {
-      // a group is mb blocks of every lane of the row
+      // a group is mb blocks of every lane of the row, the first of them at group_at
+      auto group_at = [&](int b) { return (b & (mb - 1)) == 0 && (b >> sh) < p.n_group; };
       int g1[8], g2[8], gk[8];
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
@@ -378,20 +376,48 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
           g2[b] = max(max(g2[b], h2), min(g1[b], h1));
           g1[b] = max(g1[b], h1);
         }
-        const bool first = (b & (mb - 1)) == 0 && (b >> sh) < p.n_group;
-        // the second best counts only where there are two numbers to add
-        if (first && p.group_best == 2 && g2[b] <= 0) bad = true;
-        g1[b] += p.group_best == 2 ? g2[b] : 0;
-        g1[b] = gk[b] = first ? g1[b] * 8 + (7 - (b >> sh)) : INT_MIN;
+      }
+      if (!SCORES && p.group_best == 2) {  // the scores of the two best logits
+        int most = g1[0];
+#pragma unroll
+        for (int b = 1; b < 8; ++b) most = max(most, g1[b]);
+        if (most >= 8388607) bad = true;
+        constexpr float STEP = 256.f / 8388607.f * LOG2E;
+        auto score = [&](int n) {
+          return soft ? ex2_approx((float)(n - most) * STEP)
+                      : rcp_approx(1.f + ex2_approx(fmaf((float)(n - 4194304), -STEP, -0.5f * STEP)));
+        };
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          if (g2[b] <= 0 && group_at(b)) bad = true;  // the second best counts only where there are two numbers to add
+          g1[b] = (int)((score(g1[b]) + score(g2[b])) * 67108864.f);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if (SCORES && p.group_best == 2) {
+          if (g2[b] <= 0 && group_at(b)) bad = true;
+          g1[b] += g2[b];
+        }
+        g1[b] = gk[b] = group_at(b) ? g1[b] * 8 + (7 - (b >> sh)) : INT_MIN;
       }
       sort8_desc(gk);
       int thr = gk[0], nxt = gk[1];
 #pragma unroll
       for (int r = 1; r < 7; ++r)
         if (r < p.top_group) thr = gk[r], nxt = gk[r + 1];
-      // the sum of two scores' keys can be three steps off either way; equal keys of
-      // logits may stand in either order, unless they hold their logits exactly
-      if ((thr >> 3) - (nxt >> 3) <= 3 * near && (SCORES || !exact_n<EB>(thr >> 3))) bad = true;
+      const int kept = thr >> 3, out = nxt >> 3;
+      if (!SCORES && p.group_best == 2) {
+        // a logit's n is 0.75 steps of 3.1e-5 off at most, which changes each score by
+        // 2.3e-5 of itself (of 1 less itself, where that is less): two sums in units of
+        // 2^-26 may be 2^-14 of the sum off, and 128 units for the scores' own rounding
+        const int part = soft ? kept : min(kept, (1 << 27) - out);
+        if (kept - out <= (part >> 14) + 128) bad = true;
+      } else if (kept - out <= 3 * near && (SCORES || !exact_n<EB>(kept))) {
+        // the sum of two scores' keys can be three steps off either way; equal keys of
+        // logits may stand in either order, unless they hold their logits exactly
+        bad = true;
+      }
       unsigned keep = 0u;  // the first blocks of the kept groups
 #pragma unroll
       for (int b = 0; b < 8; ++b)
@@ -474,7 +500,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
       // or the last and the one after it (a further one may be as near), are left to the exact path
       auto value = [&](int e) {
         const float x = live_logit(Quad<X>::one(row[e]));
-        if (!has_bias || x == NEG_INF) return x;  // without a bias the logits order the experts
+        if (!SCORES || x == NEG_INF) return x;
         return (KIND == BY_SOFTMAX ? ex2_approx(fmaf(x, LOG2E, -mm)) * rs : sigmoid(x)) + p.bias[(size_t)l * p.E + e];
       };
       bool before = false;  // the pair before was open
@@ -522,7 +548,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
 #pragma unroll
       for (int q = 0; q < 4 * NQ; ++q) {
         const int e = 4 * (lane + 32 * (q / 4)) + q % 4;
-        bias[q] = has_bias && e < p.E ? p.bias[(size_t)l * p.E + e] : 0.f;
+        bias[q] = SCORES && e < p.E ? p.bias[(size_t)l * p.E + e] : 0.f;
       }
       __syncwarp();
       const int64_t at = ((int64_t)l * p.T + t0 + f) * p.k;
@@ -633,7 +659,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
 template <typename X, int G, int NB, int KT, bool WHOLE>
 cudaError_t score_fast_shape(const ScoreParams& p, cudaStream_t st) {
   const dim3 grid(p.L * p.nspan), block(SF_WARPS * 32);
-  switch (score_kind(p.bias != nullptr, p.n_group, p.group_best, p.partial != nullptr, p.score == MOER_SCORE_SOFTMAX,
+  switch (score_kind(p.bias != nullptr, p.n_group, p.partial != nullptr, p.score == MOER_SCORE_SOFTMAX,
                      p.renorm != 0)) {
     case BY_LOGIT: return launch_pdl(score_fast_kernel<X, G, NB, KT, BY_LOGIT, WHOLE, false>, grid, block, 0, st, p);
     case SOFTMAX_SUMS: return launch_pdl(score_fast_kernel<X, G, NB, KT, SOFTMAX_SUMS, WHOLE, false>, grid, block, 0, st, p);
@@ -648,7 +674,7 @@ cudaError_t score_fast_shape(const ScoreParams& p, cudaStream_t st) {
 template <typename X, int G>
 cudaError_t score_fast_split(const ScoreParams& p, cudaStream_t st) {
   const dim3 grid(p.L * p.nspan), block(SF_WARPS * 32);
-  switch (score_kind(p.bias != nullptr, p.n_group, p.group_best, false, p.score == MOER_SCORE_SOFTMAX, p.renorm != 0)) {
+  switch (score_kind(p.bias != nullptr, p.n_group, false, p.score == MOER_SCORE_SOFTMAX, p.renorm != 0)) {
     case BY_GROUP: return launch_pdl(score_fast_kernel<X, G, 8, 8, BY_GROUP, false, true>, grid, block, 0, st, p);
     case BY_SIGMOID: return launch_pdl(score_fast_kernel<X, G, 8, 8, BY_SIGMOID, false, true>, grid, block, 0, st, p);
     default: return launch_pdl(score_fast_kernel<X, G, 8, 8, BY_SOFTMAX, false, true>, grid, block, 0, st, p);

@@ -309,8 +309,7 @@ moer_status score_topk_launch(ScoreParams p, int dtype, float* score_sum, void* 
   if (fast) {
     const int sms = device_sm_count();
     if (sms <= 0) return MOER_ECUDA;
-    const int kind = score_kind(p.bias != nullptr, p.n_group, p.group_best, score_sum != nullptr, p.score == MOER_SCORE_SOFTMAX,
-                                p.renorm != 0);
+    const int kind = score_kind(p.bias != nullptr, p.n_group, score_sum != nullptr, p.score == MOER_SCORE_SOFTMAX, p.renorm != 0);
     p.span = fast_span(p.T, p.L, p.E <= 64 ? 128 : p.E <= 128 ? 64 : 32,
                        (int64_t)sms * score_resident(dtype == MOER_F32 ? 4 : 2, kind, p.k));
   } else {

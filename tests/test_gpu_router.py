@@ -652,3 +652,21 @@ def test_throughput_many_choices_special_values(env, special, E, k, n, layout, d
             at = gap[l] > tol
             _check_forward((ids[l:l + 1, at], w[l:l + 1, at], None), x[l:l + 1, at], k,
                            bias=None if bias is None else bias[l:l + 1], **o)
+
+
+# Groups whose two best scores nearly add up to the same: small logits, and sigmoids near 1
+@pytest.mark.parametrize("E,k,n,keep", [(256, 8, 8, 4), (128, 16, 8, 3), (64, 6, 4, 2), (160, 6, 8, 3)])
+@pytest.mark.parametrize("std", [0.003, 0.1, 9.0])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_throughput_near_groups(env, E, k, n, keep, std, score, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E + k)
+    dev, x = _logits(torch, rs, 1, 2600, E, dtype, std=std)
+    o = dict(score=score, renorm=True, n_group=n, top_group=keep, best=2)
+    ids, w, _ = _forward(env, dev, E, k, dtype, sums=False, **o)
+    few = [_forward(env, dev[:, a:a + 1300], E, k, dtype, sums=False, **o) for a in (0, 1300)]
+    assert np.array_equal(ids, np.concatenate([f[0] for f in few], axis=1))
+    gap = router.score_topk(x, k, **o)[3]
+    at = gap[0] > 1e-5
+    _check_forward((ids[:, at], w[:, at], None), x[:, at], k, **o)
