@@ -55,12 +55,17 @@ inline ScoreKind score_kind(bool bias, int n_group, bool sums, bool soft, bool r
   if (soft) return sums || !renorm ? SOFTMAX_SUMS : BY_LOGIT;
   return sums ? SIGMOID_SUMS : BY_LOGIT;
 }
-// Blocks of 128 threads of the fast kernel on an SM, which sets its registers.  Cases
-// of 3.1 M rows x 128 fp32 / 213 k x 256 bf16 by score / 780 k x 64 bf16 with column
-// pass: 4 blocks 341 / 87 / 72 us, 5 blocks 291 / 91 / 70 us, 6 blocks 334 / 142 / 67 us.
-// A top 16 holds 8 keys more a lane, which spills with 5.
+// Experts of the quads that a group of gs lies in, where it begins in the worst place.
+__host__ __device__ constexpr int group_span(int gs) { return (gs + ((gs & 1) ? 3 : (gs & 2)) + 3) & ~3; }
+
+// Blocks of 128 threads of the fast kernel on an SM, which sets its registers.  fp32
+// choices by group or score with 4 blocks / 5 (which spill): 192 / 214 us by sigmoid with
+// bias, 137 / 167 by logit, 26 x 20,000 rows of 256 in 8 groups; 122 / 161 us, 48 x 20,000
+// rows of 128 in 4.  bf16 ones: 174 / 169 and 130 / 131 us.  The others with 4 / 5 / 6:
+// 3.1 M rows x 128 fp32 341 / 291 / 334 us, 780 k x 64 bf16 with column pass 72 / 70 /
+// 67 us.  A top 16 holds 8 keys more a lane.
 constexpr int score_resident(int elem, int kind, int kt) {
-  return kt > 8 ? 4 : kind >= BY_GROUP ? 5 : elem == 2 ? 6 : 5;
+  return kt > 8 || (elem == 4 && kind >= BY_GROUP) ? 4 : kind >= BY_GROUP ? 5 : elem == 2 ? 6 : 5;
 }
 
 constexpr float NEG_INF = -__builtin_huge_valf();

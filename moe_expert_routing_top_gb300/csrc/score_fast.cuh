@@ -201,9 +201,11 @@ __device__ __noinline__ Eight far_choice(Eight x, Eight bias, float mm, float rs
 }
 
 // WHOLE: E = 8 G NB and rows on 16 bytes, every block whole.
-// SPLIT (groups of gs experts, gs a multiple of 4 but no power of two times 8 G): the
-// lane's blocks go group by group, mb to a group, and a block is the quads 2 m G + i
-// and (2 m + 1) G + i of its group, so that no block lies in two groups.
+// SPLIT (groups of gs experts, gs no power of two times 8 G): the lane's blocks go
+// group by group, mb to a group, and a block is the quads 2 m G + i and
+// (2 m + 1) G + i of its group, so that no block lies in two groups.  Where gs is no
+// multiple of 4, a group has the quads that it shares with its neighbours, too, less
+// their experts.
 template <typename X, int G, int NB, int KT, int KIND, bool WHOLE, bool SPLIT>
 __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND, KT)) score_fast_kernel(const ScoreParams p) {
   constexpr int RW = 32 / G;            // rows of a warp at a time
@@ -243,12 +245,17 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
   // rows past the unit's end read its last row again
   auto row_at = [&](int64_t t) { return base + min64(t + rl, t1 - 1) * p.ld_token; };
   Raw<EB> raw[PF];
-  const int gs = LISTS ? p.E / p.n_group : 0, per = LISTS ? (gs + 8 * G - 1) / (8 * G) : 1;
+  const int gs = LISTS ? p.E / p.n_group : 0, per = LISTS ? (group_span(gs) + 8 * G - 1) / (8 * G) : 1;
   const int sh = per > 1 ? 32 - __clz(per - 1) : 0, mb = 1 << sh;  // blocks of a lane to a group
   // first expert of a block's first quad, less the lane's part, and whether its quads lie in the row
-  auto split_at = [&](int b) { return (b >> sh) * gs + 8 * G * (b & (mb - 1)); };
+  auto split_at = [&](int b) { return ((b >> sh) * gs & ~3) + 8 * G * (b & (mb - 1)); };
   auto split_has = [&](int b, int h) {
-    return 8 * G * (b & (mb - 1)) + 4 * (G * h + i) < gs && (b >> sh) < p.n_group;
+    return split_at(b) + 4 * (G * h + i) < ((b >> sh) + 1) * gs && (b >> sh) < p.n_group;
+  };
+  const bool shared = SPLIT && (gs & 3) != 0;  // quads of two groups; whether expert j of a block is its group's own
+  auto split_own = [&](int b, int j) {
+    const int r = split_at(b) + 4 * (G * (j / 4) + i) + j % 4 - (b >> sh) * gs;
+    return r >= 0 && r < gs;
   };
   auto fetch = [&](Raw<EB>& to, int b, const X* of, float fill = KIND >= BY_SIGMOID ? 0.f : NEG_INF) {
     const int e = 8 * (i + G * b);
@@ -295,7 +302,8 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
         float x[8];
         again.template get<X>(x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z += ex2_approx(fmaf(fmaxf(x[j], NEG_INF), LOG2E, -mm));
+        for (int j = 0; j < 8; ++j)
+          if (!shared || split_own(b, j)) z += ex2_approx(fmaf(fmaxf(x[j], NEG_INF), LOG2E, -mm));
       }
       rs = rcp_approx(row_sum<G>(z));
     }
@@ -338,6 +346,10 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
           for (int j = 0; j < 8; ++j)
             if (SPLIT ? !split_has(b, j / 4) : e + (j & 4) >= p.E) c[j] &= 255;
         }
+        if (shared)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (!split_own(b, j)) c[j] &= 255;
         sort8_desc(c);
         if (LISTS && p.n_group > 1) {
           lists[warp][b][0][lane] = make_int4(c[0], c[1], c[2], c[3]);
@@ -670,7 +682,7 @@ cudaError_t score_fast_shape(const ScoreParams& p, cudaStream_t st) {
   }
 }
 
-// Groups of quads that are no blocks of 8 on every lane.
+// Groups that are no blocks of 8 on every lane.
 template <typename X, int G>
 cudaError_t score_fast_split(const ScoreParams& p, cudaStream_t st) {
   const dim3 grid(p.L * p.nspan), block(SF_WARPS * 32);

@@ -60,8 +60,7 @@ int fast_span(int64_t T, int L, int step, int64_t slots) {
 }
 
 // The fast kernel's options (score_fast.cuh): k <= 16, aligned quads, and groups,
-// where there are any, of quads that make at most eight blocks of a lane (k > 8:
-// of whole blocks).
+// where there are any, that make at most eight blocks of a lane (k > 8: whole ones).
 // Few rows leave it idle lanes: at 1,024 / 2,048 / 4,096 rows it took 2.6 / 2.6 / 4.2 us
 // (a warp per row: 3.2 / 3.3 / 5.2) with E = 128 fp32, 4.3 / 4.3 / 4.3 (4.5 / 5.6 / 9.7)
 // with 256 bf16 experts in groups, 5.3 / 5.6 / 5.3 (4.1 / 5.3 / 8.9) with 64 bf16
@@ -72,9 +71,9 @@ bool fast_supported(const ScoreParams& p) {
   if (p.n_group == 1) return true;
   const int lanes = p.E <= 64 ? 1 : p.E <= 128 ? 2 : 4, gs = p.E / p.n_group;
   int mb = 1;  // blocks of a lane to a group
-  while (mb * 8 * lanes < gs) mb *= 2;
+  while (mb * 8 * lanes < group_span(gs)) mb *= 2;
   if (p.k > 8 && (gs % (8 * lanes) != 0 || mb * 8 * lanes != gs)) return false;
-  return gs % 4 == 0 && p.n_group * mb <= 8;
+  return p.n_group * mb <= 8;
 }
 
 // Sorts four keys in descending order.

@@ -670,3 +670,20 @@ def test_throughput_near_groups(env, E, k, n, keep, std, score, dtype):
     gap = router.score_topk(x, k, **o)[3]
     at = gap[0] > 1e-5
     _check_forward((ids[:, at], w[:, at], None), x[:, at], k, **o)
+
+
+# groups that share quads of experts with their neighbours
+@pytest.mark.parametrize("E,k,n,keep", [(72, 6, 4, 2), (72, 8, 4, 3), (36, 4, 6, 2), (100, 8, 4, 1), (60, 5, 4, 2), (20, 3, 4, 2), (252, 8, 4, 2),
+                                        (28, 2, 4, 3), (132, 7, 3, 2), (200, 8, 8, 4), (12, 3, 4, 2), (252, 8, 2, 1)])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_throughput_shared_quads(env, E, k, n, keep, best, score, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E + n + 2)
+    for special in (None, "masks"):
+        dev, x = _logits(torch, rs, 2, 1060, E, dtype, special=special)
+        for biased in (False, True):
+            bias = rs.normal(0, 0.05, size=(2, E)) if biased else None
+            o = dict(score=score, renorm=not biased, n_group=n, top_group=keep, best=best)
+            _check_forward(_forward(env, dev, E, k, dtype, bias=bias, sums=biased, **o), x, k, bias=bias, **o)
