@@ -15,9 +15,10 @@
 // comes in with the first step).
 //
 // A row's answer is kept only where it is certain: the k-th key above 0, the
-// first below the top of the range, no three neighbours among the leading keys of
-// equal n (of scores: within two steps; two are ordered by their values; 16-bit
-// logits of size 2^-5 and more have exact keys, which their ids order), and, with
+// first below the top of the range, no run of neighbours among the leading keys of
+// equal n (of scores: within two steps) that their values put in another order, but
+// for its first two (16-bit logits of size 2^-5 and more have exact keys, which their
+// ids order), and, with
 // groups, the last kept group more than the rounding of its keys above the first
 // dropped one.  The warp redoes the other rows one by one with the exact keys of
 // score_row.cuh.
@@ -508,8 +509,10 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
     // all leading keys positive logits that their n hold exactly: the ids order equal ones
     const bool sure = EB == 2 && !SCORES && after > (4194304 + 1024) * 256 + 255;
     if (__any_sync(FULL, !sure && least < 256 * (near + 1))) {
-      // two neighbours that their keys do not settle stand by their own values; three,
-      // or the last and the one after it (a further one may be as near), are left to the exact path
+      // neighbours that their keys do not settle stand by their own values.  In a run of
+      // them the first two may change places, and every later pair has to be in order
+      // as it is, which makes the run sorted; other runs, and those that reach the end
+      // of the list (a further expert may be as near), are left to the exact path
       auto value = [&](int e) {
         const float x = live_logit(Quad<X>::one(row[e]));
         if (!SCORES || x == NEG_INF) return x;
@@ -519,16 +522,19 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
 #pragma unroll
       for (int j = 1; j <= KT; ++j) {
         const int hi = best[j - 1], lo = j < KT ? best[j < KT ? j : 0] : ninth;
-        const bool open = j <= p.k + 1 && (hi >> 8) - (lo >> 8) <= near && (SCORES || !exact_n<EB>(lo >> 8));
-        if (open && (before || (j == KT && p.k == KT))) bad = true;
-        before = open;
-        if (j < KT && open && j <= p.k) {
+        const bool open = (j <= p.k || before) && (hi >> 8) - (lo >> 8) <= near && (SCORES || !exact_n<EB>(lo >> 8));
+        if (open && j == KT) bad = true;
+        if (j < KT && open) {
           const int e = 255 - (hi & 255), f = 255 - (lo & 255);
           if (max(e, f) < p.E) {
             const float u = value(e), v = value(f);
-            if (v > u || (v == u && f < e)) best[j - 1] = lo, best[j < KT ? j : 0] = hi;
+            if (v > u || (v == u && f < e)) {
+              if (before) bad = true;
+              best[j - 1] = lo, best[j < KT ? j : 0] = hi;
+            }
           }
         }
+        before = open;
       }
       take();
     }

@@ -687,3 +687,40 @@ def test_throughput_shared_quads(env, E, k, n, keep, best, score, dtype):
             bias = rs.normal(0, 0.05, size=(2, E)) if biased else None
             o = dict(score=score, renorm=not biased, n_group=n, top_group=keep, best=best)
             _check_forward(_forward(env, dev, E, k, dtype, bias=bias, sums=biased, **o), x, k, bias=bias, **o)
+
+
+# Runs of equal and nearly equal choice scores: rounded logits with no, equal or nearly equal biases
+@pytest.mark.parametrize("E,k,n,keep", [(256, 8, 1, 1), (256, 7, 8, 4), (64, 16, 1, 1), (64, 5, 1, 1), (128, 12, 4, 2), (128, 8, 4, 2)])
+@pytest.mark.parametrize("scale", [0.25, 64.0])
+@pytest.mark.parametrize("spread", [0.0, 1e-6, 1e-3])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_throughput_runs(env, E, k, n, keep, scale, spread, score, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E + k)
+    x = np.round(rs.normal(0.0, 2.0, size=(1, 2400, E)) * scale) / scale
+    t = torch.from_numpy(x).to(getattr(torch, DT[dtype]))
+    dev, x = t.cuda(), t.double().numpy()
+    bias = rs.normal(0, 1, size=(1, E)) * spread + 0.25
+    o = dict(score=score, renorm=True, n_group=n, top_group=keep, best=1)
+    ids, w, _ = _forward(env, dev, E, k, dtype, bias=bias, sums=False, **o)
+    b32 = bias.astype(np.float32)
+    if spread == 0.0:  # the few rows' kernel breaks the ties alike
+        few = [_forward(env, dev[:, a:a + 1200], E, k, dtype, bias=bias, sums=False, **o) for a in (0, 1200)]
+        assert np.array_equal(ids, np.concatenate([f[0] for f in few], axis=1))
+    _, _, _, gap = router.score_topk(x, k, bias=b32, **o)
+    # whatever the order of scores that fp32 cannot tell apart: the choice falls off, and no
+    # expert of a kept group that was passed over stands above its last one
+    c = (router.scores(x, score) + b32[:, None, :])[0]
+    mine = np.take_along_axis(c, ids[0], axis=1)
+    assert (np.diff(mine, axis=1) <= 2e-6).all()
+    taken = np.zeros(c.shape, dtype=bool)
+    np.put_along_axis(taken, ids[0], True, axis=1)
+    assert (taken.sum(1) == k).all()
+    kept = taken.reshape(-1, n, E // n).any(2)
+    assert (kept.sum(1) <= keep).all()
+    over = np.where(taken | ~np.repeat(kept, E // n, axis=1), -np.inf, c).max(1)
+    assert (over <= mine[:, -1] + 2e-6).all()
+    at = gap[0] > 2e-5
+    if at.any():
+        _check_forward((ids[:, at], w[:, at], None), x[:, at], k, bias=bias, **o)
