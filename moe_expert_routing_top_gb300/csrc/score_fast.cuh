@@ -18,9 +18,9 @@
 // first below the top of the range, no run of neighbours among the leading keys of
 // equal n (of scores: within two steps) that their values put in another order, but
 // for its first two (16-bit logits of size 2^-5 and more have exact keys, which their
-// ids order), and, with
-// groups, the last kept group more than the rounding of its keys above the first
-// dropped one.  The warp redoes the other rows one by one with the exact keys of
+// ids order; so have their scores, where all experts share one bias and the slope is
+// not small), and, with groups, the last kept group more than the rounding of its keys
+// above the first dropped one.  The warp redoes the other rows one by one with the exact keys of
 // score_row.cuh.
 //
 // The weights are computed from the chosen logits, read again (they are in L1).
@@ -32,7 +32,7 @@
 // Measured (GB300): 65,536 tokens x 48 layers of 128 fp32 logits, k = 8, softmax
 // weights: 283 us, 6.14 TB/s of algorithmic bytes, 0.90 of the measured copy
 // bandwidth.  8,209 x 26 of 256 bf16 logits, sigmoid with bias, 4 of 8 groups by
-// their two best: 69 us (1.7 TB/s); the ALU pipe is 64 % busy at 2.6 instructions a
+// their two best: 70 us (1.7 TB/s); the ALU pipe is 64 % busy at 2.6 instructions a
 // clock, and the networks' minima and maxima alone would fill it for some 45 us.
 // 30,011 x 26 of 64 bf16 logits, k = 6, softmax weights and score sums: 64 us, of
 // which the column pass is about 20.
@@ -231,10 +231,15 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
                     (KIND != SIGMOID_SUMS && KIND != BY_SIGMOID && p.score == MOER_SCORE_SOFTMAX);
   const bool sums = KIND != BY_LOGIT && p.partial != nullptr;
   const bool columns = KIND == SOFTMAX_SUMS || KIND == SIGMOID_SUMS || (KIND != BY_LOGIT && (sums || (soft && !p.renorm)));
+  bool even_bias = false;  // one bias for all of the layer's experts, and 16-bit logits
   if constexpr (SCORES) {
-    for (int e = threadIdx.x; e < 256; e += SF_WARPS * 32)  // u = s / 4 + (b + 1) / 4
-      sbias[e] = e < p.E ? fmaf(p.bias[(size_t)l * p.E + e], 0.25f, 0.25f) : 0.25f;
-    __syncthreads();
+    const float* b = p.bias + (size_t)l * p.E;
+    bool same = EB == 2;
+    for (int e = threadIdx.x; e < 256; e += SF_WARPS * 32) {  // u = s / 4 + (b + 1) / 4
+      sbias[e] = e < p.E ? fmaf(b[e], 0.25f, 0.25f) : 0.25f;
+      same = same && (e >= p.E || b[e] == b[0]);
+    }
+    even_bias = __syncthreads_and(same);
   }
   constexpr int near = SCORES ? 2 : 0;  // steps of n that do not settle an order: a score is rounded before its key is
   float acc[8];
@@ -518,11 +523,29 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
         if (!SCORES || x == NEG_INF) return x;
         return (KIND == BY_SOFTMAX ? ex2_approx(fmaf(x, LOG2E, -mm)) * rs : sigmoid(x)) + p.bias[(size_t)l * p.E + e];
       };
+      // with one bias for all: the choices whose 16-bit logit's neighbours have scores 8
+      // steps and more from its own, so that keys as near as an open pair's belong to
+      // equal logits (a zero bias, 26 x 20,000 rows of 256 bf16 in groups: 198 us, 425
+      // without this, for the last choice and the one after it are often equal)
+      unsigned alone = 0u;
+      if constexpr (SCORES && EB == 2) {
+        if (even_bias) {
+#pragma unroll
+          for (int jj = 0; jj < OUT; ++jj) {
+            const float x = xj[jj], next = fabsf(x) * (std::is_same<X, __half>::value ? 1.f / 4096.f : 1.f / 512.f);
+            const float slope = KIND == BY_SOFTMAX ? ex2_approx(fmaf(x, LOG2E, -mm)) * rs : sigmoid_slope(x);
+            if (slope * next > 8.f * 4.f / 8388607.f) alone |= 1u << (i * OUT + jj);
+          }
+#pragma unroll
+          for (int o = 1; o < G; o *= 2) alone |= __shfl_xor_sync(FULL, alone, o);
+        }
+      }
       bool before = false;  // the pair before was open
 #pragma unroll
       for (int j = 1; j <= KT; ++j) {
         const int hi = best[j - 1], lo = j < KT ? best[j < KT ? j : 0] : ninth;
-        const bool open = (j <= p.k || before) && (hi >> 8) - (lo >> 8) <= near && (SCORES || !exact_n<EB>(lo >> 8));
+        bool open = (j <= p.k || before) && (hi >> 8) - (lo >> 8) <= near && (SCORES || !exact_n<EB>(lo >> 8));
+        if (SCORES && EB == 2 && (alone >> (j - 1) & 1u) != 0u) open = false;
         if (open && j == KT) bad = true;
         if (j < KT && open) {
           const int e = 255 - (hi & 255), f = 255 - (lo & 255);
