@@ -20,8 +20,8 @@
 // for its first two (16-bit logits of size 2^-5 and more have exact keys, which their
 // ids order; so have their scores, where all experts share one bias and the slope is
 // not small), and, with groups, the last kept group more than the rounding of its keys
-// above the first dropped one.  The warp redoes the other rows one by one with the exact keys of
-// score_row.cuh.
+// above the first dropped one and no key at the top of the range in a sum of two.  The warp
+// redoes the other rows one by one with the exact keys of score_row.cuh.
 //
 // The weights are computed from the chosen logits, read again (they are in L1).
 // A softmax over the row without a renormalisation, and score sums, take a pass
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
     if (LISTS && p.n_group > 1) {
       // a group is mb blocks of every lane of the row, the first of them at group_at
       auto group_at = [&](int b) { return (b & (mb - 1)) == 0 && (b >> sh) < p.n_group; };
-      int g1[8], g2[8], gk[8];
+      int g1[8], g2[8], gk[8], most = 0;
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
         const int2 two = b < NB ? *reinterpret_cast<const int2*>(&lists[warp][b < NB ? b : 0][0][lane]) : make_int2(0, 0);
@@ -395,11 +395,14 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
           g1[b] = max(g1[b], h1);
         }
       }
-      if (!SCORES && p.group_best == 2) {  // the scores of the two best logits
-        int most = g1[0];
+      if (p.group_best == 2) {
+        // a best key at the top of the range makes its group's sum too small
+        most = g1[0];
 #pragma unroll
         for (int b = 1; b < 8; ++b) most = max(most, g1[b]);
         if (most >= 8388607) bad = true;
+      }
+      if (!SCORES && p.group_best == 2) {  // the scores of the two best logits
         constexpr float STEP = 256.f / 8388607.f * LOG2E;
         auto score = [&](int n) {
           return soft ? ex2_approx((float)(n - most) * STEP)

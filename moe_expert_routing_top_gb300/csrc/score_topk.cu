@@ -149,8 +149,9 @@ __device__ void row_by_keys(const ScoreParams& p, const X* row, float (&x)[4 * N
     }
     const int n2 = second[lane] >> 8;
     const bool real = lane < p.n_group;
-    // the second best counts only where there are two numbers to add
-    if (real && p.group_best == 2 && n2 <= 0) bad = true;
+    // the second best counts only where there are two numbers to add, and the best one
+    // only within the keys' range: a sum with one past it is too small
+    if (real && p.group_best == 2 && (n2 <= 0 || best[lane] >> 8 >= 8388607)) bad = true;
     const int gk = real ? ((best[lane] >> 8) + (p.group_best == 2 ? n2 : 0)) * 32 + (31 - lane) : -1;
     int above = 0;
     for (int g = 0; g < p.n_group; ++g) above += __shfl_sync(FULL, gk, g) > gk ? 1 : 0;
