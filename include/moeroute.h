@@ -443,7 +443,8 @@ typedef struct moer_score_opts {
  *   moer_topk_signature's, so moer_ids_signature and what follows take them.
  * Per layer l and token t, over the E logits x of the row:
  *   s_e   score: softmax of the row, or 1 / (1 + exp(-x_e)); 0 for an expert
- *         whose logit is -inf or NaN (a masked expert);
+ *         whose logit is -inf or NaN (a masked expert), and for a sigmoid under
+ *         the smallest normal fp32 number (x_e < -87.3);
  *   c_e   choice score: s_e + bias[l][e] (fp32) with a bias; the order of x_e
  *         without one.  A masked expert's is -inf (NaN logit: below -inf)
  *         whatever its bias;
@@ -454,7 +455,8 @@ typedef struct moer_score_opts {
  *         the lower id, NaN below every number;
  *   w_j   scale * s_j, or with renorm scale * s_j / (sum of the k chosen s)
  *         (softmax: the softmax over the chosen logits).  Where every chosen
- *         score is 0 (a row whose experts are all masked) the weights are 0.
+ *         score is 0 (a row whose experts are all masked) the weights, and
+ *         their part of the gradient, are 0.
  * logits    row (l, t) starts at element l * ld_layer + t * ld_token; the E
  *           logits of a row are contiguous.  ld_token >= E; L > 1: ld_layer
  *           >= E.  [L][T][E] has ld_token = E, ld_layer = T * E; [T][L][E]

@@ -225,15 +225,20 @@ __device__ __forceinline__ float fma_sat(float a, float b, float c) {  // NaN ->
   asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ float mul_ftz(float a, float b) {  // numbers under the normal range are 0
+  float r;
+  asm("mul.rn.ftz.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // A logit that counts: -inf for a masked expert, NaN included.
 __device__ __forceinline__ float live_logit(float x) { return x == x ? x : NEG_INF; }
-// 1 / (1 + exp(-x)): 0 at -inf, 1 at +inf; below x = -87 the result is under
-// the smallest normal number and is 0.
+// 1 / (1 + exp(-x)): 0 at -inf, 1 at +inf; below x = -87.3 the result is under
+// the smallest normal number and is 0 (the reciprocal flushes it).
 __device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + expf(-x)); }
-// s (1 - s) without the cancellation of 1 - s: t / (1 + t)^2, t = exp(-|x|).
+// s (1 - s) without the cancellation of 1 - s: t / (1 + t)^2, t = exp(-|x|); 0 where s is.
 __device__ __forceinline__ float sigmoid_slope(float x) {
   const float t = expf(-fabsf(x)), r = rcp_approx(1.f + t);
-  return t * r * r;
+  return mul_ftz(t, r * r);
 }
 // exp(x - m) for x <= m, where m is the largest of a set: equal infinities
 // give 1 (they share the weight), and a set without any expert gives 0.

@@ -7,7 +7,8 @@
 //   softmax, renormalised:  dx_ij = q_j (g_j - sum g q), q the softmax over the
 //                           chosen logits, plus p_e (a_e - sum a p);
 //   sigmoid:                dx_e = s_e (1 - s_e) (a_e + D_e), D at the chosen ones
-//                           g_j, or (g_j - sum g s / S) / S renormalised, S = sum s.
+//                           g_j, or (g_j - sum g s / S) / S renormalised, S = sum s;
+//                           there s_e D_e is q_j (g_j - sum g q) with the shares q = s / S.
 // Every form is a dense part (absent without a, but for the plain softmax) and a
 // part at the k chosen experts, so a renormalised gate without score sums
 // reads its chosen logits alone.
@@ -103,13 +104,13 @@ __global__ void __launch_bounds__(SG_WARPS * 32) score_grad_kernel(const ScorePa
         dj = g * exp_below(xj, m) * rz;
       }
     } else {
-      dj = g;
       if (p.renorm) {
-        const float s = sigmoid(xj);
-        const float z = warp_sum(s), rs = z > 0.f ? 1.f / z : 0.f;
-        dj = (g - warp_sum(g * s) * rs) * rs;
+        const float t = expf(-fabsf(xj)), r = rcp_approx(1.f + t), s = sigmoid(xj);
+        const float z = warp_sum(s), q = z > 0.f ? s * (1.f / z) : 0.f;
+        dj = (g - warp_sum(g * q)) * (q * (xj >= 0.f ? t * r : r));
+      } else {
+        dj = g * sigmoid_slope(xj);
       }
-      dj *= sigmoid_slope(xj);
     }
     for (int j = 0; j < p.k; ++j) {
       const int e = __shfl_sync(FULL, id, j);

@@ -210,15 +210,17 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
         if (j == 0) scalar[warp][rc].z = dg;
       }
     } else {
-      // s and s (1 - s) from one exponential of -|x|
+      // s and 1 - s from one exponential of -|x|; scores that the gate takes as 0 are 0
+      // here too, and the shares q stay below 1 where 1 / sum alone may pass the range
       const float t = expf(-fabsf(xj)), r = rcp_approx(1.f + t);
-      dj = g;
       if constexpr (RENORM) {
-        const float s = ok ? (xj >= 0.f ? r : t * r) : 0.f;
-        const float z = part_sum<KL>(s), rs = z > 0.f ? 1.f / z : 0.f;
-        dj = (g - part_sum<KL>(g * s) * rs) * rs;
+        const bool up = xj >= 0.f;
+        const float s = !ok ? 0.f : up ? r : mul_ftz(t, r);
+        const float z = part_sum<KL>(s), q = z > 0.f ? s * (1.f / z) : 0.f;
+        dj = (g - part_sum<KL>(g * q)) * (q * (up ? t * r : r));
+      } else {
+        dj = g * mul_ftz(t, r * r);
       }
-      dj *= t * r * r;
     }
     const bool lost = ok && __float_as_int(*at) != j + 1;
     const bool repeats = __any_sync(FULL, lost);

@@ -12,11 +12,13 @@ NEG = -np.inf
 
 
 def scores(x, score):
-    """Scores of rows x [..., E] in 64 bits; masked experts (-inf, NaN) have 0."""
+    """Scores of rows x [..., E] in 64 bits; masked experts (-inf, NaN) have 0, and so have
+    sigmoids under the smallest normal fp32 number."""
     x = np.where(np.isnan(x), NEG, np.asarray(x, dtype=np.float64))
     if score == "sigmoid":
         with np.errstate(over="ignore"):
-            return np.where(x == NEG, 0.0, 1.0 / (1.0 + np.exp(-x)))
+            s = np.where(x == NEG, 0.0, 1.0 / (1.0 + np.exp(-x)))
+        return np.where(s < 2.0 ** -126, 0.0, s)
     m = x.max(-1, keepdims=True)
     with np.errstate(invalid="ignore"):
         e = np.where(x == NEG, 0.0, np.where(x == m, 1.0, np.exp(x - m)))

@@ -5,9 +5,32 @@ Tolerances and comparisons are those of test_gpu_router.py, whose header derives
 import numpy as np
 import pytest
 
-from tests.test_gpu_router import _check_forward, _forward, _logits, env  # noqa: F401
+from tests.test_gpu_router import DT, _backward, _check_forward, _check_grad, _forward, _ids, _logits, env  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+def _device(torch, x, dtype, layout="layer"):
+    """Logits x on the GPU in `dtype` (rows on odd elements with layout "odd"), and their values."""
+    t = torch.from_numpy(x).to(getattr(torch, DT[dtype]))
+    if layout == "layer":
+        return t.cuda(), t.double().numpy()
+    L, T, E = x.shape
+    buf = torch.full((L, T, E + 3), 7.0, dtype=t.dtype, device="cuda")
+    buf[:, :, 1:E + 1] = t.cuda()
+    return buf[:, :, 1:E + 1], t.double().numpy()
+
+
+def _small(rs, L, T, E):
+    """Logits whose sigmoids are near the smallest normal number (at -87.3365) and under it, but
+    not so near that fp32 and 64 bits may see them on different sides."""
+    x = rs.uniform(-104.0, -80.0, size=(L, T, E))
+    x[:, 1::3][rs.random_sample(x[:, 1::3].shape) < 0.1] = -30.0   # beside larger scores,
+    x[:, 2::3][rs.random_sample(x[:, 2::3].shape) < 0.5] = -np.inf  # masks,
+    x[:, 4] = -95.0                                                 # and where no score is left
+    x[:, 5] = -87.0
+    x[np.abs(x + 87.3365) < 0.02] = -87.0
+    return x
 
 
 # Choice scores past the keys' range of [-1, 3) in groups ranked by their two best: the few
@@ -29,3 +52,20 @@ def test_group_sums_of_large_biases(env, E, k, n, T, score, dtype):
         bias[l, other * gs:(other + 1) * gs] += 2.0
     o = dict(score=score, renorm=True, n_group=n, top_group=1, best=2)
     _check_forward(_forward(env, dev, E, k, dtype, bias=bias, **o), x, k, bias=bias, **o)
+
+
+@pytest.mark.parametrize("E,k", [(64, 6), (100, 12), (128, 8), (256, 20)])
+@pytest.mark.parametrize("layout", ["layer", "odd"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradient_of_small_scores(env, E, k, layout, renorm, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E)
+    dev, x = _device(torch, _small(rs, 2, 70, E), dtype, layout)
+    ids, dw, da = _ids(rs, 2, 70, E, k), rs.normal(size=(2, 70, k)), rs.normal(size=(2, E))
+    dw[:, :3] = 0.0  # nothing comes from these rows, so nothing may go back to them
+    for a in (None, da):
+        got, status = _backward(env, dev, ids, dw, a, E, k, dtype, score="sigmoid", renorm=renorm, scale=8.0)
+        assert status == 0
+        _check_grad(got, x, ids, dw, a, dtype, score="sigmoid", renorm=renorm, scale=8.0)
+        assert a is not None or (got[:, :3] == 0).all()
