@@ -154,20 +154,24 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
         if constexpr (SOFT) {
+          // exp2(x log2 e - round(m log2 e)): one factor, of the product's rounding, is
+          // common to the row, and every use of the exponentials divides it out by z
           float m = LOWEST;  // under every number lies only -inf, whose exponential is 0
 #pragma unroll
           for (int i = 0; i < 8; ++i) m = fmaxf(m, v[s][i]);
           m = part_max<LR>(m);
-          float z = 0.f, e[8];
-          const float mm = m * LOG2E;
+          float z = 0.f, e[8], mm = m * LOG2E;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             e[i] = ex2_approx(fmaf(v[s][i], LOG2E, -mm));
             z += e[i];
           }
           z = part_sum<LR>(z);
-          if (__any_sync(FULL, !(z < 3e38f))) {  // a NaN or +inf among the logits, or nothing but masks
+          // a NaN or +inf among the logits, nothing but masks, or a largest logit so far
+          // from 0 that the factor is no small one (without it z is from 1 to E)
+          if (__any_sync(FULL, !(z < 1e6f && z > 0.01f))) {
             z = 0.f;
+            mm = __uint_as_float(0x7FFFFFFFu);  // tells the chosen ones
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               e[i] = exp_below(live_logit(v[s][i]), m);
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[s][i] = e[i];
-          if (!RENORM && blk == 0) scalar[warp][s * RS + rd] = make_float4(m, rz[s], 0.f, 0.f);
+          if (!RENORM && blk == 0) scalar[warp][s * RS + rd] = make_float4(m, rz[s], 0.f, mm);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[s][i] = a[i] * sigmoid_slope(live_logit(v[s][i]));
@@ -198,12 +202,13 @@ __global__ void __launch_bounds__(SGT_WARPS * 32) score_grad_tile_kernel(const S
     if constexpr (SOFT) {
       const float4 mr = DENSE && !RENORM ? scalar[warp][rc] : make_float4(0.f, 0.f, 0.f, 0.f);
       const float m = RENORM ? fmaxf(part_max<KL>(xj), LOWEST) : mr.x;
-      const float e = xj == m ? 1.f : ex2_approx(LOG2E * (xj - m));
       if constexpr (RENORM) {
+        const float e = xj == m ? 1.f : ex2_approx(LOG2E * (xj - m));
         const float z = part_sum<KL>(e);
         const float q = z > 0.f ? e * rcp_approx(z) : 0.f;
         dj = q * (g - part_sum<KL>(g * q));
       } else {
+        const float e = mr.w == mr.w ? ex2_approx(fmaf(xj, LOG2E, -mr.w)) : exp_below(xj, m);  // as in z
         dj = g * e * mr.y;
         const float dg = part_sum<KL>(dj);
         __syncwarp();

@@ -69,3 +69,18 @@ def test_gradient_of_small_scores(env, E, k, layout, renorm, dtype):
         assert status == 0
         _check_grad(got, x, ids, dw, a, dtype, score="sigmoid", renorm=renorm, scale=8.0)
         assert a is not None or (got[:, :3] == 0).all()
+
+
+# A softmax does not change with a common offset: rows far from 0, or filled with one large number
+@pytest.mark.parametrize("E,k", [(64, 6), (100, 12), (128, 8), (256, 8)])
+@pytest.mark.parametrize("offset", [100.0, -100.0, 1e3, 1e4, 1e5, -1e9, 1e30, -3e38])
+@pytest.mark.parametrize("layout", ["layer", "odd"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_of_large_logits(env, E, k, offset, layout, renorm):
+    torch, _ = env
+    rs = np.random.RandomState(E + 2)
+    dev, x = _device(torch, rs.normal(offset, 2.0, size=(2, 70, E)).astype(np.float32), "f32", layout)
+    ids, dw, da = _ids(rs, 2, 70, E, k), rs.normal(size=(2, 70, k)), rs.normal(size=(2, E))
+    for a in (None, da):
+        got, _ = _backward(env, dev, ids, dw, a, E, k, "f32", score="softmax", renorm=renorm)
+        _check_grad(got, x, ids, dw, a, "f32", score="softmax", renorm=renorm)
