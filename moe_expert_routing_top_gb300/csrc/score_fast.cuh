@@ -659,8 +659,16 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
           for (int jj = 1; jj < OUT; ++jj) mk = fmaxf(mk, xj[jj]);
           mk = row_max<G>(mk);
         }
+        // the form that the row's sum was made with, for either carries the rounding of its
+        // own reference; biases may choose logits so low that only the difference is finite
+        if (p.renorm || careful) {
 #pragma unroll
-        for (int jj = 0; jj < OUT; ++jj) w[jj] = ex2_approx(LOG2E * (xj[jj] - mk));
+          for (int jj = 0; jj < OUT; ++jj) w[jj] = ex2_approx(LOG2E * (xj[jj] - mk));
+        } else {
+          const float mkl = mk * LOG2E;
+#pragma unroll
+          for (int jj = 0; jj < OUT; ++jj) w[jj] = ex2_approx(fmaf(xj[jj], LOG2E, -mkl));
+        }
       } else {
 #pragma unroll
         for (int jj = 0; jj < OUT; ++jj) w[jj] = rcp_approx(1.f + ex2_approx(-LOG2E * xj[jj]));

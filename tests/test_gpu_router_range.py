@@ -84,3 +84,20 @@ def test_gradient_of_large_logits(env, E, k, offset, layout, renorm):
     for a in (None, da):
         got, _ = _backward(env, dev, ids, dw, a, E, k, "f32", score="softmax", renorm=renorm)
         _check_grad(got, x, ids, dw, a, "f32", score="softmax", renorm=renorm)
+
+
+# Weights at throughput sizes: the plain softmax's, whose sum over the row is formed apart from the
+# chosen exponentials, and the others beside them
+@pytest.mark.parametrize("E,k,n", [(64, 6, 1), (128, 8, 1), (256, 8, 8), (128, 12, 1), (160, 6, 8)])
+@pytest.mark.parametrize("offset", [-100.0, 60.0, 100.0])
+@pytest.mark.parametrize("biased", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_weights_of_large_logits(env, E, k, n, offset, biased, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E + 3)
+    dev, x = _device(torch, rs.normal(offset, 2.0, size=(2, 1060, E)).astype(np.float32), dtype)
+    bias = rs.normal(0, 0.05, size=(2, E)) if biased else None
+    for renorm in (True, False):
+        for sums in (True, False):
+            o = dict(score="softmax", renorm=renorm, n_group=n, top_group=max(1, n // 2), best=1)
+            _check_forward(_forward(env, dev, E, k, dtype, bias=bias, sums=sums, **o), x, k, bias=bias, **o)
