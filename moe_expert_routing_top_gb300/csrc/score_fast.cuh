@@ -670,8 +670,10 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
           for (int jj = 0; jj < OUT; ++jj) w[jj] = ex2_approx(fmaf(xj[jj], LOG2E, -mkl));
         }
       } else {
+        // expf: a product with log2 e is rounded, which is 2.6e-6 of the score at -85
+        // (asking for such logits first and using ex2 for the others took prefill's registers: 283 -> 295 us)
 #pragma unroll
-        for (int jj = 0; jj < OUT; ++jj) w[jj] = rcp_approx(1.f + ex2_approx(-LOG2E * xj[jj]));
+        for (int jj = 0; jj < OUT; ++jj) w[jj] = sigmoid(xj[jj]);
       }
       float f = soft ? rz : 1.f;
       if (p.renorm) {
@@ -681,9 +683,9 @@ __global__ void __launch_bounds__(SF_WARPS * 32, score_resident(sizeof(X), KIND,
         z = row_sum<G>(z);
         f = z > 0.f ? rcp_approx(z) : 0.f;
       }
-      f *= p.scale;
+      // the scale last: with 1 / sum of tiny scores it may pass the range
 #pragma unroll
-      for (int jj = 0; jj < OUT; ++jj) w[jj] *= f;
+      for (int jj = 0; jj < OUT; ++jj) w[jj] = w[jj] * f * p.scale;
       if (write) put_weights<OUT>(p.weights + out, own, p.even, w);
     }
     if (write) put_ids<OUT>(p.topk + out, own, p.even, mine);

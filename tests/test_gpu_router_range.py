@@ -101,3 +101,19 @@ def test_weights_of_large_logits(env, E, k, n, offset, biased, dtype):
         for sums in (True, False):
             o = dict(score="softmax", renorm=renorm, n_group=n, top_group=max(1, n // 2), best=1)
             _check_forward(_forward(env, dev, E, k, dtype, bias=bias, sums=sums, **o), x, k, bias=bias, **o)
+
+
+# Renormalised weights of scores near the smallest normal number and under it: a large scale must
+# not meet 1 / sum first
+@pytest.mark.parametrize("E,k", [(64, 6), (128, 8), (256, 8), (128, 12), (256, 20)])
+@pytest.mark.parametrize("T", [70, 1060])
+@pytest.mark.parametrize("biased", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_weights_of_small_scores(env, E, k, T, biased, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E + 1)
+    dev, x = _device(torch, _small(rs, 2, T, E), dtype)
+    bias = rs.normal(0, 0.3, size=(2, E)) if biased else None
+    for renorm in (True, False):
+        o = dict(score="sigmoid", renorm=renorm, scale=1000.0)
+        _check_forward(_forward(env, dev, E, k, dtype, bias=bias, **o), x, k, bias=bias, **o)
