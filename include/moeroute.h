@@ -466,7 +466,8 @@ typedef struct moer_score_opts {
  * weights   [L][T][k] fp32 out or NULL.
  * score_sum [L][E] fp32 out or NULL: sum over t of s_e (a balance loss's
  *           mean score, times T).  Overwritten; summed in a fixed order.
- * ws        at least moer_score_workspace_bytes(d, T) bytes, 16-byte aligned.
+ * ws        at least moer_score_workspace_bytes(d, T) bytes (which do not fall
+ *           as T grows), 16-byte aligned.
  * T = 0 writes nothing but a zero score_sum. */
 MOER_API size_t moer_score_workspace_bytes(const moer_dims* d, int64_t T);
 MOER_API moer_status moer_score_topk(const moer_dims* d, const moer_score_opts* o, const void* logits, int64_t T,

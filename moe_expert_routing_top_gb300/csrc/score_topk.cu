@@ -294,9 +294,12 @@ cudaError_t score_run(const ScoreParams& p, cudaStream_t st) {
 }
 }  // namespace
 
-// The general kernel's units are the more numerous.
+// The general kernel's units are the more numerous.  Their number falls where the span steps;
+// the size is a bound of it that grows with T (a span is SC_WARPS and T L / SC_UNITS
+// tokens at least), so that a workspace for a batch serves every smaller one.
 size_t score_scratch_bytes(const moer_dims* d, int64_t T) {
-  return (size_t)d->L * (size_t)score_nspan(T, score_span(T, d->L, SC_WARPS)) * (size_t)d->E * 4;
+  const int64_t units = min64((T + SC_WARPS - 1) / SC_WARPS, (SC_UNITS + d->L - 1) / d->L);
+  return (size_t)d->L * (size_t)units * (size_t)d->E * 4;
 }
 
 moer_status score_topk_launch(ScoreParams p, int dtype, float* score_sum, void* ws, cudaStream_t st) {
