@@ -49,9 +49,9 @@ int score_nspan(int64_t T, int span) { return (int)((T + span - 1) / span); }
 int fast_span(int64_t T, int L, int step, int64_t slots) {
   const int most = score_nspan(T, score_span(T, L, SC_WARPS));
   int64_t best = -1, cost = 0;
-  for (int64_t rounds = 1; rounds <= 64 || best < 0; ++rounds) {
+  const int64_t each = (int64_t)most * step;  // tokens of a round of all units: with fewer rounds there are too many
+  for (int64_t rounds = (T + each - 1) / each; rounds <= 64 || best < 0; ++rounds) {
     const int64_t units = (T + rounds * step - 1) / (rounds * step);
-    if (units > most) continue;
     const int64_t c = (units * L + slots - 1) / slots * (rounds + 1);
     if (best < 0 || c < cost) best = rounds, cost = c;
     if (units == 1) break;
