@@ -184,9 +184,34 @@ class RoutingStats:
         """The weights of the last batch of T tokens, as [L][T][k]."""
         return self.weights[:self.L * T * self.k].view(self.L, T, self.k)
 
+    def _here(self, x) -> bool:
+        return x.device.type == self.device.type and (self.device.index is None or x.device.index == self.device.index)
+
+    def _check_logits(self, logits, what="logits"):
+        """The library takes addresses: a tensor of another type, shape or layout than the gate's
+        would be read, or written, past its end."""
+        if self.score_opts is None:
+            raise ValueError("no scored gate: call set_gate first")
+        dtype = {0: torch.float32, 1: torch.bfloat16, 2: torch.float16}.get(self.score_opts.dtype)
+        if logits.dtype != dtype:
+            raise ValueError(f"{what} are {logits.dtype}, the gate's options say {dtype}")
+        if logits.dim() != 3 or logits.shape[0] != self.L or logits.shape[2] != self.E:
+            raise ValueError(f"{what} have shape {tuple(logits.shape)}, expected ({self.L}, T, {self.E})")
+        if logits.stride(2) != 1:
+            raise ValueError(f"{what}: the logits of a row have to be contiguous")
+        if not self._here(logits):
+            raise ValueError(f"{what} are on {logits.device}, expected {self.device}")
+
+    def _check_f32(self, x, shape, what):
+        if x.dtype != torch.float32 or tuple(x.shape) != shape or not x.is_contiguous() or not self._here(x):
+            raise ValueError(f"{what} has to be contiguous fp32 {shape} on {self.device}")
+
     def score_topk(self, logits, score_sum=None):
-        """Top-k ids and weights of the scored gate; logits [L][T][E] with any strides between
-        rows; score_sum [L][E] fp32, if given, receives the scores' sums."""
+        """Top-k ids and weights of the scored gate; logits [L][T][E] of the gate's type with any
+        strides between rows; score_sum [L][E] fp32, if given, receives the scores' sums."""
+        self._check_logits(logits)
+        if score_sum is not None:
+            self._check_f32(score_sum, (self.L, self.E), "score_sum")
         T = logits.shape[1]
         nat.moer_score_topk(self.dims, self.score_opts, logits, T, logits.stride(1), logits.stride(0), self.bias,
                             self.topk, self.weights, score_sum, self.ws, self.ws_bytes, self.stream)
@@ -194,8 +219,13 @@ class RoutingStats:
     def score_grad(self, logits, d_weights, d_score_sum=None, out=None) -> torch.Tensor:
         """The logits' gradient from that of the weights ([L][T][k] fp32) and, if given, of the
         score sums ([L][E]), for the ids of the last score_topk call on these logits."""
+        self._check_logits(logits)
         T = logits.shape[1]
-        out = torch.empty_like(logits) if out is None else out
+        if out is None:
+            out = torch.empty_like(logits)
+        self._check_logits(out, "out's entries")
+        if out.shape != logits.shape:
+            raise ValueError("out has to have the logits' shape")
         nat.moer_score_topk_grad(self.dims, self.score_opts, logits, T, logits.stride(1), logits.stride(0), self.topk,
                                  d_weights, d_score_sum, out, out.stride(1), out.stride(0), self.ws, self.ws_bytes,
                                  self.stream)

@@ -1,0 +1,76 @@
+"""What RoutingStats' scored calls hand to the library, and what they refuse, on the CPU: the
+library's calls are replaced by a recorder, so nothing is launched."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+nat = pytest.importorskip("moe_expert_routing_top_gb300._native")
+from moe_expert_routing_top_gb300 import pipeline  # noqa: E402
+
+L, E, k, B = 2, 64, 6, 16
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    seen = []
+    for name in ("moer_score_topk", "moer_score_topk_grad", "moer_expert_order", "moer_ids_signature", "moer_block_stitch",
+                 "moer_affinity_load", "moer_route"):
+        monkeypatch.setattr(nat, name, lambda *a, _n=name: seen.append((_n, a)))
+    return seen
+
+
+def _stats(max_T=0, gate=True, **opts):
+    rs = pipeline.RoutingStats(E, k, L, [0], B, D=1, tau=0.1, centroids=np.zeros((1, E)), idf=np.ones((1, E)), loads=[0], live=False,
+                               G=1, group_of=np.zeros((L, E)), max_T=max_T, max_nblk=max_T, max_R=4, device="cpu", stream=0)
+    if gate:
+        rs.set_gate(nat.make_score_opts(**opts))
+    return rs
+
+
+def _ids(T):
+    return torch.zeros((L, T, k), dtype=torch.uint8)
+
+
+BAD_LOGITS = [("f32", torch.zeros((L, 8, E), dtype=torch.bfloat16)), ("bf16", torch.zeros((L, 8, E))), ("f16", torch.zeros((L, 8, E), dtype=torch.bfloat16)),
+              ("f32", torch.zeros((L, 8, E), dtype=torch.float64)), ("f32", torch.zeros((8, E))), ("f32", torch.zeros((L + 1, 8, E))),
+              ("f32", torch.zeros((L - 1, 8, E))), ("f32", torch.zeros((L, 8, E - 4))), ("f32", torch.zeros((L, E, 8)).transpose(1, 2)),
+              ("f32", torch.zeros((L, 8, 2 * E))[:, :, ::2]), ("f32", torch.zeros((L, 8, E), device="meta"))]
+
+
+@pytest.mark.parametrize("dtype,logits", BAD_LOGITS)
+def test_logits_that_do_not_fit_the_gate(calls, dtype, logits):
+    rs = _stats(8, dtype=dtype)
+    with pytest.raises(ValueError):
+        rs.score_topk(logits)
+    with pytest.raises(ValueError):
+        rs.score_grad(logits, torch.zeros((L, 8, k)))
+    assert not calls
+
+
+@pytest.mark.parametrize("dtype,of", [("f32", torch.float32), ("bf16", torch.bfloat16), ("f16", torch.float16)])
+def test_logits_that_fit(calls, dtype, of):
+    rs = _stats(8, dtype=dtype)
+    for x in (torch.zeros((L, 8, E), dtype=of), torch.zeros((8, L, E), dtype=of).permute(1, 0, 2), torch.zeros((L, 8, E + 8), dtype=of)[:, :, 4:E + 4]):
+        rs.score_topk(x)
+        name, a = calls.pop()
+        assert name == "moer_score_topk" and a[2] is x and a[3:6] == (8, x.stride(1), x.stride(0))
+
+
+def test_no_gate(calls):
+    with pytest.raises(ValueError):
+        _stats(8, gate=False).score_topk(torch.zeros((L, 8, E)))
+    assert not calls
+
+
+@pytest.mark.parametrize("sums", [torch.zeros((L, E), dtype=torch.float64), torch.zeros((L, E + 4)), torch.zeros((E, L)).t(), torch.zeros(E)])
+def test_score_sums_that_do_not_fit(calls, sums):
+    with pytest.raises(ValueError):
+        _stats(8).score_topk(torch.zeros((L, 8, E)), sums)
+    assert not calls
+
+
+@pytest.mark.parametrize("out", [torch.zeros((L, 8, E), dtype=torch.bfloat16), torch.zeros((L, 7, E)), torch.zeros((L, E, 8)).transpose(1, 2)])
+def test_gradient_buffers_that_do_not_fit(calls, out):
+    with pytest.raises(ValueError):
+        _stats(8).score_grad(torch.zeros((L, 8, E)), torch.zeros((L, 8, k)), out=out)
+    assert not calls
