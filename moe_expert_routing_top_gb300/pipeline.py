@@ -146,6 +146,7 @@ class RoutingStats:
     def _alloc(self, T, nblk, R):
         dev, E, k, L, m, D = self.device, self.E, self.k, self.L, self.m, self.D
         self.cap = (T, nblk, R)
+        self.ids_T = None  # tokens of the batch whose ids self.topk holds
         self.topk = torch.empty(L * max(T, 1) * k, dtype=torch.uint8, device=dev)
         self.blk_cnt = torch.empty((max(nblk, 1), m, E), dtype=torch.uint8, device=dev)
         self.req_cnt = torch.empty((max(R, 1), m, E), dtype=torch.int32, device=dev)
@@ -213,6 +214,8 @@ class RoutingStats:
         if score_sum is not None:
             self._check_f32(score_sum, (self.L, self.E), "score_sum")
         T = logits.shape[1]
+        self.ensure(T, *self.cap[1:])
+        self.ids_T = T
         nat.moer_score_topk(self.dims, self.score_opts, logits, T, logits.stride(1), logits.stride(0), self.bias,
                             self.topk, self.weights, score_sum, self.ws, self.ws_bytes, self.stream)
 
@@ -221,6 +224,8 @@ class RoutingStats:
         score sums ([L][E]), for the ids of the last score_topk call on these logits."""
         self._check_logits(logits)
         T = logits.shape[1]
+        if T != self.ids_T:
+            raise ValueError(f"logits of {T} tokens, but the ids held are of {self.ids_T}")
         if out is None:
             out = torch.empty_like(logits)
         self._check_logits(out, "out's entries")
@@ -234,6 +239,8 @@ class RoutingStats:
     def expert_order(self, T: int, align: int = 1):
         """The experts' token lists of the last batch: offsets [L][E+1], pairs in expert order
         [L][rows] (segments padded to `align`) and each pair's row [L][T][k]."""
+        if T > self.cap[0]:
+            raise ValueError(f"{T} tokens, but the ids' buffer holds {self.cap[0]}")
         n = T * self.k
         ld = n + min(self.E, n) * (align - 1)
         i32, dev = torch.int32, self.device
@@ -246,9 +253,13 @@ class RoutingStats:
     def score_step(self, logits, bd: BatchDev, align=1, score_sum=None, write_sig=True):
         """All rows of the path over one batch through the scored gate, and the experts' token
         lists (returned).  Co-activation and loads need E <= 128 and k in {6, 8}
-        (moer_ids_signature's limit) and are left as they are otherwise."""
+        (moer_ids_signature's limit) and are left as they are otherwise.  Logits padded past
+        the batch's tokens are taken up to them."""
+        self._check_logits(logits)
+        if logits.shape[1] < bd.T:
+            raise ValueError(f"logits of {logits.shape[1]} tokens, but the batch has {bd.T}")
         self.ensure(bd.T, bd.nblk, bd.R)
-        self.score_topk(logits, score_sum)
+        self.score_topk(logits[:, :bd.T], score_sum)
         counted = self.E <= 128 and self.k in (6, 8)
         self.ids_signature(bd, blk_counts=True, affinity=counted)
         self.block_stitch(bd)
@@ -264,6 +275,8 @@ class RoutingStats:
     def topk_signature(self, logits, bd: BatchDev, write_topk=True, blk_counts=True):
         """Top-k ids and co-activation, plus the block counts unless ``blk_counts`` is False
         (then ``ids_signature`` can produce them from the ids)."""
+        if write_topk:
+            self.ids_T = bd.T
         nat.moer_topk_signature(self.dims, logits, bd.T, bd.blk_tab, bd.nblk,
                                 self.topk if write_topk else None,
                                 self.blk_cnt if blk_counts else None, self.affinity,
@@ -273,6 +286,7 @@ class RoutingStats:
         """hidden bf16 [T][H] x w_gate bf16 [L][H][E] -> top-k and, unless ``counts`` is False,
         block counts and co-activation (else ``ids_signature`` produces them from the ids)."""
         H = hidden.shape[-1]
+        self.ids_T = bd.T
         nat.moer_gate_topk(self.dims, hidden, bd.T, H, w_gate, bd.blk_tab, bd.nblk, logits,
                            self.topk, self.blk_cnt if counts else None,
                            self.affinity if counts else None, self.ws, self.ws_bytes,

@@ -41,3 +41,35 @@ def test_smaller_batches_after_a_large_one(env, L, E, k, most, then):
         assert rs.status() == 0
         p = torch.softmax(x.double(), -1).sum(1)
         assert ((sums - p).abs() <= 6e-6 * p).all()
+
+
+def test_batches_larger_than_the_buffers(env):
+    torch, nat, pipeline = env
+    L, E, k = 3, 64, 6
+    rs = _stats(pipeline, nat, L, E, k, max_T=10, renorm=False)
+    for T in (10, 3000, 41):
+        x = torch.randn((L, T, E), device="cuda")
+        rs.score_topk(x)
+        _check(rs, x.double().cpu().numpy(), T, k, renorm=False)
+        off, order, inv = rs.expert_order(T)
+        assert (order.sort(1).values.cpu() == torch.arange(T * k, dtype=torch.int32)).all()
+        dw = torch.randn((L, T, k), device="cuda")
+        dx = rs.score_grad(x, dw)
+        g, mag = router.score_topk_grad(x.double().cpu().numpy(), rs.topk_for(T).cpu().numpy(), dw.cpu().numpy(), renorm=False)
+        assert (np.abs(dx.cpu().numpy() - g) <= 1e-5 * mag + 1e-37).all()
+    assert rs.status() == 0
+
+
+def test_step_of_padded_logits(env):
+    torch, nat, pipeline = env
+    L, E, k = 2, 128, 8
+    new = np.array([30, 17, 40])
+    bd = pipeline.BatchDev.from_lengths(new, np.zeros(3, int), 16)
+    x = torch.randn((L, 128, E), device="cuda")
+    a, b = (_stats(pipeline, nat, L, E, k) for _ in range(2))
+    off, order, inv = a.score_step(x, bd)
+    off2, order2, inv2 = b.score_step(x[:, :bd.T].contiguous(), bd)
+    assert a.status() == 0 and b.status() == 0
+    assert torch.equal(a.topk_for(bd.T), b.topk_for(bd.T)) and torch.equal(a.affinity, b.affinity)
+    assert torch.equal(order, order2) and torch.equal(inv, inv2) and torch.equal(off, off2)
+    assert torch.equal(a.req_cnt[:3], b.req_cnt[:3])

@@ -74,3 +74,49 @@ def test_gradient_buffers_that_do_not_fit(calls, out):
     with pytest.raises(ValueError):
         _stats(8).score_grad(torch.zeros((L, 8, E)), torch.zeros((L, 8, k)), out=out)
     assert not calls
+
+
+def _batch(T):
+    z = torch.zeros(T + 1, dtype=torch.int32)
+    return pipeline.BatchDev(T=T, R=1, nblk=1, blk_tab=z, req_blk_off=z, cache_idx=None, req_cache_off=None, insert_slot=None)
+
+
+def test_buffers_grow_with_the_logits(calls):
+    """A batch larger than what the buffers were made for, given to score_topk itself."""
+    rs = _stats(8)
+    rs.score_topk(torch.zeros((L, 100, E)))
+    name, a = calls.pop()
+    ids, w, ws, n = a[7], a[8], a[10], a[11]
+    assert ids.numel() >= L * 100 * k and w.numel() >= L * 100 * k and n >= nat.moer_score_workspace_bytes(rs.dims, 100) and ws.numel() >= n
+    rs.expert_order(100)
+    assert calls.pop()[1][-1 - 1] >= nat.moer_expert_order_workspace_bytes(rs.dims, 100)
+
+
+def test_step_takes_the_batchs_tokens_of_padded_logits(calls):
+    rs = _stats(8)
+    x = torch.zeros((L, 128, E))
+    rs.score_step(x, _batch(100))
+    a = dict(calls)["moer_score_topk"]
+    assert a[2].data_ptr() == x.data_ptr() and a[3:6] == (100, E, 128 * E)
+    assert dict(calls)["moer_ids_signature"][2] == 100 and dict(calls)["moer_expert_order"][2] == 100
+    calls.clear()
+    with pytest.raises(ValueError):
+        rs.score_step(torch.zeros((L, 99, E)), _batch(100))
+    assert not calls
+
+
+def test_lists_and_gradient_of_the_last_batch_only(calls):
+    rs = _stats(8)
+    rs.score_topk(torch.zeros((L, 8, E)))
+    calls.clear()
+    with pytest.raises(ValueError):
+        rs.expert_order(9)      # more ids than there are
+    for T in (9, 7):            # another batch's layout
+        with pytest.raises(ValueError):
+            rs.score_grad(torch.zeros((L, T, E)), torch.zeros((L, T, k)))
+    rs.score_grad(torch.zeros((L, 8, E)), torch.zeros((L, 8, k)))
+    assert calls.pop()[0] == "moer_score_topk_grad"
+    rs.ensure(16, 1, 1)         # the ids went with the smaller buffer
+    with pytest.raises(ValueError):
+        rs.score_grad(torch.zeros((L, 8, E)), torch.zeros((L, 8, k)))
+    assert not calls
