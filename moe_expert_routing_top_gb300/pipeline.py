@@ -207,6 +207,12 @@ class RoutingStats:
         if x.dtype != torch.float32 or tuple(x.shape) != shape or not x.is_contiguous() or not self._here(x):
             raise ValueError(f"{what} has to be contiguous fp32 {shape} on {self.device}")
 
+    def _as_f32(self, x, shape, what):
+        """x as contiguous fp32, itself where it is that already."""
+        if not x.is_floating_point() or tuple(x.shape) != shape or not self._here(x):
+            raise ValueError(f"{what} has to be a floating tensor of shape {shape} on {self.device}")
+        return x if x.dtype == torch.float32 and x.is_contiguous() else x.to(torch.float32).contiguous()
+
     def score_topk(self, logits, score_sum=None):
         """Top-k ids and weights of the scored gate; logits [L][T][E] of the gate's type with any
         strides between rows; score_sum [L][E] fp32, if given, receives the scores' sums."""
@@ -220,12 +226,16 @@ class RoutingStats:
                             self.topk, self.weights, score_sum, self.ws, self.ws_bytes, self.stream)
 
     def score_grad(self, logits, d_weights, d_score_sum=None, out=None) -> torch.Tensor:
-        """The logits' gradient from that of the weights ([L][T][k] fp32) and, if given, of the
-        score sums ([L][E]), for the ids of the last score_topk call on these logits."""
+        """The logits' gradient from that of the weights ([L][T][k]) and, if given, of the
+        score sums ([L][E]), for the ids of the last score_topk call on these logits.  Gradients
+        that are not contiguous fp32 are copied to it."""
         self._check_logits(logits)
         T = logits.shape[1]
         if T != self.ids_T:
             raise ValueError(f"logits of {T} tokens, but the ids held are of {self.ids_T}")
+        d_weights = self._as_f32(d_weights, (self.L, T, self.k), "d_weights")
+        if d_score_sum is not None:
+            d_score_sum = self._as_f32(d_score_sum, (self.L, self.E), "d_score_sum")
         if out is None:
             out = torch.empty_like(logits)
         self._check_logits(out, "out's entries")

@@ -73,3 +73,16 @@ def test_step_of_padded_logits(env):
     assert torch.equal(a.topk_for(bd.T), b.topk_for(bd.T)) and torch.equal(a.affinity, b.affinity)
     assert torch.equal(order, order2) and torch.equal(inv, inv2) and torch.equal(off, off2)
     assert torch.equal(a.req_cnt[:3], b.req_cnt[:3])
+
+
+def test_gradient_of_a_sum_and_of_other_layouts(env):
+    torch, nat, pipeline = env
+    L, T, E, k = 2, 70, 64, 6
+    rs = _stats(pipeline, nat, L, E, k)
+    x = torch.randn((L, T, E), device="cuda")
+    rs.score_topk(x)
+    for dw in (torch.ones((), device="cuda").expand(L, T, k), torch.randn((T, L, k), device="cuda").transpose(0, 1),
+               torch.randn((L, T, k), device="cuda").to(torch.bfloat16)):
+        dx = rs.score_grad(x, dw)
+        g, mag = router.score_topk_grad(x.double().cpu().numpy(), rs.topk_for(T).cpu().numpy(), dw.float().cpu().numpy())
+        assert (np.abs(dx.cpu().numpy() - g) <= 1e-5 * mag + 1e-37).all()

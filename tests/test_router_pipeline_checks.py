@@ -120,3 +120,38 @@ def test_lists_and_gradient_of_the_last_batch_only(calls):
     with pytest.raises(ValueError):
         rs.score_grad(torch.zeros((L, 8, E)), torch.zeros((L, 8, k)))
     assert not calls
+
+
+GRADS = [torch.ones(()).expand(L, 8, k), torch.randn((8, L, k)).transpose(0, 1), torch.randn((L, 8, k)).to(torch.bfloat16),
+         torch.randn((L, 8, k), dtype=torch.float64), torch.randn((L, 8, 2 * k))[..., ::2]]
+
+
+@pytest.mark.parametrize("dw", GRADS)
+def test_gradients_of_any_layout_are_laid_out(calls, dw):
+    """An expanded gradient (of a sum), a transposed one, another type: the library reads fp32 rows."""
+    rs = _stats(8)
+    rs.score_topk(torch.zeros((L, 8, E)))
+    rs.score_grad(torch.zeros((L, 8, E)), dw, torch.ones(()).expand(L, E))
+    a = calls.pop()[1]
+    assert a[7].dtype == torch.float32 and a[7].is_contiguous() and torch.equal(a[7], dw.float())
+    assert a[8].dtype == torch.float32 and a[8].is_contiguous() and torch.equal(a[8], torch.ones((L, E)))
+
+
+def test_gradients_that_fit_are_not_copied(calls):
+    rs = _stats(8)
+    rs.score_topk(torch.zeros((L, 8, E)))
+    dw, da = torch.zeros((L, 8, k)), torch.zeros((L, E))
+    rs.score_grad(torch.zeros((L, 8, E)), dw, da)
+    assert calls[-1][1][7] is dw and calls[-1][1][8] is da
+
+
+@pytest.mark.parametrize("dw,da", [(torch.zeros((L, 7, k)), None), (torch.zeros((L, 8, k + 1)), None), (torch.zeros((L, 8, k)), torch.zeros(E)),
+                                   (torch.zeros((L, 8, k)), torch.zeros((L, E + 4))), (torch.zeros((L, 8, k), dtype=torch.int32), None),
+                                   (torch.zeros((L, 8, k), device="meta"), None)])
+def test_gradients_of_other_shapes(calls, dw, da):
+    rs = _stats(8)
+    rs.score_topk(torch.zeros((L, 8, E)))
+    calls.clear()
+    with pytest.raises(ValueError):
+        rs.score_grad(torch.zeros((L, 8, E)), dw, da)
+    assert not calls
