@@ -225,14 +225,20 @@ class RoutingStats:
         nat.moer_score_topk(self.dims, self.score_opts, logits, T, logits.stride(1), logits.stride(0), self.bias,
                             self.topk, self.weights, score_sum, self.ws, self.ws_bytes, self.stream)
 
-    def score_grad(self, logits, d_weights, d_score_sum=None, out=None) -> torch.Tensor:
+    def score_grad(self, logits, d_weights, d_score_sum=None, out=None, topk=None) -> torch.Tensor:
         """The logits' gradient from that of the weights ([L][T][k]) and, if given, of the
-        score sums ([L][E]), for the ids of the last score_topk call on these logits.  Gradients
+        score sums ([L][E]), for the ids `topk` ([L][T][k] uint8) that the weights belong to.
+        Without `topk` they are those of the last score_topk call: with several batches under
+        way, keep a copy of each one's ids (topk_for(T).clone()) and give it here.  Gradients
         that are not contiguous fp32 are copied to it."""
         self._check_logits(logits)
         T = logits.shape[1]
-        if T != self.ids_T:
-            raise ValueError(f"logits of {T} tokens, but the ids held are of {self.ids_T}")
+        if topk is None:
+            if T != self.ids_T:
+                raise ValueError(f"logits of {T} tokens, but the ids held are of {self.ids_T}")
+            topk = self.topk
+        elif topk.dtype != torch.uint8 or tuple(topk.shape) != (self.L, T, self.k) or not topk.is_contiguous() or not self._here(topk):
+            raise ValueError(f"topk has to be contiguous uint8 {(self.L, T, self.k)} on {self.device}")
         d_weights = self._as_f32(d_weights, (self.L, T, self.k), "d_weights")
         if d_score_sum is not None:
             d_score_sum = self._as_f32(d_score_sum, (self.L, self.E), "d_score_sum")
@@ -241,7 +247,7 @@ class RoutingStats:
         self._check_logits(out, "out's entries")
         if out.shape != logits.shape:
             raise ValueError("out has to have the logits' shape")
-        nat.moer_score_topk_grad(self.dims, self.score_opts, logits, T, logits.stride(1), logits.stride(0), self.topk,
+        nat.moer_score_topk_grad(self.dims, self.score_opts, logits, T, logits.stride(1), logits.stride(0), topk,
                                  d_weights, d_score_sum, out, out.stride(1), out.stride(0), self.ws, self.ws_bytes,
                                  self.stream)
         return out

@@ -86,3 +86,19 @@ def test_gradient_of_a_sum_and_of_other_layouts(env):
         dx = rs.score_grad(x, dw)
         g, mag = router.score_topk_grad(x.double().cpu().numpy(), rs.topk_for(T).cpu().numpy(), dw.float().cpu().numpy())
         assert (np.abs(dx.cpu().numpy() - g) <= 1e-5 * mag + 1e-37).all()
+
+
+def test_gradients_of_two_batches_under_way(env):
+    torch, nat, pipeline = env
+    L, T, E, k = 2, 70, 64, 6
+    rs = _stats(pipeline, nat, L, E, k)
+    x = [torch.randn((L, T, E), device="cuda") for _ in range(2)]
+    ids = []
+    for b in range(2):
+        rs.score_topk(x[b])
+        ids.append(rs.topk_for(T).clone())
+    dw = torch.randn((L, T, k), device="cuda")
+    for b in range(2):
+        dx = rs.score_grad(x[b], dw, topk=ids[b])
+        g, mag = router.score_topk_grad(x[b].double().cpu().numpy(), ids[b].cpu().numpy(), dw.cpu().numpy())
+        assert (np.abs(dx.cpu().numpy() - g) <= 1e-5 * mag + 1e-37).all()

@@ -155,3 +155,19 @@ def test_gradients_of_other_shapes(calls, dw, da):
     with pytest.raises(ValueError):
         rs.score_grad(torch.zeros((L, 8, E)), dw, da)
     assert not calls
+
+
+def test_gradient_of_an_earlier_batch_by_its_ids(calls):
+    rs = _stats(64)
+    rs.score_topk(torch.zeros((L, 8, E)))
+    ids = torch.arange(L * 8 * k, dtype=torch.uint8).view(L, 8, k)
+    rs.score_topk(torch.zeros((L, 33, E)))
+    rs.score_grad(torch.zeros((L, 8, E)), torch.zeros((L, 8, k)), topk=ids)
+    assert calls[-1][1][6] is ids
+    with pytest.raises(ValueError):
+        rs.score_grad(torch.zeros((L, 8, E)), torch.zeros((L, 8, k)))
+    calls.clear()
+    for bad in (ids[:, :7], ids.long(), ids.expand(L, 8, k).transpose(0, 1), torch.zeros((L, 8, 2 * k), dtype=torch.uint8)[..., ::2], ids.to("meta")):
+        with pytest.raises(ValueError):
+            rs.score_grad(torch.zeros((L, 8, E)), torch.zeros((L, 8, k)), topk=bad)
+    assert not calls
