@@ -62,12 +62,28 @@ class BatchDev:
         """A batch's tables made on the GPU from the requests' lengths (host arrays: tokens to
         compute, tokens held in the KV cache).  `pages` [R][width] int32 (device) is the KV
         cache's block table, with the held tokens' pages in it; the pages newly needed come
-        from `free_pages` (device) in request order and are written into it.  Without `pages`
-        the batch has no slots and no signature cache."""
-        new = np.ascontiguousarray(new_len, dtype=np.int32)
-        ctx = np.ascontiguousarray(ctx_len, dtype=np.int32)
-        B, R = int(block), len(new)
-        n, c = new.astype(np.int64), ctx.astype(np.int64)
+        from `free_pages` [n] int32 (device) in request order and are written into it.  A table
+        that is a slice of a wider one is copied and written back.  Without `pages` the batch
+        has no slots and no signature cache."""
+        n, c = np.asarray(new_len), np.asarray(ctx_len)
+        if n.ndim != 1 or n.shape != c.shape:
+            raise ValueError(f"lengths of shapes {n.shape} and {c.shape}: expected one of each per request")
+        n, c = n.astype(np.int64), c.astype(np.int64)
+        if max(n.max(initial=0), c.max(initial=0)) >= 1 << 31 or min(n.min(initial=0), c.min(initial=0)) < -(1 << 31):
+            raise ValueError("a length does not fit 32 bits")
+        new, ctx, B, R = n.astype(np.int32), c.astype(np.int32), int(block), len(n)
+        where = torch.device(device).type
+        if pages is None and free_pages is not None:
+            raise ValueError("free pages without a block table")
+        if pages is not None and (pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] < R or pages.device.type != where):
+            raise ValueError(f"pages has to be int32 [{R} requests or more][width] on {device}")
+        if free_pages is not None and (free_pages.dtype != torch.int32 or free_pages.dim() != 1 or free_pages.device.type != where):
+            raise ValueError(f"free_pages has to be int32 [n] on {device}")
+        table = pages
+        if pages is not None:
+            pages = pages.contiguous()
+        if free_pages is not None:
+            free_pages = free_pages.contiguous()
         T, nblk = int(n.sum()), int(np.where(n > 0, -(-(c % B + n) // B), 0).sum())
         ncached = int((c // B).sum()) if pages is not None else 0
         i32 = torch.int32
@@ -87,6 +103,8 @@ class BatchDev:
         ws = torch.zeros(wsb, dtype=torch.uint8, device=device)
         nat.moer_block_plan(args, ws, wsb, stream)
         code = nat.moer_ws_status(ws, stream)
+        if pages is not table:
+            table.copy_(pages)
         if code != 0:
             raise nat.MoerError("moer_block_plan", code, nat.moer_status_str(code))
         return BatchDev(T=T, R=R, nblk=nblk, blk_tab=b["blk_tab"], req_blk_off=b["req_blk_off"],

@@ -102,3 +102,31 @@ def test_gradients_of_two_batches_under_way(env):
         dx = rs.score_grad(x[b], dw, topk=ids[b])
         g, mag = router.score_topk_grad(x[b].double().cpu().numpy(), ids[b].cpu().numpy(), dw.cpu().numpy())
         assert (np.abs(dx.cpu().numpy() - g) <= 1e-5 * mag + 1e-37).all()
+
+
+def _lengths(rs, R, B, most_new, most_ctx):
+    new, ctx = rs.randint(0, most_new, size=R), rs.randint(0, most_ctx, size=R)
+    have, total = -(-ctx // B), -(-(ctx + new) // B)
+    pool = rs.permutation(int(total.sum()) + 5).astype(np.int32)
+    pages, at = np.full((R, int(total.max()) + 1), -1, dtype=np.int32), 0
+    for r in range(R):
+        pages[r, :have[r]] = pool[at:at + have[r]]
+        at += have[r]
+    return new, ctx, pages, pool[at:]
+
+
+@pytest.mark.parametrize("R", [9, 3000])
+@pytest.mark.parametrize("slice_", ["columns", "transposed"])
+def test_block_table_that_is_a_slice(env, R, slice_):
+    torch, nat, pipeline = env
+    new, ctx, pages, free = _lengths(np.random.RandomState(R), R, 16, 60, 100)
+    W = pages.shape[1]
+    wide = torch.full((R, W + 9), 12345, dtype=torch.int32, device="cuda") if slice_ == "columns" else torch.full((W + 9, R), 12345, dtype=torch.int32, device="cuda")
+    t = wide[:, 4:4 + W] if slice_ == "columns" else wide[4:4 + W].t()
+    t.copy_(torch.from_numpy(pages).cuda())
+    bd = pipeline.BatchDev.from_lengths(new, ctx, 16, t, torch.from_numpy(free).cuda())
+    ref = router.block_plan(new, ctx, 16, pages, free)
+    assert np.array_equal(t.cpu().numpy(), pages) and np.array_equal(bd.slot_map.cpu().numpy(), ref["slot_map"])
+    assert np.array_equal(bd.cache_idx.cpu().numpy()[:bd.ncached], ref["cache_idx"]) and np.array_equal(bd.insert_slot.cpu().numpy(), ref["insert_slot"])
+    t.fill_(12345)
+    assert (wide == 12345).all()
