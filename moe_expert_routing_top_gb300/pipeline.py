@@ -40,6 +40,13 @@ import torch
 from . import _native as nat
 
 
+def _as_stream(stream, device):
+    """A torch stream of a torch stream or a handle."""
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+
+
 @dataclasses.dataclass
 class BatchDev:
     """Device copies of one batch's metadata (see gen.workloads.Batch)."""
@@ -62,7 +69,8 @@ class BatchDev:
         """A batch's tables made on the GPU from the requests' lengths (host arrays: tokens to
         compute, tokens held in the KV cache).  `pages` [R][width] int32 (device) is the KV
         cache's block table, with the held tokens' pages in it; the pages newly needed come
-        from `free_pages` [n] int32 (device) in request order and are written into it.  A table
+        from `free_pages` [n] int32 (device) in request order and are written into it.  The call
+        runs on `stream`, after what the current stream has under way, and waits for it.  A table
         that is a slice of a wider one is copied and written back.  Without `pages` the batch
         has no slots and no signature cache."""
         n, c = np.asarray(new_len), np.asarray(ctx_len)
@@ -101,6 +109,10 @@ class BatchDev:
                                    n_free=0 if free_pages is None else free_pages.numel(), **b)
         wsb = nat.moer_block_plan_workspace_bytes(R)
         ws = torch.zeros(wsb, dtype=torch.uint8, device=device)
+        if stream is not None and where == "cuda":
+            # the launch comes after the workspace's zeroing, the copies and the table's producer,
+            # which are on the current stream; what is made there is safe to use after the wait below
+            _as_stream(stream, ws.device).wait_stream(torch.cuda.current_stream(ws.device))
         nat.moer_block_plan(args, ws, wsb, stream)
         code = nat.moer_ws_status(ws, stream)
         if pages is not table:

@@ -130,3 +130,28 @@ def test_block_table_that_is_a_slice(env, R, slice_):
     assert np.array_equal(bd.cache_idx.cpu().numpy()[:bd.ncached], ref["cache_idx"]) and np.array_equal(bd.insert_slot.cpu().numpy(), ref["insert_slot"])
     t.fill_(12345)
     assert (wide == 12345).all()
+
+
+def _busy(torch):
+    """Some milliseconds of work on the current stream."""
+    a = torch.randn((4096, 4096), device="cuda")
+    for _ in range(40):
+        a = (a @ a).mul_(1e-2)
+    return a
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_tables_on_another_stream(env, handle):
+    """What the current stream still has to do (the workspace's zeroing, the table's making) comes first."""
+    torch, nat, pipeline = env
+    side = torch.cuda.Stream()
+    for R in (9, 3000):
+        new, ctx, pages, free = _lengths(np.random.RandomState(R + 1), R, 16, 60, 100)
+        host, fr = torch.from_numpy(pages).cuda(), torch.from_numpy(free).cuda()
+        torch.cuda.synchronize()
+        busy = _busy(torch)
+        t = host + 0 * busy[0, 0].nan_to_num(0.0, 0.0, 0.0).int()
+        bd = pipeline.BatchDev.from_lengths(new, ctx, 16, t, fr, stream=side.cuda_stream if handle else side)
+        ref = router.block_plan(new, ctx, 16, pages, free)
+        assert np.array_equal(t.cpu().numpy(), pages) and np.array_equal(bd.slot_map.cpu().numpy(), ref["slot_map"])
+        assert np.array_equal(bd.req_off.cpu().numpy(), ref["req_off"]) and np.array_equal(bd.blk_tab.cpu().numpy(), ref["blk_tab"])
