@@ -31,6 +31,7 @@ path runs in the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Optional
 
@@ -141,7 +142,9 @@ class BatchDev:
 
 
 class RoutingStats:
-    """Holds the model/serving state of the path and runs steps over batches."""
+    """Holds the model/serving state of the path and runs steps over batches on `stream` (the one
+    that is current when it is made, if none is given).  Inputs have to be ready on that stream,
+    and a reader on another one has to wait for it."""
 
     def __init__(self, E, k, L, mask, block, *, D, tau, centroids, idf, loads, live, G, group_of,
                  nslots=0, max_T=0, max_nblk=0, max_R=0, device="cuda", stream=None):
@@ -151,32 +154,55 @@ class RoutingStats:
         dev = torch.device(device)
         self.device = dev
         self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
-        f32, i32 = torch.float32, torch.int32
-        self.centroids = torch.as_tensor(np.asarray(centroids), dtype=f32).to(dev).contiguous()
-        self.idf = torch.as_tensor(np.asarray(idf), dtype=f32).to(dev).contiguous()
-        self.loads = torch.as_tensor(np.asarray(loads), dtype=i32).to(dev).contiguous()
-        self.group_of = torch.as_tensor(np.asarray(group_of), dtype=i32).to(dev).contiguous()
-        self.affinity = torch.zeros((L, E, E), dtype=i32, device=dev)
-        self.W = torch.empty((L, E), dtype=torch.int64, device=dev)
-        self.Wg = torch.empty((L, G), dtype=torch.int64, device=dev)
-        self.rho_g = torch.empty(L, dtype=torch.float64, device=dev)
-        self.rho_e = torch.empty(L, dtype=torch.float64, device=dev)
-        self.n_rep = torch.empty(L, dtype=i32, device=dev)
-        self.rep_src = torch.empty(L, dtype=i32, device=dev)
-        self.hot = torch.empty((L, E), dtype=torch.uint8, device=dev)
-        self.rep_dst = torch.empty((L, G), dtype=i32, device=dev)
-        self.w_pred = torch.empty((L, G), dtype=torch.float64, device=dev)
-        self.cache = (torch.zeros((nslots, self.m, E), dtype=torch.uint8, device=dev)
-                      if nslots > 0 else None)
+        with self._on_stream():
+            f32, i32 = torch.float32, torch.int32
+            self.centroids = torch.as_tensor(np.asarray(centroids), dtype=f32).to(dev).contiguous()
+            self.idf = torch.as_tensor(np.asarray(idf), dtype=f32).to(dev).contiguous()
+            self.loads = torch.as_tensor(np.asarray(loads), dtype=i32).to(dev).contiguous()
+            self.group_of = torch.as_tensor(np.asarray(group_of), dtype=i32).to(dev).contiguous()
+            self.affinity = torch.zeros((L, E, E), dtype=i32, device=dev)
+            self.W = torch.empty((L, E), dtype=torch.int64, device=dev)
+            self.Wg = torch.empty((L, G), dtype=torch.int64, device=dev)
+            self.rho_g = torch.empty(L, dtype=torch.float64, device=dev)
+            self.rho_e = torch.empty(L, dtype=torch.float64, device=dev)
+            self.n_rep = torch.empty(L, dtype=i32, device=dev)
+            self.rep_src = torch.empty(L, dtype=i32, device=dev)
+            self.hot = torch.empty((L, E), dtype=torch.uint8, device=dev)
+            self.rep_dst = torch.empty((L, G), dtype=i32, device=dev)
+            self.w_pred = torch.empty((L, G), dtype=torch.float64, device=dev)
+            self.cache = (torch.zeros((nslots, self.m, E), dtype=torch.uint8, device=dev)
+                          if nslots > 0 else None)
         self.nslots = nslots
         self.gate_H = 0
         self.score_opts = self.bias = None
         self._alloc(max_T, max_nblk, max_R)
 
+    def _on_stream(self):
+        """Makes the launches' stream the current one: what is allocated, filled or copied within
+        is in order with them, and its memory goes back to that stream."""
+        return torch.cuda.stream(_as_stream(self.stream, self.device)) if self._elsewhere() else contextlib.nullcontext()
+
+    def _elsewhere(self):
+        if self.device.type != "cuda":
+            return False
+        handle = self.stream if isinstance(self.stream, int) else self.stream.cuda_stream
+        return torch.cuda.current_stream(self.device).cuda_stream != handle
+
+    def _results(self, *tensors):
+        """Tensors made on the launches' stream, for a caller on the current one."""
+        if self._elsewhere():
+            for t in tensors:
+                t.record_stream(torch.cuda.current_stream(self.device))
+        return tensors
+
     def _alloc(self, T, nblk, R):
-        dev, E, k, L, m, D = self.device, self.E, self.k, self.L, self.m, self.D
         self.cap = (T, nblk, R)
         self.ids_T = None  # tokens of the batch whose ids self.topk holds
+        with self._on_stream():
+            self._make(T, nblk, R)
+
+    def _make(self, T, nblk, R):
+        dev, E, k, L, m, D = self.device, self.E, self.k, self.L, self.m, self.D
         self.topk = torch.empty(L * max(T, 1) * k, dtype=torch.uint8, device=dev)
         self.blk_cnt = torch.empty((max(nblk, 1), m, E), dtype=torch.uint8, device=dev)
         self.req_cnt = torch.empty((max(R, 1), m, E), dtype=torch.int32, device=dev)
@@ -208,7 +234,8 @@ class RoutingStats:
         """The scored gate of `score_step` (options from make_score_opts) and its balance bias
         ([L][E] fp32, or None), which the caller may go on changing in place."""
         self.score_opts = opts
-        self.bias = None if bias is None else torch.as_tensor(bias, dtype=torch.float32).to(self.device).contiguous()
+        with self._on_stream():
+            self.bias = None if bias is None else torch.as_tensor(bias, dtype=torch.float32).to(self.device).contiguous()
         self._alloc(*self.cap)
 
     def weights_for(self, T: int) -> torch.Tensor:
@@ -269,17 +296,21 @@ class RoutingStats:
             topk = self.topk
         elif topk.dtype != torch.uint8 or tuple(topk.shape) != (self.L, T, self.k) or not topk.is_contiguous() or not self._here(topk):
             raise ValueError(f"topk has to be contiguous uint8 {(self.L, T, self.k)} on {self.device}")
-        d_weights = self._as_f32(d_weights, (self.L, T, self.k), "d_weights")
-        if d_score_sum is not None:
-            d_score_sum = self._as_f32(d_score_sum, (self.L, self.E), "d_score_sum")
-        if out is None:
-            out = torch.empty_like(logits)
+        made = out is None
+        with self._on_stream():
+            d_weights = self._as_f32(d_weights, (self.L, T, self.k), "d_weights")
+            if d_score_sum is not None:
+                d_score_sum = self._as_f32(d_score_sum, (self.L, self.E), "d_score_sum")
+            if made:
+                out = torch.empty_like(logits)
         self._check_logits(out, "out's entries")
         if out.shape != logits.shape:
             raise ValueError("out has to have the logits' shape")
         nat.moer_score_topk_grad(self.dims, self.score_opts, logits, T, logits.stride(1), logits.stride(0), topk,
                                  d_weights, d_score_sum, out, out.stride(1), out.stride(0), self.ws, self.ws_bytes,
                                  self.stream)
+        if made:
+            self._results(out)
         return out
 
     def expert_order(self, T: int, align: int = 1):
@@ -290,11 +321,12 @@ class RoutingStats:
         n = T * self.k
         ld = n + min(self.E, n) * (align - 1)
         i32, dev = torch.int32, self.device
-        off = torch.empty((self.L, self.E + 1), dtype=i32, device=dev)
-        order = torch.empty((self.L, ld), dtype=i32, device=dev)
-        inv = torch.empty((self.L, T, self.k), dtype=i32, device=dev)
+        with self._on_stream():
+            off = torch.empty((self.L, self.E + 1), dtype=i32, device=dev)
+            order = torch.empty((self.L, ld), dtype=i32, device=dev)
+            inv = torch.empty((self.L, T, self.k), dtype=i32, device=dev)
         nat.moer_expert_order(self.dims, self.topk, T, align, off, order, ld, inv, self.ws, self.ws_bytes, self.stream)
-        return off, order, inv
+        return self._results(off, order, inv)
 
     def score_step(self, logits, bd: BatchDev, align=1, score_sum=None, write_sig=True):
         """All rows of the path over one batch through the scored gate, and the experts' token
@@ -315,7 +347,8 @@ class RoutingStats:
         return self.expert_order(bd.T, align)
 
     def reset_stats(self):
-        self.affinity.zero_()
+        with self._on_stream():
+            self.affinity.zero_()
 
     # ------------------------------------------------------------ the step
     def topk_signature(self, logits, bd: BatchDev, write_topk=True, blk_counts=True):

@@ -155,3 +155,46 @@ def test_tables_on_another_stream(env, handle):
         ref = router.block_plan(new, ctx, 16, pages, free)
         assert np.array_equal(t.cpu().numpy(), pages) and np.array_equal(bd.slot_map.cpu().numpy(), ref["slot_map"])
         assert np.array_equal(bd.req_off.cpu().numpy(), ref["req_off"]) and np.array_equal(bd.blk_tab.cpu().numpy(), ref["blk_tab"])
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_buffers_on_the_launches_stream(env, handle):
+    """A RoutingStats on a stream of its own, while the current one still has to fill memory that it
+    has given back: neither side's writes reach the other's tensors."""
+    torch, nat, pipeline = env
+    L, T, E, k = 2, 4000, 64, 6
+    side = torch.cuda.Stream()
+    rs = _stats(pipeline, nat, L, E, k, max_T=T, stream=side.cuda_stream if handle else side)
+    x = torch.randn((L, T, E), device="cuda")
+    dw = torch.randn((T, L, k), device="cuda").transpose(0, 1)
+    torch.cuda.synchronize()
+    _busy(torch)
+    sizes = [(L * (E + 1), torch.int32), (L * T * k, torch.int32), (L * T * k, torch.int32), (L * T * E, torch.float32), (L * T * k, torch.float32)]
+    late = [torch.empty(n, dtype=d, device="cuda").fill_(77) for n, d in sizes]
+    del late  # the fills are still to come
+    rs.score_topk(x)
+    off, order, inv = rs.expert_order(T)
+    dx = rs.score_grad(x, dw)
+    torch.cuda.synchronize()
+    assert rs.status() == 0
+    ids = rs.topk_for(T).cpu().numpy()
+    ro, rr, ri = router.expert_order(ids, E, 1, T * k)
+    assert np.array_equal(off.cpu().numpy(), ro) and np.array_equal(order.cpu().numpy(), rr) and np.array_equal(inv.cpu().numpy(), ri)
+    g, mag = router.score_topk_grad(x.double().cpu().numpy(), ids, dw.cpu().numpy())
+    assert (np.abs(dx.cpu().numpy() - g) <= 1e-5 * mag + 1e-37).all()
+
+
+def test_step_on_a_stream_of_its_own(env):
+    torch, nat, pipeline = env
+    L, E, k = 2, 64, 6
+    side = torch.cuda.Stream()
+    new = np.array([300, 17, 40])
+    bd = pipeline.BatchDev.from_lengths(new, np.zeros(3, int), 16)
+    x = torch.randn((L, bd.T, E), device="cuda")
+    torch.cuda.synchronize()
+    a = _stats(pipeline, nat, L, E, k, stream=side)
+    b = _stats(pipeline, nat, L, E, k)
+    out = [s.score_step(x, bd) for s in (a, b)]
+    torch.cuda.synchronize()
+    assert a.status() == 0 and b.status() == 0
+    assert all(torch.equal(u, v) for u, v in zip(*out)) and torch.equal(a.affinity, b.affinity) and torch.equal(a.W, b.W)
