@@ -232,10 +232,14 @@ class RoutingStats:
     # ------------------------------------------------------ scored gates
     def set_gate(self, opts: "nat.moer_score_opts", bias=None):
         """The scored gate of `score_step` (options from make_score_opts) and its balance bias
-        ([L][E] fp32, or None), which the caller may go on changing in place."""
-        self.score_opts = opts
+        ([L][E], or None).  The tensor in use is `self.bias`, which may be changed in place: the
+        given one if it is contiguous fp32 on this device, else a copy of it."""
         with self._on_stream():
-            self.bias = None if bias is None else torch.as_tensor(bias, dtype=torch.float32).to(self.device).contiguous()
+            if bias is not None:
+                bias = torch.as_tensor(bias, dtype=torch.float32).to(self.device).contiguous()
+                if tuple(bias.shape) != (self.L, self.E):
+                    raise ValueError(f"bias has shape {tuple(bias.shape)}, expected {(self.L, self.E)}")
+        self.score_opts, self.bias = opts, bias
         self._alloc(*self.cap)
 
     def weights_for(self, T: int) -> torch.Tensor:

@@ -171,3 +171,20 @@ def test_gradient_of_an_earlier_batch_by_its_ids(calls):
         with pytest.raises(ValueError):
             rs.score_grad(torch.zeros((L, 8, E)), torch.zeros((L, 8, k)), topk=bad)
     assert not calls
+
+
+def test_bias_in_use(calls):
+    """The gate's bias is the tensor `bias`: the given one where the library can take it as it is."""
+    own = torch.zeros((L, E))
+    rs = _stats(8)
+    rs.set_gate(nat.make_score_opts(), own)
+    assert rs.bias is own
+    for given in (torch.arange(L * E, dtype=torch.float64).view(L, E), torch.arange(L * E).view(E, L).t(), np.ones((L, E))):
+        rs.set_gate(nat.make_score_opts(), given)
+        assert rs.bias.dtype == torch.float32 and rs.bias.is_contiguous() and torch.equal(rs.bias, torch.as_tensor(given, dtype=torch.float32))
+        rs.bias += 1
+        rs.score_topk(torch.zeros((L, 8, E)))
+        assert calls[-1][1][6] is rs.bias
+    for bad in (torch.zeros(E), torch.zeros((L, E + 1)), torch.zeros((E, L)), torch.zeros((L + 1, E))):
+        with pytest.raises(ValueError):
+            rs.set_gate(nat.make_score_opts(), bad)
