@@ -57,6 +57,9 @@ struct PlanParams {
   int vec_len;             // 1: the lengths take vector loads
   int vec_tab;             // 1: blk_tab's pairs are on 8 bytes
   int lanes;               // to a KV block when tokens are written: a power of two
+  // blocks that have room, or whose tokens have (b blocks hold b tokens at least): a batch
+  // of absurd lengths has up to 2^31 more, of which only pages are written
+  int limit;
 };
 
 // x / B for x < 2^31: with s = ceil(log2 B) the multiplier is floor(2^(31 + s) / B) + 1,
@@ -304,6 +307,18 @@ struct Run {
   int tok0, len, pos, req;
 };
 
+// New pages of the blocks from `last` on, as far as the table reaches.
+__device__ __forceinline__ void fill_pages(const PlanParams& p, const Tables& tb, int last) {
+  const moer_block_plan_args& a = p.a;
+  for (int64_t r = (int64_t)blockIdx.x * BP_THREADS + threadIdx.x; r < a.R; r += (int64_t)gridDim.x * BP_THREADS) {
+    const Request q = request(tb, (int)r);
+    const uint32_t held = pages_of(p, q.c), end = min(pages_of(p, q.c + q.n), (uint32_t)a.ld_pages);
+    const uint32_t past = (uint32_t)max(last - tb.blk[r], 0);  // its blocks that are done
+    for (uint32_t i = max(held, div_b(p, q.c) + past); i < end; ++i)
+      a.pages[r * a.ld_pages + i] = page_of(p, tb, (int)r, held, i);
+  }
+}
+
 // The batch's KV blocks, and with each its tokens.
 __device__ void fill_blocks(const PlanParams& p, const Tables& tb) {
   __shared__ Run runs[BP_THREADS];
@@ -313,8 +328,9 @@ __device__ void fill_blocks(const PlanParams& p, const Tables& tb) {
   const bool tokens = a.slot_map != nullptr || a.tok_req != nullptr || a.tok_pos != nullptr;
   const uint32_t B = (uint32_t)a.block;
   const int room = (int)min64(a.T, 0x7FFFFFFF);
-  for (int64_t b0 = (int64_t)blockIdx.x * BP_THREADS; b0 < nblk; b0 += (int64_t)gridDim.x * BP_THREADS) {
-    const int n = (int)min64(BP_THREADS, nblk - b0);
+  const int last = min(nblk, p.limit);
+  for (int64_t b0 = (int64_t)blockIdx.x * BP_THREADS; b0 < last; b0 += (int64_t)gridDim.x * BP_THREADS) {
+    const int n = (int)min64(BP_THREADS, last - b0);
     find_range(tb.blk, a.R, (int)b0, n, range);
     if ((int)threadIdx.x < n) {
       const int b = (int)b0 + (int)threadIdx.x;
@@ -367,8 +383,9 @@ __device__ void fill_blocks(const PlanParams& p, const Tables& tb) {
     }
     __syncthreads();
   }
-  // room that the batch leaves
   const int64_t step = (int64_t)gridDim.x * BP_THREADS, first = (int64_t)blockIdx.x * BP_THREADS + threadIdx.x;
+  if (last < nblk && a.pages != nullptr && a.free_pages != nullptr) fill_pages(p, tb, last);
+  // room that the batch leaves
   for (int64_t t = tb.req[a.R] + first; t < a.T; t += step) {
     if (a.slot_map != nullptr) a.slot_map[t] = -1;
     if (a.tok_req != nullptr) a.tok_req[t] = -1;
@@ -440,6 +457,8 @@ moer_status block_plan_launch(const moer_block_plan_args* a, void* ws, cudaStrea
   p.mul = B == 1 ? 0u : (uint32_t)((1ull << (31u + log)) / B + 1ull);
   p.shift = B == 1 ? 32u : log - 1u;
   p.lanes = 1 << (log < 5u ? log : 5u);
+  const bool tokens = a->slot_map != nullptr || a->tok_req != nullptr || a->tok_pos != nullptr;
+  p.limit = (int)max64(a->nblk, tokens ? a->T : 0);
   p.status = static_cast<uint32_t*>(ws);
   char* scratch = static_cast<char*>(ws) + WS_HEADER;
   p.taken_off = reinterpret_cast<int32_t*>(scratch);

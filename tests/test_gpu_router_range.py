@@ -2,6 +2,8 @@
 
 Tolerances and comparisons are those of test_gpu_router.py, whose header derives them.
 """
+import time
+
 import numpy as np
 import pytest
 
@@ -117,3 +119,56 @@ def test_weights_of_small_scores(env, E, k, T, biased, dtype):
     for renorm in (True, False):
         o = dict(score="sigmoid", renorm=renorm, scale=1000.0)
         _check_forward(_forward(env, dev, E, k, dtype, bias=bias, **o), x, k, bias=bias, **o)
+
+
+# Lengths that a batch cannot have: what fits is written, in a time that goes by the room
+@pytest.mark.parametrize("B", [1, 16, 255])
+@pytest.mark.parametrize("R,at", [(3, 0), (1000, 2), (3000, 2)])
+@pytest.mark.parametrize("maps", [True, False])
+def test_block_plan_of_absurd_lengths(env, B, R, at, maps):
+    torch, nat = env
+    rs = np.random.RandomState(B + R)
+    new, ctx = rs.randint(1, 20, size=R).astype(np.int64), rs.randint(0, 30, size=R).astype(np.int64)
+    ctx[at] = 2 * B + 1 if B > 1 else 2
+    new[at:] = 2 ** 31 - 1 - ctx[at:]
+    have, total = -(-ctx // B), -(-(ctx + new) // B)
+    width = int(max(have.max(), total[:at].max(initial=0))) + 4
+    pages = np.full((R, width), -5, dtype=np.int32)
+    for r in range(R):
+        pages[r, :have[r]] = 7 * r + np.arange(have[r])
+    free = (1000000 + np.arange(int((total - have)[:at].sum()) + 2)).astype(np.int32)
+    taken = np.concatenate([[0], np.cumsum(total - have)])
+    want = pages.copy()
+    for r in range(R):
+        for i in range(int(have[r]), int(min(total[r], width))):
+            f = taken[r] + i - have[r]
+            want[r, i] = free[f] if f < len(free) else -1
+    blocks = np.where(new > 0, -(-(ctx % B + new) // B), 0)
+    nb, T = int(blocks[:at].sum()) + 5, int(new[:at].sum()) + 3
+    tab, tok = [], []
+    for r in range(at + 1):
+        p, t = int(ctx[r]), int(new[:r].sum())
+        while p < ctx[r] + new[r] and len(tab) < nb:
+            end = min(int(ctx[r] + new[r]), (p // B + 1) * B)
+            tab.append((t, end - p))
+            t, p = t + end - p, end
+        tok += [(r, int(ctx[r]) + i) for i in range(min(int(new[r]), T - len(tok)))]
+    t32 = lambda a: torch.from_numpy(np.ascontiguousarray(a).astype(np.int32)).cuda()  # noqa: E731
+    e = lambda *s, dtype=torch.int32: torch.full(s, 77, dtype=dtype, device="cuda")  # noqa: E731
+    b = {"new_len": t32(new), "ctx_len": t32(ctx), "pages": t32(pages), "free_pages": t32(free), "req_off": e(R + 1),
+         "req_blk_off": e(R + 1), "blk_tab": e(nb, 2), "insert_slot": e(nb), "totals": e(4)}
+    if maps:
+        b.update(tok_req=e(T), tok_pos=e(T), slot_map=e(T, dtype=torch.int64))
+    n = nat.moer_block_plan_workspace_bytes(R)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    args = nat.make_block_plan(R=R, block=B, T=T, nblk=nb, ld_pages=width, n_free=len(free), **b)
+    torch.cuda.synchronize()
+    start = time.perf_counter()
+    nat.moer_block_plan(args, ws, n)
+    assert nat.moer_ws_status(ws) == 6
+    assert time.perf_counter() - start < 0.5
+    assert np.array_equal(b["pages"].cpu().numpy(), want)
+    assert b["blk_tab"].cpu().numpy().tolist() == [list(x) for x in tab]
+    assert b["totals"].cpu().numpy().tolist()[0] == min(int(new.sum()), 2 ** 31 - 1)
+    if maps:
+        assert list(zip(b["tok_req"].tolist(), b["tok_pos"].tolist())) == tok
