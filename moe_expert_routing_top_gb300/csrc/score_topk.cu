@@ -1,6 +1,6 @@
 // score_topk.cu -- moer_score_topk: scores, choice and weights of the router.
 //
-// Batches of some thousand rows with k <= 16 go to the fast kernel
+// Batches of two or three thousand rows with k <= 16 go to the fast kernel
 // (score_fast.cuh).  The kernel here takes any E <= 256 with E % 4 == 0, any
 // k <= 32, options and alignment, and is the faster one for few rows: one warp
 // per row, a lane with the quads of neighbouring experts 4 (lane + 32 i).  The
@@ -33,7 +33,8 @@ namespace {
 constexpr int SC_WARPS = 8;
 constexpr int SC_UNITS = 4864;  // units asked for: 152 SMs x 32
 
-constexpr int64_t SC_FAST_ROWS = 2048;  // rows from which the fast kernel is taken
+constexpr int64_t SC_FAST_ROWS = 2048;    // rows from which the fast kernel is taken,
+constexpr int64_t SC_FAST16_ROWS = 2816;  // and with k > 8
 
 // Tokens of a unit: a multiple of `step`, the rows that a block takes at a time.
 int score_span(int64_t T, int L, int step) {
@@ -64,10 +65,14 @@ int fast_span(int64_t T, int L, int step, int64_t slots) {
 // Few rows leave it idle lanes: at 1,024 / 2,048 / 4,096 rows it took 2.6 / 2.6 / 4.2 us
 // (a warp per row: 3.2 / 3.3 / 5.2) with E = 128 fp32, 4.3 / 4.3 / 4.3 (4.5 / 5.6 / 9.7)
 // with 256 bf16 experts in groups, 5.3 / 5.6 / 5.3 (4.1 / 5.3 / 8.9) with 64 bf16
-// experts and score sums.  With k = 10, 48 x 42,076 rows of 72 fp32 experts and score
+// experts and score sums.  With k > 8, at 2,048 / 2,816 / 4,096 rows: 4.0 / 4.0 / 4.1 us
+// (a warp per row: 3.7 / 4.2 / 4.8) with E = 128 fp32, k = 10, 6.1 / 6.2 / 6.1 (5.9 / 7.7 /
+// 10.3) with 256 bf16 experts in groups, k = 16, 7.7 / 7.6 / 7.5 (5.7 / 7.3 / 9.2) with 64 bf16
+// experts and sums, k = 12, 8.7 / 9.3 / 8.9 (6.9 / 8.9 / 11.3) with 160 fp32 ones, bias and
+// sums, k = 10.  With k = 10, 48 x 42,076 rows of 72 fp32 experts and score
 // sums took 1,072 us a warp per row, about 445 here (k = 9 and 16: 443 and 454).
 bool fast_supported(const ScoreParams& p) {
-  if (p.k > 16 || p.vec == 0 || p.E < 16 || p.L * p.T < SC_FAST_ROWS) return false;
+  if (p.k > 16 || p.vec == 0 || p.E < 16 || p.L * p.T < (p.k > 8 ? SC_FAST16_ROWS : SC_FAST_ROWS)) return false;
   if (p.n_group == 1) return true;
   const int lanes = p.E <= 64 ? 1 : p.E <= 128 ? 2 : 4, gs = p.E / p.n_group;
   int mb = 1;  // blocks of a lane to a group

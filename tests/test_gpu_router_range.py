@@ -7,6 +7,7 @@ import time
 import numpy as np
 import pytest
 
+from oracle import router
 from tests.test_gpu_router import DT, _backward, _check_forward, _check_grad, _forward, _ids, _logits, env  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -172,3 +173,29 @@ def test_block_plan_of_absurd_lengths(env, B, R, at, maps):
     assert b["totals"].cpu().numpy().tolist()[0] == min(int(new.sum()), 2 ** 31 - 1)
     if maps:
         assert list(zip(b["tok_req"].tolist(), b["tok_pos"].tolist())) == tok
+
+
+# More than eight choices at sizes past the rule's 2,816 rows, and the same rows a few at a time
+@pytest.mark.parametrize("E,k,n,keep", [(16, 9, 1, 1), (24, 12, 1, 1), (64, 16, 1, 1), (72, 10, 1, 1), (128, 10, 1, 1), (160, 12, 1, 1), (256, 16, 1, 1),
+                                        (256, 10, 8, 4), (128, 16, 8, 3), (64, 9, 8, 2), (160, 12, 5, 2)])
+@pytest.mark.parametrize("special", [None, "masks", "ties", "inf", "lowest"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_many_choices(env, E, k, n, keep, special, dtype):
+    torch, _ = env
+    rs = np.random.RandomState(E + k + 5)
+    dev, x = _logits(torch, rs, 2, 1500, E, dtype, special=special)
+    for biased, score, renorm in ((False, "softmax", False), (True, "softmax", True), (True, "sigmoid", True), (False, "sigmoid", False)):
+        bias = rs.normal(0, 0.3, size=(2, E)) if biased else None
+        o = dict(score=score, renorm=renorm, n_group=n, top_group=keep, best=1 + biased)
+        ids, w, ss = _forward(env, dev, E, k, dtype, bias=bias, sums=renorm, **o)
+        few = [_forward(env, dev[:, a:a + 750], E, k, dtype, bias=bias, sums=False, **o) for a in (0, 750)]
+        gap = router.score_topk(x, k, bias=None if bias is None else bias.astype(np.float32), **o)[3]
+        tol = 1e-5 * (1 + (0 if bias is None else np.abs(bias).max()))
+        for l in range(2):
+            at = gap[l] > tol  # other rows may go either way in fp32
+            assert np.array_equal(ids[l, at], np.concatenate([f[0][l] for f in few])[at])
+            if at.any():
+                _check_forward((ids[l:l + 1, at], w[l:l + 1, at], None), x[l:l + 1, at], k, bias=None if bias is None else bias[l:l + 1], **o)
+        if renorm:
+            sums = router.scores(x, score).sum(1)
+            assert (np.abs(ss - sums) <= 6e-6 * sums + 1e-30).all()
