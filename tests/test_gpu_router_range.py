@@ -2,6 +2,7 @@
 
 Tolerances and comparisons are those of test_gpu_router.py, whose header derives them.
 """
+import math
 import time
 
 import numpy as np
@@ -178,8 +179,7 @@ def test_block_plan_of_absurd_lengths(env, B, R, at, maps):
 # More than eight choices at sizes past the rule's 2,816 rows, and the same rows a few at a time
 @pytest.mark.parametrize("E,k,n,keep", [(16, 9, 1, 1), (24, 12, 1, 1), (64, 16, 1, 1), (72, 10, 1, 1), (128, 10, 1, 1), (160, 12, 1, 1), (256, 16, 1, 1),
                                         (256, 10, 8, 4), (128, 16, 8, 3), (64, 9, 8, 2), (160, 12, 5, 2)])
-@pytest.mark.parametrize("special", [None, "masks", "ties", "inf", "lowest"])
-@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("special,dtype", [(None, "f32"), ("masks", "bf16"), ("ties", "f16"), ("ties", "f32"), ("inf", "f32"), ("lowest", "bf16")])
 def test_many_choices(env, E, k, n, keep, special, dtype):
     torch, _ = env
     rs = np.random.RandomState(E + k + 5)
@@ -199,3 +199,50 @@ def test_many_choices(env, E, k, n, keep, special, dtype):
         if renorm:
             sums = router.scores(x, score).sum(1)
             assert (np.abs(ss - sums) <= 6e-6 * sums + 1e-30).all()
+
+
+# Several tiles to a warp (4,864 units share the rows: from 155,648 rows with k <= 8, 77,824 with
+# k <= 16 and 38,912 beyond): the loads ahead and the shared rows of the second and later tiles
+@pytest.mark.parametrize("E,k,L,T", [(64, 6, 3, 70001), (128, 8, 1, 200003), (256, 8, 2, 90007), (60, 5, 2, 100001), (128, 12, 2, 50003), (256, 20, 1, 50021)])
+@pytest.mark.parametrize("score,renorm,sums", [("softmax", False, True), ("softmax", False, False), ("softmax", True, True), ("softmax", True, False),
+                                               ("sigmoid", False, True), ("sigmoid", True, True), ("sigmoid", True, False)])
+@pytest.mark.parametrize("dtype,layout", [("f32", "layer"), ("bf16", "token")])
+def test_gradient_of_many_rows(env, E, k, L, T, score, renorm, sums, dtype, layout):
+    """The whole result against the formulas in 64 bits, with masks, on the GPU; the bounds are _check_grad's."""
+    torch, nat = env
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(E + k)
+    x = torch.randn((L, T, E) if layout == "layer" else (T, L, E), device="cuda", generator=gen)
+    x = x if layout == "layer" else x.permute(1, 0, 2)
+    x = x.mul_(2.0).masked_fill_(torch.rand((L, T, E), device="cuda", generator=gen) < 0.02, -math.inf).to(getattr(torch, DT[dtype]))
+    ids = torch.rand((L, T, E), device="cuda", generator=gen).topk(k, -1).indices
+    dw = torch.randn((L, T, k), device="cuda", generator=gen)
+    da = torch.randn((L, E), device="cuda", generator=gen) if sums else None
+    d, o = nat.make_dims(E, k, L, [], 16), nat.make_score_opts(dtype=dtype, score=score, renorm=renorm, scale=1.5)
+    out = torch.full_like(x, 9.0)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    nat.moer_score_topk_grad(d, o, x, T, x.stride(1), x.stride(0), ids.to(torch.uint8), dw, da, out, out.stride(1), out.stride(0), ws, 256)
+    assert nat.moer_ws_status(ws) == 0
+    for l in range(L):
+        z = x[l].double()
+        s = torch.sigmoid(z) if score == "sigmoid" else torch.softmax(z, -1)
+        at, g = ids[l], dw[l].double() * 1.5
+        p = s.gather(1, at)
+        q = p / p.sum(-1, keepdim=True).clamp_min(1e-300)
+        dx, mag = torch.zeros_like(s), torch.zeros_like(s)
+        for to, sign, gg, a in ((dx, -1.0, g, None if da is None else da[l].double()), (mag, 1.0, g.abs(), None if da is None else da[l].double().abs())):
+            part = q * (gg + sign * (gg * q).sum(-1, keepdim=True)) if renorm else gg * p
+            if score == "sigmoid":
+                part = part * (1 - p)
+                if a is not None:
+                    to += a * s * (1 - s)
+            else:
+                if a is not None:
+                    to += s * (a + sign * (a * s).sum(-1, keepdim=True))
+                if not renorm:
+                    to += sign * s * (gg * p).sum(-1, keepdim=True)
+            to.scatter_add_(1, at, part)
+        lim = 1e-5 * mag + 1e-37
+        lo, hi = ((dx + f * lim).to(x.dtype).double() for f in (-1.0, 1.0))
+        got = out[l].double()
+        assert bool(((got >= lo) & (got <= hi)).all()), (l, int((~((got >= lo) & (got <= hi))).sum()))
