@@ -449,8 +449,8 @@ typedef struct moer_score_opts {
  *         without one.  A masked expert's is -inf (NaN logit: below -inf)
  *         whatever its bias;
  *   groups (n_group > 1): a group's score is the best c of its experts, or
- *         the sum of its two best (of s without a bias); the top_group best
- *         groups stay, ties to the lower group;
+ *         the sum of its two best (of s without a bias), -inf where none is
+ *         left; the top_group best groups stay, ties to the lower group;
  *   topk  the k largest c among the groups that stay, in that order, ties to
  *         the lower id, NaN below every number;
  *   w_j   scale * s_j, or with renorm scale * s_j / (sum of the k chosen s)

@@ -31,6 +31,7 @@ __device__ uint32_t group_keys(const ScoreParams& p, const uint32_t (&key)[4 * N
       const float sum = rank_value(gk) + rank_value(second);
       gk = rank_key(sum == sum ? sum : NEG_INF);
     }
+    gk = max(gk, rank_key(NEG_INF));  // a group of NaN alone ties with one of -inf
     if (lane == g) mine = gk;
   }
   return mine;

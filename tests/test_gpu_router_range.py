@@ -246,3 +246,19 @@ def test_gradient_of_many_rows(env, E, k, L, T, score, renorm, sums, dtype, layo
         lo, hi = ((dx + f * lim).to(x.dtype).double() for f in (-1.0, 1.0))
         got = out[l].double()
         assert bool(((got >= lo) & (got <= hi)).all()), (l, int((~((got >= lo) & (got <= hi))).sum()))
+
+
+# Groups without a live expert score -inf and tie, whether their logits are -inf or NaN
+@pytest.mark.parametrize("E,k,n,keep", [(16, 4, 8, 4), (64, 6, 8, 3), (128, 8, 4, 2), (256, 8, 8, 4)])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("T", [70, 2100])
+def test_groups_of_masks(env, E, k, n, keep, best, T):
+    torch, _ = env
+    rs = np.random.RandomState(E + T)
+    x = rs.normal(size=(1, T, n, E // n))
+    x[rs.random_sample((1, T, n)) < 0.4] = -np.inf
+    x[rs.random_sample((1, T, n)) < 0.4] = np.nan
+    dev, x = _device(torch, x.reshape(1, T, E), "f32")
+    for bias in (None, rs.normal(0, 0.3, size=(1, E))):
+        o = dict(score="sigmoid", renorm=True, n_group=n, top_group=keep, best=best)
+        _check_forward(_forward(env, dev, E, k, "f32", bias=bias, **o), x, k, bias=bias, **o)
