@@ -23,9 +23,9 @@
 // two, 32 at most), from what was found once.  Finding request and page for
 // every four tokens instead took five times the instructions.
 // Measured (GB300): 14,000 requests, 12.9 M tokens in 0.8 M KV blocks with slots, owners
-// and positions (227 MB): 49 us, 4.6 TB/s, 0.68 of the copy bandwidth; the sums take
+// and positions (227 MB): 50 us, 4.6 TB/s, 0.67 of the copy bandwidth; the sums take
 // 8 us of it, the fill's stores (16 bytes a token) the rest.  256 requests with one
-// new token each: 5.7 us in the small form, a chain of dependent steps.
+// new token each: 6.0 us in the small form, a chain of dependent steps.
 // Small batches take one launch: one block does it all, in shared memory.
 #include "common.cuh"
 #include "pdl.cuh"

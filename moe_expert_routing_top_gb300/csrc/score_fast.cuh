@@ -30,16 +30,17 @@
 // lanes, and the columns' sums in registers, so that no atomics are needed.
 //
 // Measured (GB300): 65,536 tokens x 48 layers of 128 fp32 logits, k = 8, softmax
-// weights: 283 us, 6.14 TB/s of algorithmic bytes, 0.90 of the measured copy
-// bandwidth.  8,209 x 26 of 256 bf16 logits, sigmoid with bias, 4 of 8 groups by
-// their two best: 70 us (1.7 TB/s); the ALU pipe is 64 % busy at 2.6 instructions a
-// clock, and the networks' minima and maxima alone would fill it for some 45 us.
-// 30,011 x 26 of 64 bf16 logits, k = 6, softmax weights and score sums: 64 us, of
-// which the column pass is about 20.
+// weights: 282 us, 6.15 TB/s of algorithmic bytes, 0.91 of the measured copy
+// bandwidth (bf16 logits, half the bytes at the same comparators: 277 us).  8,209 x
+// 26 of 256 bf16 logits, sigmoid with bias, 4 of 8 groups by their two best: 71 us
+// (1.7 TB/s): 247 warp instructions a row, issued at 2.6 of 4 a clock; the networks are
+// 30 % of them (580 minima and maxima a lane, 27 us of the ALU pipe at its full rate),
+// and with the others the pipe is 63 % busy.  30,011 x 26 of 64 bf16 logits, k = 6,
+// softmax weights and score sums: 64 us, of which the column pass is about 20.
 // Why lanes by columns of blocks: the networks cost the same per logit in every
-// split, but more lanes a row merge more lists (G = 4 and 32 logits a lane: 92
-// minima and maxima a row of 128 logits against 71), while one lane for 128 and
-// more logits cannot hold them in registers.
+// split, but more lanes a row merge more lists (a row of 128 logits: 80 minima and
+// maxima for 8 logits with G = 4 and 32 logits a lane, 71 with G = 2 and 64), while one
+// lane for 128 and more logits cannot hold them in registers.
 #pragma once
 
 #include "pdl.cuh"

@@ -7,7 +7,7 @@
 // chosen experts' parts reach their blocks through a row of shared memory.
 //
 // Measured (GB300): 30,011 tokens x 26 layers of 64 bf16 logits, k = 6, plain softmax
-// and score sums, token-major: 53 us, 4.2 TB/s of algorithmic bytes; issue-bound (3.0
+// and score sums, token-major: 54 us, 4.2 TB/s of algorithmic bytes; issue-bound (3.1
 // of 4 instructions a clock).  16,384 x 48 of 256 bf16 logits, renormalised sigmoid
 // (chosen logits only): 119 us; ncu counts 395 MB read for 13 MB of chosen logits
 // and 31 MB of ids and gradients, for DRAM moves 64-byte pieces, and 350 MB written:

@@ -1,7 +1,7 @@
 // score_row.cuh -- one row of the scored top-k gate by one warp, for any E <= 256,
 // k <= 32 and any options, with exact keys: the path of the rows that neither kernel's
 // fixed-point keys settle (score_fast.cuh).  Some 4 to 8 us of one warp; taken for
-// every row it needs 2,367 us where the fast kernel takes 283.
+// every row it needs 2,367 us where the fast kernel takes 282.
 #pragma once
 
 #include "score.cuh"
