@@ -150,16 +150,21 @@ def _ptr(x):
 _current = None  # (current device, its current stream's handle), bound at the first call without a stream
 
 
+def current_handle(index=None) -> int:
+    """The handle of the current stream of a device (the current one, if none is given), without
+    the stream object that torch.cuda.current_stream() makes (0.2 instead of 2.9 us a call, a
+    third of a small call's time on the host)."""
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.init()
+        _current = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    return _current[1](_current[0]() if index is None else index)
+
+
 def _stream(s):
     if s is None:
-        # the current stream's handle without the stream object that torch.cuda.current_stream()
-        # makes (0.2 instead of 2.9 us a call, a third of a small call's time on the host)
-        global _current
-        if _current is None:
-            import torch
-            torch.cuda.init()
-            _current = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
-        return _current[1](_current[0]())
+        return current_handle()
     return s if isinstance(s, int) else s.cuda_stream
 
 

@@ -41,6 +41,10 @@ import torch
 from . import _native as nat
 
 
+_AS_IT_IS = contextlib.nullcontext()
+_GATE_DTYPES = {0: torch.float32, 1: torch.bfloat16, 2: torch.float16}  # by moer_dtype
+
+
 def _as_stream(stream, device):
     """A torch stream of a torch stream or a handle."""
     if not isinstance(stream, int):
@@ -74,13 +78,12 @@ class BatchDev:
         runs on `stream`, after what the current stream has under way, and waits for it.  A table
         that is a slice of a wider one is copied and written back.  Without `pages` the batch
         has no slots and no signature cache."""
-        n, c = np.asarray(new_len), np.asarray(ctx_len)
+        n, c = np.asarray(new_len, dtype=np.int64), np.asarray(ctx_len, dtype=np.int64)
         if n.ndim != 1 or n.shape != c.shape:
             raise ValueError(f"lengths of shapes {n.shape} and {c.shape}: expected one of each per request")
-        n, c = n.astype(np.int64), c.astype(np.int64)
-        if max(n.max(initial=0), c.max(initial=0)) >= 1 << 31 or min(n.min(initial=0), c.min(initial=0)) < -(1 << 31):
-            raise ValueError("a length does not fit 32 bits")
         new, ctx, B, R = n.astype(np.int32), c.astype(np.int32), int(block), len(n)
+        if (new != n).any() or (ctx != c).any():
+            raise ValueError("a length does not fit 32 bits")
         where = torch.device(device).type
         if pages is None and free_pages is not None:
             raise ValueError("free pages without a block table")
@@ -180,13 +183,12 @@ class RoutingStats:
     def _on_stream(self):
         """Makes the launches' stream the current one: what is allocated, filled or copied within
         is in order with them, and its memory goes back to that stream."""
-        return torch.cuda.stream(_as_stream(self.stream, self.device)) if self._elsewhere() else contextlib.nullcontext()
+        return torch.cuda.stream(_as_stream(self.stream, self.device)) if self._elsewhere() else _AS_IT_IS
 
     def _elsewhere(self):
         if self.device.type != "cuda":
             return False
-        handle = self.stream if isinstance(self.stream, int) else self.stream.cuda_stream
-        return torch.cuda.current_stream(self.device).cuda_stream != handle
+        return nat.current_handle(self.device.index) != (self.stream if isinstance(self.stream, int) else self.stream.cuda_stream)
 
     def _results(self, *tensors):
         """Tensors made on the launches' stream, for a caller on the current one."""
@@ -246,42 +248,43 @@ class RoutingStats:
         """The weights of the last batch of T tokens, as [L][T][k]."""
         return self.weights[:self.L * T * self.k].view(self.L, T, self.k)
 
-    def _here(self, x) -> bool:
-        return x.device.type == self.device.type and (self.device.index is None or x.device.index == self.device.index)
-
     def _check_logits(self, logits, what="logits"):
         """The library takes addresses: a tensor of another type, shape or layout than the gate's
         would be read, or written, past its end."""
         if self.score_opts is None:
             raise ValueError("no scored gate: call set_gate first")
-        dtype = {0: torch.float32, 1: torch.bfloat16, 2: torch.float16}.get(self.score_opts.dtype)
-        if logits.dtype != dtype:
-            raise ValueError(f"{what} are {logits.dtype}, the gate's options say {dtype}")
-        if logits.dim() != 3 or logits.shape[0] != self.L or logits.shape[2] != self.E:
-            raise ValueError(f"{what} have shape {tuple(logits.shape)}, expected ({self.L}, T, {self.E})")
+        if logits.dtype != _GATE_DTYPES.get(self.score_opts.dtype):
+            raise ValueError(f"{what} are {logits.dtype}, the gate's options say {_GATE_DTYPES.get(self.score_opts.dtype)}")
+        shape = logits.shape
+        if len(shape) != 3 or shape[0] != self.L or shape[2] != self.E:
+            raise ValueError(f"{what} have shape {tuple(shape)}, expected ({self.L}, T, {self.E})")
         if logits.stride(2) != 1:
             raise ValueError(f"{what}: the logits of a row have to be contiguous")
-        if not self._here(logits):
-            raise ValueError(f"{what} are on {logits.device}, expected {self.device}")
+        if logits.device != self.ws.device:
+            raise ValueError(f"{what} are on {logits.device}, expected {self.ws.device}")
 
-    def _check_f32(self, x, shape, what):
-        if x.dtype != torch.float32 or tuple(x.shape) != shape or not x.is_contiguous() or not self._here(x):
-            raise ValueError(f"{what} has to be contiguous fp32 {shape} on {self.device}")
+    def _is(self, x, dtype, shape) -> bool:
+        return x.dtype == dtype and x.shape == shape and x.is_contiguous() and x.device == self.ws.device
 
     def _as_f32(self, x, shape, what):
         """x as contiguous fp32, itself where it is that already."""
-        if not x.is_floating_point() or tuple(x.shape) != shape or not self._here(x):
-            raise ValueError(f"{what} has to be a floating tensor of shape {shape} on {self.device}")
-        return x if x.dtype == torch.float32 and x.is_contiguous() else x.to(torch.float32).contiguous()
+        if self._is(x, torch.float32, shape):
+            return x
+        if not x.is_floating_point() or x.shape != shape or x.device != self.ws.device:
+            raise ValueError(f"{what} has to be a floating tensor of shape {shape} on {self.ws.device}")
+        with self._on_stream():
+            return x.to(torch.float32).contiguous()
 
     def score_topk(self, logits, score_sum=None):
         """Top-k ids and weights of the scored gate; logits [L][T][E] of the gate's type with any
         strides between rows; score_sum [L][E] fp32, if given, receives the scores' sums."""
         self._check_logits(logits)
-        if score_sum is not None:
-            self._check_f32(score_sum, (self.L, self.E), "score_sum")
-        T = logits.shape[1]
-        self.ensure(T, *self.cap[1:])
+        self.ensure(logits.shape[1], 0, 0)
+        self._score_topk(logits, logits.shape[1], score_sum)
+
+    def _score_topk(self, logits, T, score_sum):
+        if score_sum is not None and not self._is(score_sum, torch.float32, (self.L, self.E)):
+            raise ValueError(f"score_sum has to be contiguous fp32 {(self.L, self.E)} on {self.ws.device}")
         self.ids_T = T
         nat.moer_score_topk(self.dims, self.score_opts, logits, T, logits.stride(1), logits.stride(0), self.bias,
                             self.topk, self.weights, score_sum, self.ws, self.ws_bytes, self.stream)
@@ -298,18 +301,19 @@ class RoutingStats:
             if T != self.ids_T:
                 raise ValueError(f"logits of {T} tokens, but the ids held are of {self.ids_T}")
             topk = self.topk
-        elif topk.dtype != torch.uint8 or tuple(topk.shape) != (self.L, T, self.k) or not topk.is_contiguous() or not self._here(topk):
-            raise ValueError(f"topk has to be contiguous uint8 {(self.L, T, self.k)} on {self.device}")
+        elif not self._is(topk, torch.uint8, (self.L, T, self.k)):
+            raise ValueError(f"topk has to be contiguous uint8 {(self.L, T, self.k)} on {self.ws.device}")
+        d_weights = self._as_f32(d_weights, (self.L, T, self.k), "d_weights")
+        if d_score_sum is not None:
+            d_score_sum = self._as_f32(d_score_sum, (self.L, self.E), "d_score_sum")
         made = out is None
-        with self._on_stream():
-            d_weights = self._as_f32(d_weights, (self.L, T, self.k), "d_weights")
-            if d_score_sum is not None:
-                d_score_sum = self._as_f32(d_score_sum, (self.L, self.E), "d_score_sum")
-            if made:
+        if made:
+            with self._on_stream():
                 out = torch.empty_like(logits)
-        self._check_logits(out, "out's entries")
-        if out.shape != logits.shape:
-            raise ValueError("out has to have the logits' shape")
+        else:
+            self._check_logits(out, "out's entries")
+            if out.shape != logits.shape:
+                raise ValueError("out has to have the logits' shape")
         nat.moer_score_topk_grad(self.dims, self.score_opts, logits, T, logits.stride(1), logits.stride(0), topk,
                                  d_weights, d_score_sum, out, out.stride(1), out.stride(0), self.ws, self.ws_bytes,
                                  self.stream)
@@ -338,10 +342,11 @@ class RoutingStats:
         (moer_ids_signature's limit) and are left as they are otherwise.  Logits padded past
         the batch's tokens are taken up to them."""
         self._check_logits(logits)
-        if logits.shape[1] < bd.T:
-            raise ValueError(f"logits of {logits.shape[1]} tokens, but the batch has {bd.T}")
+        T = logits.shape[1]
+        if T < bd.T:
+            raise ValueError(f"logits of {T} tokens, but the batch has {bd.T}")
         self.ensure(bd.T, bd.nblk, bd.R)
-        self.score_topk(logits[:, :bd.T], score_sum)
+        self._score_topk(logits if T == bd.T else logits[:, :bd.T], bd.T, score_sum)
         counted = self.E <= 128 and self.k in (6, 8)
         self.ids_signature(bd, blk_counts=True, affinity=counted)
         self.block_stitch(bd)

@@ -198,3 +198,12 @@ def test_step_on_a_stream_of_its_own(env):
     torch.cuda.synchronize()
     assert a.status() == 0 and b.status() == 0
     assert all(torch.equal(u, v) for u, v in zip(*out)) and torch.equal(a.affinity, b.affinity) and torch.equal(a.W, b.W)
+
+
+def test_current_streams_handle(env):
+    """The library's default stream is torch's current one, inside and outside a stream's context."""
+    torch, nat, pipeline = env
+    assert nat.current_handle() == torch.cuda.current_stream().cuda_stream == nat.current_handle(torch.cuda.current_device())
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert nat.current_handle() == side.cuda_stream
