@@ -420,8 +420,8 @@ MOER_API moer_status moer_idf_fit(const moer_dims* d, const int32_t* req_cnt, in
  * and gradient, the block plan of a batch, and the experts' token lists.
  * ------------------------------------------------------------------------ */
 
-/* Element types of router logits. */
-typedef enum moer_dtype { MOER_F32 = 0, MOER_BF16 = 1, MOER_F16 = 2 } moer_dtype;
+/* Element types (E4M3: the 8-bit rows of the expert operators alone). */
+typedef enum moer_dtype { MOER_F32 = 0, MOER_BF16 = 1, MOER_F16 = 2, MOER_E4M3 = 3 } moer_dtype;
 
 /* How logits become scores. */
 typedef enum moer_score_fn { MOER_SCORE_SOFTMAX = 0, MOER_SCORE_SIGMOID = 1 } moer_score_fn;
@@ -567,6 +567,166 @@ MOER_API size_t moer_expert_order_workspace_bytes(const moer_dims* d, int64_t T)
 MOER_API moer_status moer_expert_order(const moer_dims* d, const uint8_t* topk, int64_t T, int32_t align,
                                        int32_t* expert_off, int32_t* order, int64_t ld_order, int32_t* inv, void* ws,
                                        size_t ws_bytes, moer_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Expert operators: what a layer computes with the router's lists.  The norm
+ * before the router and the experts, the experts' matrix products over their
+ * token lists, the gated activation between two products, the combination of
+ * the experts' rows per token, and the gradient of each.
+ *   No passage of the pages corresponds to them: [GRACE] section 1 dispatches
+ *   tokens to the experts that they chose and combines what those return, and
+ *   leaves the products to the engine.
+ * Each takes a struct of arguments (pointers are device pointers; those marked
+ * "or NULL" are optional; ld_* are elements between neighbouring rows).  Rows
+ * that a call does not name are left as they were.  Sums are held in fp32 and
+ * rounded once, to the type of the output.  A buffer may be given twice only
+ * where its comment says so.
+ *
+ * 8-bit rows: a row of e4m3 values (largest 448) with one fp32 scale for each
+ * block of 128 neighbouring columns (the last one may be shorter); column c
+ * stands for q[c] * scale[c / 128].  scale = max(largest |value| of the block,
+ * 1e-30) / 448, taken from the fp32 values and not from their 16-bit roundings.  A
+ * NaN stays NaN and does not enter the scale; an infinity makes its block's
+ * scale infinite and its values NaN.
+ * ------------------------------------------------------------------------ */
+
+/* Root-mean-square norm of rows, with the residual's addition in front.
+ *   s = x + residual, rounded to dtype (x itself without a residual);
+ *   rstd = 1 / sqrt(mean over the row of s^2 + eps);  y = s * rstd * weight.
+ * Gradient (moer_rms_norm_grad), from sum and rstd as the forward call left
+ * them, with n = s * rstd:
+ *   d_x = rstd * (d_y * weight - n * mean(d_y * weight * n)) + d_sum
+ *   (the gradient of x and of the residual alike), d_weight = sum over rows of
+ *   d_y * n, summed in a fixed order. */
+typedef struct moer_norm_args {
+  int64_t T;            /* rows, 0 .. 2^31 - 1                                        */
+  int32_t H;            /* columns, 1 .. 16384                                         */
+  int32_t dtype;        /* moer_dtype (F32, BF16, F16) of x, residual, weight, sum, y  */
+  float eps;            /* >= 0, finite                                                */
+  int64_t ld_x, ld_residual, ld_sum, ld_y, ld_q, ld_scale; /* >= the row's columns (ld_scale: blocks) */
+  int64_t ld_d_y, ld_d_sum, ld_d_x;
+  const void* x;        /* [T][H]                                          forward     */
+  const void* residual; /* [T][H] or NULL                                  forward     */
+  const void* weight;   /* [H]                                                         */
+  void* sum;            /* [T][H]: forward out or NULL (may be x or residual, with the
+                           same rows); gradient in                                     */
+  void* y;              /* [T][H] out or NULL (may be x)                   forward     */
+  void* q;              /* [T][H] e4m3 out or NULL                         forward     */
+  float* scale;         /* [T][blocks] out, with q                         forward     */
+  float* rstd;          /* [T]: forward out or NULL; gradient in                       */
+  const void* d_y;      /* [T][H] of dtype                                 gradient    */
+  const void* d_sum;    /* [T][H] of dtype or NULL: the gradient by sum    gradient    */
+  void* d_x;            /* [T][H] of dtype out (may be d_y or d_sum)       gradient    */
+  float* d_weight;      /* [H] out or NULL                                 gradient    */
+} moer_norm_args;
+
+/* ws  at least moer_rms_norm_workspace_bytes(T, H) bytes (which do not fall as T
+ * grows), 16-byte aligned; the forward call needs none (NULL, 0).  T = 0
+ * writes nothing but a zero d_weight. */
+MOER_API size_t moer_rms_norm_workspace_bytes(int64_t T, int32_t H);
+MOER_API moer_status moer_rms_norm(const moer_norm_args* a, void* ws, size_t ws_bytes, moer_stream_t stream);
+MOER_API moer_status moer_rms_norm_grad(const moer_norm_args* a, void* ws, size_t ws_bytes, moer_stream_t stream);
+
+/* Which of an expert's products. */
+typedef enum moer_gemm_op {
+  MOER_GEMM_FORWARD = 0,     /* out[p][n] = sum_k x[r(p)][k] * w[e][n][k]               */
+  MOER_GEMM_GRAD_INPUT = 1,  /* out[p][k] = sum_n x[r(p)][n] * w[e][n][k], x: d_out     */
+  MOER_GEMM_GRAD_WEIGHT = 2  /* out[e][n][k] = sum over e's p of d_y[p][n] * x[r(p)][k] */
+} moer_gemm_op;
+
+/* Matrix products grouped by expert, on the tensor cores.  Row p of expert e's
+ * segment [expert_off[e], expert_off[e+1]) is row r(p) of x: order[p] / k with
+ * an order (the tokens that the expert's list names; nothing is gathered in
+ * between), p itself without one.  A row with order[p] < 0 (padding) gives a row
+ * of zeros, and nothing to the weights' gradient, whatever d_y holds there.
+ * Rows from expert_off[E] on are left as they were; an expert without rows has
+ * a gradient of zeros.
+ *   E4M3: x and w are 8-bit, x in rows as above and w with one scale for each
+ *   block of 128 x 128; the products of a block of 128 are summed in fp32, and
+ *   so are the blocks' sums times their two scales.  FORWARD only. */
+typedef struct moer_expert_gemm_args {
+  int32_t op;           /* moer_gemm_op                                                 */
+  int32_t E;            /* experts, 1 .. 1024                                           */
+  int32_t N, K;         /* an expert's weights are [N][K]; 1 .. 65536                   */
+  int32_t k;            /* choices per token (with order), 1 .. 2^20                    */
+  int32_t dtype;        /* moer_dtype of x, w, d_y: BF16, F16 or E4M3                   */
+  int32_t out_dtype;    /* F32, BF16 or F16                                             */
+  int64_t rows;         /* rows of the lists, 0 .. 2^31 - 1                             */
+  int64_t tokens;       /* rows of x, 0 .. 2^31 - 1 (without order: >= rows)            */
+  int64_t ld_x, ld_d_y, ld_w, ld_out;   /* >= the row's columns                         */
+  int64_t stride_w, stride_out;         /* elements between neighbouring experts        */
+  int64_t ld_x_scale;                   /* E4M3: >= blocks of a row                     */
+  const int32_t* expert_off; /* [E+1] non-decreasing, within [0, rows]                  */
+  const int32_t* order;      /* [rows] or NULL                                          */
+  const void* x;             /* [tokens][K] (GRAD_INPUT: [tokens][N])                   */
+  const float* x_scale;      /* E4M3: [tokens][ceil(K/128)]                             */
+  const void* w;             /* [E][N][K]; not for GRAD_WEIGHT                          */
+  const float* w_scale;      /* E4M3: [E][ceil(N/128)][ceil(K/128)], dense              */
+  const void* d_y;           /* [rows][N], GRAD_WEIGHT                                  */
+  void* out;                 /* [rows][N], [rows][K] or [E][N][K]                       */
+} moer_expert_gemm_args;
+
+/* x, w and d_y are 16-byte aligned, and so is each of their rows (ld and stride_w a
+ * multiple of 8, with E4M3 of 16); out is aligned to its element.  An offset
+ * outside the limits is moved to the nearest one within them and records
+ * MOER_EDATA in ws; an order entry that names no row of x counts as padding
+ * and records it too.
+ * ws  at least moer_expert_gemm_workspace_bytes(a) bytes, 16-byte aligned. */
+MOER_API size_t moer_expert_gemm_workspace_bytes(const moer_expert_gemm_args* a);
+MOER_API moer_status moer_expert_gemm(const moer_expert_gemm_args* a, void* ws, size_t ws_bytes, moer_stream_t stream);
+
+/* Gated activation of the experts' rows: with h = [a | b], two halves of I columns,
+ *   y = a / (1 + exp(-a)) * b, rounded to dtype and/or as 8-bit rows.
+ * Gradient: d_h = [d_y * b * s * (1 + a * (1 - s)) | d_y * a * s], s = 1 / (1 + exp(-a)). */
+typedef struct moer_expert_act_args {
+  int64_t rows;         /* 0 .. 2^31 - 1                                                */
+  int32_t I;            /* 1 .. 65536                                                   */
+  int32_t dtype;        /* F32, BF16 or F16                                             */
+  int64_t ld_h, ld_y, ld_q, ld_scale, ld_d_y, ld_d_h;
+  const int32_t* used;  /* [1] or NULL: rows [0, *used) are taken (expert_off + E), the
+                           others left as they were; NULL: all                          */
+  const void* h;        /* [rows][2 I]                                                  */
+  void* y;              /* [rows][I] out or NULL                           forward      */
+  void* q;              /* [rows][I] e4m3 out or NULL                      forward      */
+  float* scale;         /* [rows][ceil(I/128)] out, with q                 forward      */
+  const void* d_y;      /* [rows][I]                                       gradient     */
+  void* d_h;            /* [rows][2 I] out (may be h, with the same rows)  gradient     */
+} moer_expert_act_args;
+
+MOER_API moer_status moer_expert_act(const moer_expert_act_args* a, moer_stream_t stream);
+MOER_API moer_status moer_expert_act_grad(const moer_expert_act_args* a, moer_stream_t stream);
+
+/* The experts' rows back to their tokens:
+ *   out[t] = add[t] + sum_j weights[t][j] * z[inv[t][j]], j in ascending order.
+ * Gradient: d_z[p] = weights[t][j] * d_out[t] for the pair t * k + j = order[p],
+ * zeros in every row with order[p] < 0; d_weights[t][j] = sum over the columns
+ * of d_out[t] * z[inv[t][j]]. */
+typedef struct moer_expert_combine_args {
+  int64_t T;            /* tokens, 0 .. 2^31 - 1                                        */
+  int32_t H;            /* columns, 1 .. 65536                                          */
+  int32_t k;            /* choices per token, 1 .. 32                                   */
+  int64_t rows;         /* rows of z, 0 .. 2^31 - 1                                     */
+  int32_t dtype;        /* F32, BF16 or F16                                             */
+  int64_t ld_z, ld_add, ld_out, ld_d_out, ld_d_z;
+  const int32_t* inv;   /* [T][k]: each pair's row; < 0: none (adds nothing, gradient 0) */
+  const int32_t* order; /* [rows], gradient: the pair of each row                       */
+  const float* weights; /* [T][k] or NULL: all 1                                        */
+  const void* z;        /* [rows][H] (gradient: or NULL where d_weights is)             */
+  const void* add;      /* [T][H] or NULL                                  forward      */
+  void* out;            /* [T][H] out (may be add, with the same rows)     forward      */
+  const void* d_out;    /* [T][H]                                          gradient     */
+  void* d_z;            /* [rows][H] out or NULL                           gradient     */
+  float* d_weights;     /* [T][k] out or NULL                              gradient     */
+} moer_expert_combine_args;
+
+/* A row past `rows` counts as none and records MOER_EDATA in ws; so does, in
+ * the gradient, a pair whose row's order entry names another pair (its
+ * d_z is then not written).
+ * ws  at least 256 bytes, 16-byte aligned (the status word). */
+MOER_API moer_status moer_expert_combine(const moer_expert_combine_args* a, void* ws, size_t ws_bytes,
+                                         moer_stream_t stream);
+MOER_API moer_status moer_expert_combine_grad(const moer_expert_combine_args* a, void* ws, size_t ws_bytes,
+                                              moer_stream_t stream);
 
 /* Waits for `stream`, then returns the status recorded in the workspace
  * (MOER_OK, MOER_EDATA or MOER_ETIMEOUT) and clears it.  `ws` is a device

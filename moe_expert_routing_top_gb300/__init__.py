@@ -12,4 +12,8 @@ from ._native import (moer_dims, make_dims, MoerError, moer_workspace_bytes,  # 
                       moer_extent_checks, moer_buffer_holds, moer_score_opts, make_score_opts,
                       moer_score_workspace_bytes, moer_score_topk, moer_score_topk_grad,
                       moer_block_plan_args, make_block_plan, moer_block_plan_workspace_bytes, moer_block_plan,
-                      moer_expert_order_workspace_bytes, moer_expert_order, EXPORTS)
+                      moer_expert_order_workspace_bytes, moer_expert_order,
+                      moer_norm_args, make_norm, moer_rms_norm_workspace_bytes, moer_rms_norm, moer_rms_norm_grad,
+                      moer_expert_gemm_args, make_expert_gemm, moer_expert_gemm_workspace_bytes, moer_expert_gemm,
+                      moer_expert_act_args, make_expert_act, moer_expert_act, moer_expert_act_grad,
+                      moer_expert_combine_args, make_expert_combine, moer_expert_combine, moer_expert_combine_grad, EXPORTS)

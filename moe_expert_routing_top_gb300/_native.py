@@ -43,7 +43,37 @@ class moer_block_plan_args(ctypes.Structure):
                                                 "tok_req", "tok_pos", "totals")])
 
 
-DTYPES = {"f32": 0, "bf16": 1, "f16": 2}
+def _fields(i32="", i64="", ptr="", f32="", order=None):
+    kinds = {n: t for names, t in ((i32, ctypes.c_int32), (i64, ctypes.c_int64), (f32, ctypes.c_float), (ptr, ctypes.c_void_p))
+             for n in names.split()}
+    return [(n, kinds[n]) for n in (order or " ".join((i32, i64, f32, ptr))).split()]
+
+
+class moer_norm_args(ctypes.Structure):
+    _fields_ = _fields(i64="T ld_x ld_residual ld_sum ld_y ld_q ld_scale ld_d_y ld_d_sum ld_d_x", i32="H dtype", f32="eps",
+                       ptr="x residual weight sum y q scale rstd d_y d_sum d_x d_weight",
+                       order="T H dtype eps ld_x ld_residual ld_sum ld_y ld_q ld_scale ld_d_y ld_d_sum ld_d_x "
+                             "x residual weight sum y q scale rstd d_y d_sum d_x d_weight")
+
+
+class moer_expert_gemm_args(ctypes.Structure):
+    _fields_ = _fields(i32="op E N K k dtype out_dtype", i64="rows tokens ld_x ld_d_y ld_w ld_out stride_w stride_out ld_x_scale",
+                       ptr="expert_off order x x_scale w w_scale d_y out")
+
+
+class moer_expert_act_args(ctypes.Structure):
+    _fields_ = _fields(i64="rows ld_h ld_y ld_q ld_scale ld_d_y ld_d_h", i32="I dtype", ptr="used h y q scale d_y d_h",
+                       order="rows I dtype ld_h ld_y ld_q ld_scale ld_d_y ld_d_h used h y q scale d_y d_h")
+
+
+class moer_expert_combine_args(ctypes.Structure):
+    _fields_ = _fields(i64="T rows ld_z ld_add ld_out ld_d_out ld_d_z", i32="H k dtype",
+                       ptr="inv order weights z add out d_out d_z d_weights",
+                       order="T H k rows dtype ld_z ld_add ld_out ld_d_out ld_d_z inv order weights z add out d_out d_z d_weights")
+
+
+DTYPES = {"f32": 0, "bf16": 1, "f16": 2, "e4m3": 3}
+GEMM_OPS = {"forward": 0, "grad_input": 1, "grad_weight": 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 
@@ -65,6 +95,55 @@ def make_block_plan(*, R, block, T=0, nblk=0, ncached=0, ld_pages=0, n_free=0, *
         setattr(a, n, _ptr(x))
     a._keepalive = buffers
     return a
+
+
+def _make(cls, values, strides):
+    """A struct of arguments from values, tensors and addresses by field name.  A tensor's row
+    stride goes to its ld field unless that is given; its elements in a row have to be contiguous.
+    The buffers are kept alive on the struct."""
+    a, kinds = cls(), dict(cls._fields_)
+    for n, x in values.items():
+        if n not in kinds:
+            raise TypeError(f"{cls.__name__} has no field {n!r}")
+        if kinds[n] is not ctypes.c_void_p:
+            setattr(a, n, DTYPES.get(x, x) if n in ("dtype", "out_dtype") else GEMM_OPS.get(x, x) if n == "op" else x)
+            continue
+        setattr(a, n, _ptr(x))
+        if n in strides and hasattr(x, "stride"):
+            if x.dim() < 2 or x.shape[-1] > 1 and x.stride(-1) != 1:
+                raise ValueError(f"{n}: the elements of a row have to be contiguous")
+            for ld, dim in strides[n]:
+                if ld not in values and x.dim() >= -dim:
+                    setattr(a, ld, max(x.stride(dim), x.shape[-1]) if x.shape[dim] == 1 else x.stride(dim))
+        elif hasattr(x, "is_contiguous") and not x.is_contiguous():
+            raise ValueError(f"{n} has to be contiguous")
+    a._keepalive = values
+    return a
+
+
+def _rows_of(*names):
+    return {n: [("ld_" + n, -2)] for n in names}
+
+
+def make_norm(**values) -> moer_norm_args:
+    """Arguments of moer_rms_norm and moer_rms_norm_grad by field name (dtype by name or number)."""
+    return _make(moer_norm_args, values, _rows_of("x", "residual", "sum", "y", "q", "scale", "d_y", "d_sum", "d_x"))
+
+
+def make_expert_gemm(**values) -> moer_expert_gemm_args:
+    """Arguments of moer_expert_gemm by field name (op and types by name or number)."""
+    return _make(moer_expert_gemm_args, values,
+                 {**_rows_of("x", "d_y", "x_scale"), "w": [("ld_w", -2), ("stride_w", -3)], "out": [("ld_out", -2), ("stride_out", -3)]})
+
+
+def make_expert_act(**values) -> moer_expert_act_args:
+    """Arguments of moer_expert_act and moer_expert_act_grad by field name."""
+    return _make(moer_expert_act_args, values, _rows_of("h", "y", "q", "scale", "d_y", "d_h"))
+
+
+def make_expert_combine(**values) -> moer_expert_combine_args:
+    """Arguments of moer_expert_combine and moer_expert_combine_grad by field name."""
+    return _make(moer_expert_combine_args, values, _rows_of("z", "add", "out", "d_out", "d_z"))
 
 
 def make_dims(E: int, k: int, L: int, mask, block: int = 16) -> moer_dims:
@@ -112,6 +191,15 @@ def _load():
         "moer_block_plan": ([ctypes.POINTER(moer_block_plan_args), vp, sz, vp], ctypes.c_int),
         "moer_expert_order_workspace_bytes": ([dp, i64], sz),
         "moer_expert_order": ([dp, vp, i64, i32, vp, vp, i64, vp, vp, sz, vp], ctypes.c_int),
+        "moer_rms_norm_workspace_bytes": ([i64, i32], sz),
+        "moer_rms_norm": ([ctypes.POINTER(moer_norm_args), vp, sz, vp], ctypes.c_int),
+        "moer_rms_norm_grad": ([ctypes.POINTER(moer_norm_args), vp, sz, vp], ctypes.c_int),
+        "moer_expert_gemm_workspace_bytes": ([ctypes.POINTER(moer_expert_gemm_args)], sz),
+        "moer_expert_gemm": ([ctypes.POINTER(moer_expert_gemm_args), vp, sz, vp], ctypes.c_int),
+        "moer_expert_act": ([ctypes.POINTER(moer_expert_act_args), vp], ctypes.c_int),
+        "moer_expert_act_grad": ([ctypes.POINTER(moer_expert_act_args), vp], ctypes.c_int),
+        "moer_expert_combine": ([ctypes.POINTER(moer_expert_combine_args), vp, sz, vp], ctypes.c_int),
+        "moer_expert_combine_grad": ([ctypes.POINTER(moer_expert_combine_args), vp, sz, vp], ctypes.c_int),
         "moer_ws_status": ([vp, vp], ctypes.c_int),
         "moer_wait_selftest": ([vp, sz, ctypes.c_uint32, vp], ctypes.c_int),
         "moer_status_str": ([ctypes.c_int], ctypes.c_char_p),
@@ -138,6 +226,9 @@ EXPORTS = ("moer_workspace_bytes", "moer_topk_signature", "moer_topk_signature_n
            "moer_score_workspace_bytes", "moer_score_topk", "moer_score_topk_grad",
            "moer_block_plan_workspace_bytes", "moer_block_plan",
            "moer_expert_order_workspace_bytes", "moer_expert_order",
+           "moer_rms_norm_workspace_bytes", "moer_rms_norm", "moer_rms_norm_grad",
+           "moer_expert_gemm_workspace_bytes", "moer_expert_gemm", "moer_expert_act", "moer_expert_act_grad",
+           "moer_expert_combine", "moer_expert_combine_grad",
            "moer_ws_status", "moer_wait_selftest",
            "moer_status_str", "moer_version", "moer_set_extent_checks", "moer_extent_checks",
            "moer_buffer_holds")
@@ -315,6 +406,47 @@ def moer_expert_order(dims, topk, T, align, expert_off, order, ld_order, inv, ws
     _check("moer_expert_order", LIB.moer_expert_order(
         ctypes.byref(dims), _ptr(topk), int(T), int(align), _ptr(expert_off), _ptr(order), int(ld_order),
         _ptr(inv), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moer_rms_norm_workspace_bytes(T: int, H: int) -> int:
+    return int(LIB.moer_rms_norm_workspace_bytes(int(T), int(H)))
+
+
+def moer_rms_norm(args, ws=None, ws_bytes=0, stream=None) -> None:
+    """Residual addition, norm and 8-bit rows; `args` from make_norm."""
+    _check("moer_rms_norm", LIB.moer_rms_norm(ctypes.byref(args), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moer_rms_norm_grad(args, ws, ws_bytes, stream=None) -> None:
+    _check("moer_rms_norm_grad", LIB.moer_rms_norm_grad(ctypes.byref(args), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moer_expert_gemm_workspace_bytes(args) -> int:
+    return int(LIB.moer_expert_gemm_workspace_bytes(ctypes.byref(args)))
+
+
+def moer_expert_gemm(args, ws, ws_bytes, stream=None) -> None:
+    """The experts' products over their token lists; `args` from make_expert_gemm."""
+    _check("moer_expert_gemm", LIB.moer_expert_gemm(ctypes.byref(args), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moer_expert_act(args, stream=None) -> None:
+    """Gated activation of the experts' rows; `args` from make_expert_act."""
+    _check("moer_expert_act", LIB.moer_expert_act(ctypes.byref(args), _stream(stream)))
+
+
+def moer_expert_act_grad(args, stream=None) -> None:
+    _check("moer_expert_act_grad", LIB.moer_expert_act_grad(ctypes.byref(args), _stream(stream)))
+
+
+def moer_expert_combine(args, ws, ws_bytes, stream=None) -> None:
+    """The experts' rows back to their tokens; `args` from make_expert_combine."""
+    _check("moer_expert_combine", LIB.moer_expert_combine(ctypes.byref(args), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def moer_expert_combine_grad(args, ws, ws_bytes, stream=None) -> None:
+    _check("moer_expert_combine_grad", LIB.moer_expert_combine_grad(ctypes.byref(args), _ptr(ws), int(ws_bytes),
+                                                                   _stream(stream)))
 
 
 def moer_ws_status(ws, stream=None) -> int:

@@ -20,7 +20,8 @@ SOURCES = ["api.cu", "topk_signature.cu", "topk_signature_tpr.cu", "block_counts
            "replicate.cu", "mask_select.cu", "spectral.cu", "selftest.cu",
            "score_topk.cu", "score_fast_f32.cu", "score_fast_bf16.cu", "score_fast_f16.cu",
            "score_fast16_f32.cu", "score_fast16_bf16.cu", "score_fast16_f16.cu",
-           "score_grad.cu", "score_grad_f32.cu", "score_grad_bf16.cu", "score_grad_f16.cu", "block_plan.cu", "expert_order.cu"]
+           "score_grad.cu", "score_grad_f32.cu", "score_grad_bf16.cu", "score_grad_f16.cu", "block_plan.cu", "expert_order.cu",
+           "norm.cu", "expert_gemm.cu", "expert_act.cu", "expert_combine.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", os.path.join(os.path.dirname(HERE), "include")]

@@ -61,6 +61,12 @@ moer_status block_plan_launch(const moer_block_plan_args* a, void* ws, cudaStrea
 size_t expert_order_scratch_bytes(const moer_dims* d, int64_t T);
 moer_status expert_order_launch(const moer_dims* d, const uint8_t* topk, int64_t T, int32_t align, int32_t* off,
                                 int32_t* order, int64_t ld, int32_t* inv, void* ws, cudaStream_t st);
+size_t rms_norm_scratch_bytes(int32_t H);
+moer_status rms_norm_launch(const moer_norm_args* a, cudaStream_t st);
+moer_status rms_norm_grad_launch(const moer_norm_args* a, void* scratch, cudaStream_t st);
+moer_status expert_gemm_launch(const moer_expert_gemm_args* a, void* ws, cudaStream_t st);
+moer_status expert_act_launch(const moer_expert_act_args* a, bool grad, cudaStream_t st);
+moer_status expert_combine_launch(const moer_expert_combine_args* a, bool grad, void* ws, cudaStream_t st);
 
 namespace {
 
@@ -190,6 +196,64 @@ ScoreParams score_params(const moer_dims* d, const moer_score_opts* o, const voi
   p.group_best = o->group_best;
   p.scale = o->scale;
   return p;
+}
+
+// A matrix argument of the expert operators: rows of `cols` elements, `ld` apart.
+struct Matrix {
+  const void* p;
+  int64_t rows, cols, ld;
+  int elem;
+  size_t align;
+  bool needed;
+};
+constexpr int64_t MOST_LD = int64_t(1) << 36;  // elements between rows (a TMA stride has 40 bits of bytes)
+
+// Bytes from the first row's start to the last row's end.
+size_t extent_of(const Matrix& m) {
+  return m.p == nullptr || m.rows <= 0 ? 0 : (sz(m.rows - 1) * sz(m.ld) + sz(m.cols)) * sz(m.elem);
+}
+
+moer_status check_matrices(std::initializer_list<Matrix> list) {
+  for (const Matrix& m : list) {
+    if (m.p == nullptr && m.needed) return MOER_EINVAL;
+    if (m.p != nullptr && !aligned(m.p, m.align)) return MOER_EINVAL;
+  }
+  for (const Matrix& m : list) {
+    if (m.p == nullptr) continue;
+    if (m.ld < m.cols || m.ld > MOST_LD) return MOER_ESHAPE;
+    if (m.rows > 1 && m.ld > (int64_t(1) << 60) / m.rows) return MOER_ESHAPE;
+  }
+  return MOER_OK;
+}
+
+bool is_float_dtype(int dtype) { return dtype == MOER_F32 || dtype == MOER_BF16 || dtype == MOER_F16; }
+constexpr int64_t MOST_ROWS = (int64_t(1) << 31) - 1;
+int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+
+moer_status check_norm(const moer_norm_args* a) {
+  if (a == nullptr) return MOER_EINVAL;
+  if (!is_float_dtype(a->dtype)) return MOER_EINVAL;
+  if (a->T < 0 || a->T > MOST_ROWS || a->H < 1 || a->H > 16384) return MOER_ERANGE;
+  if (!(a->eps >= 0.f) || !(a->eps - a->eps == 0.f)) return MOER_ERANGE;
+  return MOER_OK;
+}
+
+moer_status check_act(const moer_expert_act_args* a) {
+  if (a == nullptr) return MOER_EINVAL;
+  if (!is_float_dtype(a->dtype)) return MOER_EINVAL;
+  if (a->rows < 0 || a->rows > MOST_ROWS || a->I < 1 || a->I > 65536) return MOER_ERANGE;
+  return aligned(a->used, 4) ? MOER_OK : MOER_EINVAL;
+}
+
+moer_status check_combine(const moer_expert_combine_args* a, const void* ws, size_t ws_bytes) {
+  if (a == nullptr) return MOER_EINVAL;
+  if (!is_float_dtype(a->dtype)) return MOER_EINVAL;
+  if (a->T < 0 || a->T > MOST_ROWS || a->rows < 0 || a->rows > MOST_ROWS) return MOER_ERANGE;
+  if (a->H < 1 || a->H > 65536 || a->k < 1 || a->k > 32 || a->T * a->k > MOST_ROWS) return MOER_ERANGE;
+  if (!aligned(a->inv, 4) || !aligned(a->order, 4) || !aligned(a->weights, 4) || !aligned(a->d_weights, 4)) return MOER_EINVAL;
+  if (a->T > 0 && a->inv == nullptr) return MOER_EINVAL;
+  if (ws == nullptr || !aligned(ws, 16)) return MOER_EINVAL;
+  return ws_bytes < WS_HEADER ? MOER_ENOMEM : MOER_OK;
 }
 
 // Extents of the logits-pass buffers (moer_topk_signature and its no-alloc form).
@@ -753,6 +817,164 @@ moer_status moer_expert_order(const moer_dims* d, const uint8_t* topk, int64_t T
   }
   return moer::expert_order_launch(d, topk, T, align, expert_off, order, ld_order, inv, ws,
                                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moer_rms_norm_workspace_bytes(int64_t T, int32_t H) {
+  (void)T;
+  return WS_HEADER + (H >= 1 && H <= 16384 ? moer::rms_norm_scratch_bytes(H) : 0);
+}
+
+moer_status moer_rms_norm(const moer_norm_args* a, void* ws, size_t ws_bytes, moer_stream_t stream) {
+  moer_status s = check_norm(a);
+  if (s != MOER_OK) return s;
+  (void)ws, (void)ws_bytes;
+  if (a->T == 0) return MOER_OK;
+  const int eb = elem_bytes(a->dtype);
+  const size_t al = sz(eb);
+  const Matrix x{a->x, a->T, a->H, a->ld_x, eb, al, true}, r{a->residual, a->T, a->H, a->ld_residual, eb, al, false},
+      w{a->weight, 1, a->H, a->H, eb, al, true}, sum{a->sum, a->T, a->H, a->ld_sum, eb, al, false},
+      y{a->y, a->T, a->H, a->ld_y, eb, al, false}, q{a->q, a->T, a->H, a->ld_q, 1, 1, false},
+      sc{a->scale, a->T, blocks128(a->H), a->ld_scale, 4, 4, a->q != nullptr}, rs{a->rstd, a->T, 1, 1, 4, 4, false};
+  s = check_matrices({x, r, w, sum, y, q, sc, rs});
+  if (s != MOER_OK) return s;
+  s = check_extents({{x.p, extent_of(x)}, {r.p, extent_of(r)}, {w.p, extent_of(w)}, {sum.p, extent_of(sum)}, {y.p, extent_of(y)},
+                     {q.p, extent_of(q)}, {q.p != nullptr ? sc.p : nullptr, extent_of(sc)}, {rs.p, extent_of(rs)}});
+  if (s != MOER_OK) return s;
+  return moer::rms_norm_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moer_status moer_rms_norm_grad(const moer_norm_args* a, void* ws, size_t ws_bytes, moer_stream_t stream) {
+  moer_status s = check_norm(a);
+  if (s != MOER_OK) return s;
+  const int eb = elem_bytes(a->dtype);
+  const size_t al = sz(eb);
+  const bool any = a->T > 0;
+  const Matrix sum{a->sum, a->T, a->H, a->ld_sum, eb, al, any}, w{a->weight, 1, a->H, a->H, eb, al, any},
+      rs{a->rstd, a->T, 1, 1, 4, 4, any}, dy{a->d_y, a->T, a->H, a->ld_d_y, eb, al, any},
+      ds{a->d_sum, a->T, a->H, a->ld_d_sum, eb, al, false}, dx{a->d_x, a->T, a->H, a->ld_d_x, eb, al, any},
+      dw{a->d_weight, 1, a->H, a->H, 4, 4, false};
+  if (any) s = check_matrices({sum, w, rs, dy, ds, dx, dw});
+  else s = check_matrices({dw});
+  if (s != MOER_OK) return s;
+  if (ws == nullptr || !aligned(ws, 16)) return MOER_EINVAL;
+  if (ws_bytes < moer_rms_norm_workspace_bytes(a->T, a->H)) return MOER_ENOMEM;
+  s = any ? check_extents({{sum.p, extent_of(sum)}, {w.p, extent_of(w)}, {rs.p, extent_of(rs)}, {dy.p, extent_of(dy)},
+                           {ds.p, extent_of(ds)}, {dx.p, extent_of(dx)}, {dw.p, extent_of(dw)}, {ws, ws_bytes}})
+          : check_extents({{dw.p, extent_of(dw)}, {ws, ws_bytes}});
+  if (s != MOER_OK) return s;
+  return moer::rms_norm_grad_launch(a, static_cast<char*>(ws) + WS_HEADER, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moer_expert_gemm_workspace_bytes(const moer_expert_gemm_args* a) {
+  (void)a;
+  return WS_HEADER;
+}
+
+moer_status moer_expert_gemm(const moer_expert_gemm_args* a, void* ws, size_t ws_bytes, moer_stream_t stream) {
+  if (a == nullptr) return MOER_EINVAL;
+  if (a->op < MOER_GEMM_FORWARD || a->op > MOER_GEMM_GRAD_WEIGHT) return MOER_EINVAL;
+  const bool fp8 = a->dtype == MOER_E4M3, gw = a->op == MOER_GEMM_GRAD_WEIGHT;
+  if (!fp8 && a->dtype != MOER_BF16 && a->dtype != MOER_F16) return MOER_EINVAL;
+  if (fp8 && a->op != MOER_GEMM_FORWARD) return MOER_EINVAL;
+  if (!is_float_dtype(a->out_dtype)) return MOER_EINVAL;
+  if (a->E < 1 || a->E > 1024 || a->N < 1 || a->N > 65536 || a->K < 1 || a->K > 65536) return MOER_ERANGE;
+  if (a->rows < 0 || a->rows > MOST_ROWS || a->tokens < 0 || a->tokens > MOST_ROWS) return MOER_ERANGE;
+  if (a->order != nullptr && (a->k < 1 || a->k > (1 << 20))) return MOER_ERANGE;
+  if (a->order == nullptr && a->tokens < a->rows) return MOER_ESHAPE;
+  if (a->rows == 0 && !gw) return MOER_OK;
+  if (a->expert_off == nullptr || !aligned(a->expert_off, 4) || !aligned(a->order, 4)) return MOER_EINVAL;
+  const int eb = fp8 ? 1 : 2, ob = elem_bytes(a->out_dtype);
+  const int64_t xc = a->op == MOER_GEMM_GRAD_INPUT ? a->N : a->K, oc = a->op == MOER_GEMM_FORWARD ? a->N : a->K;
+  const int64_t nkb = blocks128(a->K), nnb = blocks128(a->N);
+  const bool any = a->rows > 0;
+  const Matrix x{a->x, a->tokens, xc, a->ld_x, eb, 16, any && a->tokens > 0}, w{gw ? nullptr : a->w, a->N, a->K, a->ld_w, eb, 16, !gw},
+      dy{gw ? a->d_y : nullptr, a->rows, a->N, a->ld_d_y, eb, 16, gw && any}, out{a->out, gw ? a->N : a->rows, oc, a->ld_out, ob, sz(ob), true},
+      xs{fp8 ? a->x_scale : nullptr, a->tokens, nkb, a->ld_x_scale, 4, 4, fp8 && a->tokens > 0}, ws8{fp8 ? a->w_scale : nullptr, a->E * nnb, nkb, nkb, 4, 4, fp8};
+  moer_status s = check_matrices({x, w, dy, out, xs, ws8});
+  if (s != MOER_OK) return s;
+  for (const Matrix& m : {x, w, dy})
+    if (m.p != nullptr && m.ld * eb % 16 != 0) return MOER_EINVAL;
+  const int64_t most = int64_t(1) << 48;
+  if (a->E > 1 && !gw && (a->stride_w < 0 || a->stride_w > most)) return MOER_ESHAPE;
+  if (a->E > 1 && !gw && a->stride_w * eb % 16 != 0) return MOER_EINVAL;
+  if (a->E > 1 && gw && (a->stride_out < (a->N - 1) * a->ld_out + a->K || a->stride_out > most)) return MOER_ESHAPE;
+  if (ws == nullptr || !aligned(ws, 16)) return MOER_EINVAL;
+  if (ws_bytes < moer_expert_gemm_workspace_bytes(a)) return MOER_ENOMEM;
+  const size_t more = sz(a->E - 1);
+  s = check_extents({{a->expert_off, (sz(a->E) + 1) * 4},
+                     {a->order, sz(a->rows) * 4},
+                     {x.p, extent_of(x)},
+                     {w.p, extent_of(w) + more * sz(a->stride_w) * sz(eb)},
+                     {dy.p, extent_of(dy)},
+                     {out.p, extent_of(out) + (gw ? more * sz(a->stride_out) * sz(ob) : 0)},
+                     {xs.p, extent_of(xs)},
+                     {ws8.p, extent_of(ws8)},
+                     {ws, ws_bytes}});
+  if (s != MOER_OK) return s;
+  return moer::expert_gemm_launch(a, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moer_status moer_expert_act(const moer_expert_act_args* a, moer_stream_t stream) {
+  moer_status s = check_act(a);
+  if (s != MOER_OK) return s;
+  if (a->rows == 0) return MOER_OK;
+  const int eb = elem_bytes(a->dtype);
+  const size_t al = sz(eb);
+  const Matrix h{a->h, a->rows, 2 * (int64_t)a->I, a->ld_h, eb, al, true}, y{a->y, a->rows, a->I, a->ld_y, eb, al, false},
+      q{a->q, a->rows, a->I, a->ld_q, 1, 1, false}, sc{a->q != nullptr ? a->scale : nullptr, a->rows, blocks128(a->I), a->ld_scale, 4, 4, a->q != nullptr};
+  s = check_matrices({h, y, q, sc});
+  if (s != MOER_OK) return s;
+  if (a->y == nullptr && a->q == nullptr) return MOER_EINVAL;
+  s = check_extents({{h.p, extent_of(h)}, {y.p, extent_of(y)}, {q.p, extent_of(q)}, {sc.p, extent_of(sc)}, {a->used, 4}});
+  if (s != MOER_OK) return s;
+  return moer::expert_act_launch(a, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moer_status moer_expert_act_grad(const moer_expert_act_args* a, moer_stream_t stream) {
+  moer_status s = check_act(a);
+  if (s != MOER_OK) return s;
+  if (a->rows == 0) return MOER_OK;
+  const int eb = elem_bytes(a->dtype);
+  const size_t al = sz(eb);
+  const Matrix h{a->h, a->rows, 2 * (int64_t)a->I, a->ld_h, eb, al, true}, dy{a->d_y, a->rows, a->I, a->ld_d_y, eb, al, true},
+      dh{a->d_h, a->rows, 2 * (int64_t)a->I, a->ld_d_h, eb, al, true};
+  s = check_matrices({h, dy, dh});
+  if (s != MOER_OK) return s;
+  s = check_extents({{h.p, extent_of(h)}, {dy.p, extent_of(dy)}, {dh.p, extent_of(dh)}, {a->used, 4}});
+  if (s != MOER_OK) return s;
+  return moer::expert_act_launch(a, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moer_status moer_expert_combine(const moer_expert_combine_args* a, void* ws, size_t ws_bytes, moer_stream_t stream) {
+  moer_status s = check_combine(a, ws, ws_bytes);
+  if (s != MOER_OK) return s;
+  if (a->T == 0) return MOER_OK;
+  const int eb = elem_bytes(a->dtype);
+  const size_t al = sz(eb), pairs = sz(a->T) * sz(a->k);
+  const Matrix z{a->z, a->rows, a->H, a->ld_z, eb, al, a->rows > 0}, add{a->add, a->T, a->H, a->ld_add, eb, al, false},
+      out{a->out, a->T, a->H, a->ld_out, eb, al, true};
+  s = check_matrices({z, add, out});
+  if (s != MOER_OK) return s;
+  s = check_extents({{z.p, extent_of(z)}, {add.p, extent_of(add)}, {out.p, extent_of(out)}, {a->inv, pairs * 4}, {a->weights, pairs * 4}, {ws, ws_bytes}});
+  if (s != MOER_OK) return s;
+  return moer::expert_combine_launch(a, false, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moer_status moer_expert_combine_grad(const moer_expert_combine_args* a, void* ws, size_t ws_bytes, moer_stream_t stream) {
+  moer_status s = check_combine(a, ws, ws_bytes);
+  if (s != MOER_OK) return s;
+  const int eb = elem_bytes(a->dtype);
+  const size_t al = sz(eb), pairs = sz(a->T) * sz(a->k);
+  const bool rows = a->rows > 0;
+  const Matrix z{a->d_weights != nullptr ? a->z : nullptr, a->rows, a->H, a->ld_z, eb, al, a->d_weights != nullptr && rows},
+      dout{a->d_out, a->T, a->H, a->ld_d_out, eb, al, a->T > 0}, dz{a->d_z, a->rows, a->H, a->ld_d_z, eb, al, false};
+  s = check_matrices({z, dout, dz});
+  if (s != MOER_OK) return s;
+  if (a->d_z != nullptr && rows && a->order == nullptr) return MOER_EINVAL;
+  s = check_extents({{z.p, extent_of(z)}, {dout.p, extent_of(dout)}, {dz.p, extent_of(dz)}, {a->inv, pairs * 4}, {a->weights, pairs * 4},
+                     {a->d_weights, pairs * 4}, {a->d_z != nullptr ? a->order : nullptr, sz(a->rows) * 4}, {ws, ws_bytes}});
+  if (s != MOER_OK) return s;
+  return moer::expert_combine_launch(a, true, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 moer_status moer_wait_selftest(void* ws, size_t ws_bytes, uint32_t limit_us, moer_stream_t stream) {
