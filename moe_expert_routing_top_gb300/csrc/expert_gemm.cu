@@ -12,13 +12,16 @@
 // (m or j contiguous) from 64 x 64 panels.
 //
 // Clusters of two CTAs, persistent over tiles of 256 m x up to 256 j (tcgen05.mma.cta_group::2,
-// M = 256), K in blocks of 128 bytes, six stages of 32 KB.  A CTA loads its 128 of m and half
-// of the j rows.  Rows of x are fetched by the list's entries, four at a time (TMA gather), so no
-// permuted copy of x exists; where rows are contracted (GRAD_WEIGHT) the last block of
-// a segment, and any block with padding, is cleared of other rows in shared memory before
-// its MMAs.  Accumulators are fp32 in TMEM, two of 256 columns, drained while the next tile runs.
-// E4M3: the sum of each block of 128 is taken out of TMEM and added in fp32 registers, times its
-// two scales, by eight warps.
+// M = 256), c in blocks of 128 bytes, six stages of 32 KB.  A CTA loads its 128 of m and half
+// of the j rows: weights (and d_y) by TMA, rows of x by warps of cp.async that follow the
+// list's entries, so no permuted copy of x exists.  (TMA's row gather takes some 72 clocks for
+// four rows: 3.4 ms where this takes XX, 262,144 rows of 2,048 x 1,536.)  Where rows are contracted
+// (GRAD_WEIGHT), those past the segment or of padding are filled with zeros in both operands.
+// Accumulators are fp32 in TMEM, two of 256 columns, drained by eight warps while the MMAs go
+// on.  TMEM sums are cut, not rounded, so that their error grows with their length: after
+// 8 blocks (512 terms) a sum is added to fp32 registers (weights' gradient over 1,500 rows: relative
+// error 2.2e-6 without that).  E4M3 does so after each block of 128, times its two scales; tiles
+// of up to 64 j hand over four blocks at a time.
 // Every wait is bounded; on expiry the kernel records MOER_ETIMEOUT and returns.
 #include "rows.cuh"
 #include "umma.cuh"
@@ -29,16 +32,32 @@ constexpr int EG_STAGES = 6;
 constexpr int EG_HALF = 16384;               // one operand's part of a stage: 128 rows (or 2 panels of 64) x 128 bytes
 constexpr int EG_STAGE_BYTES = 2 * EG_HALF;
 constexpr int EG_PANEL = 8192;               // 64 rows x 128 bytes
+constexpr int EG_EPI_WARPS = 16;
+constexpr int EG_THREADS = (8 + EG_EPI_WARPS) * 32;
 constexpr int EG_J = 256;                    // most j of a tile
+constexpr int EG_COLS = EG_J / (EG_EPI_WARPS / 4);  // columns that an epilogue warp holds
 constexpr int EG_SLOTS = 4, EG_SLOT_KB = 4;  // E4M3: ring of the scales' products, blocks a slot
 constexpr int EG_SCALE_BYTES = EG_SLOTS * EG_SLOT_KB * EG_J * 4;
 constexpr int EG_TMEM_COLS = 512;
+constexpr int EG_ROUND = 8;                  // blocks summed in TMEM (not E4M3)
 constexpr size_t EG_OFF_BAR = (size_t)EG_STAGES * EG_STAGE_BYTES;
 constexpr size_t EG_OFF_SCALE = EG_OFF_BAR + 512;
+// Barriers, as byte offsets from the stages' start.
+constexpr uint32_t EG_FULL = (uint32_t)EG_OFF_BAR;            // [stage] in the leader: both operands of both CTAs
+constexpr uint32_t EG_EMPTY = EG_FULL + 8 * EG_STAGES;        // [stage] the MMAs have read it
+constexpr uint32_t EG_TFULL = EG_EMPTY + 8 * EG_STAGES;       // [2] an accumulator is complete
+constexpr uint32_t EG_TEMPTY = EG_TFULL + 16;                 // [2] in the leader: it is drained in both CTAs
+constexpr uint32_t EG_DRAIN = EG_TEMPTY + 16;
+constexpr uint32_t EG_SFULL = EG_DRAIN + 8;                   // [slot] scales (E4M3)
+constexpr uint32_t EG_SEMPTY = EG_SFULL + 8 * EG_SLOTS;
+constexpr uint32_t EG_TMEM = EG_SEMPTY + 8 * EG_SLOTS;        // TMEM address, failure flag
+static_assert(EG_TMEM + 8 <= EG_OFF_SCALE, "barrier area");
 
 struct GemmParams {
-  CUtensorMap tmx;   // x, fetched row by row: box of one row x 128 bytes
   CUtensorMap tmw;   // w [E][N][K], or d_y [rows][N]
+  const char* x;
+  const char* dy;    // GRAD_WEIGHT
+  int64_t ld_x, ld_dy;  // bytes
   const int32_t* off;
   const int32_t* order;
   int64_t rows, tokens;
@@ -65,27 +84,24 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// Four rows r[0..3] of a row-by-row map, 128 bytes each from column c0 on, one after the other.
-__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap* tm, int c0, const int (&r)[4], uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
-      "%3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(tm), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
-      : "memory");
+// 16 bytes to shared memory, those past `bytes` as zeros (nothing is read when it is 0).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const char* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+// The operands' descriptors come as 32-bit halves: the high one is the same for every stage.
 template <bool FP8>
-__device__ __forceinline__ void umma_pair(uint32_t dt, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+__device__ __forceinline__ void umma_pair(uint32_t dt, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accum) {
   if constexpr (FP8)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(dt),
-        "l"(a), "l"(b), "r"(idesc), "r"(accum));
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %4, p;\n\t}" ::"r"(dt),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accum));
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dt),
-        "l"(a), "l"(b), "r"(idesc), "r"(accum));
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(dt),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accum));
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -96,7 +112,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Descriptor of an operand whose m (or j) is contiguous: panels of 64 of it, EG_PANEL bytes
 // apart, rows of c of 128 bytes, groups of eight rows 1024 bytes apart, 128-byte swizzle.
@@ -104,9 +120,52 @@ __device__ __forceinline__ uint64_t umma_desc_panels(uint32_t saddr) {
   return (umma_desc_sw128(saddr) & ~(0x3FFFull << 16)) | ((uint64_t)(EG_PANEL >> 4) << 16);
 }
 
-// Waits by a whole warp, with one answer for it.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  return __all_sync(FULL, mbar_wait_cl(bar, parity, status));
+// Bounded wait by one thread on a barrier of this CTA.  Scope: the block.  What the other CTA of the
+// pair hands over through a barrier is read by the tensor cores alone (each from its own SM's
+// shared memory), after the writer's proxy fence; nothing that threads wrote is read across the
+// pair.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool one_wait(uint32_t bar, uint32_t parity, uint32_t* status) {
+  if (try_wait(bar, parity)) return true;
+  unsigned long long t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (try_wait(bar, parity)) return true;
+    if ((it & 63u) == 63u) {
+      const unsigned long long t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > WAIT_LIMIT_NS || it >= WAIT_LIMIT_ITERS) {
+        atomicOr(status, WS_BIT_ETIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// Arrival on a barrier of either CTA, with the same scope: released at cluster scope each
+// arrival would first wait for the thread's memory operations (1.7 us a stage instead of 0.3).
+__device__ __forceinline__ void pair_arrive(uint32_t caddr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
+
+__device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// Waits by a whole warp: lane 0 polls, and its answer is everyone's.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t* status, int lane) {
+  bool ok = true;
+  if (lane == 0) ok = one_wait(bar, parity, status);
+  return __shfl_sync(FULL, (int)ok, 0) != 0;
 }
 
 // ------------------------------------------------------------ tiles
@@ -162,10 +221,10 @@ struct Tile {
 };
 
 template <int OP, int KE>
-__device__ __forceinline__ Tile tile_of(const GemmParams& p, const TileTable& tt, int64_t t) {
+__device__ __forceinline__ Tile tile_of(const GemmParams& p, const TileTable& tt, int t) {
   Tile x;
-  const int col = (int)(t / p.nmb);
-  x.mb = (int)(t - (int64_t)col * p.nmb);
+  const int col = t / p.nmb;
+  x.mb = t - col * p.nmb;
   int a = 0, b = p.E - 1;  // the last expert with first[e] <= col: the one that has tile column col
   while (a < b) {
     const int m = (a + b + 1) >> 1;
@@ -206,17 +265,157 @@ __device__ __forceinline__ int source_row(const GemmParams& p, int q, bool& bad)
   return -1;
 }
 
+// GRAD_WEIGHT: the rows of x behind the 64 list rows of a block, two to a lane (r0: row lane, r1: row
+// 32 + lane; -1: past the segment or padding), with the next block's entries under way.
+struct RowPair {
+  int r0, r1;
+  int n0, n1;
+  bool bad;
+  __device__ __forceinline__ int entry(const GemmParams& p, const Tile& x, uint32_t q) const {
+    return q < (uint32_t)(x.hi - x.p0) ? (p.order == nullptr ? x.p0 + (int)q : p.order[x.p0 + (int)q]) : -1;
+  }
+  __device__ __forceinline__ int row(const GemmParams& p, int o) {
+    if (p.order == nullptr || o < 0) return o;
+    const int r = o / p.k;
+    if (r < p.tokens) return r;
+    bad = true;
+    return -1;
+  }
+  __device__ __forceinline__ RowPair(const GemmParams& p, const Tile& x, int kb, int lane) : r0(-1), r1(-1), bad(false) {
+    n0 = entry(p, x, (uint32_t)kb * 64 + lane);
+    n1 = entry(p, x, (uint32_t)kb * 64 + 32 + lane);
+  }
+  // The rows of the block whose entries are under way, and block kb's entries; whether one of the
+  // rows is none.
+  __device__ __forceinline__ bool next(const GemmParams& p, const Tile& x, int kb, int lane) {
+    r0 = row(p, n0);
+    r1 = row(p, n1);
+    n0 = entry(p, x, (uint32_t)kb * 64 + lane);
+    n1 = entry(p, x, (uint32_t)kb * 64 + 32 + lane);
+    return __any_sync(FULL, r0 < 0 || r1 < 0);
+  }
+};
+
+// Columns of a block's sums in a round of E4M3: a round is EG_J / width blocks side by side.
+template <bool FP8>
+__device__ __forceinline__ int round_width(const Tile& x) {
+  return !FP8 ? EG_J : x.ncol <= 64 ? 64 : x.ncol <= 128 ? 128 : 256;
+}
+
+// ------------------------------------------------------------ rows of x
+// One of the row warps (6; E4M3: 5): it brings every sixth (fifth) stage by itself, from the release
+// of the stage to the copies' landing, so that as many stages are under way without one warp's wait
+// holding up another's (four warps sharing every stage: 2,284 us where this takes XX).  Row indices
+// lie with the lanes and go round by shuffles.
+template <int OP, bool FP8>
+__device__ __forceinline__ void load_rows(const GemmParams& p, const TileTable& tt, char* sm, uint32_t base, int w, int rank, int lane, int ntiles,
+                                          int t_step) {
+  constexpr int EB = FP8 ? 1 : 2, KE = 128 / EB, NW = FP8 ? 5 : 6;
+  constexpr bool GW = OP == MOER_GEMM_GRAD_WEIGHT;
+  const uint32_t bar0 = mapa_u32(base + EG_FULL, 0);
+  uint32_t g = 0;       // stages of the tiles so far
+  uint32_t mine = w;    // the next one that is this warp's
+  bool ok = true;
+  // the stage's copies have landed: visible to the MMA, handed over
+  auto hand_over = [&](uint32_t s) {
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) pair_arrive(bar0 + 8u * s);
+  };
+  // the ring's slot of stage `mine` is free
+  auto take = [&](uint32_t& s) -> bool {
+    const uint32_t round = mine / EG_STAGES;
+    s = mine - round * EG_STAGES;
+    return round == 0 || warp_wait(base + EG_EMPTY + 8u * s, (round - 1) & 1u, p.status, lane);
+  };
+  for (int t = blockIdx.x >> 1; t < ntiles && ok; t += t_step) {
+    const Tile x = tile_of<OP, KE>(p, tt, t);
+    if constexpr (!GW) {
+      // eight lanes a row: rows 4 i + lane / 8 of this CTA's half; lane l holds rows l, 32 + l, ...
+      const int half = x.ncol >> 1, sub = lane >> 3, c = lane & 7;
+      int src[4];
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // rows past the tile repeat its last one; padding takes any row
+        const int j = min(rank * half + 32 * i + lane, x.rows - 1);
+        src[i] = 32 * i < half ? max(source_row(p, x.p0 + j, bad), 0) : 0;
+      }
+      for (int kb = (int)(mine - g); kb < x.nkb; kb += NW, mine += NW) {
+        uint32_t s;
+        if (!take(s)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = base + s * EG_STAGE_BYTES + EG_HALF + (uint32_t)sub * 128;
+        const int off = kb * 128 + c * 16, n = max(0, min(16, p.C * EB - off));
+        const char* xk = p.x + (n > 0 ? off : 0);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (4 * i >= half) break;  // half is a multiple of eight
+          const int r = __shfl_sync(FULL, src[i / 8], (4 * i + sub) & 31);
+          cp_async16(dst + 512u * i + ((uint32_t)(c ^ ((4 * i + sub) & 7)) << 4), xk + (int64_t)r * p.ld_x, n);
+        }
+        hand_over(s);
+      }
+    } else {
+      // sixteen lanes a row: rows 2 i + lane / 16 of the block
+      const int sub = lane >> 4, c = lane & 15;
+      const int acol = x.mb * 256 + rank * 128 + c * 8, bcol = x.j0 + rank * 128 + c * 8;
+      const int an = max(0, min(16, (p.M - acol) * 2)), bn = max(0, min(16, (p.J - bcol) * 2));
+      RowPair rp(p, x, (int)(mine - g), lane);
+      for (int kb = (int)(mine - g); kb < x.nkb; kb += NW, mine += NW) {
+        const bool dirty = rp.next(p, x, kb + NW, lane);
+        uint32_t s;
+        if (!take(s)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = base + s * EG_STAGE_BYTES + (uint32_t)((c >> 3) * EG_PANEL + sub * 128);
+        const char* ax = p.x + (an > 0 ? (int64_t)acol * 2 : 0);
+        const char* bx = p.dy + (int64_t)(x.p0 + (int64_t)kb * KE + sub) * p.ld_dy + (bn > 0 ? (int64_t)bcol * 2 : 0);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int r = __shfl_sync(FULL, i < 16 ? rp.r0 : rp.r1, (2 * i + sub) & 31);
+          const uint32_t at = 256u * i + ((uint32_t)((c & 7) ^ ((2 * i + sub) & 7)) << 4);
+          cp_async16(dst + at, ax + (int64_t)max(r, 0) * p.ld_x, r >= 0 ? an : 0);
+          // (a block that is all the segment's own comes by TMA)
+          if (dirty) cp_async16(dst + EG_HALF + at, r >= 0 ? bx + (int64_t)(2 * i) * p.ld_dy : p.dy, r >= 0 ? bn : 0);
+        }
+        hand_over(s);
+      }
+      if (rp.bad) atomicOr(p.status, WS_BIT_EDATA);
+    }
+    g += (uint32_t)x.nkb;
+  }
+  if (!ok && lane == 0) *reinterpret_cast<volatile int*>(sm + EG_TMEM + 4) = 1;
+}
+
 // ------------------------------------------------------------ epilogue
+// a.x += r0 * x, a.y += r1 * y (two lanes of one instruction).
+__device__ __forceinline__ void fma2(float2& a, uint32_t r0, uint32_t r1, float x, float y) {
+  asm("{\n\t.reg .b64 d, u, v;\n\tmov.b64 d, {%0, %1};\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\t"
+      "fma.rn.f32x2 d, u, v, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "r"(r0), "r"(r1), "f"(x), "f"(y));
+}
+__device__ __forceinline__ void add2(float2& a, uint32_t r0, uint32_t r1) {
+  asm("{\n\t.reg .b64 d, u;\n\tmov.b64 d, {%0, %1};\n\tmov.b64 u, {%2, %3};\n\t"
+      "add.rn.f32x2 d, u, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "r"(r0), "r"(r1));
+}
+
 template <typename T>
-__device__ __forceinline__ void store_cols(T* o, int64_t ld, const uint32_t* v, int n, uint32_t zero) {
+__device__ __forceinline__ void store_cols(T* o, int64_t ld, const float2* v, int n, uint32_t zero) {
 #pragma unroll
   for (int c = 0; c < 32; ++c)
-    if (c < n) o[(int64_t)c * ld] = from_f32<T>((zero >> c) & 1u ? 0.f : __uint_as_float(v[c]));
+    if (c < n) o[(int64_t)c * ld] = from_f32<T>((zero >> c) & 1u ? 0.f : (c & 1 ? v[c / 2].y : v[c / 2].x));
 }
 
 // 32 columns (output rows) of one m; `first`: element of the first; n: valid rows; zero: rows that
 // are padding.
-__device__ __forceinline__ void store_chunk(const GemmParams& p, int64_t first, const uint32_t* v, int n, uint32_t zero) {
+__device__ __forceinline__ void store_chunk(const GemmParams& p, int64_t first, const float2* v, int n, uint32_t zero) {
   if (p.out_dtype == MOER_F32) store_cols(static_cast<float*>(p.out) + first, p.ld_out, v, n, zero);
   else if (p.out_dtype == MOER_BF16) store_cols(static_cast<__nv_bfloat16*>(p.out) + first, p.ld_out, v, n, zero);
   else store_cols(static_cast<__half*>(p.out) + first, p.ld_out, v, n, zero);
@@ -239,365 +438,281 @@ __device__ __forceinline__ uint32_t pad_mask(const GemmParams& p, const Tile& x,
 }
 
 // ------------------------------------------------------------ the kernel
-// Warps: 0 loads, 1 allocates TMEM and issues the MMAs (in the leader), 2 and 3 form the scales'
-// products (E4M3), the last four (E4M3: eight) drain the accumulators.
-template <bool FP8>
-constexpr int eg_threads() {
-  return FP8 ? 384 : 192;
-}
-
+// Warps: 0 loads by TMA, 1 allocates TMEM and issues the MMAs (in the leader), 2 to 7 load rows (E4M3: 2
+// forms the scales' products), 8 to 23 drain the accumulators, each 64 columns of its TMEM
+// lanes.  Registers go to the last
+// sixteen: the six warpgroups' shares, 64 + 64 + 4 x 88, are the block's 6 x 80.
 template <int OP, bool FP8>
-__global__ void __launch_bounds__(eg_threads<FP8>(), 1) expert_gemm_kernel(const __grid_constant__ GemmParams p) {
-  constexpr int KE = FP8 ? 128 : 64;         // elements of c a block: 128 bytes
+__global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid_constant__ GemmParams p) {
+  constexpr int EB = FP8 ? 1 : 2, KE = 128 / EB;  // bytes of an element, elements of c a block
   constexpr bool GW = OP == MOER_GEMM_GRAD_WEIGHT;
   constexpr bool A_PANELS = OP != MOER_GEMM_FORWARD, B_PANELS = GW;
-  constexpr int EPI0 = FP8 ? 4 : 2, EPI_WARPS = FP8 ? 8 : 4;
   extern __shared__ __align__(1024) char eg_raw[];
-  char* sm = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(eg_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + EG_OFF_BAR);  // used in the leader
-  uint64_t* empty = full + EG_STAGES;
-  uint64_t* tfull = empty + EG_STAGES;
-  uint64_t* tempty = tfull + 2;   // used in the leader
-  uint64_t* drain = tempty + 2;
-  uint64_t* fix = drain + 1;      // GRAD_WEIGHT: this CTA's copies of a block that has to be cleared
-  uint64_t* sfull = fix + 1;
-  uint64_t* sempty = sfull + EG_SLOTS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + EG_SLOTS);
-  volatile int& failed = *reinterpret_cast<int*>(tmem_slot + 1);
-  float* scales = reinterpret_cast<float*>(sm + EG_OFF_SCALE);  // [slot][block][j]
+  const uint32_t base = (smem_u32(eg_raw) + 1023) & ~1023u;  // the same in both CTAs, as the MMA's descriptors require
+  char* sm = eg_raw + (base - smem_u32(eg_raw));
+  volatile int& failed = *reinterpret_cast<int*>(sm + EG_TMEM + 4);
   int* lo = reinterpret_cast<int*>(sm + EG_OFF_SCALE + (FP8 ? EG_SCALE_BYTES : 0));
-  int* first = lo + p.E + 1;
+  const TileTable tt{lo, lo + p.E + 1};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const bool leader = rank == 0;
-  const int64_t cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const int rank = (int)cluster_rank();
 
   if (threadIdx.x == 32) {
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm);
     for (int s = 0; s < EG_STAGES; ++s) {
-      mbar_init(&full[s], GW ? 2 : 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(bar + EG_FULL / 8 + s, 3);  // the leader's TMA warp, a row warp of either CTA
+      mbar_init(bar + EG_EMPTY / 8 + s, 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * EPI_WARPS);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar + EG_TFULL / 8 + i, 1);
+      mbar_init(bar + EG_TEMPTY / 8 + i, 2 * EG_EPI_WARPS);
     }
-    mbar_init(drain, 1);
-    mbar_init(fix, 1);
+    mbar_init(bar + EG_DRAIN / 8, 1);
     for (int i = 0; i < EG_SLOTS; ++i) {
-      mbar_init(&sfull[i], 2);
-      mbar_init(&sempty[i], EPI_WARPS);
+      mbar_init(bar + EG_SFULL / 8 + i, 1);
+      mbar_init(bar + EG_SEMPTY / 8 + i, EG_EPI_WARPS);
     }
     failed = 0;
     fence_mbar_init();
   }
-  if (warp == 0) make_tile_table(p, !GW, lo, first, lane);
+  if (warp == 0) make_tile_table(p, !GW, lo, lo + p.E + 1, lane);
   cluster_sync();
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(EG_TMEM_COLS));
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + EG_TMEM), "r"(EG_TMEM_COLS));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const TileTable tt{lo, first};
-  const int64_t ntiles = (int64_t)first[p.E] * p.nmb;
+  const int ntiles = tt.first[p.E] * p.nmb, t_step = gridDim.x >> 1;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- loads
-    const uint32_t bar0 = mapa_u32(smem_u32(full), 0), base = smem_u32(sm);
-    const uint32_t fixc = mapa_u32(smem_u32(fix), rank);
-    int64_t g = 0;     // stages filled so far
-    int s = 0;
-    uint32_t ph = 1;   // parity of the release that the next fill of stage s waits for
-    uint32_t fph = 0;
-    bool ok = true;
-    for (int64_t t = cluster; t < ntiles && ok; t += nclusters) {
-      const Tile x = tile_of<OP, KE>(p, tt, t);
-      const int m0 = x.mb * 256 + (int)rank * 128;
-      if constexpr (!GW) {
-        const int half = x.ncol >> 1;
-        int r[4];
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // rows past the tile repeat its last one; padding takes any row
-          const int j = min((int)rank * half + 4 * lane + i, x.rows - 1);
-          r[i] = max(source_row(p, x.p0 + j, bad), 0);
-        }
-        const uint32_t tx = 2u * EG_HALF + (uint32_t)x.ncol * 128u;
-        for (int kb = 0; kb < x.nkb; ++kb, ++g) {
-          if (g >= EG_STAGES && !warp_wait(&empty[s], ph, p.status)) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0) {
+      // -------------------------------------------------------- TMA: w, or d_y
+      const uint32_t bar0 = mapa_u32(base + EG_FULL, 0);
+      int s = 0;
+      uint32_t fills = 0, ph = 1;  // parity of the release that the next fill of stage s waits for
+      bool ok = true;
+      for (int t = blockIdx.x >> 1; t < ntiles && ok; t += t_step) {
+        const Tile x = tile_of<OP, KE>(p, tt, t);
+        const int m0 = x.mb * 256 + rank * 128;
+        const int e = p.one_w ? 0 : x.e;
+        RowPair rp(p, x, 0, lane);
+        for (int kb = 0; kb < x.nkb; ++kb) {
+          bool dirty = false;
+          if constexpr (GW) dirty = rp.next(p, x, kb + 1, lane);
+          if (fills >= EG_STAGES && !warp_wait(base + EG_EMPTY + 8u * s, ph, p.status, lane)) {
             ok = false;
             break;
           }
+          fills += fills < EG_STAGES;
           const uint32_t st = base + (uint32_t)(s * EG_STAGE_BYTES), bar = bar0 + 8u * s;
           if (lane == 0) {
-            if (leader) mbar_arrive_expect_tx(&full[s], tx);
-            const int e = p.one_w ? 0 : x.e;
+            if (rank == 0) {
+              if (dirty) pair_arrive(bar);  // the row warps bring both operands
+              else arrive_expect(base + EG_FULL + 8u * s, 2u * EG_HALF);
+            }
             if (OP == MOER_GEMM_FORWARD) {
               tma_load_3d_pair(st, &p.tmw, kb * KE, m0, e, bar);
-            } else {
+            } else if (OP == MOER_GEMM_GRAD_INPUT) {
               tma_load_3d_pair(st, &p.tmw, m0, kb * KE, e, bar);
               tma_load_3d_pair(st + EG_PANEL, &p.tmw, m0 + 64, kb * KE, e, bar);
+            } else if (!dirty) {
+              const int n0 = x.j0 + rank * 128;
+              tma_load_3d_pair(st + EG_HALF, &p.tmw, n0, x.p0 + kb * KE, 0, bar);
+              tma_load_3d_pair(st + EG_HALF + EG_PANEL, &p.tmw, n0 + 64, x.p0 + kb * KE, 0, bar);
             }
-          }
-          if (4 * lane < half) tma_gather4_pair(st + EG_HALF + 512u * lane, &p.tmx, kb * KE, r, bar);
-          if (++s == EG_STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-      } else {
-        // lane: panel lane / 16 of A, rows 4 (lane % 16) .. + 3 of the block
-        const int r0 = 4 * (lane & 15), pan = lane >> 4;
-        int r[4], nx[4];
-        bool bad = false;
-        auto rows_of = [&](int kb, int (&v)[4]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t q = (uint32_t)kb * KE + r0 + i;
-            v[i] = q < (uint32_t)(x.hi - x.p0) ? source_row(p, x.p0 + (int)q, bad) : -1;
-          }
-        };
-        if (x.nkb > 0) rows_of(0, nx);
-        for (int kb = 0; kb < x.nkb; ++kb, ++g) {
-          uint32_t dead = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dead |= nx[i] < 0 ? 1u << i : 0u;
-            r[i] = max(nx[i], 0);
-          }
-          const bool dirty = __any_sync(FULL, dead != 0);
-          if (kb + 1 < x.nkb) rows_of(kb + 1, nx);
-          if (g >= EG_STAGES && !warp_wait(&empty[s], ph, p.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = base + (uint32_t)(s * EG_STAGE_BYTES);
-          const uint32_t bar = dirty ? fixc : bar0 + 8u * s;
-          if (lane == 0) {
-            if (dirty) mbar_arrive_expect_tx(fix, EG_STAGE_BYTES);
-            else if (leader) mbar_arrive_expect_tx(&full[s], 2u * EG_STAGE_BYTES);
-            else mbar_arrive_cluster(bar0 + 8u * s);
-          }
-          __syncwarp();
-          if (lane < 2)
-            tma_load_3d_pair(st + EG_HALF + EG_PANEL * lane, &p.tmw, x.j0 + (int)rank * 128 + 64 * lane, x.p0 + kb * KE, 0, bar);
-          tma_gather4_pair(st + EG_PANEL * pan + 128u * r0, &p.tmx, m0 + 64 * pan, r, bar);
-          if (dirty) {
-            if (!warp_wait(fix, fph, p.status)) {
-              ok = false;
-              break;
-            }
-            fph ^= 1u;
-            char* row = sm + (size_t)s * EG_STAGE_BYTES + (lane >> 3) * EG_PANEL + (lane & 7) * 16;
-            for (int i = 0; i < KE; ++i)
-              if ((__shfl_sync(FULL, dead, i >> 2) >> (i & 3)) & 1u) *reinterpret_cast<uint4*>(row + i * 128) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(bar0 + 8u * s);
           }
           if (++s == EG_STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
-        if (bad) atomicOr(p.status, WS_BIT_EDATA);
       }
-    }
-    // the last fills' stages have been released: no MMA still reads them
-    for (int64_t q = (g > EG_STAGES ? g - EG_STAGES : 0); q < g && ok; ++q)
-      if (!mbar_wait_cl(&empty[q % EG_STAGES], (uint32_t)((q / EG_STAGES) & 1), p.status)) ok = false;
-    if (!ok && lane == 0) failed = 1;
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA
-    if (lane == 0) {
-      bool ok = true;
-      if (leader) {
-        const uint32_t base = smem_u32(sm);
-        const uint64_t da0 = A_PANELS ? umma_desc_panels(base) : umma_desc_sw128(base);
-        const uint64_t db0 = B_PANELS ? umma_desc_panels(base + EG_HALF) : umma_desc_sw128(base + EG_HALF);
-        // one instruction takes 32 bytes of a row of c, or 16 rows of panels (16-byte units)
-        constexpr uint64_t A_STEP = A_PANELS ? 128 : 2, B_STEP = B_PANELS ? 128 : 2;
-        int s = 0;
-        uint32_t ph = 0;
-        int64_t j = 0;  // accumulators begun
-        for (int64_t t = cluster; t < ntiles && ok; t += nclusters) {
-          const Tile x = tile_of<OP, KE>(p, tt, t);
-          const uint32_t idesc = p.idesc | ((uint32_t)(x.ncol >> 3) << 17);
-          for (int kb = 0; kb < x.nkb; ++kb) {
-            const int a = (int)(j & 1);
-            if (FP8 || kb == 0) {
-              if (j >= 2 && !mbar_wait_cl(&tempty[a], (uint32_t)(((j >> 1) - 1) & 1), p.status)) {
-                ok = false;
-                break;
-              }
-            }
-            if (!mbar_wait_cl(&full[s], ph, p.status)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t da = da0 + (uint64_t)(s * (EG_STAGE_BYTES >> 4)), db = db0 + (uint64_t)(s * (EG_STAGE_BYTES >> 4));
-            const uint32_t dt = tmem + (uint32_t)(a * EG_J);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              umma_pair<FP8>(dt, da + A_STEP * i, db + B_STEP * i, idesc, (i > 0 || (!FP8 && kb > 0)) ? 1u : 0u);
-            umma_commit_pair(&empty[s]);
-            if (FP8 || kb == x.nkb - 1) {
-              umma_commit_pair(&tfull[a]);
-              ++j;
-            }
-            if (++s == EG_STAGES) {
-              s = 0;
-              ph ^= 1u;
-            }
-          }
+      // the last fills' stages have been released: no MMA still reads them
+      for (uint32_t i = 0; i < fills && ok; ++i) {
+        if (fills < EG_STAGES) {  // the ring was never full: stages 0 .. fills - 1, first round
+          ok = one_wait(base + EG_EMPTY + 8u * i, 0, p.status);
+          continue;
         }
-        umma_commit_pair(drain);
-      }
-      if (!mbar_wait_cl(drain, 0, p.status)) ok = false;
-      if (!ok) failed = 1;
-    }
-  } else if (FP8 && warp < EPI0) {
-    // ---------------------------------------------------------- scales (E4M3)
-    if constexpr (FP8) {
-      const int th = threadIdx.x - 64;  // 64 threads, four j each
-      const int nkw = (p.C + 127) / 128, nnb = (p.M + 127) / 128;
-      int64_t it = 0;
-      bool ok = true;
-      for (int64_t t = cluster; t < ntiles && ok; t += nclusters) {
-        const Tile x = tile_of<OP, KE>(p, tt, t);
-        const float* sx[4];
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = th + 64 * i;
-          const int r = j < x.rows ? source_row(p, x.p0 + j, bad) : -1;
-          sx[i] = r >= 0 ? p.sx + (int64_t)r * p.ld_sx : nullptr;
-        }
-        const int mb = x.mb * 2 + (int)rank;
-        const float* sw = mb < nnb ? p.sw + ((int64_t)x.e * nnb + mb) * nkw : nullptr;
-        for (int k0 = 0; k0 < x.nkb; k0 += EG_SLOT_KB, ++it) {
-          const int slot = (int)(it % EG_SLOTS);
-          float v[EG_SLOT_KB][4];
-#pragma unroll
-          for (int b = 0; b < EG_SLOT_KB; ++b) {
-            const bool in = k0 + b < x.nkb;
-            const float w = in && sw != nullptr ? sw[k0 + b] : 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[b][i] = in && sx[i] != nullptr ? sx[i][k0 + b] * w : 0.f;
-          }
-          if (it >= EG_SLOTS && !warp_wait(&sempty[slot], (uint32_t)((it / EG_SLOTS - 1) & 1), p.status)) {
-            ok = false;
-            break;
-          }
-          float* d = scales + slot * EG_SLOT_KB * EG_J + th;
-#pragma unroll
-          for (int b = 0; b < EG_SLOT_KB; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[b * EG_J + 64 * i] = v[b][i];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sfull[slot]);
+        ok = one_wait(base + EG_EMPTY + 8u * s, ph, p.status);
+        if (++s == EG_STAGES) {
+          s = 0;
+          ph ^= 1u;
         }
       }
       if (!ok && lane == 0) failed = 1;
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA
+      if (lane == 0) {
+        bool ok = true;
+        int s = 0;
+        uint32_t ph = 0;
+        if (rank == 0) {
+          const uint64_t d0 = A_PANELS ? umma_desc_panels(base) : umma_desc_sw128(base);
+          const uint64_t d1 = B_PANELS ? umma_desc_panels(base + EG_HALF) : umma_desc_sw128(base + EG_HALF);
+          const uint32_t hi = (uint32_t)(d0 >> 32);  // the same for both
+          // one instruction takes 32 bytes of a row of c, or 16 rows of panels (16-byte units)
+          constexpr uint32_t A_STEP = A_PANELS ? 128 : 2, B_STEP = B_PANELS ? 128 : 2;
+          const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + EG_TMEM);
+          uint32_t j = 0;  // rounds begun
+          for (int t = blockIdx.x >> 1; t < ntiles && ok; t += t_step) {
+            const Tile x = tile_of<OP, KE>(p, tt, t);
+            const uint32_t idesc = p.idesc | ((uint32_t)(x.ncol >> 3) << 17);
+            const int w = round_width<FP8>(x), len = FP8 ? EG_J / w : EG_ROUND;
+            for (int kb = 0, r = 0; kb < x.nkb; ++kb) {
+              const uint32_t a = j & 1u;
+              if (r == 0 && j >= 2 && !one_wait(base + EG_TEMPTY + 8u * a, ((j >> 1) - 1) & 1u, p.status)) {
+                ok = false;
+                break;
+              }
+              if (!one_wait(base + EG_FULL + 8u * s, ph, p.status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t da = (uint32_t)d0 + (uint32_t)s * (EG_STAGE_BYTES >> 4), db = (uint32_t)d1 + (uint32_t)s * (EG_STAGE_BYTES >> 4);
+              const uint32_t dt = tmem + a * EG_J + (FP8 ? r * w : 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                umma_pair<FP8>(dt, da + A_STEP * i, db + B_STEP * i, hi, idesc, (i > 0 || (!FP8 && r > 0)) ? 1u : 0u);
+              umma_commit_pair(base + EG_EMPTY + 8u * s);
+              if (++r == len || kb == x.nkb - 1) {
+                umma_commit_pair(base + EG_TFULL + 8u * a);
+                ++j;
+                r = 0;
+              }
+              if (++s == EG_STAGES) {
+                s = 0;
+                ph ^= 1u;
+              }
+            }
+          }
+          umma_commit_pair(base + EG_DRAIN);
+        }
+        if (!one_wait(base + EG_DRAIN, 0, p.status)) ok = false;
+        if (!ok) failed = 1;
+      }
+    } else if (FP8 && warp == 2) {
+      // -------------------------------------------------------- scales (E4M3): eight j a lane
+      if constexpr (FP8) {
+        const int nkw = (p.C + 127) / 128, nnb = (p.M + 127) / 128;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = blockIdx.x >> 1; t < ntiles && ok; t += t_step) {
+          const Tile x = tile_of<OP, KE>(p, tt, t);
+          int r[8];
+          bool bad = false;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[i] = lane + 32 * i < x.rows ? source_row(p, x.p0 + lane + 32 * i, bad) : -1;
+          const int mb = x.mb * 2 + rank;
+          const float* sw = p.sw + ((int64_t)x.e * nnb + min(mb, nnb - 1)) * nkw;
+          for (int k0 = 0; k0 < x.nkb; k0 += EG_SLOT_KB, ++it) {
+            const uint32_t slot = it % EG_SLOTS;
+            if (it >= EG_SLOTS && !warp_wait(base + EG_SEMPTY + 8u * slot, (it / EG_SLOTS - 1) & 1u, p.status, lane)) {
+              ok = false;
+              break;
+            }
+            const int nb = min(EG_SLOT_KB, x.nkb - k0);
+            float* d = reinterpret_cast<float*>(sm + EG_OFF_SCALE) + slot * EG_SLOT_KB * EG_J + lane;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              if (g * 128 >= x.ncol) break;
+              float v[4][EG_SLOT_KB];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float* sx = p.sx + (int64_t)max(r[4 * g + i], 0) * p.ld_sx + k0;
+#pragma unroll
+                for (int b = 0; b < EG_SLOT_KB; ++b) v[i][b] = b < nb && r[4 * g + i] >= 0 ? __ldg(sx + b) : 0.f;
+              }
+#pragma unroll
+              for (int b = 0; b < EG_SLOT_KB; ++b) {
+                const float w = b < nb ? __ldg(sw + k0 + b) : 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[b * EG_J + 32 * (4 * g + i)] = v[i][b] * w;
+              }
+            }
+            __syncwarp();
+            if (lane == 0) pair_arrive(mapa_u32(base + EG_SFULL + 8u * slot, (uint32_t)rank));
+          }
+        }
+        if (!ok && lane == 0) failed = 1;
+      }
+    } else {
+      load_rows<OP, FP8>(p, tt, sm, base, warp - (FP8 ? 3 : 2), rank, lane, ntiles, t_step);
     }
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    load_rows<OP, FP8>(p, tt, sm, base, warp - (FP8 ? 3 : 2), rank, lane, ntiles, t_step);
   } else {
     // ---------------------------------------------------------- epilogue
-    const int q = warp & 3;  // TMEM lane quarter this warp may access
-    const uint32_t tempty0 = mapa_u32(smem_u32(tempty), 0);
-    int64_t j = 0, it = 0;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    const int h0 = ((warp - 8) >> 2) * EG_COLS;  // first of the warp's columns
+    const uint32_t tempty = mapa_u32(base + EG_TEMPTY, 0);
+    // the TMEM lane quarter that this warp may access
+    const uint32_t t0 = *reinterpret_cast<const uint32_t*>(sm + EG_TMEM) + ((uint32_t)((warp & 3) * 32) << 16) + h0;
+    uint32_t j = 0, it = 0;
     bool ok = true;
-    for (int64_t t = cluster; t < ntiles && ok; t += nclusters) {
+    for (int t = blockIdx.x >> 1; t < ntiles && ok; t += t_step) {
       const Tile x = tile_of<OP, KE>(p, tt, t);
-      const int m = x.mb * 256 + (int)rank * 128 + q * 32 + lane;
-      const bool mine = m < p.M;
-      const int64_t o = out_first<OP>(p, x, m);
-      if constexpr (FP8) {
-        const int h = (warp - EPI0) >> 2;  // columns h * 128 .. + 127
-        float acc[128];
+      const int w = round_width<FP8>(x), len = FP8 ? EG_J / w : EG_ROUND;
+      const int nch = max(0, min(EG_COLS / 16, (x.ncol - h0) >> 4));  // chunks of 16 columns that this warp holds
+      float2 acc[EG_COLS / 2];
 #pragma unroll
-        for (int c = 0; c < 128; ++c) acc[c] = 0.f;
-        for (int kb = 0; kb < x.nkb; ++kb, ++j) {
-          const int slot = (int)(it % EG_SLOTS), b = kb % EG_SLOT_KB;
-          if (b == 0 && !warp_wait(&sfull[slot], (uint32_t)((it / EG_SLOTS) & 1), p.status)) ok = false;
-          const int a = (int)(j & 1);
-          if (!ok || !warp_wait(&tfull[a], (uint32_t)((j >> 1) & 1), p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * EG_J + h * 128);
-          const float4* sc = reinterpret_cast<const float4*>(scales + (slot * EG_SLOT_KB + b) * EG_J + h * 128);
+      for (int c = 0; c < EG_COLS / 2; ++c) acc[c] = make_float2(0.f, 0.f);
+      for (int kb = 0; kb < x.nkb; kb += len, ++j) {
+        const uint32_t a = j & 1u, slot = it % EG_SLOTS;
+        if constexpr (FP8) {
+          if (kb % EG_SLOT_KB == 0) ok = warp_wait(base + EG_SFULL + 8u * slot, (it / EG_SLOTS) & 1u, p.status, lane);
+        }
+        if (!ok || !warp_wait(base + EG_TFULL + 8u * a, (j >> 1) & 1u, p.status, lane)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int nsub = FP8 ? min(len, x.nkb - kb) : 1;
+        for (int sub = 0; sub < nsub; ++sub) {
+          const uint32_t ta = t0 + a * EG_J + (FP8 ? sub * w : 0);
+          const float4* sc = reinterpret_cast<const float4*>(sm + EG_OFF_SCALE) + ((slot * EG_SLOT_KB + (kb + sub) % EG_SLOT_KB) * EG_J + h0) / 4;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (h * 128 + c * 16 < x.ncol) {
+          for (int c = 0; c < EG_COLS / 16; ++c) {
+            if (c < nch) {
               uint32_t r[16];
               tmem_ld16(ta + 16u * c, r);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float4 f = sc[c * 4 + i];
-                acc[c * 16 + 4 * i + 0] = fmaf(__uint_as_float(r[4 * i + 0]), f.x, acc[c * 16 + 4 * i + 0]);
-                acc[c * 16 + 4 * i + 1] = fmaf(__uint_as_float(r[4 * i + 1]), f.y, acc[c * 16 + 4 * i + 1]);
-                acc[c * 16 + 4 * i + 2] = fmaf(__uint_as_float(r[4 * i + 2]), f.z, acc[c * 16 + 4 * i + 2]);
-                acc[c * 16 + 4 * i + 3] = fmaf(__uint_as_float(r[4 * i + 3]), f.w, acc[c * 16 + 4 * i + 3]);
+                if constexpr (FP8) {
+                  const float4 f = sc[c * 4 + i];
+                  fma2(acc[c * 8 + 2 * i], r[4 * i], r[4 * i + 1], f.x, f.y);
+                  fma2(acc[c * 8 + 2 * i + 1], r[4 * i + 2], r[4 * i + 3], f.z, f.w);
+                } else {
+                  add2(acc[c * 8 + 2 * i], r[4 * i], r[4 * i + 1]);
+                  add2(acc[c * 8 + 2 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                }
               }
             }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_cluster(tempty0 + (uint32_t)(a * 8));
-            if (b == EG_SLOT_KB - 1 || kb == x.nkb - 1) mbar_arrive(&sempty[slot]);
-          }
-          if (b == EG_SLOT_KB - 1 || kb == x.nkb - 1) ++it;
-        }
-        if (!ok) break;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int j0 = h * 128 + c * 32;
-          if (j0 < x.rows) {
-            const uint32_t zero = pad_mask<OP>(p, x, j0 / 32, lane);
-            uint32_t v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[c * 32 + i]);
-            if (mine) store_chunk(p, o + (int64_t)j0 * p.ld_out, v, x.rows - j0, zero);
-          }
-        }
-      } else {
-        if (GW && x.nkb == 0) {  // an expert without rows
-          uint32_t z[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) z[c] = 0u;
-          if (mine)
-            for (int j0 = 0; j0 < x.rows; j0 += 32) store_chunk(p, o + (int64_t)j0 * p.ld_out, z, x.rows - j0, 0u);
-          continue;
-        }
-        const int a = (int)(j & 1);
-        uint32_t zero[EG_J / 32];
-#pragma unroll
-        for (int c = 0; c < EG_J / 32; ++c) zero[c] = c * 32 < x.rows ? pad_mask<OP>(p, x, c, lane) : 0u;
-        if (!warp_wait(&tfull[a], (uint32_t)((j >> 1) & 1), p.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * EG_J);
-#pragma unroll
-        for (int c = 0; c < EG_J / 32; ++c) {
-          if (c * 32 < x.rows) {
-            uint32_t r[32];
-            tmem_ld32(ta + 32u * c, r);
-            tmem_ld_wait();
-            if (mine) store_chunk(p, o + (int64_t)(c * 32) * p.ld_out, r, x.rows - c * 32, zero[c]);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(a * 8));
-        ++j;
+        if (lane == 0) pair_arrive(tempty + 8u * a);
+        if constexpr (FP8) {
+          if ((kb + len) % EG_SLOT_KB == 0 || kb + len >= x.nkb) {
+            if (lane == 0) pair_arrive(mapa_u32(base + EG_SEMPTY + 8u * slot, (uint32_t)rank));
+            ++it;
+          }
+        }
+      }
+      if (!ok) break;
+      const int m = x.mb * 256 + rank * 128 + (warp & 3) * 32 + lane;
+#pragma unroll
+      for (int c = 0; c < EG_COLS / 32; ++c) {
+        const int j0 = h0 + c * 32;
+        if (j0 < x.rows) {
+          const uint32_t zero = pad_mask<OP>(p, x, j0 / 32, lane);
+          if (m < p.M) store_chunk(p, out_first<OP>(p, x, m) + (int64_t)j0 * p.ld_out, &acc[c * 16], x.rows - j0, zero);
+        }
       }
     }
     if (!ok && lane == 0) failed = 1;
@@ -612,7 +727,8 @@ __global__ void __launch_bounds__(eg_threads<FP8>(), 1) expert_gemm_kernel(const
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(EG_TMEM_COLS));
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(*reinterpret_cast<const uint32_t*>(sm + EG_TMEM)), "r"(EG_TMEM_COLS));
   cluster_sync();
 }
 
@@ -661,10 +777,10 @@ bool map_of(CUtensorMap* m, const void* base, int dtype, int rank, const uint64_
 
 size_t smem_bytes(int E, bool fp8) { return EG_OFF_SCALE + (fp8 ? EG_SCALE_BYTES : 0) + (size_t)2 * (E + 1) * 4 + 1024; }
 
-cudaLaunchConfig_t pair_config(int clusters, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute* at) {
+cudaLaunchConfig_t pair_config(int clusters, size_t smem, cudaStream_t st, cudaLaunchAttribute* at) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)clusters);
-  cfg.blockDim = dim3(threads);
+  cfg.blockDim = dim3(EG_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -680,7 +796,6 @@ template <int OP, bool FP8>
 cudaError_t gemm_run(const GemmParams& p, int64_t most_tiles, cudaStream_t st) {
   static std::atomic<unsigned long long> set{0};
   static std::atomic<int> cached[64];
-  constexpr int threads = eg_threads<FP8>();
   cudaError_t e = smem_optin(expert_gemm_kernel<OP, FP8>, (int)smem_bytes(1024, FP8), set);
   if (e != cudaSuccess) return e;
   int dev = 0;
@@ -689,13 +804,13 @@ cudaError_t gemm_run(const GemmParams& p, int64_t most_tiles, cudaStream_t st) {
   cudaLaunchAttribute at[1];
   int most = dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
   if (most <= 0) {  // clusters that fit on the device at once, one CTA an SM
-    const cudaLaunchConfig_t cfg = pair_config(1, threads, smem_bytes(1024, FP8), nullptr, at);
+    const cudaLaunchConfig_t cfg = pair_config(1, smem_bytes(1024, FP8), nullptr, at);
     e = cudaOccupancyMaxActiveClusters(&most, expert_gemm_kernel<OP, FP8>, &cfg);
     if (e != cudaSuccess) return e;
     if (most <= 0) return cudaErrorInvalidConfiguration;
     if (dev < 64) cached[dev].store(most, std::memory_order_relaxed);
   }
-  const cudaLaunchConfig_t cfg = pair_config((int)min64(most_tiles, most), threads, smem_bytes(p.E, FP8), st, at);
+  const cudaLaunchConfig_t cfg = pair_config((int)min64(most_tiles, most), smem_bytes(p.E, FP8), st, at);
   e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<OP, FP8>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -746,11 +861,10 @@ moer_status expert_gemm_launch(const moer_expert_gemm_args* a, void* ws, cudaStr
   // D fp32; A and B bf16, fp16 or e4m3; transposed operands; M = 256
   const uint32_t fmt = a->dtype == MOER_BF16 ? 1u : 0u;
   p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((fwd ? 0u : 1u) << 15) | ((gw ? 1u : 0u) << 16) | ((256u >> 4) << 24);
-  {
-    const uint64_t dims[2] = {(uint64_t)(a->op == MOER_GEMM_GRAD_INPUT ? a->N : a->K), (uint64_t)a->tokens}, str[1] = {(uint64_t)a->ld_x * eb};
-    const uint32_t box[2] = {(uint32_t)ke, 1};
-    if (!map_of(&p.tmx, a->x, a->dtype, 2, dims, str, box)) return MOER_ECUDA;
-  }
+  p.x = static_cast<const char*>(a->x);
+  p.dy = static_cast<const char*>(a->d_y);
+  p.ld_x = a->ld_x * (int64_t)eb;
+  p.ld_dy = a->ld_d_y * (int64_t)eb;
   if (gw) {
     const uint64_t dims[3] = {(uint64_t)a->N, (uint64_t)a->rows, 1}, str[2] = {(uint64_t)a->ld_d_y * eb, (uint64_t)a->ld_d_y * eb};
     const uint32_t box[3] = {64, 64, 1};
@@ -762,7 +876,9 @@ moer_status expert_gemm_launch(const moer_expert_gemm_args* a, void* ws, cudaStr
     const uint32_t box[3] = {(uint32_t)ke, fwd ? 128u : 64u, 1};
     if (!map_of(&p.tmw, a->w, a->dtype, 3, dims, str, box)) return MOER_ECUDA;
   }
+  // tiles are counted in 32 bits
   const int64_t most = (gw ? (int64_t)a->E * p.njb : (a->rows + EG_J - 1) / EG_J + min64(a->E, a->rows)) * p.nmb;
+  if (most >= (int64_t(1) << 30)) return MOER_ERANGE;
   const cudaError_t e = fp8   ? gemm_run<MOER_GEMM_FORWARD, true>(p, most, st)
                         : fwd ? gemm_run<MOER_GEMM_FORWARD, false>(p, most, st)
                         : gw  ? gemm_run<MOER_GEMM_GRAD_WEIGHT, false>(p, most, st)
