@@ -17,11 +17,15 @@
 // list's entries, so no permuted copy of x exists.  (TMA's row gather takes some 72 clocks for
 // four rows: 3.4 ms where this takes XX, 262,144 rows of 2,048 x 1,536.)  Where rows are contracted
 // (GRAD_WEIGHT), those past the segment or of padding are filled with zeros in both operands.
-// Accumulators are fp32 in TMEM, two of 256 columns, drained by eight warps while the MMAs go
+// Accumulators are fp32 in TMEM, two of 256 columns, drained by sixteen warps while the MMAs go
 // on.  TMEM sums are cut, not rounded, so that their error grows with their length: after
 // 8 blocks (512 terms) a sum is added to fp32 registers (weights' gradient over 1,500 rows: relative
-// error 2.2e-6 without that).  E4M3 does so after each block of 128, times its two scales; tiles
-// of up to 64 j hand over four blocks at a time.
+// error 2.2e-6 without that, 5e-7 with it).
+// E4M3 adds up after each block of 128, times its two scales.  There the rows of x are the
+// instruction's 256 m and the weights its 256 columns, so that a thread, which reads one TMEM lane,
+// has one scale of either operand a block; with the scales along the columns their loads from
+// shared memory, 1,024 clocks a block, took twice the MMAs' time (2,626 us for 262,144 rows of
+// 2,048 x 1,536; this way XX).
 // Every wait is bounded; on expiry the kernel records MOER_ETIMEOUT and returns.
 #include "rows.cuh"
 #include "umma.cuh"
@@ -36,22 +40,18 @@ constexpr int EG_EPI_WARPS = 16;
 constexpr int EG_THREADS = (8 + EG_EPI_WARPS) * 32;
 constexpr int EG_J = 256;                    // most j of a tile
 constexpr int EG_COLS = EG_J / (EG_EPI_WARPS / 4);  // columns that an epilogue warp holds
-constexpr int EG_SLOTS = 4, EG_SLOT_KB = 4;  // E4M3: ring of the scales' products, blocks a slot
-constexpr int EG_SCALE_BYTES = EG_SLOTS * EG_SLOT_KB * EG_J * 4;
 constexpr int EG_TMEM_COLS = 512;
 constexpr int EG_ROUND = 8;                  // blocks summed in TMEM (not E4M3)
 constexpr size_t EG_OFF_BAR = (size_t)EG_STAGES * EG_STAGE_BYTES;
-constexpr size_t EG_OFF_SCALE = EG_OFF_BAR + 512;
+constexpr size_t EG_OFF_TABLE = EG_OFF_BAR + 256;  // the experts' tiles: 3 x (E + 1) ints
 // Barriers, as byte offsets from the stages' start.
 constexpr uint32_t EG_FULL = (uint32_t)EG_OFF_BAR;            // [stage] in the leader: both operands of both CTAs
 constexpr uint32_t EG_EMPTY = EG_FULL + 8 * EG_STAGES;        // [stage] the MMAs have read it
 constexpr uint32_t EG_TFULL = EG_EMPTY + 8 * EG_STAGES;       // [2] an accumulator is complete
 constexpr uint32_t EG_TEMPTY = EG_TFULL + 16;                 // [2] in the leader: it is drained in both CTAs
 constexpr uint32_t EG_DRAIN = EG_TEMPTY + 16;
-constexpr uint32_t EG_SFULL = EG_DRAIN + 8;                   // [slot] scales (E4M3)
-constexpr uint32_t EG_SEMPTY = EG_SFULL + 8 * EG_SLOTS;
-constexpr uint32_t EG_TMEM = EG_SEMPTY + 8 * EG_SLOTS;        // TMEM address, failure flag
-static_assert(EG_TMEM + 8 <= EG_OFF_SCALE, "barrier area");
+constexpr uint32_t EG_TMEM = EG_DRAIN + 8;                    // TMEM address, failure flag
+static_assert(EG_TMEM + 8 <= EG_OFF_TABLE, "barrier area");
 
 struct GemmParams {
   CUtensorMap tmw;   // w [E][N][K], or d_y [rows][N]
@@ -169,15 +169,20 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_
 }
 
 // ------------------------------------------------------------ tiles
-// The experts' rows and tiles, in shared memory: lo[e] .. lo[e + 1] are e's rows (offsets
-// held within [0, rows] and non-decreasing), first[e] its first tile column.
+// The experts' rows and tiles, in shared memory: lo[e] .. lo[e + 1] are e's rows (offsets held
+// within [0, rows] and non-decreasing), first[e] its first tile column, high[e] the rows of each of its
+// tiles but the last.
 struct TileTable {
   const int* lo;
   const int* first;
+  const int* high;
 };
 
-// One warp.  With `by_rows` an expert has a tile column for each 256 of its rows.
-__device__ __forceinline__ void make_tile_table(const GemmParams& p, bool by_rows, int* lo, int* first, int lane) {
+// One warp.  With `by_rows` an expert has as few tile columns as hold its rows, of equal height
+// (in steps of 16) but for the last.
+__device__ __forceinline__ void make_tile_table(const GemmParams& p, bool by_rows, int* lo, int lane) {
+  int* first = lo + p.E + 1;
+  int* high = first + p.E + 1;
   int most = 0, sum = 0;  // running maximum of the offsets, tile columns so far
   bool bad = false;
   for (int e0 = 0; e0 <= p.E; e0 += 32) {
@@ -195,7 +200,9 @@ __device__ __forceinline__ void make_tile_table(const GemmParams& p, bool by_row
     if (lane == 0) prev = most;
     most = __shfl_sync(FULL, v, 31);
     // tile columns of expert e - 1, whose rows are prev .. v
-    int t = e >= 1 && e <= p.E ? (by_rows ? (int)(((uint32_t)(v - prev) + EG_J - 1) / EG_J) : p.njb) : 0;
+    const uint32_t n = (uint32_t)(v - prev), nt = (n + EG_J - 1) / EG_J;
+    int t = e >= 1 && e <= p.E ? (by_rows ? (int)nt : p.njb) : 0;
+    if (e >= 1 && e <= p.E) high[e - 1] = nt > 0 ? (int)(((n + nt - 1) / nt + 15) & ~15u) : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int u = __shfl_up_sync(FULL, t, d);
@@ -216,54 +223,70 @@ struct Tile {
   int hi;     // end of the segment
   int j0;     // GRAD_WEIGHT: first n
   int rows;   // valid j
-  int ncol;   // j rounded up to 16: N of the instruction
+  int ncol;   // N of the instruction: j rounded up to 16 (E4M3: 256 of m)
   int nkb;    // blocks of c
 };
 
-template <int OP, int KE>
-__device__ __forceinline__ Tile tile_of(const GemmParams& p, const TileTable& tt, int t) {
-  Tile x;
-  const int col = t / p.nmb;
-  x.mb = t - col * p.nmb;
-  int a = 0, b = p.E - 1;  // the last expert with first[e] <= col: the one that has tile column col
-  while (a < b) {
-    const int m = (a + b + 1) >> 1;
-    if (tt.first[m] <= col) a = m;
-    else b = m - 1;
+// A cluster's tiles, every t_step-th, m blocks first.  Kept by each warp for itself; steps take no
+// division and no search, since a division and a binary search a tile left gaps between tiles.
+template <int OP, bool FP8>
+struct TileWalk {
+  int left;  // tiles that remain, this one included
+  int col, mb, e, dcol, dmb;
+  __device__ __forceinline__ TileWalk(const GemmParams& p, const TileTable& tt) {
+    const int t = blockIdx.x >> 1, step = gridDim.x >> 1, n = tt.first[p.E] * p.nmb;
+    left = t < n ? (n - t + step - 1) / step : 0;
+    col = t / p.nmb;
+    mb = t - col * p.nmb;
+    dcol = step / p.nmb;
+    dmb = step - dcol * p.nmb;
+    e = 0;
   }
-  x.e = a;
-  const int lo = tt.lo[a], i = col - tt.first[a];
-  x.hi = tt.lo[a + 1];
-  const uint32_t n = (uint32_t)(x.hi - lo);
-  if (OP == MOER_GEMM_GRAD_WEIGHT) {
-    x.p0 = lo;
-    x.j0 = i * EG_J;
-    x.rows = min(EG_J, p.J - x.j0);
-    x.ncol = EG_J;
-    x.nkb = (int)((n + KE - 1) / KE);
-  } else {
-    // as few tiles as hold the segment, of equal height but for the last
-    const uint32_t nt = (n + EG_J - 1) / EG_J;
-    const int h = (int)(((n + nt - 1) / nt + 15) & ~15u);
-    x.p0 = lo + i * h;
-    x.j0 = 0;
-    x.rows = min(h, x.hi - x.p0);
-    x.ncol = (x.rows + 15) & ~15;
-    x.nkb = (p.C + KE - 1) / KE;
+  __device__ __forceinline__ void advance(const GemmParams& p) {
+    --left;
+    col += dcol;
+    mb += dmb;
+    if (mb >= p.nmb) {
+      mb -= p.nmb;
+      ++col;
+    }
   }
-  return x;
-}
+  // Of the present position, when tiles remain.
+  __device__ __forceinline__ Tile tile(const GemmParams& p, const TileTable& tt) {
+    constexpr int KE = FP8 ? 128 : 64;
+    while (tt.first[e + 1] <= col) ++e;
+    Tile x;
+    x.e = e;
+    x.mb = mb;
+    const int lo = tt.lo[e], i = col - tt.first[e];
+    x.hi = tt.lo[e + 1];
+    if (OP == MOER_GEMM_GRAD_WEIGHT) {
+      x.p0 = lo;
+      x.j0 = i * EG_J;
+      x.rows = min(EG_J, p.J - x.j0);
+      x.ncol = EG_J;
+      x.nkb = (int)(((uint32_t)(x.hi - lo) + KE - 1) / KE);
+    } else {
+      const int h = tt.high[e];
+      x.p0 = lo + i * h;
+      x.j0 = 0;
+      x.rows = min(h, x.hi - x.p0);
+      x.ncol = FP8 ? EG_J : (x.rows + 15) & ~15;
+      x.nkb = (p.C + KE - 1) / KE;
+    }
+    return x;
+  }
+};
 
-// The row of x behind list row q, or -1; `bad`: its entry names no token.
-__device__ __forceinline__ int source_row(const GemmParams& p, int q, bool& bad) {
-  if (p.order == nullptr) return q;
-  const int o = p.order[q];
-  if (o < 0) return -1;
+// The row of x behind a list row's entry, or -1; `bad`: it names no token.
+__device__ __forceinline__ int entry_row(const GemmParams& p, int o, bool& bad) {
+  if (p.order == nullptr || o < 0) return o;
   const int r = o / p.k;
   if (r < p.tokens) return r;
   bad = true;
   return -1;
 }
+__device__ __forceinline__ int list_entry(const GemmParams& p, int q) { return p.order == nullptr ? q : p.order[q]; }
 
 // GRAD_WEIGHT: the rows of x behind the 64 list rows of a block, two to a lane (r0: row lane, r1: row
 // 32 + lane; -1: past the segment or padding), with the next block's entries under way.
@@ -272,14 +295,7 @@ struct RowPair {
   int n0, n1;
   bool bad;
   __device__ __forceinline__ int entry(const GemmParams& p, const Tile& x, uint32_t q) const {
-    return q < (uint32_t)(x.hi - x.p0) ? (p.order == nullptr ? x.p0 + (int)q : p.order[x.p0 + (int)q]) : -1;
-  }
-  __device__ __forceinline__ int row(const GemmParams& p, int o) {
-    if (p.order == nullptr || o < 0) return o;
-    const int r = o / p.k;
-    if (r < p.tokens) return r;
-    bad = true;
-    return -1;
+    return q < (uint32_t)(x.hi - x.p0) ? list_entry(p, x.p0 + (int)q) : -1;
   }
   __device__ __forceinline__ RowPair(const GemmParams& p, const Tile& x, int kb, int lane) : r0(-1), r1(-1), bad(false) {
     n0 = entry(p, x, (uint32_t)kb * 64 + lane);
@@ -288,33 +304,53 @@ struct RowPair {
   // The rows of the block whose entries are under way, and block kb's entries; whether one of the
   // rows is none.
   __device__ __forceinline__ bool next(const GemmParams& p, const Tile& x, int kb, int lane) {
-    r0 = row(p, n0);
-    r1 = row(p, n1);
+    r0 = entry_row(p, n0, bad);
+    r1 = entry_row(p, n1, bad);
     n0 = entry(p, x, (uint32_t)kb * 64 + lane);
     n1 = entry(p, x, (uint32_t)kb * 64 + 32 + lane);
     return __any_sync(FULL, r0 < 0 || r1 < 0);
   }
 };
 
-// Columns of a block's sums in a round of E4M3: a round is EG_J / width blocks side by side.
-template <bool FP8>
-__device__ __forceinline__ int round_width(const Tile& x) {
-  return !FP8 ? EG_J : x.ncol <= 64 ? 64 : x.ncol <= 128 ? 128 : 256;
-}
+// Which of the first 16 blocks from kb on hold a row that is none, as bits (GRAD_WEIGHT).
+struct DirtyBlocks {
+  static constexpr int N = 8;  // blocks looked at in one go
+  int v[2 * N];
+  uint32_t bits;
+  __device__ __forceinline__ void fetch(const GemmParams& p, const Tile& x, int kb, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) {
+      const uint32_t q = (uint32_t)kb * 64 + 32 * i + lane;
+      v[i] = q < (uint32_t)(x.hi - x.p0) ? list_entry(p, x.p0 + (int)q) : -1;
+    }
+  }
+  __device__ __forceinline__ void settle(const GemmParams& p) {
+    const int64_t end = p.order == nullptr ? p.rows : p.tokens * p.k;
+    bits = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool none = v[2 * i] < 0 || v[2 * i + 1] < 0 || v[2 * i] >= end || v[2 * i + 1] >= end;
+      bits |= __any_sync(FULL, none) ? 1u << i : 0u;
+    }
+  }
+};
 
 // ------------------------------------------------------------ rows of x
-// One of the row warps (6; E4M3: 5): it brings every sixth (fifth) stage by itself, from the release
-// of the stage to the copies' landing, so that as many stages are under way without one warp's wait
-// holding up another's (four warps sharing every stage: 2,284 us where this takes XX).  Row indices
-// lie with the lanes and go round by shuffles.
+// One of the six row warps: it brings every sixth stage by itself, from the release of the stage to
+// the copies' landing, so that as many stages are under way without one warp's wait holding up
+// another's (four warps sharing every stage: 2,284 us where this takes XX).  Row indices lie with
+// the lanes and go round by shuffles; the next tile's are under way while this one's are used.
+constexpr int EG_ROW_WARPS = 6;
+// A barrier's parity tells neighbouring rounds apart, no more: with more warps than stages one could
+// ask for a slot two rounds ahead of the MMAs and be let through.
+static_assert(EG_ROW_WARPS <= EG_STAGES, "row warps");
+
 template <int OP, bool FP8>
-__device__ __forceinline__ void load_rows(const GemmParams& p, const TileTable& tt, char* sm, uint32_t base, int w, int rank, int lane, int ntiles,
-                                          int t_step) {
-  constexpr int EB = FP8 ? 1 : 2, KE = 128 / EB, NW = FP8 ? 5 : 6;
+__device__ __forceinline__ void load_rows(const GemmParams& p, const TileTable& tt, char* sm, uint32_t base, int w, int rank, int lane) {
+  constexpr int EB = FP8 ? 1 : 2, KE = 128 / EB;
   constexpr bool GW = OP == MOER_GEMM_GRAD_WEIGHT;
   const uint32_t bar0 = mapa_u32(base + EG_FULL, 0);
-  uint32_t g = 0;       // stages of the tiles so far
-  uint32_t mine = w;    // the next one that is this warp's
+  uint32_t mine = w;    // the next stage that is this warp's
   bool ok = true;
   // the stage's copies have landed: visible to the MMA, handed over
   auto hand_over = [&](uint32_t s) {
@@ -329,19 +365,34 @@ __device__ __forceinline__ void load_rows(const GemmParams& p, const TileTable& 
     s = mine - round * EG_STAGES;
     return round == 0 || warp_wait(base + EG_EMPTY + 8u * s, (round - 1) & 1u, p.status, lane);
   };
-  for (int t = blockIdx.x >> 1; t < ntiles && ok; t += t_step) {
-    const Tile x = tile_of<OP, KE>(p, tt, t);
-    if constexpr (!GW) {
-      // eight lanes a row: rows 4 i + lane / 8 of this CTA's half; lane l holds rows l, 32 + l, ...
-      const int half = x.ncol >> 1, sub = lane >> 3, c = lane & 7;
+  TileWalk<OP, FP8> walk(p, tt);
+  if (walk.left == 0) return;
+  Tile x = walk.tile(p, tt);
+  int kb = w;  // block of the tile that stage `mine` holds
+  if constexpr (!GW) {
+    // eight lanes a row: rows 4 i + lane / 8 of this CTA's part; lane l holds rows l, 32 + l, ...
+    const int sub = lane >> 3, c = lane & 7;
+    int ent[4];
+    auto fetch = [&](const Tile& y) {
+      const int part = FP8 ? 128 : y.ncol >> 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // rows past the tile repeat its last one
+        ent[i] = 32 * i < part ? list_entry(p, y.p0 + min(rank * part + 32 * i + lane, y.rows - 1)) : 0;
+    };
+    fetch(x);
+    for (;;) {
+      const int part = FP8 ? max(0, min(128, x.rows - rank * 128)) : x.ncol >> 1;  // rows to bring
       int src[4];
       bool bad = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // rows past the tile repeat its last one; padding takes any row
-        const int j = min(rank * half + 32 * i + lane, x.rows - 1);
-        src[i] = 32 * i < half ? max(source_row(p, x.p0 + j, bad), 0) : 0;
+      for (int i = 0; i < 4; ++i) src[i] = max(entry_row(p, ent[i], bad), 0);  // padding takes any row
+      walk.advance(p);
+      const int nkb = x.nkb;
+      if (walk.left > 0) {
+        x = walk.tile(p, tt);
+        fetch(x);
       }
-      for (int kb = (int)(mine - g); kb < x.nkb; kb += NW, mine += NW) {
+      for (; kb < nkb; kb += EG_ROW_WARPS, mine += EG_ROW_WARPS) {
         uint32_t s;
         if (!take(s)) {
           ok = false;
@@ -352,20 +403,25 @@ __device__ __forceinline__ void load_rows(const GemmParams& p, const TileTable& 
         const char* xk = p.x + (n > 0 ? off : 0);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          if (4 * i >= half) break;  // half is a multiple of eight
+          if (4 * i >= part) break;
           const int r = __shfl_sync(FULL, src[i / 8], (4 * i + sub) & 31);
           cp_async16(dst + 512u * i + ((uint32_t)(c ^ ((4 * i + sub) & 7)) << 4), xk + (int64_t)r * p.ld_x, n);
         }
         hand_over(s);
       }
-    } else {
-      // sixteen lanes a row: rows 2 i + lane / 16 of the block
-      const int sub = lane >> 4, c = lane & 15;
+      if (!ok || walk.left == 0) break;
+      kb -= nkb;
+    }
+  } else {
+    // sixteen lanes a row: rows 2 i + lane / 16 of the block
+    const int sub = lane >> 4, c = lane & 15;
+    bool bad = false;
+    for (;;) {
       const int acol = x.mb * 256 + rank * 128 + c * 8, bcol = x.j0 + rank * 128 + c * 8;
       const int an = max(0, min(16, (p.M - acol) * 2)), bn = max(0, min(16, (p.J - bcol) * 2));
-      RowPair rp(p, x, (int)(mine - g), lane);
-      for (int kb = (int)(mine - g); kb < x.nkb; kb += NW, mine += NW) {
-        const bool dirty = rp.next(p, x, kb + NW, lane);
+      RowPair rp(p, x, kb, lane);
+      for (; kb < x.nkb; kb += EG_ROW_WARPS, mine += EG_ROW_WARPS) {
+        const bool dirty = rp.next(p, x, kb + EG_ROW_WARPS, lane);
         uint32_t s;
         if (!take(s)) {
           ok = false;
@@ -373,20 +429,29 @@ __device__ __forceinline__ void load_rows(const GemmParams& p, const TileTable& 
         }
         const uint32_t dst = base + s * EG_STAGE_BYTES + (uint32_t)((c >> 3) * EG_PANEL + sub * 128);
         const char* ax = p.x + (an > 0 ? (int64_t)acol * 2 : 0);
-        const char* bx = p.dy + (int64_t)(x.p0 + (int64_t)kb * KE + sub) * p.ld_dy + (bn > 0 ? (int64_t)bcol * 2 : 0);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const int r = __shfl_sync(FULL, i < 16 ? rp.r0 : rp.r1, (2 * i + sub) & 31);
-          const uint32_t at = 256u * i + ((uint32_t)((c & 7) ^ ((2 * i + sub) & 7)) << 4);
-          cp_async16(dst + at, ax + (int64_t)max(r, 0) * p.ld_x, r >= 0 ? an : 0);
-          // (a block that is all the segment's own comes by TMA)
-          if (dirty) cp_async16(dst + EG_HALF + at, r >= 0 ? bx + (int64_t)(2 * i) * p.ld_dy : p.dy, r >= 0 ? bn : 0);
+          cp_async16(dst + 256u * i + ((uint32_t)((c & 7) ^ ((2 * i + sub) & 7)) << 4), ax + (int64_t)max(r, 0) * p.ld_x, r >= 0 ? an : 0);
+        }
+        if (dirty) {  // (a block that is all the segment's own comes by TMA)
+          const char* bx = p.dy + ((int64_t)x.p0 + (int64_t)kb * KE + sub) * p.ld_dy + (bn > 0 ? (int64_t)bcol * 2 : 0);
+#pragma unroll 4
+          for (int i = 0; i < 32; ++i) {
+            const int r = __shfl_sync(FULL, i < 16 ? rp.r0 : rp.r1, (2 * i + sub) & 31);
+            cp_async16(dst + EG_HALF + 256u * i + ((uint32_t)((c & 7) ^ ((2 * i + sub) & 7)) << 4),
+                       r >= 0 ? bx + (int64_t)(2 * i) * p.ld_dy : p.dy, r >= 0 ? bn : 0);
+          }
         }
         hand_over(s);
       }
-      if (rp.bad) atomicOr(p.status, WS_BIT_EDATA);
+      bad |= rp.bad;
+      walk.advance(p);
+      if (!ok || walk.left == 0) break;
+      kb -= x.nkb;
+      x = walk.tile(p, tt);
     }
-    g += (uint32_t)x.nkb;
+    if (bad) atomicOr(p.status, WS_BIT_EDATA);
   }
   if (!ok && lane == 0) *reinterpret_cast<volatile int*>(sm + EG_TMEM + 4) = 1;
 }
@@ -421,6 +486,26 @@ __device__ __forceinline__ void store_chunk(const GemmParams& p, int64_t first, 
   else store_cols(static_cast<__half*>(p.out) + first, p.ld_out, v, n, zero);
 }
 
+// A thread's neighbouring columns of one row (E4M3).  n: columns that exist.
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T* o, const float2 (&v)[N], int n, bool zero) {
+  constexpr int PER = 16 / (int)sizeof(T);
+  const bool wide = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
+#pragma unroll
+  for (int c = 0; c < 2 * N; c += PER) {
+    T t[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) t[i] = from_f32<T>(zero ? 0.f : ((c + i) & 1 ? v[(c + i) / 2].y : v[(c + i) / 2].x));
+    if (wide && c + PER <= n) {
+      *reinterpret_cast<uint4*>(o + c) = *reinterpret_cast<const uint4*>(t);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (c + i < n) o[c + i] = t[i];
+    }
+  }
+}
+
 template <int OP>
 __device__ __forceinline__ int64_t out_first(const GemmParams& p, const Tile& x, int m) {
   return OP == MOER_GEMM_GRAD_WEIGHT ? x.e * p.stride_out + (int64_t)x.j0 * p.ld_out + m : (int64_t)x.p0 * p.ld_out + m;
@@ -432,27 +517,27 @@ __device__ __forceinline__ uint32_t pad_mask(const GemmParams& p, const Tile& x,
   if (OP == MOER_GEMM_GRAD_WEIGHT || p.order == nullptr) return 0u;
   bool bad = false;
   const int j = c * 32 + lane;
-  const bool pad = j < x.rows && source_row(p, x.p0 + j, bad) < 0;
+  const bool pad = j < x.rows && entry_row(p, list_entry(p, x.p0 + j), bad) < 0;
   if (bad) atomicOr(p.status, WS_BIT_EDATA);
   return __ballot_sync(FULL, pad);
 }
 
 // ------------------------------------------------------------ the kernel
-// Warps: 0 loads by TMA, 1 allocates TMEM and issues the MMAs (in the leader), 2 to 7 load rows (E4M3: 2
-// forms the scales' products), 8 to 23 drain the accumulators, each 64 columns of its TMEM
-// lanes.  Registers go to the last
+// Warps: 0 loads by TMA, 1 allocates TMEM and issues the MMAs (in the leader), 2 to 7 load rows, 8 to 23
+// drain the accumulators, each 64 columns of its TMEM lanes.  Registers go to the last
 // sixteen: the six warpgroups' shares, 64 + 64 + 4 x 88, are the block's 6 x 80.
 template <int OP, bool FP8>
 __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int EB = FP8 ? 1 : 2, KE = 128 / EB;  // bytes of an element, elements of c a block
   constexpr bool GW = OP == MOER_GEMM_GRAD_WEIGHT;
   constexpr bool A_PANELS = OP != MOER_GEMM_FORWARD, B_PANELS = GW;
+  constexpr int ROUND = FP8 ? 1 : EG_ROUND;
   extern __shared__ __align__(1024) char eg_raw[];
   const uint32_t base = (smem_u32(eg_raw) + 1023) & ~1023u;  // the same in both CTAs, as the MMA's descriptors require
   char* sm = eg_raw + (base - smem_u32(eg_raw));
   volatile int& failed = *reinterpret_cast<int*>(sm + EG_TMEM + 4);
-  int* lo = reinterpret_cast<int*>(sm + EG_OFF_SCALE + (FP8 ? EG_SCALE_BYTES : 0));
-  const TileTable tt{lo, lo + p.E + 1};
+  int* lo = reinterpret_cast<int*>(sm + EG_OFF_TABLE);
+  const TileTable tt{lo, lo + p.E + 1, lo + 2 * (p.E + 1)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
 
@@ -467,14 +552,10 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
       mbar_init(bar + EG_TEMPTY / 8 + i, 2 * EG_EPI_WARPS);
     }
     mbar_init(bar + EG_DRAIN / 8, 1);
-    for (int i = 0; i < EG_SLOTS; ++i) {
-      mbar_init(bar + EG_SFULL / 8 + i, 1);
-      mbar_init(bar + EG_SEMPTY / 8 + i, EG_EPI_WARPS);
-    }
     failed = 0;
     fence_mbar_init();
   }
-  if (warp == 0) make_tile_table(p, !GW, lo, lo + p.E + 1, lane);
+  if (warp == 0) make_tile_table(p, !GW, lo, lane);
   cluster_sync();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + EG_TMEM), "r"(EG_TMEM_COLS));
@@ -483,7 +564,6 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  const int ntiles = tt.first[p.E] * p.nmb, t_step = gridDim.x >> 1;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -493,14 +573,21 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
       int s = 0;
       uint32_t fills = 0, ph = 1;  // parity of the release that the next fill of stage s waits for
       bool ok = true;
-      for (int t = blockIdx.x >> 1; t < ntiles && ok; t += t_step) {
-        const Tile x = tile_of<OP, KE>(p, tt, t);
+      for (TileWalk<OP, FP8> walk(p, tt); walk.left > 0 && ok; walk.advance(p)) {
+        const Tile x = walk.tile(p, tt);
         const int m0 = x.mb * 256 + rank * 128;
         const int e = p.one_w ? 0 : x.e;
-        RowPair rp(p, x, 0, lane);
+        DirtyBlocks db;
+        if constexpr (GW) db.fetch(p, x, 0, lane);
         for (int kb = 0; kb < x.nkb; ++kb) {
           bool dirty = false;
-          if constexpr (GW) dirty = rp.next(p, x, kb + 1, lane);
+          if constexpr (GW) {
+            if (kb % DirtyBlocks::N == 0) {
+              db.settle(p);
+              if (kb + DirtyBlocks::N < x.nkb) db.fetch(p, x, kb + DirtyBlocks::N, lane);
+            }
+            dirty = (db.bits >> (kb % DirtyBlocks::N)) & 1u;
+          }
           if (fills >= EG_STAGES && !warp_wait(base + EG_EMPTY + 8u * s, ph, p.status, lane)) {
             ok = false;
             break;
@@ -546,21 +633,35 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
       // -------------------------------------------------------- MMA
       if (lane == 0) {
         bool ok = true;
-        int s = 0;
-        uint32_t ph = 0;
         if (rank == 0) {
-          const uint64_t d0 = A_PANELS ? umma_desc_panels(base) : umma_desc_sw128(base);
-          const uint64_t d1 = B_PANELS ? umma_desc_panels(base + EG_HALF) : umma_desc_sw128(base + EG_HALF);
+          int s = 0;
+          uint32_t ph = 0, j = 0;  // parity of the full barriers; rounds begun
+          // E4M3 has the rows of x as the instruction's m and the weights as its columns
+          const uint32_t at_w = base, at_x = base + EG_HALF;
+          const uint64_t d0 = FP8 ? umma_desc_sw128(at_x) : A_PANELS ? umma_desc_panels(at_w) : umma_desc_sw128(at_w);
+          const uint64_t d1 = FP8 ? umma_desc_sw128(at_w) : B_PANELS ? umma_desc_panels(at_x) : umma_desc_sw128(at_x);
           const uint32_t hi = (uint32_t)(d0 >> 32);  // the same for both
           // one instruction takes 32 bytes of a row of c, or 16 rows of panels (16-byte units)
           constexpr uint32_t A_STEP = A_PANELS ? 128 : 2, B_STEP = B_PANELS ? 128 : 2;
           const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + EG_TMEM);
-          uint32_t j = 0;  // rounds begun
-          for (int t = blockIdx.x >> 1; t < ntiles && ok; t += t_step) {
-            const Tile x = tile_of<OP, KE>(p, tt, t);
-            const uint32_t idesc = p.idesc | ((uint32_t)(x.ncol >> 3) << 17);
-            const int w = round_width<FP8>(x), len = FP8 ? EG_J / w : EG_ROUND;
-            for (int kb = 0, r = 0; kb < x.nkb; ++kb) {
+          TileWalk<OP, FP8> walk(p, tt);
+          int nkb = 0;
+          uint32_t idesc = 0;
+          auto look = [&]() {
+            const Tile x = walk.tile(p, tt);
+            nkb = x.nkb;
+            idesc = p.idesc | ((uint32_t)(x.ncol >> 3) << 17);
+          };
+          if (walk.left > 0) look();
+          while (walk.left > 0 && ok) {
+            const int nk = nkb;
+            const uint32_t id = idesc;
+            if (nk == 0) {
+              walk.advance(p);
+              if (walk.left > 0) look();
+              continue;
+            }
+            for (int kb = 0, r = 0; kb < nk; ++kb) {
               const uint32_t a = j & 1u;
               if (r == 0 && j >= 2 && !one_wait(base + EG_TEMPTY + 8u * a, ((j >> 1) - 1) & 1u, p.status)) {
                 ok = false;
@@ -572,12 +673,11 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
               }
               tc_fence_after();
               const uint32_t da = (uint32_t)d0 + (uint32_t)s * (EG_STAGE_BYTES >> 4), db = (uint32_t)d1 + (uint32_t)s * (EG_STAGE_BYTES >> 4);
-              const uint32_t dt = tmem + a * EG_J + (FP8 ? r * w : 0);
+              const uint32_t dt = tmem + a * EG_J;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                umma_pair<FP8>(dt, da + A_STEP * i, db + B_STEP * i, hi, idesc, (i > 0 || (!FP8 && r > 0)) ? 1u : 0u);
+              for (int i = 0; i < 4; ++i) umma_pair<FP8>(dt, da + A_STEP * i, db + B_STEP * i, hi, id, (i > 0 || r > 0) ? 1u : 0u);
               umma_commit_pair(base + EG_EMPTY + 8u * s);
-              if (++r == len || kb == x.nkb - 1) {
+              if (++r == ROUND || kb == nk - 1) {
                 umma_commit_pair(base + EG_TFULL + 8u * a);
                 ++j;
                 r = 0;
@@ -586,6 +686,10 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
                 s = 0;
                 ph ^= 1u;
               }
+              if (kb == 0) {  // the next tile, while this one's MMAs run
+                walk.advance(p);
+                if (walk.left > 0) look();
+              }
             }
           }
           umma_commit_pair(base + EG_DRAIN);
@@ -593,57 +697,12 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
         if (!one_wait(base + EG_DRAIN, 0, p.status)) ok = false;
         if (!ok) failed = 1;
       }
-    } else if (FP8 && warp == 2) {
-      // -------------------------------------------------------- scales (E4M3): eight j a lane
-      if constexpr (FP8) {
-        const int nkw = (p.C + 127) / 128, nnb = (p.M + 127) / 128;
-        uint32_t it = 0;
-        bool ok = true;
-        for (int t = blockIdx.x >> 1; t < ntiles && ok; t += t_step) {
-          const Tile x = tile_of<OP, KE>(p, tt, t);
-          int r[8];
-          bool bad = false;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) r[i] = lane + 32 * i < x.rows ? source_row(p, x.p0 + lane + 32 * i, bad) : -1;
-          const int mb = x.mb * 2 + rank;
-          const float* sw = p.sw + ((int64_t)x.e * nnb + min(mb, nnb - 1)) * nkw;
-          for (int k0 = 0; k0 < x.nkb; k0 += EG_SLOT_KB, ++it) {
-            const uint32_t slot = it % EG_SLOTS;
-            if (it >= EG_SLOTS && !warp_wait(base + EG_SEMPTY + 8u * slot, (it / EG_SLOTS - 1) & 1u, p.status, lane)) {
-              ok = false;
-              break;
-            }
-            const int nb = min(EG_SLOT_KB, x.nkb - k0);
-            float* d = reinterpret_cast<float*>(sm + EG_OFF_SCALE) + slot * EG_SLOT_KB * EG_J + lane;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              if (g * 128 >= x.ncol) break;
-              float v[4][EG_SLOT_KB];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float* sx = p.sx + (int64_t)max(r[4 * g + i], 0) * p.ld_sx + k0;
-#pragma unroll
-                for (int b = 0; b < EG_SLOT_KB; ++b) v[i][b] = b < nb && r[4 * g + i] >= 0 ? __ldg(sx + b) : 0.f;
-              }
-#pragma unroll
-              for (int b = 0; b < EG_SLOT_KB; ++b) {
-                const float w = b < nb ? __ldg(sw + k0 + b) : 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d[b * EG_J + 32 * (4 * g + i)] = v[i][b] * w;
-              }
-            }
-            __syncwarp();
-            if (lane == 0) pair_arrive(mapa_u32(base + EG_SFULL + 8u * slot, (uint32_t)rank));
-          }
-        }
-        if (!ok && lane == 0) failed = 1;
-      }
     } else {
-      load_rows<OP, FP8>(p, tt, sm, base, warp - (FP8 ? 3 : 2), rank, lane, ntiles, t_step);
+      load_rows<OP, FP8>(p, tt, sm, base, warp - 2, rank, lane);
     }
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    load_rows<OP, FP8>(p, tt, sm, base, warp - (FP8 ? 3 : 2), rank, lane, ntiles, t_step);
+    load_rows<OP, FP8>(p, tt, sm, base, warp - 2, rank, lane);
   } else {
     // ---------------------------------------------------------- epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
@@ -651,67 +710,91 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
     const uint32_t tempty = mapa_u32(base + EG_TEMPTY, 0);
     // the TMEM lane quarter that this warp may access
     const uint32_t t0 = *reinterpret_cast<const uint32_t*>(sm + EG_TMEM) + ((uint32_t)((warp & 3) * 32) << 16) + h0;
-    uint32_t j = 0, it = 0;
+    uint32_t j = 0;
     bool ok = true;
-    for (int t = blockIdx.x >> 1; t < ntiles && ok; t += t_step) {
-      const Tile x = tile_of<OP, KE>(p, tt, t);
-      const int w = round_width<FP8>(x), len = FP8 ? EG_J / w : EG_ROUND;
-      const int nch = max(0, min(EG_COLS / 16, (x.ncol - h0) >> 4));  // chunks of 16 columns that this warp holds
+    for (TileWalk<OP, FP8> walk(p, tt); walk.left > 0 && ok; walk.advance(p)) {
+      const Tile x = walk.tile(p, tt);
+      const int l = rank * 128 + (warp & 3) * 32 + lane;  // this thread's m in the tile (E4M3: its row)
       float2 acc[EG_COLS / 2];
 #pragma unroll
       for (int c = 0; c < EG_COLS / 2; ++c) acc[c] = make_float2(0.f, 0.f);
-      for (int kb = 0; kb < x.nkb; kb += len, ++j) {
-        const uint32_t a = j & 1u, slot = it % EG_SLOTS;
-        if constexpr (FP8) {
-          if (kb % EG_SLOT_KB == 0) ok = warp_wait(base + EG_SFULL + 8u * slot, (it / EG_SLOTS) & 1u, p.status, lane);
+      if constexpr (FP8) {
+        // a thread has one row and 64 neighbouring columns: one scale of either operand a block
+        const int nkw = x.nkb, nnb = (p.M + 127) / 128;
+        bool bad = false;
+        const int row = l < x.rows ? entry_row(p, list_entry(p, x.p0 + l), bad) : -1;
+        if (bad) atomicOr(p.status, WS_BIT_EDATA);
+        const bool some = rank * 128 + (warp & 3) * 32 < x.rows;  // (a warp without rows only hands buffers back)
+        const float* sx = p.sx + (int64_t)max(row, 0) * p.ld_sx;
+        const float* sw = p.sw + ((int64_t)x.e * nnb + min(x.mb * 2 + h0 / 128, nnb - 1)) * nkw;
+        float fx = row >= 0 ? __ldg(sx) : 0.f, fw = __ldg(sw);
+        for (int kb = 0; kb < nkw; ++kb, ++j) {
+          const float f = fx * fw;
+          if (kb + 1 < nkw) {  // the next block's, under way
+            fx = row >= 0 ? __ldg(sx + kb + 1) : 0.f;
+            fw = __ldg(sw + kb + 1);
+          }
+          const uint32_t a = j & 1u;
+          if (!warp_wait(base + EG_TFULL + 8u * a, (j >> 1) & 1u, p.status, lane)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (some) {
+#pragma unroll
+            for (int c = 0; c < EG_COLS / 16; ++c) {
+              uint32_t r[16];
+              tmem_ld16(t0 + a * EG_J + 16u * c, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], r[2 * i], r[2 * i + 1], f, f);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) pair_arrive(tempty + 8u * a);
         }
-        if (!ok || !warp_wait(base + EG_TFULL + 8u * a, (j >> 1) & 1u, p.status, lane)) {
-          ok = false;
-          break;
+        if (!ok) break;
+        const int m = x.mb * 256 + h0;
+        if (l < x.rows && m < p.M) {
+          const int64_t o = ((int64_t)x.p0 + l) * p.ld_out + m;
+          const int n = min(EG_COLS, p.M - m);
+          if (p.out_dtype == MOER_F32) store_row(static_cast<float*>(p.out) + o, acc, n, row < 0);
+          else if (p.out_dtype == MOER_BF16) store_row(static_cast<__nv_bfloat16*>(p.out) + o, acc, n, row < 0);
+          else store_row(static_cast<__half*>(p.out) + o, acc, n, row < 0);
         }
-        tc_fence_after();
-        const int nsub = FP8 ? min(len, x.nkb - kb) : 1;
-        for (int sub = 0; sub < nsub; ++sub) {
-          const uint32_t ta = t0 + a * EG_J + (FP8 ? sub * w : 0);
-          const float4* sc = reinterpret_cast<const float4*>(sm + EG_OFF_SCALE) + ((slot * EG_SLOT_KB + (kb + sub) % EG_SLOT_KB) * EG_J + h0) / 4;
+      } else {
+        const int nch = max(0, min(EG_COLS / 16, (x.ncol - h0) >> 4));  // chunks of 16 columns that this warp holds
+        for (int kb = 0; kb < x.nkb; kb += ROUND, ++j) {
+          const uint32_t a = j & 1u;
+          if (!warp_wait(base + EG_TFULL + 8u * a, (j >> 1) & 1u, p.status, lane)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll
           for (int c = 0; c < EG_COLS / 16; ++c) {
             if (c < nch) {
               uint32_t r[16];
-              tmem_ld16(ta + 16u * c, r);
+              tmem_ld16(t0 + a * EG_J + 16u * c, r);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if constexpr (FP8) {
-                  const float4 f = sc[c * 4 + i];
-                  fma2(acc[c * 8 + 2 * i], r[4 * i], r[4 * i + 1], f.x, f.y);
-                  fma2(acc[c * 8 + 2 * i + 1], r[4 * i + 2], r[4 * i + 3], f.z, f.w);
-                } else {
-                  add2(acc[c * 8 + 2 * i], r[4 * i], r[4 * i + 1]);
-                  add2(acc[c * 8 + 2 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-                }
-              }
+              for (int i = 0; i < 8; ++i) add2(acc[c * 8 + i], r[2 * i], r[2 * i + 1]);
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) pair_arrive(tempty + 8u * a);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) pair_arrive(tempty + 8u * a);
-        if constexpr (FP8) {
-          if ((kb + len) % EG_SLOT_KB == 0 || kb + len >= x.nkb) {
-            if (lane == 0) pair_arrive(mapa_u32(base + EG_SEMPTY + 8u * slot, (uint32_t)rank));
-            ++it;
-          }
-        }
-      }
-      if (!ok) break;
-      const int m = x.mb * 256 + rank * 128 + (warp & 3) * 32 + lane;
+        if (!ok) break;
+        const int m = x.mb * 256 + l;
 #pragma unroll
-      for (int c = 0; c < EG_COLS / 32; ++c) {
-        const int j0 = h0 + c * 32;
-        if (j0 < x.rows) {
-          const uint32_t zero = pad_mask<OP>(p, x, j0 / 32, lane);
-          if (m < p.M) store_chunk(p, out_first<OP>(p, x, m) + (int64_t)j0 * p.ld_out, &acc[c * 16], x.rows - j0, zero);
+        for (int c = 0; c < EG_COLS / 32; ++c) {
+          const int j0 = h0 + c * 32;
+          if (j0 < x.rows) {
+            const uint32_t zero = pad_mask<OP>(p, x, j0 / 32, lane);
+            if (m < p.M) store_chunk(p, out_first<OP>(p, x, m) + (int64_t)j0 * p.ld_out, &acc[c * 16], x.rows - j0, zero);
+          }
         }
       }
     }
@@ -775,7 +858,7 @@ bool map_of(CUtensorMap* m, const void* base, int dtype, int rank, const uint64_
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t smem_bytes(int E, bool fp8) { return EG_OFF_SCALE + (fp8 ? EG_SCALE_BYTES : 0) + (size_t)2 * (E + 1) * 4 + 1024; }
+size_t smem_bytes(int E) { return EG_OFF_TABLE + (size_t)3 * (E + 1) * 4 + 1024; }
 
 cudaLaunchConfig_t pair_config(int clusters, size_t smem, cudaStream_t st, cudaLaunchAttribute* at) {
   cudaLaunchConfig_t cfg = {};
@@ -796,7 +879,7 @@ template <int OP, bool FP8>
 cudaError_t gemm_run(const GemmParams& p, int64_t most_tiles, cudaStream_t st) {
   static std::atomic<unsigned long long> set{0};
   static std::atomic<int> cached[64];
-  cudaError_t e = smem_optin(expert_gemm_kernel<OP, FP8>, (int)smem_bytes(1024, FP8), set);
+  cudaError_t e = smem_optin(expert_gemm_kernel<OP, FP8>, (int)smem_bytes(1024), set);
   if (e != cudaSuccess) return e;
   int dev = 0;
   e = cudaGetDevice(&dev);
@@ -804,13 +887,13 @@ cudaError_t gemm_run(const GemmParams& p, int64_t most_tiles, cudaStream_t st) {
   cudaLaunchAttribute at[1];
   int most = dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
   if (most <= 0) {  // clusters that fit on the device at once, one CTA an SM
-    const cudaLaunchConfig_t cfg = pair_config(1, smem_bytes(1024, FP8), nullptr, at);
+    const cudaLaunchConfig_t cfg = pair_config(1, smem_bytes(1024), nullptr, at);
     e = cudaOccupancyMaxActiveClusters(&most, expert_gemm_kernel<OP, FP8>, &cfg);
     if (e != cudaSuccess) return e;
     if (most <= 0) return cudaErrorInvalidConfiguration;
     if (dev < 64) cached[dev].store(most, std::memory_order_relaxed);
   }
-  const cudaLaunchConfig_t cfg = pair_config((int)min64(most_tiles, most), smem_bytes(p.E, FP8), st, at);
+  const cudaLaunchConfig_t cfg = pair_config((int)min64(most_tiles, most), smem_bytes(p.E), st, at);
   e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<OP, FP8>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
