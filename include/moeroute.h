@@ -667,7 +667,8 @@ typedef struct moer_expert_gemm_args {
 } moer_expert_gemm_args;
 
 /* x, w and d_y are 16-byte aligned, and so is each of their rows (ld and stride_w a
- * multiple of 8, with E4M3 of 16); out is aligned to its element.  An offset
+ * multiple of 8, with E4M3 of 16; ld below 2^30); out is aligned to its element.
+ * rows / 256 * N / 256 (GRAD_INPUT: K) below 2^30, else MOER_ERANGE.  An offset
  * outside the limits is moved to the nearest one within them and records
  * MOER_EDATA in ws; an order entry that names no row of x counts as padding
  * and records it too.

@@ -892,8 +892,10 @@ moer_status moer_expert_gemm(const moer_expert_gemm_args* a, void* ws, size_t ws
       xs{fp8 ? a->x_scale : nullptr, a->tokens, nkb, a->ld_x_scale, 4, 4, fp8 && a->tokens > 0}, ws8{fp8 ? a->w_scale : nullptr, a->E * nnb, nkb, nkb, 4, 4, fp8};
   moer_status s = check_matrices({x, w, dy, out, xs, ws8});
   if (s != MOER_OK) return s;
-  for (const Matrix& m : {x, w, dy})
+  for (const Matrix& m : {x, w, dy}) {
     if (m.p != nullptr && m.ld * eb % 16 != 0) return MOER_EINVAL;
+    if (m.p != nullptr && m.ld >= (int64_t(1) << 30)) return MOER_ESHAPE;  // a row's step in bytes has 32 bits
+  }
   const int64_t most = int64_t(1) << 48;
   if (a->E > 1 && !gw && (a->stride_w < 0 || a->stride_w > most)) return MOER_ESHAPE;
   if (a->E > 1 && !gw && a->stride_w * eb % 16 != 0) return MOER_EINVAL;

@@ -57,7 +57,7 @@ struct GemmParams {
   CUtensorMap tmw;   // w [E][N][K], or d_y [rows][N]
   const char* x;
   const char* dy;    // GRAD_WEIGHT
-  int64_t ld_x, ld_dy;  // bytes
+  uint32_t ld_x, ld_dy;  // bytes
   const int32_t* off;
   const int32_t* order;
   int64_t rows, tokens;
@@ -151,6 +151,23 @@ __device__ __forceinline__ bool one_wait(uint32_t bar, uint32_t parity, uint32_t
   }
 }
 
+// Waits by the epilogue's warps: one thread polls (sixteen polling warps took the issue slots of the
+// thread that issues the MMAs), the others stand at a named barrier, which passes its answer on.
+__device__ __forceinline__ bool epilogue_wait(uint32_t bar, uint32_t parity, uint32_t* status) {
+  uint32_t ok = 1;
+  if (threadIdx.x == 256) ok = one_wait(bar, parity, status);
+  __syncwarp();
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(ok), "n"(EG_EPI_WARPS * 32)
+      : "memory");
+  return all != 0;
+}
+
 // Arrival on a barrier of either CTA, with the same scope: released at cluster scope each
 // arrival would first wait for the thread's memory operations (1.7 us a stage instead of 0.3).
 __device__ __forceinline__ void pair_arrive(uint32_t caddr) {
@@ -159,6 +176,14 @@ __device__ __forceinline__ void pair_arrive(uint32_t caddr) {
 
 __device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// One lane of the warp, which the compiler knows to be one: descriptors then go to uniform registers
+// without a loop over lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // Waits by a whole warp: lane 0 polls, and its answer is everyone's.
@@ -340,7 +365,7 @@ struct DirtyBlocks {
 // the copies' landing, so that as many stages are under way without one warp's wait holding up
 // another's (four warps sharing every stage: 2,284 us where this takes XX).  Row indices lie with
 // the lanes and go round by shuffles; the next tile's are under way while this one's are used.
-constexpr int EG_ROW_WARPS = 6;
+constexpr int EG_ROW_WARPS = 5;
 // A barrier's parity tells neighbouring rounds apart, no more: with more warps than stages one could
 // ask for a slot two rounds ahead of the MMAs and be let through.
 static_assert(EG_ROW_WARPS <= EG_STAGES, "row warps");
@@ -402,10 +427,15 @@ __device__ __forceinline__ void load_rows(const GemmParams& p, const TileTable& 
         const int off = kb * 128 + c * 16, n = max(0, min(16, p.C * EB - off));
         const char* xk = p.x + (n > 0 ? off : 0);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (4 * i >= part) break;
-          const int r = __shfl_sync(FULL, src[i / 8], (4 * i + sub) & 31);
-          cp_async16(dst + 512u * i + ((uint32_t)(c ^ ((4 * i + sub) & 7)) << 4), xk + (int64_t)r * p.ld_x, n);
+        for (int i8 = 0; i8 < 4; ++i8) {
+          if (32 * i8 >= part) break;
+          uint32_t r[8];  // (in groups, so that the shuffles' latencies overlap)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[i] = (uint32_t)__shfl_sync(FULL, src[i8], 4 * i + sub);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (32 * i8 + 4 * i < part)
+              cp_async16(dst + 4096u * i8 + 512u * i + ((uint32_t)(c ^ ((4 * i + sub) & 7)) << 4), xk + (uint64_t)r[i] * p.ld_x, n);
         }
         hand_over(s);
       }
@@ -430,17 +460,22 @@ __device__ __forceinline__ void load_rows(const GemmParams& p, const TileTable& 
         const uint32_t dst = base + s * EG_STAGE_BYTES + (uint32_t)((c >> 3) * EG_PANEL + sub * 128);
         const char* ax = p.x + (an > 0 ? (int64_t)acol * 2 : 0);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int r = __shfl_sync(FULL, i < 16 ? rp.r0 : rp.r1, (2 * i + sub) & 31);
-          cp_async16(dst + 256u * i + ((uint32_t)((c & 7) ^ ((2 * i + sub) & 7)) << 4), ax + (int64_t)max(r, 0) * p.ld_x, r >= 0 ? an : 0);
+        for (int i8 = 0; i8 < 4; ++i8) {
+          int r[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[i] = __shfl_sync(FULL, i8 < 2 ? rp.r0 : rp.r1, (16 * i8 + 2 * i + sub) & 31);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            cp_async16(dst + 2048u * i8 + 256u * i + ((uint32_t)((c & 7) ^ ((2 * i + sub) & 7)) << 4),
+                       ax + (uint64_t)(uint32_t)max(r[i], 0) * p.ld_x, r[i] >= 0 ? an : 0);
         }
         if (dirty) {  // (a block that is all the segment's own comes by TMA)
-          const char* bx = p.dy + ((int64_t)x.p0 + (int64_t)kb * KE + sub) * p.ld_dy + (bn > 0 ? (int64_t)bcol * 2 : 0);
+          const char* bx = p.dy + (uint64_t)((int64_t)x.p0 + (int64_t)kb * KE + sub) * p.ld_dy + (bn > 0 ? (int64_t)bcol * 2 : 0);
 #pragma unroll 4
           for (int i = 0; i < 32; ++i) {
             const int r = __shfl_sync(FULL, i < 16 ? rp.r0 : rp.r1, (2 * i + sub) & 31);
             cp_async16(dst + EG_HALF + 256u * i + ((uint32_t)((c & 7) ^ ((2 * i + sub) & 7)) << 4),
-                       r >= 0 ? bx + (int64_t)(2 * i) * p.ld_dy : p.dy, r >= 0 ? bn : 0);
+                       r >= 0 ? bx + (uint64_t)(2 * i) * p.ld_dy : p.dy, r >= 0 ? bn : 0);
           }
         }
         hand_over(s);
@@ -631,7 +666,7 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
       if (!ok && lane == 0) failed = 1;
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA
-      if (lane == 0) {
+      if (elect_one()) {
         bool ok = true;
         if (rank == 0) {
           int s = 0;
@@ -702,7 +737,7 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
     }
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    load_rows<OP, FP8>(p, tt, sm, base, warp - 2, rank, lane);
+    if (warp != 5) load_rows<OP, FP8>(p, tt, sm, base, warp == 4 ? 4 : warp - 4, rank, lane);
   } else {
     // ---------------------------------------------------------- epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
@@ -767,7 +802,7 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
         const int nch = max(0, min(EG_COLS / 16, (x.ncol - h0) >> 4));  // chunks of 16 columns that this warp holds
         for (int kb = 0; kb < x.nkb; kb += ROUND, ++j) {
           const uint32_t a = j & 1u;
-          if (!warp_wait(base + EG_TFULL + 8u * a, (j >> 1) & 1u, p.status, lane)) {
+          if (!epilogue_wait(base + EG_TFULL + 8u * a, (j >> 1) & 1u, p.status)) {
             ok = false;
             break;
           }
@@ -946,8 +981,8 @@ moer_status expert_gemm_launch(const moer_expert_gemm_args* a, void* ws, cudaStr
   p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((fwd ? 0u : 1u) << 15) | ((gw ? 1u : 0u) << 16) | ((256u >> 4) << 24);
   p.x = static_cast<const char*>(a->x);
   p.dy = static_cast<const char*>(a->d_y);
-  p.ld_x = a->ld_x * (int64_t)eb;
-  p.ld_dy = a->ld_d_y * (int64_t)eb;
+  p.ld_x = (uint32_t)(a->ld_x * (int64_t)eb);
+  p.ld_dy = (uint32_t)(a->ld_d_y * (int64_t)eb);
   if (gw) {
     const uint64_t dims[3] = {(uint64_t)a->N, (uint64_t)a->rows, 1}, str[2] = {(uint64_t)a->ld_d_y * eb, (uint64_t)a->ld_d_y * eb};
     const uint32_t box[3] = {64, 64, 1};
