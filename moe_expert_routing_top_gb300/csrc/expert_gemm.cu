@@ -13,10 +13,9 @@
 //
 // Clusters of two CTAs, persistent over tiles of 256 m x up to 256 j (tcgen05.mma.cta_group::2,
 // M = 256), c in blocks of 128 bytes, six stages of 32 KB.  A CTA loads its 128 of m and half
-// of the j rows: weights (and d_y) by TMA, rows of x by warps of cp.async that follow the
-// list's entries, so no permuted copy of x exists.  (TMA's row gather takes some 72 clocks for
-// four rows: 3.4 ms where this takes XX, 262,144 rows of 2,048 x 1,536.)  Where rows are contracted
-// (GRAD_WEIGHT), those past the segment or of padding are filled with zeros in both operands.
+// of the j rows, all by TMA: rows of x by its row gather, which follows the list's entries, so no
+// permuted copy of x exists.  Where rows are contracted (GRAD_WEIGHT), those past the segment or of
+// padding are gathered from past the map's end, in both operands: zeros.
 // Accumulators are fp32 in TMEM, two of 256 columns, drained by sixteen warps while the MMAs go
 // on.  TMEM sums are cut, not rounded, so that their error grows with their length: after
 // 8 blocks (512 terms) a sum is added to fp32 registers (weights' gradient over 1,500 rows: relative
@@ -43,21 +42,26 @@ constexpr int EG_COLS = EG_J / (EG_EPI_WARPS / 4);  // columns that an epilogue 
 constexpr int EG_TMEM_COLS = 512;
 constexpr int EG_ROUND = 8;                  // blocks summed in TMEM (not E4M3)
 constexpr size_t EG_OFF_BAR = (size_t)EG_STAGES * EG_STAGE_BYTES;
-constexpr size_t EG_OFF_TABLE = EG_OFF_BAR + 256;  // the experts' tiles: 3 x (E + 1) ints
+constexpr int EG_LISTS = 8;                            // row lists under way: of tiles (2 x 128 rows used), or of blocks of 64
+constexpr int EG_LIST = 128;                           // entries of a list
+constexpr size_t EG_OFF_LIST = EG_OFF_BAR + 512;       // [list][EG_LIST] ints
+constexpr size_t EG_OFF_TABLE = EG_OFF_LIST + (size_t)EG_LISTS * EG_LIST * 4;  // the experts' tiles: 3 x (E + 1) ints
 // Barriers, as byte offsets from the stages' start.
 constexpr uint32_t EG_FULL = (uint32_t)EG_OFF_BAR;            // [stage] in the leader: both operands of both CTAs
 constexpr uint32_t EG_EMPTY = EG_FULL + 8 * EG_STAGES;        // [stage] the MMAs have read it
 constexpr uint32_t EG_TFULL = EG_EMPTY + 8 * EG_STAGES;       // [2] an accumulator is complete
 constexpr uint32_t EG_TEMPTY = EG_TFULL + 16;                 // [2] in the leader: it is drained in both CTAs
 constexpr uint32_t EG_DRAIN = EG_TEMPTY + 16;
-constexpr uint32_t EG_TMEM = EG_DRAIN + 8;                    // TMEM address, failure flag
-static_assert(EG_TMEM + 8 <= EG_OFF_TABLE, "barrier area");
+constexpr uint32_t EG_LFULL = EG_DRAIN + 8;                   // [list] written
+constexpr uint32_t EG_LEMPTY = EG_LFULL + 8 * EG_LISTS;       // [list] read
+constexpr uint32_t EG_TMEM = EG_LEMPTY + 8 * EG_LISTS;        // TMEM address, failure flag
+constexpr uint32_t EG_DIRTY = EG_TMEM + 8;                    // [list] GRAD_WEIGHT: whether one of the block's rows is none
+static_assert(EG_DIRTY + 4 * EG_LISTS <= EG_OFF_LIST, "barrier area");
 
 struct GemmParams {
+  CUtensorMap tmx;   // x by single rows: boxes of 128 bytes of one
   CUtensorMap tmw;   // w [E][N][K], or d_y [rows][N]
-  const char* x;
-  const char* dy;    // GRAD_WEIGHT
-  uint32_t ld_x, ld_dy;  // bytes
+  CUtensorMap tmy;   // GRAD_WEIGHT: d_y by single rows
   const int32_t* off;
   const int32_t* order;
   int64_t rows, tokens;
@@ -84,9 +88,14 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// 16 bytes to shared memory, those past `bytes` as zeros (nothing is read when it is 0).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const char* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// 128 bytes from column c0 on of four rows of a row-by-row map, one after the other; a row past the
+// map's end gives zeros.
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap* tm, int c0, const int4& r, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+      "%3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(tm), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+      : "memory");
 }
 
 // The operands' descriptors come as 32-bit halves: the high one is the same for every stage.
@@ -111,8 +120,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Descriptor of an operand whose m (or j) is contiguous: panels of 64 of it, EG_PANEL bytes
 // apart, rows of c of 128 bytes, groups of eight rows 1024 bytes apart, 128-byte swizzle.
@@ -313,182 +320,140 @@ __device__ __forceinline__ int entry_row(const GemmParams& p, int o, bool& bad) 
 }
 __device__ __forceinline__ int list_entry(const GemmParams& p, int q) { return p.order == nullptr ? q : p.order[q]; }
 
-// GRAD_WEIGHT: the rows of x behind the 64 list rows of a block, two to a lane (r0: row lane, r1: row
-// 32 + lane; -1: past the segment or padding), with the next block's entries under way.
-struct RowPair {
-  int r0, r1;
-  int n0, n1;
-  bool bad;
-  __device__ __forceinline__ int entry(const GemmParams& p, const Tile& x, uint32_t q) const {
-    return q < (uint32_t)(x.hi - x.p0) ? list_entry(p, x.p0 + (int)q) : -1;
-  }
-  __device__ __forceinline__ RowPair(const GemmParams& p, const Tile& x, int kb, int lane) : r0(-1), r1(-1), bad(false) {
-    n0 = entry(p, x, (uint32_t)kb * 64 + lane);
-    n1 = entry(p, x, (uint32_t)kb * 64 + 32 + lane);
-  }
-  // The rows of the block whose entries are under way, and block kb's entries; whether one of the
-  // rows is none.
-  __device__ __forceinline__ bool next(const GemmParams& p, const Tile& x, int kb, int lane) {
-    r0 = entry_row(p, n0, bad);
-    r1 = entry_row(p, n1, bad);
-    n0 = entry(p, x, (uint32_t)kb * 64 + lane);
-    n1 = entry(p, x, (uint32_t)kb * 64 + 32 + lane);
-    return __any_sync(FULL, r0 < 0 || r1 < 0);
-  }
-};
-
-// Which of the first 16 blocks from kb on hold a row that is none, as bits (GRAD_WEIGHT).
-struct DirtyBlocks {
-  static constexpr int N = 8;  // blocks looked at in one go
-  int v[2 * N];
-  uint32_t bits;
-  __device__ __forceinline__ void fetch(const GemmParams& p, const Tile& x, int kb, int lane) {
-#pragma unroll
-    for (int i = 0; i < 2 * N; ++i) {
-      const uint32_t q = (uint32_t)kb * 64 + 32 * i + lane;
-      v[i] = q < (uint32_t)(x.hi - x.p0) ? list_entry(p, x.p0 + (int)q) : -1;
-    }
-  }
-  __device__ __forceinline__ void settle(const GemmParams& p) {
-    const int64_t end = p.order == nullptr ? p.rows : p.tokens * p.k;
-    bits = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const bool none = v[2 * i] < 0 || v[2 * i + 1] < 0 || v[2 * i] >= end || v[2 * i + 1] >= end;
-      bits |= __any_sync(FULL, none) ? 1u << i : 0u;
-    }
-  }
-};
-
 // ------------------------------------------------------------ rows of x
-// One of the six row warps: it brings every sixth stage by itself, from the release of the stage to
-// the copies' landing, so that as many stages are under way without one warp's wait holding up
-// another's (four warps sharing every stage: 2,284 us where this takes XX).  Row indices lie with
-// the lanes and go round by shuffles; the next tile's are under way while this one's are used.
-constexpr int EG_ROW_WARPS = 5;
-// A barrier's parity tells neighbouring rounds apart, no more: with more warps than stages one could
-// ask for a slot two rounds ahead of the MMAs and be let through.
-static_assert(EG_ROW_WARPS <= EG_STAGES, "row warps");
+// The lister, one warp: turns the lists' entries into rows of x, well ahead of their use.  FORWARD,
+// GRAD_INPUT: a list of this CTA's rows for each tile (those past the tile repeat its last one;
+// padding takes any row).  GRAD_WEIGHT: a list of 64 for each block; a row past the segment or of
+// padding is given as the map's end, which reads as zeros.
+template <int OP, bool FP8>
+__device__ __forceinline__ bool write_lists(const GemmParams& p, const TileTable& tt, char* sm, uint32_t base, int rank, int lane) {
+  constexpr bool GW = OP == MOER_GEMM_GRAD_WEIGHT;
+  int* const lists = reinterpret_cast<int*>(sm + EG_OFF_LIST);
+  uint32_t i = 0;  // lists written
+  bool bad = false;
+  auto take = [&]() { return i < EG_LISTS || warp_wait(base + EG_LEMPTY + 8u * (i % EG_LISTS), (i / EG_LISTS - 1) & 1u, p.status, lane); };
+  auto give = [&]() {
+    __syncwarp();
+    if (lane == 0) pair_arrive(mapa_u32(base + EG_LFULL + 8u * (i % EG_LISTS), (uint32_t)rank));
+    ++i;
+  };
+  for (TileWalk<OP, FP8> walk(p, tt); walk.left > 0; walk.advance(p)) {
+    const Tile x = walk.tile(p, tt);
+    if constexpr (!GW) {
+      const int part = FP8 ? 128 : x.ncol >> 1;
+      int v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = 32 * c < part ? list_entry(p, x.p0 + min(rank * part + 32 * c + lane, x.rows - 1)) : 0;
+      if (!take()) return false;
+      int* d = lists + (i % EG_LISTS) * EG_LIST + lane;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) d[32 * c] = max(entry_row(p, v[c], bad), 0);
+      give();
+    } else {
+      constexpr int AHEAD = 4;  // blocks whose entries are fetched in one go, while the four before are written
+      int v[2 * AHEAD];
+      auto fetch = [&](int kb) {
+#pragma unroll
+        for (int c = 0; c < 2 * AHEAD; ++c) {
+          const uint32_t q = (uint32_t)kb * 64 + 32 * c + lane;
+          v[c] = q < (uint32_t)(x.hi - x.p0) ? list_entry(p, x.p0 + (int)q) : -1;
+        }
+      };
+      fetch(0);
+      for (int k0 = 0; k0 < x.nkb; k0 += AHEAD) {
+        int r[2 * AHEAD];
+#pragma unroll
+        for (int c = 0; c < 2 * AHEAD; ++c) r[c] = entry_row(p, v[c], bad);
+        if (k0 + AHEAD < x.nkb) fetch(k0 + AHEAD);
+#pragma unroll
+        for (int b = 0; b < AHEAD; ++b) {
+          if (k0 + b >= x.nkb) break;
+          const bool dirty = __any_sync(FULL, r[2 * b] < 0 || r[2 * b + 1] < 0);
+          if (!take()) return false;
+          int* d = lists + (i % EG_LISTS) * EG_LIST + lane;
+          d[0] = r[2 * b] < 0 ? (int)p.tokens : r[2 * b];
+          d[32] = r[2 * b + 1] < 0 ? (int)p.tokens : r[2 * b + 1];
+          if (lane == 0) *reinterpret_cast<int*>(sm + EG_DIRTY + 4 * (i % EG_LISTS)) = dirty;
+          give();
+        }
+      }
+    }
+  }
+  if (GW && bad) atomicOr(p.status, WS_BIT_EDATA);  // (else the epilogue says it)
+  return true;
+}
+
+// One thread of each of four warps brings a quarter of a stage's rows, by TMA, eight gathers of four.
+// (One warp with a gather in each lane took 72 clocks a gather and 3,408 us; the rows by cp.async,
+// with their proxy fences and two more barriers, 1,301 us; this way XX.)
+constexpr int EG_GATHERS = 8;
 
 template <int OP, bool FP8>
-__device__ __forceinline__ void load_rows(const GemmParams& p, const TileTable& tt, char* sm, uint32_t base, int w, int rank, int lane) {
-  constexpr int EB = FP8 ? 1 : 2, KE = 128 / EB;
+__device__ __forceinline__ bool gather_rows(const GemmParams& p, const TileTable& tt, char* sm, uint32_t base, int w, int rank) {
   constexpr bool GW = OP == MOER_GEMM_GRAD_WEIGHT;
+  constexpr int KE = FP8 ? 128 : 64;
   const uint32_t bar0 = mapa_u32(base + EG_FULL, 0);
-  uint32_t mine = w;    // the next stage that is this warp's
-  bool ok = true;
-  // the stage's copies have landed: visible to the MMA, handed over
-  auto hand_over = [&](uint32_t s) {
-    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) pair_arrive(bar0 + 8u * s);
+  uint32_t i = 0;  // lists read
+  int s = 0;
+  uint32_t fills = 0, ph = 1;  // parity of the release that the next fill of stage s waits for
+  int4 r[EG_GATHERS];
+  auto list = [&](int first) {  // this thread's entries, from list entry `first` on
+    const int4* d = reinterpret_cast<const int4*>(sm + EG_OFF_LIST + (i % EG_LISTS) * EG_LIST * 4) + first / 4;
+#pragma unroll
+    for (int g = 0; g < EG_GATHERS; ++g) r[g] = d[g];
   };
-  // the ring's slot of stage `mine` is free
-  auto take = [&](uint32_t& s) -> bool {
-    const uint32_t round = mine / EG_STAGES;
-    s = mine - round * EG_STAGES;
-    return round == 0 || warp_wait(base + EG_EMPTY + 8u * s, (round - 1) & 1u, p.status, lane);
+  auto wait_list = [&]() { return one_wait(base + EG_LFULL + 8u * (i % EG_LISTS), (i / EG_LISTS) & 1u, p.status); };
+  auto done = [&]() {
+    pair_arrive(mapa_u32(base + EG_LEMPTY + 8u * (i % EG_LISTS), (uint32_t)rank));
+    ++i;
   };
-  TileWalk<OP, FP8> walk(p, tt);
-  if (walk.left == 0) return;
-  Tile x = walk.tile(p, tt);
-  int kb = w;  // block of the tile that stage `mine` holds
-  if constexpr (!GW) {
-    // eight lanes a row: rows 4 i + lane / 8 of this CTA's part; lane l holds rows l, 32 + l, ...
-    const int sub = lane >> 3, c = lane & 7;
-    int ent[4];
-    auto fetch = [&](const Tile& y) {
-      const int part = FP8 ? 128 : y.ncol >> 1;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)  // rows past the tile repeat its last one
-        ent[i] = 32 * i < part ? list_entry(p, y.p0 + min(rank * part + 32 * i + lane, y.rows - 1)) : 0;
-    };
-    fetch(x);
-    for (;;) {
-      const int part = FP8 ? max(0, min(128, x.rows - rank * 128)) : x.ncol >> 1;  // rows to bring
-      int src[4];
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) src[i] = max(entry_row(p, ent[i], bad), 0);  // padding takes any row
-      walk.advance(p);
-      const int nkb = x.nkb;
-      if (walk.left > 0) {
-        x = walk.tile(p, tt);
-        fetch(x);
-      }
-      for (; kb < nkb; kb += EG_ROW_WARPS, mine += EG_ROW_WARPS) {
-        uint32_t s;
-        if (!take(s)) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = base + s * EG_STAGE_BYTES + EG_HALF + (uint32_t)sub * 128;
-        const int off = kb * 128 + c * 16, n = max(0, min(16, p.C * EB - off));
-        const char* xk = p.x + (n > 0 ? off : 0);
-#pragma unroll
-        for (int i8 = 0; i8 < 4; ++i8) {
-          if (32 * i8 >= part) break;
-          uint32_t r[8];  // (in groups, so that the shuffles' latencies overlap)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) r[i] = (uint32_t)__shfl_sync(FULL, src[i8], 4 * i + sub);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (32 * i8 + 4 * i < part)
-              cp_async16(dst + 4096u * i8 + 512u * i + ((uint32_t)(c ^ ((4 * i + sub) & 7)) << 4), xk + (uint64_t)r[i] * p.ld_x, n);
-        }
-        hand_over(s);
-      }
-      if (!ok || walk.left == 0) break;
-      kb -= nkb;
+  for (TileWalk<OP, FP8> walk(p, tt); walk.left > 0; walk.advance(p)) {
+    const Tile x = walk.tile(p, tt);
+    int n = EG_GATHERS;  // gathers that this thread makes a stage
+    if constexpr (!GW) {
+      const int part = FP8 ? max(0, min(128, x.rows - rank * 128)) : x.ncol >> 1;
+      n = min(EG_GATHERS, max(0, ((part + 3) >> 2) - w * EG_GATHERS));
+      if (!wait_list()) return false;
+      list(w * 4 * EG_GATHERS);
+      done();
     }
-  } else {
-    // sixteen lanes a row: rows 2 i + lane / 16 of the block
-    const int sub = lane >> 4, c = lane & 15;
-    bool bad = false;
-    for (;;) {
-      const int acol = x.mb * 256 + rank * 128 + c * 8, bcol = x.j0 + rank * 128 + c * 8;
-      const int an = max(0, min(16, (p.M - acol) * 2)), bn = max(0, min(16, (p.J - bcol) * 2));
-      RowPair rp(p, x, kb, lane);
-      for (; kb < x.nkb; kb += EG_ROW_WARPS, mine += EG_ROW_WARPS) {
-        const bool dirty = rp.next(p, x, kb + EG_ROW_WARPS, lane);
-        uint32_t s;
-        if (!take(s)) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = base + s * EG_STAGE_BYTES + (uint32_t)((c >> 3) * EG_PANEL + sub * 128);
-        const char* ax = p.x + (an > 0 ? (int64_t)acol * 2 : 0);
+    for (int kb = 0; kb < x.nkb; ++kb) {
+      bool dirty = false;
+      if constexpr (GW) {  // warps 0, 1: the first panel's rows 0 .. 31 and 32 .. 63, 2, 3: the second panel's
+        if (!wait_list()) return false;
+        list((w & 1) * 32);
+        dirty = *reinterpret_cast<const volatile int*>(sm + EG_DIRTY + 4 * (i % EG_LISTS)) != 0;
+        done();
+      }
+      if (fills >= EG_STAGES && !one_wait(base + EG_EMPTY + 8u * s, ph, p.status)) return false;
+      fills += fills < EG_STAGES;
+      const uint32_t st = base + (uint32_t)(s * EG_STAGE_BYTES), bar = bar0 + 8u * s;
+      if constexpr (!GW) {
 #pragma unroll
-        for (int i8 = 0; i8 < 4; ++i8) {
-          int r[8];
+        for (int g = 0; g < EG_GATHERS; ++g)
+          if (g < n) tma_gather4_pair(st + EG_HALF + 512u * (w * EG_GATHERS + g), &p.tmx, kb * KE, r[g], bar);
+      } else {
+        const uint32_t dst = st + (uint32_t)((w >> 1) * EG_PANEL + (w & 1) * 4096);
+        const int col = rank * 128 + (w >> 1) * 64;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) r[i] = __shfl_sync(FULL, i8 < 2 ? rp.r0 : rp.r1, (16 * i8 + 2 * i + sub) & 31);
+        for (int g = 0; g < EG_GATHERS; ++g) tma_gather4_pair(dst + 512u * g, &p.tmx, x.mb * 256 + col, r[g], bar);
+        if (dirty) {  // d_y's rows one by one too, those that are none as zeros (else warp 0 brings them)
+          const int first = x.p0 + kb * 64 + (w & 1) * 32, none = (int)p.rows, end = (int)p.tokens;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            cp_async16(dst + 2048u * i8 + 256u * i + ((uint32_t)((c & 7) ^ ((2 * i + sub) & 7)) << 4),
-                       ax + (uint64_t)(uint32_t)max(r[i], 0) * p.ld_x, r[i] >= 0 ? an : 0);
-        }
-        if (dirty) {  // (a block that is all the segment's own comes by TMA)
-          const char* bx = p.dy + (uint64_t)((int64_t)x.p0 + (int64_t)kb * KE + sub) * p.ld_dy + (bn > 0 ? (int64_t)bcol * 2 : 0);
-#pragma unroll 4
-          for (int i = 0; i < 32; ++i) {
-            const int r = __shfl_sync(FULL, i < 16 ? rp.r0 : rp.r1, (2 * i + sub) & 31);
-            cp_async16(dst + EG_HALF + 256u * i + ((uint32_t)((c & 7) ^ ((2 * i + sub) & 7)) << 4),
-                       r >= 0 ? bx + (uint64_t)(2 * i) * p.ld_dy : p.dy, r >= 0 ? bn : 0);
+          for (int g = 0; g < EG_GATHERS; ++g) {
+            const int q = first + 4 * g;
+            const int4 y = {r[g].x < end ? q : none, r[g].y < end ? q + 1 : none, r[g].z < end ? q + 2 : none, r[g].w < end ? q + 3 : none};
+            tma_gather4_pair(dst + EG_HALF + 512u * g, &p.tmy, x.j0 + col, y, bar);
           }
         }
-        hand_over(s);
       }
-      bad |= rp.bad;
-      walk.advance(p);
-      if (!ok || walk.left == 0) break;
-      kb -= x.nkb;
-      x = walk.tile(p, tt);
+      if (++s == EG_STAGES) {
+        s = 0;
+        ph ^= 1u;
+      }
     }
-    if (bad) atomicOr(p.status, WS_BIT_EDATA);
   }
-  if (!ok && lane == 0) *reinterpret_cast<volatile int*>(sm + EG_TMEM + 4) = 1;
+  return true;
 }
 
 // ------------------------------------------------------------ epilogue
@@ -558,9 +523,9 @@ __device__ __forceinline__ uint32_t pad_mask(const GemmParams& p, const Tile& x,
 }
 
 // ------------------------------------------------------------ the kernel
-// Warps: 0 loads by TMA, 1 allocates TMEM and issues the MMAs (in the leader), 2 to 7 load rows, 8 to 23
-// drain the accumulators, each 64 columns of its TMEM lanes.  Registers go to the last
-// sixteen: the six warpgroups' shares, 64 + 64 + 4 x 88, are the block's 6 x 80.
+// Warps: 0 loads whole tiles, 1 allocates TMEM and issues the MMAs (in the leader), 2 lists rows, 4 to 7
+// gather them, 8 to 23 drain the accumulators, each 64 columns of its TMEM lanes.  Registers go to
+// the last sixteen: the six warpgroups' shares, 64 + 64 + 4 x 88, are the block's 6 x 80.
 template <int OP, bool FP8>
 __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int EB = FP8 ? 1 : 2, KE = 128 / EB;  // bytes of an element, elements of c a block
@@ -579,7 +544,7 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
   if (threadIdx.x == 32) {
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm);
     for (int s = 0; s < EG_STAGES; ++s) {
-      mbar_init(bar + EG_FULL / 8 + s, 3);  // the leader's TMA warp, a row warp of either CTA
+      mbar_init(bar + EG_FULL / 8 + s, 1);
       mbar_init(bar + EG_EMPTY / 8 + s, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -587,6 +552,10 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
       mbar_init(bar + EG_TEMPTY / 8 + i, 2 * EG_EPI_WARPS);
     }
     mbar_init(bar + EG_DRAIN / 8, 1);
+    for (int i = 0; i < EG_LISTS; ++i) {
+      mbar_init(bar + EG_LFULL / 8 + i, 1);
+      mbar_init(bar + EG_LEMPTY / 8 + i, GW ? 5 : 4);  // the gathering threads, and warp 0's for `dirty`
+    }
     failed = 0;
     fence_mbar_init();
   }
@@ -604,66 +573,63 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
       // -------------------------------------------------------- TMA: w, or d_y
-      const uint32_t bar0 = mapa_u32(base + EG_FULL, 0);
-      int s = 0;
-      uint32_t fills = 0, ph = 1;  // parity of the release that the next fill of stage s waits for
-      bool ok = true;
-      for (TileWalk<OP, FP8> walk(p, tt); walk.left > 0 && ok; walk.advance(p)) {
-        const Tile x = walk.tile(p, tt);
-        const int m0 = x.mb * 256 + rank * 128;
-        const int e = p.one_w ? 0 : x.e;
-        DirtyBlocks db;
-        if constexpr (GW) db.fetch(p, x, 0, lane);
-        for (int kb = 0; kb < x.nkb; ++kb) {
-          bool dirty = false;
-          if constexpr (GW) {
-            if (kb % DirtyBlocks::N == 0) {
-              db.settle(p);
-              if (kb + DirtyBlocks::N < x.nkb) db.fetch(p, x, kb + DirtyBlocks::N, lane);
+      if (elect_one()) {
+        const uint32_t bar0 = mapa_u32(base + EG_FULL, 0);
+        int s = 0;
+        uint32_t fills = 0, ph = 1, i = 0;  // lists looked at
+        bool ok = true;
+        for (TileWalk<OP, FP8> walk(p, tt); walk.left > 0 && ok; walk.advance(p)) {
+          const Tile x = walk.tile(p, tt);
+          const int m0 = x.mb * 256 + rank * 128, n0 = x.j0 + rank * 128;
+          const int e = p.one_w ? 0 : x.e;
+          // bytes of a stage, both CTAs'
+          const int rows = FP8 ? ((min(x.rows, 128) + 3) & ~3) + ((max(x.rows - 128, 0) + 3) & ~3) : x.ncol;
+          const uint32_t tx = GW ? 2u * EG_STAGE_BYTES : 2u * EG_HALF + (uint32_t)rows * 128u;
+          for (int kb = 0; kb < x.nkb; ++kb) {
+            bool dirty = false;
+            if constexpr (GW) {
+              ok = one_wait(base + EG_LFULL + 8u * (i % EG_LISTS), (i / EG_LISTS) & 1u, p.status);
+              if (!ok) break;
+              dirty = *reinterpret_cast<const volatile int*>(sm + EG_DIRTY + 4 * (i % EG_LISTS)) != 0;
+              pair_arrive(mapa_u32(base + EG_LEMPTY + 8u * (i % EG_LISTS), (uint32_t)rank));
+              ++i;
             }
-            dirty = (db.bits >> (kb % DirtyBlocks::N)) & 1u;
-          }
-          if (fills >= EG_STAGES && !warp_wait(base + EG_EMPTY + 8u * s, ph, p.status, lane)) {
-            ok = false;
-            break;
-          }
-          fills += fills < EG_STAGES;
-          const uint32_t st = base + (uint32_t)(s * EG_STAGE_BYTES), bar = bar0 + 8u * s;
-          if (lane == 0) {
-            if (rank == 0) {
-              if (dirty) pair_arrive(bar);  // the row warps bring both operands
-              else arrive_expect(base + EG_FULL + 8u * s, 2u * EG_HALF);
+            if (fills >= EG_STAGES && !one_wait(base + EG_EMPTY + 8u * s, ph, p.status)) {
+              ok = false;
+              break;
             }
+            fills += fills < EG_STAGES;
+            const uint32_t st = base + (uint32_t)(s * EG_STAGE_BYTES), bar = bar0 + 8u * s;
+            if (rank == 0) arrive_expect(base + EG_FULL + 8u * s, tx);
             if (OP == MOER_GEMM_FORWARD) {
               tma_load_3d_pair(st, &p.tmw, kb * KE, m0, e, bar);
             } else if (OP == MOER_GEMM_GRAD_INPUT) {
               tma_load_3d_pair(st, &p.tmw, m0, kb * KE, e, bar);
               tma_load_3d_pair(st + EG_PANEL, &p.tmw, m0 + 64, kb * KE, e, bar);
             } else if (!dirty) {
-              const int n0 = x.j0 + rank * 128;
               tma_load_3d_pair(st + EG_HALF, &p.tmw, n0, x.p0 + kb * KE, 0, bar);
               tma_load_3d_pair(st + EG_HALF + EG_PANEL, &p.tmw, n0 + 64, x.p0 + kb * KE, 0, bar);
             }
+            if (++s == EG_STAGES) {
+              s = 0;
+              ph ^= 1u;
+            }
           }
+        }
+        // the last fills' stages have been released: no MMA still reads them
+        for (uint32_t q = 0; q < fills && ok; ++q) {
+          if (fills < EG_STAGES) {  // the ring was never full: stages 0 .. fills - 1, first round
+            ok = one_wait(base + EG_EMPTY + 8u * q, 0, p.status);
+            continue;
+          }
+          ok = one_wait(base + EG_EMPTY + 8u * s, ph, p.status);
           if (++s == EG_STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
+        if (!ok) failed = 1;
       }
-      // the last fills' stages have been released: no MMA still reads them
-      for (uint32_t i = 0; i < fills && ok; ++i) {
-        if (fills < EG_STAGES) {  // the ring was never full: stages 0 .. fills - 1, first round
-          ok = one_wait(base + EG_EMPTY + 8u * i, 0, p.status);
-          continue;
-        }
-        ok = one_wait(base + EG_EMPTY + 8u * s, ph, p.status);
-        if (++s == EG_STAGES) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-      if (!ok && lane == 0) failed = 1;
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA
       if (elect_one()) {
@@ -732,12 +698,12 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
         if (!one_wait(base + EG_DRAIN, 0, p.status)) ok = false;
         if (!ok) failed = 1;
       }
-    } else {
-      load_rows<OP, FP8>(p, tt, sm, base, warp - 2, rank, lane);
+    } else if (warp == 2) {
+      if (!write_lists<OP, FP8>(p, tt, sm, base, rank, lane) && lane == 0) failed = 1;
     }
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp != 5) load_rows<OP, FP8>(p, tt, sm, base, warp == 4 ? 4 : warp - 4, rank, lane);
+    if (elect_one() && !gather_rows<OP, FP8>(p, tt, sm, base, warp - 4, rank)) failed = 1;
   } else {
     // ---------------------------------------------------------- epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
@@ -979,14 +945,17 @@ moer_status expert_gemm_launch(const moer_expert_gemm_args* a, void* ws, cudaStr
   // D fp32; A and B bf16, fp16 or e4m3; transposed operands; M = 256
   const uint32_t fmt = a->dtype == MOER_BF16 ? 1u : 0u;
   p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((fwd ? 0u : 1u) << 15) | ((gw ? 1u : 0u) << 16) | ((256u >> 4) << 24);
-  p.x = static_cast<const char*>(a->x);
-  p.dy = static_cast<const char*>(a->d_y);
-  p.ld_x = (uint32_t)(a->ld_x * (int64_t)eb);
-  p.ld_dy = (uint32_t)(a->ld_d_y * (int64_t)eb);
+  {
+    const uint64_t dims[2] = {(uint64_t)(a->op == MOER_GEMM_GRAD_INPUT ? a->N : a->K), (uint64_t)a->tokens}, str[1] = {(uint64_t)a->ld_x * eb};
+    const uint32_t box[2] = {(uint32_t)ke, 1};
+    if (!map_of(&p.tmx, a->x, a->dtype, 2, dims, str, box)) return MOER_ECUDA;
+  }
   if (gw) {
     const uint64_t dims[3] = {(uint64_t)a->N, (uint64_t)a->rows, 1}, str[2] = {(uint64_t)a->ld_d_y * eb, (uint64_t)a->ld_d_y * eb};
     const uint32_t box[3] = {64, 64, 1};
     if (!map_of(&p.tmw, a->d_y, a->dtype, 3, dims, str, box)) return MOER_ECUDA;
+    const uint32_t row[2] = {64, 1};
+    if (!map_of(&p.tmy, a->d_y, a->dtype, 2, dims, str, row)) return MOER_ECUDA;
   } else {
     const bool one = a->E == 1 || p.one_w;
     const uint64_t dims[3] = {(uint64_t)a->K, (uint64_t)a->N, (uint64_t)(one ? 1 : a->E)};
