@@ -45,7 +45,10 @@ constexpr size_t EG_OFF_BAR = (size_t)EG_STAGES * EG_STAGE_BYTES;
 constexpr int EG_LISTS = 8;                            // row lists under way: of tiles (2 x 128 rows used), or of blocks of 64
 constexpr int EG_LIST = 128;                           // entries of a list
 constexpr size_t EG_OFF_LIST = EG_OFF_BAR + 512;       // [list][EG_LIST] ints
-constexpr size_t EG_OFF_TABLE = EG_OFF_LIST + (size_t)EG_LISTS * EG_LIST * 4;  // the experts' tiles: 3 x (E + 1) ints
+constexpr int EG_SLOTS = 8, EG_SLOT_KB = 4;            // E4M3: ring of x's scales, blocks a slot
+constexpr size_t EG_OFF_SCALE = EG_OFF_LIST + (size_t)EG_LISTS * EG_LIST * 4;  // [slot][block][128 rows]
+constexpr size_t EG_SCALE_BYTES = (size_t)EG_SLOTS * EG_SLOT_KB * 128 * 4;
+constexpr size_t EG_OFF_TABLE = EG_OFF_SCALE + EG_SCALE_BYTES;  // the experts' tiles: 3 x (E + 1) ints
 // Barriers, as byte offsets from the stages' start.
 constexpr uint32_t EG_FULL = (uint32_t)EG_OFF_BAR;            // [stage] in the leader: both operands of both CTAs
 constexpr uint32_t EG_EMPTY = EG_FULL + 8 * EG_STAGES;        // [stage] the MMAs have read it
@@ -54,7 +57,9 @@ constexpr uint32_t EG_TEMPTY = EG_TFULL + 16;                 // [2] in the lead
 constexpr uint32_t EG_DRAIN = EG_TEMPTY + 16;
 constexpr uint32_t EG_LFULL = EG_DRAIN + 8;                   // [list] written
 constexpr uint32_t EG_LEMPTY = EG_LFULL + 8 * EG_LISTS;       // [list] read
-constexpr uint32_t EG_TMEM = EG_LEMPTY + 8 * EG_LISTS;        // TMEM address, failure flag
+constexpr uint32_t EG_SFULL = EG_LEMPTY + 8 * EG_LISTS;       // [slot] E4M3: scales written
+constexpr uint32_t EG_SEMPTY = EG_SFULL + 8 * EG_SLOTS;       // [slot] read
+constexpr uint32_t EG_TMEM = EG_SEMPTY + 8 * EG_SLOTS;        // TMEM address, failure flag
 constexpr uint32_t EG_DIRTY = EG_TMEM + 8;                    // [list] GRAD_WEIGHT: whether one of the block's rows is none
 static_assert(EG_DIRTY + 4 * EG_LISTS <= EG_OFF_LIST, "barrier area");
 
@@ -62,10 +67,13 @@ struct GemmParams {
   CUtensorMap tmx;   // x by single rows: boxes of 128 bytes of one
   CUtensorMap tmw;   // w [E][N][K], or d_y [rows][N]
   CUtensorMap tmy;   // GRAD_WEIGHT: d_y by single rows
+  CUtensorMap tmr;   // without an order: x by 32 rows
   const int32_t* off;
   const int32_t* order;
   int64_t rows, tokens;
   int E, k;
+  uint64_t div_m;    // o / k = (o * div_m) >> div_s for 0 <= o < 2^31: div_m = 2^div_s / k, rounded up past it,
+  int div_s;         // div_s = 32 + ceil(log2 k), so that o times the excess (k at most) stays below 2^div_s
   int M, C, J;       // extents of m, c (FORWARD, GRAD_INPUT) and j (GRAD_WEIGHT)
   int nmb, njb;      // blocks of 256 of m, and of j (GRAD_WEIGHT)
   int one_w;         // the experts share one matrix
@@ -181,8 +189,12 @@ __device__ __forceinline__ void pair_arrive(uint32_t caddr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
-__device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+// Arrival on the leader's barrier of a stage, with the bytes that this thread brings to it, perhaps none:
+// a stage fills only when every thread that brings to stages has come by.  One that could stay behind
+// or run ahead (having nothing to bring to a narrow tile, say) would lose its place, since a
+// barrier's parity tells neighbouring rounds apart and no more.
+__device__ __forceinline__ void stage_arrive(uint32_t caddr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(caddr), "r"(bytes) : "memory");
 }
 
 // One lane of the warp, which the compiler knows to be one: descriptors then go to uniform registers
@@ -313,7 +325,7 @@ struct TileWalk {
 // The row of x behind a list row's entry, or -1; `bad`: it names no token.
 __device__ __forceinline__ int entry_row(const GemmParams& p, int o, bool& bad) {
   if (p.order == nullptr || o < 0) return o;
-  const int r = o / p.k;
+  const int r = (int)(((uint64_t)(uint32_t)o * p.div_m) >> p.div_s);
   if (r < p.tokens) return r;
   bad = true;
   return -1;
@@ -428,15 +440,21 @@ __device__ __forceinline__ bool gather_rows(const GemmParams& p, const TileTable
       if (fills >= EG_STAGES && !one_wait(base + EG_EMPTY + 8u * s, ph, p.status)) return false;
       fills += fills < EG_STAGES;
       const uint32_t st = base + (uint32_t)(s * EG_STAGE_BYTES), bar = bar0 + 8u * s;
+      stage_arrive(bar, 512u * (uint32_t)(dirty ? 2 * n : n));
       if constexpr (!GW) {
+        if (p.order == nullptr && n == EG_GATHERS)  // 32 neighbouring rows at once
+          tma_load_2d_pair(st + EG_HALF + 4096u * w, &p.tmr, kb * KE, x.p0 + rank * (FP8 ? 128 : x.ncol >> 1) + 32 * w, bar);
+        else
 #pragma unroll
         for (int g = 0; g < EG_GATHERS; ++g)
           if (g < n) tma_gather4_pair(st + EG_HALF + 512u * (w * EG_GATHERS + g), &p.tmx, kb * KE, r[g], bar);
       } else {
         const uint32_t dst = st + (uint32_t)((w >> 1) * EG_PANEL + (w & 1) * 4096);
         const int col = rank * 128 + (w >> 1) * 64;
+        if (p.order == nullptr && !dirty) tma_load_2d_pair(dst, &p.tmr, x.mb * 256 + col, x.p0 + kb * 64 + (w & 1) * 32, bar);
+        else
 #pragma unroll
-        for (int g = 0; g < EG_GATHERS; ++g) tma_gather4_pair(dst + 512u * g, &p.tmx, x.mb * 256 + col, r[g], bar);
+          for (int g = 0; g < EG_GATHERS; ++g) tma_gather4_pair(dst + 512u * g, &p.tmx, x.mb * 256 + col, r[g], bar);
         if (dirty) {  // d_y's rows one by one too, those that are none as zeros (else warp 0 brings them)
           const int first = x.p0 + kb * 64 + (w & 1) * 32, none = (int)p.rows, end = (int)p.tokens;
 #pragma unroll
@@ -525,7 +543,7 @@ __device__ __forceinline__ uint32_t pad_mask(const GemmParams& p, const Tile& x,
 // ------------------------------------------------------------ the kernel
 // Warps: 0 loads whole tiles, 1 allocates TMEM and issues the MMAs (in the leader), 2 lists rows, 4 to 7
 // gather them, 8 to 23 drain the accumulators, each 64 columns of its TMEM lanes.  Registers go to
-// the last sixteen: the six warpgroups' shares, 64 + 64 + 4 x 88, are the block's 6 x 80.
+// the last sixteen: the six warpgroups' shares, 48 + 48 + 4 x 96, are the block's 6 x 80.
 template <int OP, bool FP8>
 __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int EB = FP8 ? 1 : 2, KE = 128 / EB;  // bytes of an element, elements of c a block
@@ -544,7 +562,7 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
   if (threadIdx.x == 32) {
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm);
     for (int s = 0; s < EG_STAGES; ++s) {
-      mbar_init(bar + EG_FULL / 8 + s, 1);
+      mbar_init(bar + EG_FULL / 8 + s, 2 * 5);  // of either CTA: the tiles' thread and the four that gather
       mbar_init(bar + EG_EMPTY / 8 + s, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -555,6 +573,10 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
     for (int i = 0; i < EG_LISTS; ++i) {
       mbar_init(bar + EG_LFULL / 8 + i, 1);
       mbar_init(bar + EG_LEMPTY / 8 + i, GW ? 5 : 4);  // the gathering threads, and warp 0's for `dirty`
+    }
+    for (int i = 0; i < EG_SLOTS; ++i) {
+      mbar_init(bar + EG_SFULL / 8 + i, 1);
+      mbar_init(bar + EG_SEMPTY / 8 + i, EG_EPI_WARPS);
     }
     failed = 0;
     fence_mbar_init();
@@ -570,7 +592,7 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
   tc_fence_after();
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == 0) {
       // -------------------------------------------------------- TMA: w, or d_y
       if (elect_one()) {
@@ -582,9 +604,6 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
           const Tile x = walk.tile(p, tt);
           const int m0 = x.mb * 256 + rank * 128, n0 = x.j0 + rank * 128;
           const int e = p.one_w ? 0 : x.e;
-          // bytes of a stage, both CTAs'
-          const int rows = FP8 ? ((min(x.rows, 128) + 3) & ~3) + ((max(x.rows - 128, 0) + 3) & ~3) : x.ncol;
-          const uint32_t tx = GW ? 2u * EG_STAGE_BYTES : 2u * EG_HALF + (uint32_t)rows * 128u;
           for (int kb = 0; kb < x.nkb; ++kb) {
             bool dirty = false;
             if constexpr (GW) {
@@ -600,7 +619,7 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
             }
             fills += fills < EG_STAGES;
             const uint32_t st = base + (uint32_t)(s * EG_STAGE_BYTES), bar = bar0 + 8u * s;
-            if (rank == 0) arrive_expect(base + EG_FULL + 8u * s, tx);
+            stage_arrive(bar, dirty ? 0u : (uint32_t)EG_HALF);
             if (OP == MOER_GEMM_FORWARD) {
               tma_load_3d_pair(st, &p.tmw, kb * KE, m0, e, bar);
             } else if (OP == MOER_GEMM_GRAD_INPUT) {
@@ -700,18 +719,59 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
       }
     } else if (warp == 2) {
       if (!write_lists<OP, FP8>(p, tt, sm, base, rank, lane) && lane == 0) failed = 1;
+    } else if (FP8) {
+      // -------------------------------------------------------- x's scales (E4M3), four rows a lane
+      uint32_t it = 0;
+      bool ok = true;
+      const bool quad = p.ld_sx % 4 == 0 && reinterpret_cast<uintptr_t>(p.sx) % 16 == 0;
+      for (TileWalk<OP, FP8> walk(p, tt); walk.left > 0 && ok; walk.advance(p)) {
+        const Tile x = walk.tile(p, tt);
+        const float* sx[4];
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // rows past the tile repeat its last one
+          const int r = entry_row(p, list_entry(p, x.p0 + min(rank * 128 + 32 * i + lane, x.rows - 1)), bad);
+          sx[i] = p.sx + (int64_t)max(r, 0) * p.ld_sx;
+        }
+        for (int k0 = 0; k0 < x.nkb; k0 += EG_SLOT_KB, ++it) {
+          float v[4][EG_SLOT_KB];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (quad && k0 + EG_SLOT_KB <= x.nkb) {
+              const float4 f = __ldg(reinterpret_cast<const float4*>(sx[i] + k0));
+              v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+            } else {
+#pragma unroll
+              for (int b = 0; b < EG_SLOT_KB; ++b) v[i][b] = k0 + b < x.nkb ? __ldg(sx[i] + k0 + b) : 0.f;
+            }
+          }
+          const uint32_t slot = it % EG_SLOTS;
+          if (it >= EG_SLOTS && !warp_wait(base + EG_SEMPTY + 8u * slot, (it / EG_SLOTS - 1) & 1u, p.status, lane)) {
+            ok = false;
+            break;
+          }
+          float* d = reinterpret_cast<float*>(sm + EG_OFF_SCALE) + slot * EG_SLOT_KB * 128 + lane;
+#pragma unroll
+          for (int b = 0; b < EG_SLOT_KB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[b * 128 + 32 * i] = v[i][b];
+          __syncwarp();
+          if (lane == 0) pair_arrive(mapa_u32(base + EG_SFULL + 8u * slot, (uint32_t)rank));
+        }
+      }
+      if (!ok && lane == 0) failed = 1;
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (elect_one() && !gather_rows<OP, FP8>(p, tt, sm, base, warp - 4, rank)) failed = 1;
   } else {
     // ---------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     const int h0 = ((warp - 8) >> 2) * EG_COLS;  // first of the warp's columns
     const uint32_t tempty = mapa_u32(base + EG_TEMPTY, 0);
     // the TMEM lane quarter that this warp may access
     const uint32_t t0 = *reinterpret_cast<const uint32_t*>(sm + EG_TMEM) + ((uint32_t)((warp & 3) * 32) << 16) + h0;
-    uint32_t j = 0;
+    uint32_t j = 0, it = 0;
     bool ok = true;
     for (TileWalk<OP, FP8> walk(p, tt); walk.left > 0 && ok; walk.advance(p)) {
       const Tile x = walk.tile(p, tt);
@@ -726,34 +786,37 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
         const int row = l < x.rows ? entry_row(p, list_entry(p, x.p0 + l), bad) : -1;
         if (bad) atomicOr(p.status, WS_BIT_EDATA);
         const bool some = rank * 128 + (warp & 3) * 32 < x.rows;  // (a warp without rows only hands buffers back)
-        const float* sx = p.sx + (int64_t)max(row, 0) * p.ld_sx;
         const float* sw = p.sw + ((int64_t)x.e * nnb + min(x.mb * 2 + h0 / 128, nnb - 1)) * nkw;
-        float fx = row >= 0 ? __ldg(sx) : 0.f, fw = __ldg(sw);
+        const float* sx = reinterpret_cast<const float*>(sm + EG_OFF_SCALE) + (warp & 3) * 32 + lane;
+        float fw = __ldg(sw);
         for (int kb = 0; kb < nkw; ++kb, ++j) {
-          const float f = fx * fw;
-          if (kb + 1 < nkw) {  // the next block's, under way
-            fx = row >= 0 ? __ldg(sx + kb + 1) : 0.f;
-            fw = __ldg(sw + kb + 1);
-          }
-          const uint32_t a = j & 1u;
-          if (!warp_wait(base + EG_TFULL + 8u * a, (j >> 1) & 1u, p.status, lane)) {
+          const uint32_t a = j & 1u, slot = it % EG_SLOTS;
+          if (kb % EG_SLOT_KB == 0 && !warp_wait(base + EG_SFULL + 8u * slot, (it / EG_SLOTS) & 1u, p.status, lane)) ok = false;
+          const float f = fw * sx[(slot * EG_SLOT_KB + kb % EG_SLOT_KB) * 128];
+          if (kb + 1 < nkw) fw = __ldg(sw + kb + 1);  // the next block's, under way
+          if (!ok || !warp_wait(base + EG_TFULL + 8u * a, (j >> 1) & 1u, p.status, lane)) {
             ok = false;
             break;
           }
           tc_fence_after();
           if (some) {
+            uint32_t r[2][16];
+            tmem_ld16(t0 + a * EG_J, r[0]);
 #pragma unroll
             for (int c = 0; c < EG_COLS / 16; ++c) {
-              uint32_t r[16];
-              tmem_ld16(t0 + a * EG_J + 16u * c, r);
               tmem_ld_wait();
+              if (c + 1 < EG_COLS / 16) tmem_ld16(t0 + a * EG_J + 16u * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], r[2 * i], r[2 * i + 1], f, f);
+              for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], f, f);
             }
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) pair_arrive(tempty + 8u * a);
+          if (kb % EG_SLOT_KB == EG_SLOT_KB - 1 || kb == nkw - 1) {
+            if (lane == 0) pair_arrive(mapa_u32(base + EG_SEMPTY + 8u * slot, (uint32_t)rank));
+            ++it;
+          }
         }
         if (!ok) break;
         const int m = x.mb * 256 + h0;
@@ -928,6 +991,11 @@ moer_status expert_gemm_launch(const moer_expert_gemm_args* a, void* ws, cudaStr
   p.tokens = a->tokens;
   p.E = a->E;
   p.k = a->k;
+  if (a->order != nullptr) {
+    p.div_s = 32;
+    while ((int64_t(1) << (p.div_s - 32)) < a->k) ++p.div_s;
+    p.div_m = (uint64_t(1) << p.div_s) / (uint64_t)a->k + 1;
+  }
   p.M = fwd ? a->N : a->K;
   p.C = fwd ? a->K : a->N;
   p.J = a->N;
@@ -949,6 +1017,8 @@ moer_status expert_gemm_launch(const moer_expert_gemm_args* a, void* ws, cudaStr
     const uint64_t dims[2] = {(uint64_t)(a->op == MOER_GEMM_GRAD_INPUT ? a->N : a->K), (uint64_t)a->tokens}, str[1] = {(uint64_t)a->ld_x * eb};
     const uint32_t box[2] = {(uint32_t)ke, 1};
     if (!map_of(&p.tmx, a->x, a->dtype, 2, dims, str, box)) return MOER_ECUDA;
+    const uint32_t box32[2] = {(uint32_t)ke, 32};
+    if (a->order == nullptr && !map_of(&p.tmr, a->x, a->dtype, 2, dims, str, box32)) return MOER_ECUDA;
   }
   if (gw) {
     const uint64_t dims[3] = {(uint64_t)a->N, (uint64_t)a->rows, 1}, str[2] = {(uint64_t)a->ld_d_y * eb, (uint64_t)a->ld_d_y * eb};

@@ -96,12 +96,15 @@ __device__ __forceinline__ bool mbar_wait_cl(uint64_t* bar, uint32_t parity, uin
 
 // Tiled 2-D copy into this CTA's shared memory, completing on a barrier that
 // may sit in either CTA of the pair (caddr: its shared::cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* tm, int c0, int c1, uint32_t bar_caddr) {
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* tm, int c0, int c1, uint32_t bar_caddr) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-      "[%4];" ::"r"(smem_u32(dst)),
+      "[%4];" ::"r"(dst),
       "l"(tm), "r"(c0), "r"(c1), "r"(bar_caddr)
       : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* tm, int c0, int c1, uint32_t bar_caddr) {
+  tma_load_2d_pair(smem_u32(dst), tm, c0, c1, bar_caddr);
 }
 
 // Arrives on the barrier at this offset in both CTAs once every MMA issued so

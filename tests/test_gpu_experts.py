@@ -537,3 +537,34 @@ def test_gemm_nan_and_infinity_stay_in_their_rows(env):
                              d_y=_rand(torch, (rows, N), "bf16", 5), expert_off=torch.from_numpy(off).cuda())
     nat.moer_expert_gemm(a, ws, ws.numel())
     assert np.isfinite(_np(g)[0]).all() and np.isnan(_np(g)[1]).all() and np.isfinite(_np(g)[2]).all()
+
+
+@pytest.mark.parametrize("op,dtype", [("forward", "bf16"), ("forward", "e4m3"), ("grad_input", "bf16"), ("grad_weight", "bf16")])
+@pytest.mark.parametrize("gather", [True, False])
+def test_gemm_many_narrow_and_wide_tiles(env, op, dtype, gather):
+    """Segments of few rows among long ones, over many tiles a block and many calls: threads that have
+    nothing to bring for a tile must not lose their place in the stages (no wait expires), and every
+    call gives the same bits."""
+    torch, nat = env
+    E, N, K, k = 96, 768, 1536, 2
+    rs = np.random.RandomState(0)
+    counts = rs.choice([1, 2, 3, 9, 40, 130, 260], size=E)
+    counts[-1] += counts.sum() % k
+    off, order, _ = _lists(rs, counts, int(counts.sum()) // k, k, 1)
+    rows, T = len(order), int(counts.sum()) // k
+    n = T if gather else rows
+    dev = dict(expert_off=torch.from_numpy(off).cuda(), order=torch.from_numpy(order).cuda() if gather else None)
+    if dtype == "e4m3":
+        q = torch.randint(0, 120, (n, K), dtype=torch.uint8, generator=torch.Generator().manual_seed(1)).cuda()
+        w = torch.randint(0, 120, (E, N, K), dtype=torch.uint8, generator=torch.Generator().manual_seed(2)).cuda()
+        dev.update(x=q, w=w, x_scale=torch.full((n, K // 128), 1e-3, device="cuda"), w_scale=torch.full((E, N // 128, K // 128), 1e-3, device="cuda"))
+    else:
+        dev.update(x=_rand(torch, (n, N if op == "grad_input" else K), dtype, 1), w=_rand(torch, (E, N, K), dtype, 2), d_y=_rand(torch, (rows, N), dtype, 3))
+    out = torch.zeros({"forward": (rows, N), "grad_input": (rows, K), "grad_weight": (E, N, K)}[op], device="cuda")
+    a = nat.make_expert_gemm(op=op, E=E, N=N, K=K, k=k, dtype=dtype, out_dtype="f32", rows=rows, tokens=n, out=out, **dev)
+    ws = _ws(torch)
+    nat.moer_expert_gemm(a, ws, 256)
+    first = out.clone()
+    for _ in range(150):
+        nat.moer_expert_gemm(a, ws, 256)
+    assert nat.moer_ws_status(ws) == 0 and torch.equal(out, first) and torch.isfinite(out).all()
