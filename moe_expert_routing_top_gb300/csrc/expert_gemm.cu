@@ -24,7 +24,7 @@
 // instruction's 256 m and the weights its 256 columns, so that a thread, which reads one TMEM lane,
 // has one scale of either operand a block; with the scales along the columns their loads from
 // shared memory, 1,024 clocks a block, took twice the MMAs' time (2,626 us for 262,144 rows of
-// 2,048 x 1,536; this way XX).
+// 2,048 x 1,536; this way 1,211).
 // Every wait is bounded; on expiry the kernel records MOER_ETIMEOUT and returns.
 #include "rows.cuh"
 #include "umma.cuh"
@@ -397,7 +397,8 @@ __device__ __forceinline__ bool write_lists(const GemmParams& p, const TileTable
 
 // One thread of each of four warps brings a quarter of a stage's rows, by TMA, eight gathers of four.
 // (One warp with a gather in each lane took 72 clocks a gather and 3,408 us; the rows by cp.async,
-// with their proxy fences and two more barriers, 1,301 us; this way XX.)
+// with their proxy fences and two more barriers, 1,301 us; this way 1,291, and the weights' gradient
+// 914 instead of 1,894.)
 constexpr int EG_GATHERS = 8;
 
 template <int OP, bool FP8>
@@ -543,7 +544,9 @@ __device__ __forceinline__ uint32_t pad_mask(const GemmParams& p, const Tile& x,
 // ------------------------------------------------------------ the kernel
 // Warps: 0 loads whole tiles, 1 allocates TMEM and issues the MMAs (in the leader), 2 lists rows, 4 to 7
 // gather them, 8 to 23 drain the accumulators, each 64 columns of its TMEM lanes.  Registers go to
-// the last sixteen: the six warpgroups' shares, 48 + 48 + 4 x 96, are the block's 6 x 80.
+// the last sixteen: the six warpgroups' shares, 64 + 64 + 4 x 88 (E4M3, whose epilogue has two loads
+// from TMEM under way: 48 + 48 + 4 x 96), are the block's 6 x 80.  With the latter for all, prefill
+// takes 1,397 instead of 1,291 us; with the former for all, E4M3 1,281 instead of 1,211.
 template <int OP, bool FP8>
 __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int EB = FP8 ? 1 : 2, KE = 128 / EB;  // bytes of an element, elements of c a block
@@ -592,7 +595,8 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
   tc_fence_after();
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
       // -------------------------------------------------------- TMA: w, or d_y
       if (elect_one()) {
@@ -762,11 +766,13 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
       if (!ok && lane == 0) failed = 1;
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (elect_one() && !gather_rows<OP, FP8>(p, tt, sm, base, warp - 4, rank)) failed = 1;
   } else {
     // ---------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     const int h0 = ((warp - 8) >> 2) * EG_COLS;  // first of the warp's columns
     const uint32_t tempty = mapa_u32(base + EG_TEMPTY, 0);
     // the TMEM lane quarter that this warp may access

@@ -1,13 +1,15 @@
 // norm.cu -- moer_rms_norm and its gradient: y = s * rstd * weight with s = x + residual, rounded
 // to 16 bits and/or to e4m3 with a scale for each block of 128 columns.
 //
-// A row lies with W warps, eight columns a lane and step, and stays in registers between
-// the sum of squares and the outputs: each input is read once.  Bound by DRAM.
+// A row lies with W warps, eight columns a lane and step, at most four steps (gradient: two), and stays in registers
+// between the sum of squares and the outputs: each input is read once.  Bound by DRAM; with eight steps a
+// warp (half the warps, twice the registers) the gradient of 30,011 rows of 2,048 took 228 us, since
+// one block an SM could not cover the latency from its loads to its stores.
 #include "rows.cuh"
 
 namespace moer {
 
-constexpr int NORM_THREADS = 256;
+constexpr int NORM_MAX_THREADS = 512;  // a row of 16,384
 constexpr int NORM_STEP = 256;  // columns that a warp takes a step: 32 lanes x 8
 
 // Sum over the W warps of a row (W a power of two), in a fixed order.  Every thread of the block
@@ -27,10 +29,10 @@ __device__ __forceinline__ float row_sum(float v, int W, float* part) {
 }
 
 template <typename T, bool VEC, int NC>
-__global__ void __launch_bounds__(NORM_THREADS) rms_norm_kernel(const __grid_constant__ moer_norm_args a, int W) {
-  __shared__ float part[NORM_THREADS / 32];
+__global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_kernel(const __grid_constant__ moer_norm_args a, int W) {
+  __shared__ float part[NORM_MAX_THREADS / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * (NORM_THREADS / 32 / W) + warp / W;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / 32 / W) + warp / W;
   const bool live = row < a.T;
   const int H = live ? a.H : 0, c0 = (warp % W) * NORM_STEP + lane * 8, dc = W * NORM_STEP;
   Raw8<T> s[NC];
@@ -81,12 +83,12 @@ __global__ void __launch_bounds__(NORM_THREADS) rms_norm_kernel(const __grid_con
 // of the weight's gradient in registers; the block's groups add theirs in order into a row of
 // `partial` [gridDim.x][H].
 template <typename T, bool VEC, int NC>
-__global__ void __launch_bounds__(NORM_THREADS) rms_norm_grad_kernel(const __grid_constant__ moer_norm_args a, int W,
+__global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_grad_kernel(const __grid_constant__ moer_norm_args a, int W,
                                                                      float* __restrict__ partial) {
   extern __shared__ float dsum[];  // [H] with a weight's gradient
-  __shared__ float part[NORM_THREADS / 32];
+  __shared__ float part[NORM_MAX_THREADS / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = NORM_THREADS / 32 / W, g = warp / W;
+  const int groups = blockDim.x / 32 / W, g = warp / W;
   const int c0 = (warp % W) * NORM_STEP + lane * 8, dc = W * NORM_STEP;
   float acc[NC][8];
 #pragma unroll
@@ -104,6 +106,12 @@ __global__ void __launch_bounds__(NORM_THREADS) rms_norm_grad_kernel(const __gri
     for (int c = 0; c < NC; ++c) s[c] = load8<T, VEC>(sp + c0 + c * dc, H - c0 - c * dc);
 #pragma unroll
     for (int c = 0; c < NC; ++c) d[c] = load8_rw<T, VEC>(dp + c0 + c * dc, H - c0 - c * dc);
+    Raw8<T> e[NC];
+    if (a.d_sum != nullptr) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        e[c] = load8_rw<T, VEC>(static_cast<const T*>(a.d_sum) + row * a.ld_d_sum + c0 + c * dc, H - c0 - c * dc);
+    }
     const float rstd = live ? a.rstd[row] : 0.f;
     float dot = 0.f;
 #pragma unroll
@@ -126,9 +134,8 @@ __global__ void __launch_bounds__(NORM_THREADS) rms_norm_grad_kernel(const __gri
       for (int i = 0; i < 8; ++i)
         dx[i] = rstd * (to_f32(d[c].v[i]) * to_f32(w.v[i]) - to_f32(s[c].v[i]) * rstd * dot);
       if (a.d_sum != nullptr) {
-        const Raw8<T> e = load8_rw<T, VEC>(static_cast<const T*>(a.d_sum) + row * a.ld_d_sum + col, n);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dx[i] += to_f32(e.v[i]);
+        for (int i = 0; i < 8; ++i) dx[i] += to_f32(e[c].v[i]);
       }
       store8<T, VEC>(static_cast<T*>(a.d_x) + row * a.ld_d_x + col, pack8<T>(dx), n);
     }
@@ -146,7 +153,7 @@ __global__ void __launch_bounds__(NORM_THREADS) rms_norm_grad_kernel(const __gri
     }
     __syncthreads();
   }
-  for (int col = threadIdx.x; col < a.H; col += NORM_THREADS) partial[(size_t)blockIdx.x * a.H + col] = dsum[col];
+  for (int col = threadIdx.x; col < a.H; col += blockDim.x) partial[(size_t)blockIdx.x * a.H + col] = dsum[col];
 }
 
 // d_weight[h] = the sum over the blocks' rows, in a fixed order: a block takes 32 columns, warp w
@@ -167,12 +174,15 @@ __global__ void __launch_bounds__(256) norm_dweight_kernel(const float* __restri
 }
 
 namespace {
-// Warps a row: as few as hold it with 8 steps of 256 columns each.
-int norm_warps(int H) {
+// Steps of 256 columns a warp, and warps a row: as few as hold it.  The gradient, which also keeps its
+// part of the weight's gradient, takes two steps a warp while that leaves 16 warps a row.
+int norm_steps(int H, bool grad) { return H <= NORM_STEP ? 1 : grad && H <= 16 * 2 * NORM_STEP ? 2 : 4; }
+int norm_warps(int H, bool grad) {
   int W = 1;
-  while (W * NORM_STEP * 8 < H) W *= 2;
+  while (W * NORM_STEP * norm_steps(H, grad) < H) W *= 2;
   return W;
 }
+int norm_threads(int H, bool grad) { return norm_warps(H, grad) * 32 > 256 ? norm_warps(H, grad) * 32 : 256; }
 
 bool row_vec(const moer_norm_args* a, int eb) {
   const void* const p[] = {a->x, a->residual, a->weight, a->sum, a->y, a->d_y, a->d_sum, a->d_x};
@@ -185,9 +195,10 @@ bool row_vec(const moer_norm_args* a, int eb) {
 
 template <typename T, bool VEC, int NC>
 cudaError_t norm_run(const moer_norm_args* a, bool grad, float* partial, int blocks, cudaStream_t st) {
-  const int W = norm_warps(a->H), groups = NORM_THREADS / 32 / W;
+  const int W = norm_warps(a->H, grad), threads = norm_threads(a->H, grad), groups = threads / 32 / W;
   if (!grad) {
-    rms_norm_kernel<T, VEC, NC><<<(unsigned)((a->T + groups - 1) / groups), NORM_THREADS, 0, st>>>(*a, W);
+    if constexpr (NC == 2) return cudaErrorInvalidValue;  // the gradient's alone
+    else rms_norm_kernel<T, VEC, NC><<<(unsigned)((a->T + groups - 1) / groups), threads, 0, st>>>(*a, W);
     return cudaGetLastError();
   }
   const size_t smem = partial != nullptr ? (size_t)a->H * 4 : 0;
@@ -196,15 +207,18 @@ cudaError_t norm_run(const moer_norm_args* a, bool grad, float* partial, int blo
     const cudaError_t e = smem_optin(rms_norm_grad_kernel<T, VEC, NC>, 64 * 1024, set);
     if (e != cudaSuccess) return e;
   }
-  rms_norm_grad_kernel<T, VEC, NC><<<blocks, NORM_THREADS, smem, st>>>(*a, W, partial);
+  rms_norm_grad_kernel<T, VEC, NC><<<blocks, threads, smem, st>>>(*a, W, partial);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t norm_pick(const moer_norm_args* a, bool grad, float* partial, int blocks, cudaStream_t st) {
-  const bool vec = row_vec(a, sizeof(T)), few = a->H <= 2 * NORM_STEP;
-  if (vec) return few ? norm_run<T, true, 2>(a, grad, partial, blocks, st) : norm_run<T, true, 8>(a, grad, partial, blocks, st);
-  return few ? norm_run<T, false, 2>(a, grad, partial, blocks, st) : norm_run<T, false, 8>(a, grad, partial, blocks, st);
+  const bool vec = row_vec(a, sizeof(T));
+  switch (norm_steps(a->H, grad)) {
+    case 1: return vec ? norm_run<T, true, 1>(a, grad, partial, blocks, st) : norm_run<T, false, 1>(a, grad, partial, blocks, st);
+    case 2: return vec ? norm_run<T, true, 2>(a, grad, partial, blocks, st) : norm_run<T, false, 2>(a, grad, partial, blocks, st);
+    default: return vec ? norm_run<T, true, 4>(a, grad, partial, blocks, st) : norm_run<T, false, 4>(a, grad, partial, blocks, st);
+  }
 }
 
 cudaError_t norm_any(const moer_norm_args* a, bool grad, float* partial, int blocks, cudaStream_t st) {
@@ -213,7 +227,7 @@ cudaError_t norm_any(const moer_norm_args* a, bool grad, float* partial, int blo
   return norm_pick<__half>(a, grad, partial, blocks, st);
 }
 
-constexpr int NORM_GRAD_BLOCKS = 2 * 152;  // most blocks of the gradient, and rows of its partial sums
+constexpr int NORM_GRAD_BLOCKS = 4 * 152;  // most blocks of the gradient, and rows of its partial sums
 }  // namespace
 
 size_t rms_norm_scratch_bytes(int32_t H) { return (size_t)NORM_GRAD_BLOCKS * H * 4; }
@@ -223,7 +237,7 @@ moer_status rms_norm_launch(const moer_norm_args* a, cudaStream_t st) {
 }
 
 moer_status rms_norm_grad_launch(const moer_norm_args* a, void* scratch, cudaStream_t st) {
-  const int groups = NORM_THREADS / 32 / norm_warps(a->H);
+  const int groups = norm_threads(a->H, true) / 32 / norm_warps(a->H, true);
   const int blocks = (int)min64((a->T + groups - 1) / groups, NORM_GRAD_BLOCKS);
   float* partial = a->d_weight != nullptr ? static_cast<float*>(scratch) : nullptr;
   if (a->T > 0 && norm_any(a, true, partial, blocks, st) != cudaSuccess) return MOER_ECUDA;
