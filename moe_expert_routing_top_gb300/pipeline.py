@@ -19,6 +19,9 @@ With a scored gate (`set_gate`: softmax or sigmoid scores, a balance bias, exper
 groups, renormalised weights) the step runs on the ids of `moer_score_topk`
 instead and also gives the experts' weights and token lists (`score_step`;
 `moer_expert_order`); `score_grad` is the gate's gradient for training.
+`ExpertLayer` runs what a layer computes with those lists: the norm, the experts' products and
+activation, the combination per token and the gradients (`moer_rms_norm`, `moer_expert_gemm`,
+`moer_expert_act`, `moer_expert_combine`).
 `BatchDev.from_lengths` makes a batch's tables on the GPU from its requests'
 lengths (`moer_block_plan`).
 
@@ -144,7 +147,28 @@ class BatchDev:
                         ncached=int(len(b.cache_idx)) if with_cache else 0)
 
 
-class RoutingStats:
+class _OnStream:
+    """What owns buffers on `self.device` and launches on `self.stream`."""
+
+    def _on_stream(self):
+        """Makes the launches' stream the current one: what is allocated, filled or copied within
+        is in order with them, and its memory goes back to that stream."""
+        return torch.cuda.stream(_as_stream(self.stream, self.device)) if self._elsewhere() else _AS_IT_IS
+
+    def _elsewhere(self):
+        if self.device.type != "cuda":
+            return False
+        return nat.current_handle(self.device.index) != (self.stream if isinstance(self.stream, int) else self.stream.cuda_stream)
+
+    def _results(self, *tensors):
+        """Tensors made on the launches' stream, for a caller on the current one."""
+        if self._elsewhere():
+            for t in tensors:
+                t.record_stream(torch.cuda.current_stream(self.device))
+        return tensors
+
+
+class RoutingStats(_OnStream):
     """Holds the model/serving state of the path and runs steps over batches on `stream` (the one
     that is current when it is made, if none is given).  Inputs have to be ready on that stream,
     and a reader on another one has to wait for it."""
@@ -179,23 +203,6 @@ class RoutingStats:
         self.gate_H = 0
         self.score_opts = self.bias = None
         self._alloc(max_T, max_nblk, max_R)
-
-    def _on_stream(self):
-        """Makes the launches' stream the current one: what is allocated, filled or copied within
-        is in order with them, and its memory goes back to that stream."""
-        return torch.cuda.stream(_as_stream(self.stream, self.device)) if self._elsewhere() else _AS_IT_IS
-
-    def _elsewhere(self):
-        if self.device.type != "cuda":
-            return False
-        return nat.current_handle(self.device.index) != (self.stream if isinstance(self.stream, int) else self.stream.cuda_stream)
-
-    def _results(self, *tensors):
-        """Tensors made on the launches' stream, for a caller on the current one."""
-        if self._elsewhere():
-            for t in tensors:
-                t.record_stream(torch.cuda.current_stream(self.device))
-        return tensors
 
     def _alloc(self, T, nblk, R):
         self.cap = (T, nblk, R)
@@ -458,6 +465,220 @@ class RoutingStats:
                             centroids=wl.centroids, idf=wl.idf, loads=wl.loads0, live=wl.live,
                             G=wl.G, group_of=wl.group_of, nslots=wl.nslots, max_T=max_T,
                             max_nblk=max_nblk, max_R=max_R, device=device, stream=stream)
+
+
+def to_8bit_blocks(w):
+    """Weights [E][N][K] as e4m3 with an fp32 scale for each block of 128 x 128 (moer_expert_gemm's
+    layout), by torch operations: done once, when a model is loaded."""
+    E, N, K = w.shape
+    pad = torch.nn.functional.pad(w.float(), (0, -K % 128, 0, -N % 128))
+    b = pad.view(E, -(-N // 128), 128, -(-K // 128), 128)
+    scale = (b.abs().amax((2, 4)) / 448.0).clamp_(min=1e-30)
+    q = (b / scale[:, :, None, :, None]).view(E, pad.shape[1], pad.shape[2])[:, :N, :K]
+    return q.to(torch.float8_e4m3fn).contiguous(), scale.contiguous()
+
+
+@dataclasses.dataclass
+class ExpertPass:
+    """What a forward pass of ExpertLayer leaves for its backward pass."""
+    x: torch.Tensor
+    h: torch.Tensor
+    a: torch.Tensor
+    z: torch.Tensor
+    off: torch.Tensor
+    order: torch.Tensor
+    inv: torch.Tensor
+    weights: torch.Tensor
+
+
+class ExpertLayer(_OnStream):
+    """One layer's experts behind a router: the norm in front (`norm`, if it has a weight), the gated
+    products over the experts' token lists and their combination per token (`forward`), and the
+    gradients (`norm_grad`, `backward`).  The lists are one layer's of RoutingStats.expert_order or
+    score_step, the weights one layer's of weights_for:
+
+        off, order, inv = rs.score_step(logits, batch, align=128)
+        y, hidden, _ = layer.norm(x, hidden)
+        out, kept = layer.forward(y, off[l], order[l], inv[l], rs.weights_for(T)[l], add=hidden)
+
+    w1 [E][2 I][H] (the halves a and b of the activation one after the other) and w2 [E][H][I], both
+    bf16 or fp16; or both e4m3 with `scales` (of w1 and w2, from to_8bit_blocks), which serve only:
+    the rows then go through both products in 8 bits.  Calls run on `stream` (the current one when
+    the layer is made, if none is given); inputs have to be ready there."""
+
+    def __init__(self, w1, w2, scales=None, norm_weight=None, eps=1e-6, dtype=torch.bfloat16, stream=None):
+        self.device = w1.device
+        if w1.dim() != 3 or w2.dim() != 3 or w1.shape[1] % 2 or w2.shape != (w1.shape[0], w1.shape[2], w1.shape[1] // 2):
+            raise ValueError(f"weights of shapes {tuple(w1.shape)} and {tuple(w2.shape)}: expected [E][2 I][H] and [E][H][I]")
+        self.E, self.H, self.I = w1.shape[0], w1.shape[2], w2.shape[2]
+        self.eight = w1.dtype == torch.float8_e4m3fn
+        self.dtype = dtype if self.eight else w1.dtype
+        if not 1 <= self.H <= 16384:
+            raise ValueError(f"H {self.H}: at most 16384")
+        if w1.dtype != w2.dtype or self.dtype not in (torch.bfloat16, torch.float16) or w2.device != self.device:
+            raise ValueError("weights have to be bf16, fp16 or e4m3, both of one type, on one device")
+        if not (w1.is_contiguous() and w2.is_contiguous()):
+            raise ValueError("weights have to be contiguous")
+        unit = 16 if self.eight else 8
+        if self.H % unit or self.I % unit:
+            raise ValueError(f"H {self.H} and I {self.I} have to be multiples of {unit}: a row starts on 16 bytes")
+        if self.eight != (scales is not None):
+            raise ValueError("e4m3 weights need their scales, and no others have any")
+        if self.eight:
+            for w, s in zip((w1, w2), scales):
+                want = (self.E, -(-w.shape[1] // 128), -(-w.shape[2] // 128))
+                if tuple(s.shape) != want or s.dtype != torch.float32 or not s.is_contiguous() or s.device != self.device:
+                    raise ValueError(f"scales have to be contiguous fp32 {want} on {self.device}")
+        if norm_weight is not None and (norm_weight.shape != (self.H,) or norm_weight.dtype != self.dtype or
+                                        not norm_weight.is_contiguous() or norm_weight.device != self.device):
+            raise ValueError(f"the norm's weight has to be contiguous {self.dtype} of {self.H} on {self.device}")
+        self.w1, self.w2, self.scales, self.norm_weight, self.eps = w1, w2, scales, norm_weight, float(eps)
+        self.stream = stream if stream is not None or self.device.type != "cuda" else torch.cuda.current_stream(self.device)
+        # one workspace for every call, of a size that does not go by the batch: a captured graph keeps its address
+        with self._on_stream():
+            self.ws = torch.zeros(nat.moer_rms_norm_workspace_bytes(1, self.H), dtype=torch.uint8, device=self.device)
+        self.ws_bytes = self.ws.numel()
+
+    # ---------------------------------------------------------------- pieces
+    def _name(self):
+        return "bf16" if self.dtype == torch.bfloat16 else "f16"
+
+    def _rows(self, x, cols, what, rows=None, dtype=None):
+        dtype = dtype or self.dtype
+        if x.dim() != 2 or x.shape[1] != cols or (rows is not None and x.shape[0] != rows) or x.dtype != dtype or x.device != self.device:
+            raise ValueError(f"{what} has to be {dtype} [{'rows' if rows is None else rows}][{cols}] on {self.device}, "
+                             f"got {x.dtype} {tuple(x.shape)} on {x.device}")
+        if x.stride(1) != 1 and cols > 1:
+            raise ValueError(f"{what}: the elements of a row have to be contiguous")
+        return x
+
+    def _lists(self, off, order, inv, weights):
+        def ints(t, shape, what):
+            if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
+                raise ValueError(f"{what} has to be contiguous int32 {shape} on {self.device}")
+        ints(off, (self.E + 1,), "off")
+        if order.dim() != 1 or inv.dim() != 2:
+            raise ValueError("the lists are one layer's: off [E + 1], order [rows], inv [T][k]")
+        ints(order, tuple(order.shape), "order")
+        ints(inv, tuple(inv.shape), "inv")
+        if weights is not None and (weights.dtype != torch.float32 or weights.shape != inv.shape or not weights.is_contiguous() or
+                                    weights.device != self.device):
+            raise ValueError(f"weights have to be contiguous fp32 {tuple(inv.shape)} on {self.device}")
+
+    def _new(self, *shape, dtype=None):
+        return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
+
+    def _gemm(self, op, out, **values):
+        a = nat.make_expert_gemm(op=op, E=self.E, out=out, dtype="e4m3" if self.eight else self._name(),
+                                 out_dtype="f32" if out.dtype == torch.float32 else self._name(), **values)
+        nat.moer_expert_gemm(a, self.ws, self.ws_bytes, self.stream)
+        return out
+
+    def _combine(self, z, inv, weights, add):
+        T, k = inv.shape
+        out = self._new(T, self.H)
+        nat.moer_expert_combine(nat.make_expert_combine(T=T, H=self.H, k=k, rows=z.shape[0], dtype=self._name(), z=z, inv=inv, weights=weights,
+                                                        add=add, out=out), self.ws, self.ws_bytes, self.stream)
+        return out
+
+    # ------------------------------------------------------------------ norm
+    def norm(self, x, residual=None):
+        """(y, sum, rstd): the norm's output, the residual stream x + residual, and what norm_grad
+        needs.  With 8-bit weights y is (e4m3 rows, scales, 16-bit rows): the first two for
+        `forward`, the last for the router's gate."""
+        if self.norm_weight is None:
+            raise ValueError("the layer was made without a norm's weight")
+        self._rows(x, self.H, "x")
+        T = x.shape[0]
+        if residual is not None:
+            self._rows(residual, self.H, "residual", T)
+        with self._on_stream():
+            y, rstd = self._new(T, self.H), self._new(T, dtype=torch.float32)
+            s = x if residual is None else self._new(T, self.H)
+            q, scale = (self._new(T, self.H, dtype=torch.float8_e4m3fn), self._new(T, -(-self.H // 128), dtype=torch.float32)) if self.eight else (None, None)
+            nat.moer_rms_norm(nat.make_norm(T=T, H=self.H, dtype=self._name(), eps=self.eps, x=x, residual=residual, weight=self.norm_weight,
+                                            sum=s if residual is not None else None, y=y, q=q, scale=scale, rstd=rstd), None, 0, self.stream)
+        self._results(*(t for t in (y, s, rstd, q, scale) if t is not None))
+        return (y if not self.eight else (q, scale, y)), s, rstd
+
+    def norm_grad(self, s, rstd, d_y, d_sum=None):
+        """(d_x, d_weight): the gradient by x and the residual alike, and by the norm's weight."""
+        if self.norm_weight is None:
+            raise ValueError("the layer was made without a norm's weight")
+        T = s.shape[0]
+        for t, what in ((s, "sum"), (d_y, "d_y"), (d_sum, "d_sum")):
+            if t is not None:
+                self._rows(t, self.H, what, T)
+        if rstd.shape != (T,) or rstd.dtype != torch.float32 or not rstd.is_contiguous() or rstd.device != self.device:
+            raise ValueError(f"rstd has to be contiguous fp32 of {T} on {self.device}")
+        with self._on_stream():
+            d_x, d_w = self._new(T, self.H), self._new(self.H, dtype=torch.float32)
+            nat.moer_rms_norm_grad(nat.make_norm(T=T, H=self.H, dtype=self._name(), eps=self.eps, sum=s, weight=self.norm_weight, rstd=rstd, d_y=d_y,
+                                                 d_sum=d_sum, d_x=d_x, d_weight=d_w), self.ws, self.ws_bytes, self.stream)
+        return self._results(d_x, d_w)
+
+    # --------------------------------------------------------------- experts
+    def forward(self, x, off, order, inv, weights=None, add=None):
+        """(out, kept): the combined outputs [T][H] of rows x [T][H] (8-bit weights: of a pair of e4m3
+        rows and scales, as `norm` gives them), on top of `add` if given, and what `backward` needs
+        (None with 8-bit weights)."""
+        self._lists(off, order, inv, weights)
+        T, rows, k = inv.shape[0], order.shape[0], inv.shape[1]
+        if self.eight:
+            x, sx = x[0], x[1]
+            self._rows(x, self.H, "x", T, torch.float8_e4m3fn)
+            self._rows(sx, -(-self.H // 128), "x's scales", T, torch.float32)
+        else:
+            self._rows(x, self.H, "x", T)
+        if add is not None:
+            self._rows(add, self.H, "add", T)
+        used = off[self.E:]
+        with self._on_stream():
+            lists = dict(expert_off=off, rows=rows)
+            h = self._gemm("forward", self._new(rows, 2 * self.I), N=2 * self.I, K=self.H, k=k, tokens=T, order=order, x=x, w=self.w1, **lists,
+                           **({"x_scale": sx, "w_scale": self.scales[0]} if self.eight else {}))
+            act = dict(rows=rows, I=self.I, dtype=self._name(), h=h, used=used)
+            if self.eight:
+                a, sa = self._new(rows, self.I, dtype=torch.float8_e4m3fn), self._new(rows, -(-self.I // 128), dtype=torch.float32)
+                nat.moer_expert_act(nat.make_expert_act(q=a, scale=sa, **act), self.stream)
+                more = {"x_scale": sa, "w_scale": self.scales[1]}
+            else:
+                a, more = self._new(rows, self.I), {}
+                nat.moer_expert_act(nat.make_expert_act(y=a, **act), self.stream)
+            z = self._gemm("forward", self._new(rows, self.H), N=self.H, K=self.I, tokens=rows, x=a, w=self.w2, **lists, **more)
+            out = self._combine(z, inv, weights, add)
+        self._results(out)
+        return out, None if self.eight else ExpertPass(x, h, a, z, off, order, inv, weights)
+
+    def backward(self, kept: ExpertPass, d_out):
+        """The gradients of a forward pass, by name: x [T][H], w1 and w2 (fp32) and weights [T][k]
+        (that of `add` is d_out itself)."""
+        if self.eight:
+            raise ValueError("8-bit weights serve only")
+        off, order, inv, (T, k), rows = kept.off, kept.order, kept.inv, kept.inv.shape, kept.order.shape[0]
+        self._rows(d_out, self.H, "d_out", T)
+        with self._on_stream():
+            f32 = torch.float32
+            lists = dict(expert_off=off, rows=rows)
+            d_z, d_weights = self._new(rows, self.H), self._new(T, k, dtype=f32)
+            nat.moer_expert_combine_grad(nat.make_expert_combine(
+                T=T, H=self.H, k=k, rows=rows, dtype=self._name(), z=kept.z, inv=inv, order=order, weights=kept.weights, d_out=d_out, d_z=d_z,
+                d_weights=d_weights), self.ws, self.ws_bytes, self.stream)
+            w2 = dict(N=self.H, K=self.I, tokens=rows)
+            d_a = self._gemm("grad_input", self._new(rows, self.I), x=d_z, w=self.w2, **w2, **lists)
+            d_w2 = self._gemm("grad_weight", self._new(self.E, self.H, self.I, dtype=f32), x=kept.a, d_y=d_z, **w2, **lists)
+            d_h = self._new(rows, 2 * self.I)
+            nat.moer_expert_act_grad(nat.make_expert_act(rows=rows, I=self.I, dtype=self._name(), h=kept.h, used=off[self.E:], d_y=d_a, d_h=d_h),
+                                     self.stream)
+            w1 = dict(N=2 * self.I, K=self.H)
+            d_w1 = self._gemm("grad_weight", self._new(self.E, 2 * self.I, self.H, dtype=f32), tokens=T, k=k, order=order, x=kept.x, d_y=d_h, **w1, **lists)
+            d_rows = self._gemm("grad_input", self._new(rows, self.H), tokens=rows, x=d_h, w=self.w1, **w1, **lists)
+            d_x = self._combine(d_rows, inv, None, None)
+        self._results(d_x, d_w1, d_w2, d_weights)
+        return {"x": d_x, "w1": d_w1, "w2": d_w2, "weights": d_weights}
+
+    def status(self) -> int:
+        return nat.moer_ws_status(self.ws, self.stream)
 
 
 @dataclasses.dataclass
