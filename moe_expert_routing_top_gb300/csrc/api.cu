@@ -250,6 +250,7 @@ moer_status check_combine(const moer_expert_combine_args* a, const void* ws, siz
   if (!is_float_dtype(a->dtype)) return MOER_EINVAL;
   if (a->T < 0 || a->T > MOST_ROWS || a->rows < 0 || a->rows > MOST_ROWS) return MOER_ERANGE;
   if (a->H < 1 || a->H > 65536 || a->k < 1 || a->k > 32 || a->T * a->k > MOST_ROWS) return MOER_ERANGE;
+  if (a->T * ((a->H + 255) / 256) >= (int64_t(1) << 33)) return MOER_ERANGE;  // eight warps a block, 2^31 blocks
   if (!aligned(a->inv, 4) || !aligned(a->order, 4) || !aligned(a->weights, 4) || !aligned(a->d_weights, 4)) return MOER_EINVAL;
   if (a->T > 0 && a->inv == nullptr) return MOER_EINVAL;
   if (ws == nullptr || !aligned(ws, 16)) return MOER_EINVAL;

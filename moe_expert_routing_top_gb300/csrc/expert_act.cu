@@ -1,14 +1,15 @@
 // expert_act.cu -- moer_expert_act and its gradient: y = silu(a) * b over the experts' rows, rounded
 // to 16 bits and/or to e4m3 with a scale for each block of 128 columns.
 //
-// Sixteen lanes take a block of 128 columns, eight each; a half-warp has several blocks'
-// loads in flight.  Bound by DRAM.
+// Sixteen lanes take a block of 128 columns, eight each; a half-warp has two blocks' loads in flight.
+// Bound by DRAM: 5.9 TB/s to 8 bits, 6.7 in the gradient (four blocks an SM: 201 us, three: 213,
+// 96,006 rows of 1,408).
 #include "rows.cuh"
 
 namespace moer {
 
 constexpr int ACT_THREADS = 256;
-constexpr int ACT_UNROLL = 4;
+constexpr int ACT_UNROLL = 2;  // blocks in flight a half-warp (four: 204 us where two take 176, 270,208 rows of 768 to 8 bits)
 
 // (row, block of 128 columns) of a half-warp's next unit, `step` units on.
 struct ActUnit {
@@ -16,12 +17,12 @@ struct ActUnit {
   int blk;
 };
 
-// To 2 + 1.2 |a| steps of the exponential and two of the division (an exact division: 352 us where this
-// takes XX, 270,208 rows of 768 to 8 bits); 0 for an exponential past 2^126.
+// To 2 + 1.2 |a| steps of the exponential and two of the division (an exact division: 352 us
+// where this took 213, 270,208 rows of 768 to 8 bits); 0 for an exponential past 2^126.
 __device__ __forceinline__ float sigmoid_of(float a) { return __fdividef(1.f, 1.f + __expf(-a)); }
 
 template <typename T, bool VEC, bool GRAD>
-__global__ void __launch_bounds__(ACT_THREADS) expert_act_kernel(const __grid_constant__ moer_expert_act_args a) {
+__global__ void __launch_bounds__(ACT_THREADS, GRAD ? 4 : 1) expert_act_kernel(const __grid_constant__ moer_expert_act_args a) {
   const int lane = threadIdx.x & 31, half = threadIdx.x >> 4;
   const int nb = (a.I + 127) / 128;
   int64_t rows = a.rows;
@@ -111,7 +112,7 @@ moer_status expert_act_launch(const moer_expert_act_args* a, bool grad, cudaStre
   const int sms = device_sm_count();
   if (sms <= 0) return MOER_ECUDA;
   const int64_t blocks = (a->rows * ((a->I + 127) / 128) + ACT_THREADS / 16 - 1) / (ACT_THREADS / 16);
-  const unsigned grid = (unsigned)min64(blocks, (int64_t)sms * 8);
+  const unsigned grid = (unsigned)min64(blocks, (int64_t)sms * 16);
   const cudaError_t e = a->dtype == MOER_F32    ? act_run<float>(a, grad, grid, st)
                         : a->dtype == MOER_BF16 ? act_run<__nv_bfloat16>(a, grad, grid, st)
                                                 : act_run<__half>(a, grad, grid, st);

@@ -13,9 +13,12 @@
 //
 // Clusters of two CTAs, persistent over tiles of 256 m x up to 256 j (tcgen05.mma.cta_group::2,
 // M = 256), c in blocks of 128 bytes, six stages of 32 KB.  A CTA loads its 128 of m and half
-// of the j rows, all by TMA: rows of x by its row gather, which follows the list's entries, so no
-// permuted copy of x exists.  Where rows are contracted (GRAD_WEIGHT), those past the segment or of
-// padding are gathered from past the map's end, in both operands: zeros.
+// of the j rows, all by TMA: listed rows of x by its row gather, which follows the list's entries, so
+// no permuted copy of x exists (one made first, in the workspace: 1,432 us for 262,144 rows of
+// 2,048 x 1,536, against 1,291), rows without a list in boxes of 32.  Where rows are contracted
+// (GRAD_WEIGHT), those past the segment or of padding are gathered from past the map's end, in both
+// operands: zeros.  Bound by the operands' arrival: 1.29 PFLOP/s there, 1.40 without a list
+// (1.71 sustained by a large library product).
 // Accumulators are fp32 in TMEM, two of 256 columns, drained by sixteen warps while the MMAs go
 // on.  TMEM sums are cut, not rounded, so that their error grows with their length: after
 // 8 blocks (512 terms) a sum is added to fp32 registers (weights' gradient over 1,500 rows: relative
@@ -42,7 +45,7 @@ constexpr int EG_COLS = EG_J / (EG_EPI_WARPS / 4);  // columns that an epilogue 
 constexpr int EG_TMEM_COLS = 512;
 constexpr int EG_ROUND = 8;                  // blocks summed in TMEM (not E4M3)
 constexpr size_t EG_OFF_BAR = (size_t)EG_STAGES * EG_STAGE_BYTES;
-constexpr int EG_LISTS = 8;                            // row lists under way: of tiles (2 x 128 rows used), or of blocks of 64
+constexpr int EG_LISTS = 8;                            // row lists under way: of tiles, or (GRAD_WEIGHT) of blocks
 constexpr int EG_LIST = 128;                           // entries of a list
 constexpr size_t EG_OFF_LIST = EG_OFF_BAR + 512;       // [list][EG_LIST] ints
 constexpr int EG_SLOTS = 8, EG_SLOT_KB = 4;            // E4M3: ring of x's scales, blocks a slot

@@ -158,6 +158,8 @@ class _OnStream:
     def _elsewhere(self):
         if self.device.type != "cuda":
             return False
+        if self.device.index is not None and torch.cuda.current_device() != self.device.index:
+            return True
         return nat.current_handle(self.device.index) != (self.stream if isinstance(self.stream, int) else self.stream.cuda_stream)
 
     def _results(self, *tensors):

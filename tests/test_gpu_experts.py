@@ -568,3 +568,59 @@ def test_gemm_many_narrow_and_wide_tiles(env, op, dtype, gather, N):
     for _ in range(150):
         nat.moer_expert_gemm(a, ws, ws.numel())
     assert nat.moer_ws_status(ws) == 0 and torch.equal(out, first) and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("E,stride", [(1024, 0), (5, 8), (5, 1024)])
+def test_gemm_most_experts_and_odd_strides(env, E, stride):
+    """As many experts as there may be, most without rows, and matrices that lie any multiple of eight
+    elements apart."""
+    torch, nat = env
+    N, K = 72, 64
+    rs = np.random.RandomState(E)
+    counts = np.where(rs.rand(E) < 0.2, rs.randint(1, 40, E), 0)
+    counts[0] = 300
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rows = int(off[-1])
+    room = torch.zeros(E * (N * K + stride), dtype=torch.bfloat16, device="cuda")
+    w = room.as_strided((E, N, K), (N * K + stride, K, 1))
+    w.copy_(_rand(torch, (E, N, K), "bf16", 2))
+    x = _rand(torch, (rows, K), "bf16", 1)
+    y = torch.empty((rows, N), device="cuda")
+    a = nat.make_expert_gemm(op="forward", E=E, N=N, K=K, dtype="bf16", out_dtype="f32", rows=rows, tokens=rows, x=x, w=w, out=y,
+                             expert_off=torch.from_numpy(off).cuda())
+    ws = _ws(torch)
+    nat.moer_expert_gemm(a, ws, 256)
+    assert nat.moer_ws_status(ws) == 0
+    ref, mag = ex.gemm_rows(_np(x), _np(w), off)
+    _close(y, ref, K * 2 * U * mag + _half_step(torch, "f32", ref))
+    g = torch.empty((E, N, K), device="cuda")
+    dy = _rand(torch, (rows, N), "bf16", 3)
+    a = nat.make_expert_gemm(op="grad_weight", E=E, N=N, K=K, dtype="bf16", out_dtype="f32", rows=rows, tokens=rows, x=x, d_y=dy, out=g,
+                             expert_off=torch.from_numpy(off).cuda())
+    nat.moer_expert_gemm(a, ws, 256)
+    assert nat.moer_ws_status(ws) == 0
+    ref, mag = ex.gemm_weight_grad(_np(dy), _np(x), off)
+    _close(g, ref, 301 * 2 * U * mag + _half_step(torch, "f32", ref))
+
+
+def test_gemm_on_two_streams_at_once(env):
+    """Calls that overlap, each with its own workspace, give what each gives alone."""
+    torch, nat = env
+    counts, N, K = [300, 17, 0, 520], 520, 264
+    off, order, _, rows, x = _gemm_case(torch, counts, 1, 2, N, K, K, "bf16", True)
+    w, dy = _rand(torch, (4, N, K), "bf16", 5), _rand(torch, (rows, N), "bf16", 6)
+    lists = dict(expert_off=torch.from_numpy(off).cuda(), order=torch.from_numpy(order).cuda())
+
+    def make(op, out):
+        return nat.make_expert_gemm(op=op, E=4, N=N, K=K, k=2, dtype="bf16", out_dtype="f32", rows=rows, tokens=len(x), x=x, w=w, d_y=dy, out=out, **lists)
+    outs = [[torch.zeros((rows, N), device="cuda"), torch.zeros((4, N, K), device="cuda")] for _ in range(2)]
+    ws = [_ws(torch) for _ in range(2)]
+    for op, o in zip(("forward", "grad_weight"), outs[0]):
+        nat.moer_expert_gemm(make(op, o), ws[0], 256)
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(30):
+        for op, o, s, v in zip(("forward", "grad_weight"), outs[1], sides, ws):
+            nat.moer_expert_gemm(make(op, o), v, 256, s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(*outs)) and all(nat.moer_ws_status(v) == 0 for v in ws)
