@@ -999,7 +999,6 @@ moer_status expert_gemm_launch(const moer_expert_gemm_args* a, void* ws, cudaStr
   p.rows = a->rows;
   p.tokens = a->tokens;
   p.E = a->E;
-  p.k = a->k;
   if (a->order != nullptr) {
     p.div_s = 32;
     while ((int64_t(1) << (p.div_s - 32)) < a->k) ++p.div_s;

@@ -542,6 +542,13 @@ class ExpertLayer(_OnStream):
         self.ws_bytes = self.ws.numel()
 
     # ---------------------------------------------------------------- pieces
+    def _takes(self, *tensors):
+        """Inputs from the current stream, for launches on another: their memory stays theirs until those ran."""
+        if self._elsewhere():
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(_as_stream(self.stream, self.device))
+
     def _name(self):
         return "bf16" if self.dtype == torch.bfloat16 else "f16"
 
@@ -594,6 +601,7 @@ class ExpertLayer(_OnStream):
         T = x.shape[0]
         if residual is not None:
             self._rows(residual, self.H, "residual", T)
+        self._takes(x, residual)
         with self._on_stream():
             y, rstd = self._new(T, self.H), self._new(T, dtype=torch.float32)
             s = x if residual is None else self._new(T, self.H)
@@ -613,6 +621,7 @@ class ExpertLayer(_OnStream):
                 self._rows(t, self.H, what, T)
         if rstd.shape != (T,) or rstd.dtype != torch.float32 or not rstd.is_contiguous() or rstd.device != self.device:
             raise ValueError(f"rstd has to be contiguous fp32 of {T} on {self.device}")
+        self._takes(s, rstd, d_y, d_sum)
         with self._on_stream():
             d_x, d_w = self._new(T, self.H), self._new(self.H, dtype=torch.float32)
             nat.moer_rms_norm_grad(nat.make_norm(T=T, H=self.H, dtype=self._name(), eps=self.eps, sum=s, weight=self.norm_weight, rstd=rstd, d_y=d_y,
@@ -635,6 +644,7 @@ class ExpertLayer(_OnStream):
         if add is not None:
             self._rows(add, self.H, "add", T)
         used = off[self.E:]
+        self._takes(x, sx if self.eight else None, off, order, inv, weights, add)
         with self._on_stream():
             lists = dict(expert_off=off, rows=rows)
             h = self._gemm("forward", self._new(rows, 2 * self.I), N=2 * self.I, K=self.H, k=k, tokens=T, order=order, x=x, w=self.w1, **lists,
@@ -659,6 +669,7 @@ class ExpertLayer(_OnStream):
             raise ValueError("8-bit weights serve only")
         off, order, inv, (T, k), rows = kept.off, kept.order, kept.inv, kept.inv.shape, kept.order.shape[0]
         self._rows(d_out, self.H, "d_out", T)
+        self._takes(d_out)
         with self._on_stream():
             f32 = torch.float32
             lists = dict(expert_off=off, rows=rows)
