@@ -585,7 +585,8 @@ MOER_API moer_status moer_expert_order(const moer_dims* d, const uint8_t* topk, 
  * 8-bit rows: a row of e4m3 values (largest 448) with one fp32 scale for each
  * block of 128 neighbouring columns (the last one may be shorter); column c
  * stands for q[c] * scale[c / 128].  scale = max(largest |value| of the block,
- * 1e-30) / 448, taken from the fp32 values and not from their 16-bit roundings.  A
+ * 1e-30) / 448, taken from the fp32 values and not from their 16-bit roundings; q
+ * is the fp32 value divided by the scale, rounded to nearest (ties to even).  A
  * NaN stays NaN and does not enter the scale; an infinity makes its block's
  * scale infinite and its values NaN.
  * ------------------------------------------------------------------------ */
