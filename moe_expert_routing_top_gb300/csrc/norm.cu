@@ -208,7 +208,7 @@ cudaError_t norm_run(const moer_norm_args* a, bool grad, float* partial, int blo
     return cudaGetLastError();
   }
   const size_t smem = partial != nullptr ? (size_t)a->H * 4 : 0;
-  if (smem > 48 * 1024) {
+  if (smem + sizeof(float) * (NORM_MAX_THREADS / 32) > 48 * 1024) {  // with `part`: what a launch has by default
     static std::atomic<unsigned long long> set{0};
     const cudaError_t e = smem_optin(rms_norm_grad_kernel<T, VEC, NC>, 64 * 1024, set);
     if (e != cudaSuccess) return e;
