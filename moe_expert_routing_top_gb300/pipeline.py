@@ -482,7 +482,8 @@ def to_8bit_blocks(w):
 
 @dataclasses.dataclass
 class ExpertPass:
-    """What a forward pass of ExpertLayer leaves for its backward pass."""
+    """What a forward pass of ExpertLayer leaves for its backward pass: x and the lists as they were
+    given (they have to stay as they are until then), its own tensors, and a copy of the weights."""
     x: torch.Tensor
     h: torch.Tensor
     a: torch.Tensor
@@ -659,8 +660,10 @@ class ExpertLayer(_OnStream):
                 nat.moer_expert_act(nat.make_expert_act(y=a, **act), self.stream)
             z = self._gemm("forward", self._new(rows, self.H), N=self.H, K=self.I, tokens=rows, x=a, w=self.w2, **lists, **more)
             out = self._combine(z, inv, weights, add)
+            # its own copy of the weights: those of weights_for lie in the router's one buffer, which the next batch overwrites
+            kept = None if self.eight else ExpertPass(x, h, a, z, off, order, inv, None if weights is None else weights.clone())
         self._results(out)
-        return out, None if self.eight else ExpertPass(x, h, a, z, off, order, inv, weights)
+        return out, kept
 
     def backward(self, kept: ExpertPass, d_out):
         """The gradients of a forward pass, by name: x [T][H], w1 and w2 (fp32) and weights [T][k]
