@@ -701,8 +701,8 @@ MOER_API moer_status moer_expert_act_grad(const moer_expert_act_args* a, moer_st
 /* The experts' rows back to their tokens:
  *   out[t] = add[t] + sum_j weights[t][j] * z[inv[t][j]], j in ascending order.
  * Gradient: d_z[p] = weights[t][j] * d_out[t] for the pair t * k + j = order[p],
- * zeros in every row with order[p] < 0; d_weights[t][j] = sum over the columns
- * of d_out[t] * z[inv[t][j]]. */
+ * zeros where there is none (order[p] < 0) or the pair has no row (inv < 0);
+ * d_weights[t][j] = sum over the columns of d_out[t] * z[inv[t][j]]. */
 typedef struct moer_expert_combine_args {
   int64_t T;            /* tokens, 0 .. 2^31 - 1                                        */
   int32_t H;            /* columns, 1 .. 65536                                          */
@@ -722,8 +722,9 @@ typedef struct moer_expert_combine_args {
 } moer_expert_combine_args;
 
 /* A row past `rows` counts as none and records MOER_EDATA in ws; so does, in
- * the gradient, a pair whose row's order entry names another pair (its
- * d_z is then not written).
+ * the gradient, an order entry past the pairs.  It records it too where order and
+ * inv name different rows for a pair: d_z is then not written in a row whose
+ * entry's pair has another one.
  * ws  at least 256 bytes, 16-byte aligned (the status word). */
 MOER_API moer_status moer_expert_combine(const moer_expert_combine_args* a, void* ws, size_t ws_bytes,
                                          moer_stream_t stream);

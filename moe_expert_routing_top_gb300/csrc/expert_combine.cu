@@ -2,8 +2,8 @@
 // per token.
 //
 // Forward: a warp takes 256 columns of a token and has its k rows' loads in flight at once.
-// Gradient: a warp takes a token, so that the k dot products stay in its lanes; rows that
-// are padding are zeroed by further blocks of the same launch.  Bound by DRAM: 6.3 TB/s forward
+// Gradient: a warp takes a token, so that the k dot products stay in its lanes; rows that no pair
+// takes (padding, dropped pairs) are zeroed by further blocks of the same launch.  Bound by DRAM: 6.3 TB/s forward
 // (32,768 tokens of 8 rows of 2,048 bf16: 213 us with four blocks an SM, 244 with fewer), 5.1 in the gradient.
 #include "rows.cuh"
 
@@ -70,10 +70,22 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(COMB_THREADS) combine_grad_kernel(const __grid_constant__ moer_expert_combine_args a,
                                                                     unsigned token_blocks, uint32_t* status) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x >= token_blocks) {  // padding rows: a warp finds 32 rows' entries at once
-    const int64_t nw = (int64_t)(gridDim.x - token_blocks) * COMB_WARPS;
+  if (blockIdx.x >= token_blocks) {  // rows that no pair takes: a warp looks at 32 rows' entries at once
+    const int64_t nw = (int64_t)(gridDim.x - token_blocks) * COMB_WARPS, pairs = a.T * a.k;
+    bool bad = false;
     for (int64_t p0 = ((int64_t)(blockIdx.x - token_blocks) * COMB_WARPS + warp) * 32; p0 < a.rows; p0 += nw * 32) {
-      unsigned pad = __ballot_sync(FULL, p0 + lane < a.rows && a.order[p0 + lane] < 0);
+      bool none = false;
+      if (p0 + lane < a.rows) {
+        const int o = a.order[p0 + lane];
+        none = o < 0 || o >= pairs;
+        bad |= o >= pairs;
+        if (!none) {
+          const int r = a.inv[o];
+          none = r < 0 || r >= a.rows;  // (the latter is said by its token's warp)
+          bad |= !none && r != p0 + lane;
+        }
+      }
+      unsigned pad = __ballot_sync(FULL, none);
       for (; pad != 0; pad &= pad - 1) {
         T* o = static_cast<T*>(a.d_z) + (p0 + __ffs(pad) - 1) * a.ld_d_z;
         Raw8<T> zero;
@@ -82,6 +94,7 @@ __global__ void __launch_bounds__(COMB_THREADS) combine_grad_kernel(const __grid
         for (int col = lane * 8; col < a.H; col += COMB_STEP) store8<T, VEC>(o + col, zero, a.H - col);
       }
     }
+    if (bad) atomicOr(status, WS_BIT_EDATA);
     return;
   }
   const int64_t t = (int64_t)blockIdx.x * COMB_WARPS + warp;
@@ -167,7 +180,7 @@ cudaError_t comb_run(const moer_expert_combine_args* a, bool grad, uint32_t* sta
     else combine_kernel<T, false><<<grid, COMB_THREADS, 0, st>>>(*a, nc, status);
   } else {
     const unsigned tb = (unsigned)((a->T + COMB_WARPS - 1) / COMB_WARPS);
-    const unsigned pb = a->d_z != nullptr ? (unsigned)min64((a->rows + 32 * COMB_WARPS - 1) / (32 * COMB_WARPS), sms) : 0;
+    const unsigned pb = a->d_z != nullptr ? (unsigned)min64((a->rows + 32 * COMB_WARPS - 1) / (32 * COMB_WARPS), 8 * sms) : 0;
     if (tb + pb == 0) return cudaSuccess;
     if (vec) combine_grad_kernel<T, true><<<tb + pb, COMB_THREADS, 0, st>>>(*a, tb, status);
     else combine_grad_kernel<T, false><<<tb + pb, COMB_THREADS, 0, st>>>(*a, tb, status);

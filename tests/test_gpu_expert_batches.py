@@ -1,7 +1,7 @@
 """ExpertLayer with more than one batch, stream or graph under way."""
 import pytest
 
-from tests.test_gpu_expert_layer import E, H, _layer, _router
+from tests.test_gpu_expert_layer import E, H, I, _layer, _lists, _router, k
 from tests.test_gpu_experts import _rand
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +35,28 @@ def test_two_batches_under_way(env):
     got = layer.backward(first, d)
     assert layer.status() == 0 and rs.status() == 0
     assert all(torch.equal(got[n], want[n]) for n in want) and not torch.equal(other["w1"], want["w1"])
+
+
+def test_backward_of_dropped_pairs(env):
+    """Pairs without a row, by the lists' inverse, have the gradients of pairs of weight 0, whatever lay in
+    the memory that the pass takes."""
+    torch, nat, pipeline = env
+    T = 150
+    off, order, inv, weights = _lists(torch, nat, pipeline, T, 16)
+    layer = _layer(torch, pipeline, "bf16")
+    x, d = _rand(torch, (T, H), "bf16", 1), _rand(torch, (T, H), "bf16", 2)
+    drop = torch.rand((T, k), generator=torch.Generator().manual_seed(3)).cuda() < 0.25
+    out, kept = layer.forward(x, off, order, inv, torch.where(drop, 0.0, weights))
+    want = layer.backward(kept, d)
+    out2, kept2 = layer.forward(x, off, order, torch.where(drop, -1, inv), weights)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    n = order.shape[0]
+    stale = [torch.full(s, float("nan"), dtype=torch.bfloat16, device="cuda") for s in ((n, H), (n, I), (n, 2 * I), (n, H)) for _ in range(2)]
+    torch.cuda.synchronize()
+    del stale
+    got = layer.backward(kept2, d)
+    assert layer.status() == 0 and torch.equal(out, out2)
+    for name in ("x", "w1", "w2"):
+        assert torch.equal(got[name], want[name]), name
+    assert (got["weights"][drop] == 0).all() and torch.equal(got["weights"][~drop], want["weights"][~drop])

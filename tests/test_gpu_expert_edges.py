@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 
 from oracle import experts as ex
-from tests.test_gpu_experts import U, _close, _half_step, _np, _rand, _ws
+from tests.test_gpu_experts import U, _close, _half_step, _lists, _np, _rand, _ws
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -46,3 +46,64 @@ def test_norm_gradient_next_to_48_KB(env, dtype):
     code = f"from tests.test_gpu_expert_edges import norm_grad_of\nfor H in (12272, 12273, 12280, 12281, 12288, 12289, 12296): norm_grad_of(H, {dtype!r})"
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ combination
+@pytest.mark.parametrize("T,k,H,align", [(1, 1, 8, 4), (33, 6, 264, 16), (17, 9, 3, 1), (8, 32, 72, 1), (300, 4, 96, 128), (2000, 8, 40, 16)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_combine_grad_of_dropped_pairs(env, T, k, H, align, dtype):
+    """A pair without a row adds nothing: the row that the lists still hold for it gets zeros, like
+    one that is padding."""
+    torch, nat = env
+    rs = np.random.RandomState(T)
+    off, order, inv = _lists(rs, np.bincount(rs.randint(0, 7, T * k), minlength=7), T, k, align)
+    order = np.concatenate([order, np.full(3, -1, np.int32)])
+    rows = len(order)
+    inv.reshape(-1)[rs.rand(T * k) < 0.3] = -1
+    inv[0, 0] = -5
+    z, w, do = _rand(torch, (rows, H), dtype, 1), torch.rand((T, k), generator=torch.Generator().manual_seed(2)).cuda(), _rand(torch, (T, H), dtype, 3)
+    dz, dw, ws = torch.full((rows, H), float("nan"), dtype=z.dtype, device="cuda"), torch.full((T, k), float("nan"), device="cuda"), _ws(torch)
+    nat.moer_expert_combine_grad(nat.make_expert_combine(T=T, H=H, k=k, rows=rows, dtype=dtype, inv=torch.from_numpy(inv).cuda(), weights=w, z=z, d_out=do,
+                                                         order=torch.from_numpy(order).cuda(), d_z=dz, d_weights=dw), ws, 256)
+    assert nat.moer_ws_status(ws) == 0
+    rz, rw, mw = ex.combine_grad(_np(z), inv, _np(w), _np(do), rows)
+    _close(dz, rz, U * np.abs(rz) + _half_step(torch, dtype, rz), "d_z")
+    _close(dw, rw, (H + 2) * 2 * U * mw, "d_weights")
+    assert (dz[torch.from_numpy(rz == 0).cuda().all(1)] == 0).all()
+
+
+def test_combine_grad_of_entries_that_name_no_pair(env):
+    """An entry past the pairs is padding and is said; one whose pair has another row is said too, and its
+    row is left."""
+    torch, nat = env
+    T, k, H, rows = 4, 2, 16, 12
+    do, ws = _rand(torch, (T, H), "f32", 2), _ws(torch)
+    order = np.concatenate([np.arange(8), [-1, -7, -1, -1]]).astype(np.int32)
+    inv = torch.arange(8, dtype=torch.int32, device="cuda").view(T, k)
+
+    def grad(order, inv, T=T):
+        dz = torch.full((rows, H), 5.0, device="cuda")
+        nat.moer_expert_combine_grad(nat.make_expert_combine(T=T, H=H, k=k, rows=rows, dtype="f32", inv=inv, order=torch.from_numpy(order).cuda(),
+                                                             d_out=do[:T], d_z=dz), ws, 256)
+        return dz, nat.moer_ws_status(ws)
+    want, status = grad(order, inv)
+    assert status == 0 and torch.equal(want[:8], do.repeat_interleave(k, 0)) and (want[8:] == 0).all()
+    for bad in (8, 9, 2 ** 31 - 1):
+        o = order.copy()
+        o[[8, 11]] = bad
+        dz, status = grad(o, inv)
+        assert status == 6 and torch.equal(dz, want)
+    o = order.copy()
+    o[9] = 3                                        # whose row is 3
+    dz, status = grad(o, inv)
+    assert status == 6 and (dz[9] == 5).all()
+    dz[9] = 0
+    assert torch.equal(dz, want)
+    past = inv.clone()
+    past[1, 1] = rows                               # counts as none, and row 3 gets nothing
+    dz, status = grad(order, past)
+    assert status == 6 and (dz[3] == 0).all()
+    dz, status = grad(order, None, 0)               # without tokens every entry is past the pairs
+    assert status == 6 and (dz == 0).all()
+    dz, status = grad(np.full(rows, -1, np.int32), None, 0)
+    assert status == 0 and (dz == 0).all()
