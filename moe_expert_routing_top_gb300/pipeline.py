@@ -537,6 +537,10 @@ class ExpertLayer(_OnStream):
             raise ValueError(f"the norm's weight has to be contiguous {self.dtype} of {self.H} on {self.device}")
         self.w1, self.w2, self.scales, self.norm_weight, self.eps = w1, w2, scales, norm_weight, float(eps)
         self.stream = stream if stream is not None or self.device.type != "cuda" else torch.cuda.current_stream(self.device)
+        if self.device.type == "cuda":  # a layer may go, with its weights, while its last launches read them
+            for t in (w1, w2, *(scales or ()), norm_weight):
+                if t is not None:
+                    t.record_stream(_as_stream(self.stream, self.device))
         # one workspace for every call, of a size that does not go by the batch: a captured graph keeps its address
         with self._on_stream():
             self.ws = torch.zeros(nat.moer_rms_norm_workspace_bytes(1, self.H), dtype=torch.uint8, device=self.device)

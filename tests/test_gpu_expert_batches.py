@@ -60,3 +60,40 @@ def test_backward_of_dropped_pairs(env):
     for name in ("x", "w1", "w2"):
         assert torch.equal(got[name], want[name]), name
     assert (got["weights"][drop] == 0).all() and torch.equal(got["weights"][~drop], want["weights"][~drop])
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_weights_dropped_while_launches_wait(env, eight):
+    """A layer on a stream of its own may go, and its weights with it, as soon as its calls are made: the
+    memory is not given out again before they ran."""
+    torch, nat, pipeline = env
+    T, h8, i8 = 300, 256, 144
+    off, order, inv, weights = _lists(torch, nat, pipeline, T, 16)
+    x = _rand(torch, (T, h8), "bf16", 1)
+
+    def layer(stream=None):
+        w1, w2 = _rand(torch, (E, 2 * i8, h8), "bf16", 11, h8 ** -0.5), _rand(torch, (E, h8, i8), "bf16", 12, i8 ** -0.5)
+        more = {}
+        if eight:
+            (w1, s1), (w2, s2) = pipeline.to_8bit_blocks(w1), pipeline.to_8bit_blocks(w2)
+            more = {"scales": (s1, s2)}
+        return pipeline.ExpertLayer(w1, w2, norm_weight=_rand(torch, (h8,), "bf16", 13), stream=stream, **more)
+
+    def run(layer):
+        y = layer.norm(x)[0]
+        return layer.forward(y[:2] if eight else y, off, order, inv, weights)[0]
+    want = run(layer())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    other = layer(side)
+    run(other)
+    shapes = [(t.shape, t.dtype) for t in (other.w1, other.w2, other.norm_weight, *(other.scales or ()))]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(500_000_000)                # a quarter of a second: the launches wait behind it
+    out = run(other)
+    assert not side.query()
+    del other
+    junk = [torch.full(s, 3.0, dtype=torch.float32, device="cuda").to(t) for s, t in shapes for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and len(junk) == 4 * len(shapes)
