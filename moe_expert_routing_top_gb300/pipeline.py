@@ -541,9 +541,10 @@ class ExpertLayer(_OnStream):
             for t in (w1, w2, *(scales or ()), norm_weight):
                 if t is not None:
                     t.record_stream(_as_stream(self.stream, self.device))
-        # one workspace for every call, of a size that does not go by the batch: a captured graph keeps its address
+        # the calls' status word; what a call writes besides (norm_grad's partial sums) is its own, since graphs captured
+        # of one layer may run at the same time
         with self._on_stream():
-            self.ws = torch.zeros(nat.moer_rms_norm_workspace_bytes(1, self.H), dtype=torch.uint8, device=self.device)
+            self.ws = torch.zeros(nat.moer_expert_gemm_workspace_bytes(nat.make_expert_gemm()), dtype=torch.uint8, device=self.device)
         self.ws_bytes = self.ws.numel()
 
     # ---------------------------------------------------------------- pieces
@@ -629,8 +630,9 @@ class ExpertLayer(_OnStream):
         self._takes(s, rstd, d_y, d_sum)
         with self._on_stream():
             d_x, d_w = self._new(T, self.H), self._new(self.H, dtype=torch.float32)
+            ws = self._new(nat.moer_rms_norm_workspace_bytes(T, self.H), dtype=torch.uint8)
             nat.moer_rms_norm_grad(nat.make_norm(T=T, H=self.H, dtype=self._name(), eps=self.eps, sum=s, weight=self.norm_weight, rstd=rstd, d_y=d_y,
-                                                 d_sum=d_sum, d_x=d_x, d_weight=d_w), self.ws, self.ws_bytes, self.stream)
+                                                 d_sum=d_sum, d_x=d_x, d_weight=d_w), ws, ws.numel(), self.stream)
         return self._results(d_x, d_w)
 
     # --------------------------------------------------------------- experts

@@ -27,3 +27,16 @@ def test_a_pass_keeps_its_own_weights(calls):
     layer.backward(kept, torch.zeros((T, H), dtype=BF))
     assert calls[0][0] == "moer_expert_combine_grad" and calls[0][1].weights == kept.weights.data_ptr()
     assert layer.forward(torch.zeros((T, H), dtype=BF), off, order, inv)[1].weights is None
+
+
+def test_partial_sums_are_the_calls_own(calls):
+    """Two gradients of a norm share no workspace, be they captured or not."""
+    layer = _layer()
+    s, rstd, dy = torch.zeros((T, H), dtype=BF), torch.zeros(T), torch.zeros((T, H), dtype=BF)
+    for _ in range(2):
+        layer.norm_grad(s, rstd, dy)
+    (_, _, first, n, _), (_, _, second, m, _) = calls
+    need = nat.moer_rms_norm_workspace_bytes(T, H)
+    assert n == m == first.numel() == second.numel() == need
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel()) for t in (first, second, layer.ws))
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))

@@ -97,3 +97,54 @@ def test_weights_dropped_while_launches_wait(env, eight):
     junk = [torch.full(s, 3.0, dtype=torch.float32, device="cuda").to(t) for s, t in shapes for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(out, want) and len(junk) == 4 * len(shapes)
+
+
+def test_captured_norm_gradients_at_the_same_time(env):
+    """Two graphs of one layer's norm and its gradient, on other inputs, replayed on two streams at once."""
+    torch, nat, pipeline = env
+    T, side = 3001, torch.cuda.Stream()
+    layer = _layer(torch, pipeline, "bf16", stream=side)
+    x, d = ([_rand(torch, (T, H), "bf16", s + i) for i in range(2)] for s in (1, 3))
+    torch.cuda.synchronize()
+
+    def step(i):
+        y, s, rstd = layer.norm(x[i], d[i])
+        return (y, s, *layer.norm_grad(s, rstd, d[i], x[i]))
+    want, graphs = [], []
+    for i in range(2):
+        out = step(i)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in out])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = step(i)
+        graphs.append((graph, out))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(100):
+        for (graph, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, out), w in zip(graphs, want):
+        assert all(torch.equal(a, b) for a, b in zip(out, w))
+    assert layer.status() == 0
+
+
+def test_norm_on_another_stream(env):
+    torch, nat, pipeline = env
+    T = 300
+    x, r, d = (_rand(torch, (T, H), "bf16", i) for i in range(3))
+    layer, side = _layer(torch, pipeline, "bf16"), torch.cuda.Stream()
+    y, s, rstd = layer.norm(x, r)
+    want = [y, s, rstd, *layer.norm_grad(s, rstd, d, r)]
+    torch.cuda.synchronize()
+    other = _layer(torch, pipeline, "bf16", stream=side)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        side.wait_stream(torch.cuda.current_stream())
+        y, s, rstd = other.norm(x.clone(), r.clone())
+        side.wait_stream(torch.cuda.current_stream())
+        got = [y, s, rstd, *other.norm_grad(s, rstd, d, r)]
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
