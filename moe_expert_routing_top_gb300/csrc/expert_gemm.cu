@@ -721,7 +721,6 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
           }
           umma_commit_pair(base + EG_DRAIN);
         }
-        if (!one_wait(base + EG_DRAIN, 0, p.status)) ok = false;
         if (!ok) failed = 1;
       }
     } else if (warp == 2) {
@@ -874,7 +873,14 @@ __global__ void __launch_bounds__(EG_THREADS, 1) expert_gemm_kernel(const __grid
     if (!ok && lane == 0) failed = 1;
   }
   __syncthreads();
-  if (failed) {
+  // The last MMAs, once this CTA has drained its accumulators, when they are done or nearly so: the other CTA's
+  // thread that waited for them from its start on gave up in calls of more than two seconds.
+  bool late = failed;
+  if (warp == 1) {
+    if (lane == 0 && !one_wait(base + EG_DRAIN, 0, p.status)) late = true;
+    __syncwarp();
+  }
+  if (late) {
     // a wait expired: give copies still in flight into this CTA time to land
     const unsigned long long t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 200000ull) {

@@ -107,3 +107,33 @@ def test_combine_grad_of_entries_that_name_no_pair(env):
     assert status == 6 and (dz == 0).all()
     dz, status = grad(np.full(rows, -1, np.int32), None, 0)
     assert status == 0 and (dz == 0).all()
+
+
+# ------------------------------------------------------------------ long calls
+def test_a_product_of_more_than_two_seconds(env):
+    """Waits are bounded to two seconds without progress, not calls: a weights' gradient over 120 million rows
+    (d_y's elements pass 2^31) takes longer.  Whole numbers, few of them not zero, so that every sum is exact;
+    NaN in rows of padding."""
+    torch, nat = env
+    N, K, rows, k = 24, 65536, 120_000_000, 1 << 20
+    T = -(-rows // k)
+    g = torch.Generator().manual_seed(0)
+    x = torch.randint(-8, 9, (T, K), generator=g).bfloat16().cuda()
+    at = torch.randperm(rows, generator=g, dtype=torch.int32)[:1024].long()
+    at[:4] = torch.tensor([0, rows - 1, rows - 2, 64])
+    at = torch.unique(at)
+    pad, at = at[1::3], torch.cat([at[::3], at[2::3]])
+    dy = torch.zeros((rows, N), dtype=torch.bfloat16, device="cuda")
+    order = torch.arange(rows, dtype=torch.int32, device="cuda")
+    some = torch.randint(-4, 5, (len(at), N), generator=g).bfloat16()
+    dy[at.cuda()] = some.cuda()
+    dy[pad.cuda()] = float("nan")
+    order[pad.cuda()] = -1
+    out, ws = torch.empty((1, N, K), device="cuda"), _ws(torch)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    a = nat.make_expert_gemm(op="grad_weight", E=1, N=N, K=K, k=k, dtype="bf16", out_dtype="f32", rows=rows, tokens=T, x=x, d_y=dy, out=out, expert_off=off,
+                             order=order)
+    nat.moer_expert_gemm(a, ws, 256)
+    assert nat.moer_ws_status(ws) == 0
+    want = some.double().T @ x.cpu().double()[at // k]
+    assert torch.equal(out[0].cpu().double(), want)
