@@ -904,20 +904,27 @@ template <typename T>
 __global__ void __launch_bounds__(256) expert_gemm_zero_kernel(T* out, int64_t ld, int64_t stride, int cols, int64_t rows, const int32_t* off,
                                                                int E, const int32_t* order, int64_t list_rows, uint32_t* status) {
   const int lane = threadIdx.x & 31;
-  int64_t most = 0, end = rows;
+  int64_t first = 0, most = 0;  // of the segments' rows; the offsets' running maximum, as in the tile table
   bool bad = false;
-  for (int e = lane; e <= E; e += 32) {
-    const int64_t v = max64(0, min64(off[e], list_rows));
-    bad |= v != off[e];
-    most = max64(most, v);
+  for (int e0 = 0; e0 <= E; e0 += 32) {
+    const int64_t raw = off[min(e0 + lane, E)];
+    int64_t v = max64(0, min64(raw, list_rows));
+    if (e0 == 0) first = __shfl_sync(FULL, v, 0);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t u = __shfl_up_sync(FULL, v, d);
+      if (lane >= d) v = max64(v, u);
+    }
+    v = max64(v, most);
+    bad |= v != raw;
+    most = __shfl_sync(FULL, v, 31);
   }
-  for (int d = 16; d >= 1; d >>= 1) most = max64(most, __shfl_xor_sync(FULL, most, d));
   const int64_t step = (int64_t)gridDim.x * 8;
   const int64_t r0 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (stride == 0) end = most;  // list rows
-  for (int64_t r = r0; r < most; r += step) bad |= order != nullptr && order[r] >= 0;
+  for (int64_t r = first + r0; r < most; r += step) bad |= order != nullptr && order[r] >= 0;
   if (bad) atomicOr(status, WS_BIT_EDATA);
-  for (int64_t r = r0; r < end; r += step) {
+  const int64_t from = stride == 0 ? first : 0, end = stride == 0 ? most : rows;  // list rows, or the gradient's
+  for (int64_t r = from + r0; r < end; r += step) {
     T* o = stride == 0 ? out + r * ld : out + r / (rows / E) * stride + r % (rows / E) * ld;
     for (int c = lane; c < cols; c += 32) o[c] = from_f32<T>(0.f);
   }

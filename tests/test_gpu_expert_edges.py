@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 
 from oracle import experts as ex
-from tests.test_gpu_experts import U, _close, _half_step, _lists, _np, _rand, _ws
+from tests.test_gpu_experts import U, _close, _half_step, _lists, _np, _rand, _types, _ws
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -107,6 +107,35 @@ def test_combine_grad_of_entries_that_name_no_pair(env):
     assert status == 6 and (dz == 0).all()
     dz, status = grad(np.full(rows, -1, np.int32), None, 0)
     assert status == 0 and (dz == 0).all()
+
+
+# ------------------------------------------------------------------ products without tokens
+@pytest.mark.parametrize("op,dtype", [("forward", "bf16"), ("forward", "e4m3"), ("grad_input", "f16"), ("grad_weight", "bf16")])
+@pytest.mark.parametrize("off,low,high,entry,status", [
+    ([0, 16, 16, 40], 0, 40, -1, 0), ([8, 16, 24, 40], 8, 40, -1, 0), ([8, 8, 8, 8], 8, 8, -1, 0), ([8, 24, 16, 40], 8, 40, -1, 6),
+    ([-4, 16, 16, 40], 0, 40, -1, 6), ([8, 16, 24, 99], 8, 50, -1, 6), ([8, 16, 24, 40], 8, 40, 0, 6)])
+def test_products_without_tokens(env, op, dtype, off, low, high, entry, status):
+    """Lists of padding alone: zeros in the rows of segments, those before the first and behind the last
+    one left; offsets that fall or leave the rows are said, and so is an entry that names a token."""
+    torch, nat = env
+    E, N, K, rows = 3, 48, 32, 50
+    order = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    order[10] = entry
+    if low == 8 and high < 50:
+        order[[0, 7, 49]] = 5                       # of no segment
+    xc, dt = N if op == "grad_input" else K, torch.uint8 if dtype == "e4m3" else _types(torch)[dtype]
+    shape = {"forward": (rows, N), "grad_input": (rows, K), "grad_weight": (E, N, K)}[op]
+    out, ws = torch.full(shape, 7.0, device="cuda"), _ws(torch)
+    more = dict(x_scale=torch.zeros((0, 1), device="cuda"), w_scale=torch.ones((E, 1, 1), device="cuda")) if dtype == "e4m3" else {}
+    a = nat.make_expert_gemm(op=op, E=E, N=N, K=K, k=2, dtype=dtype, out_dtype="f32", rows=rows, tokens=0, x=torch.zeros((0, xc), dtype=dt, device="cuda"),
+                             w=torch.zeros((E, N, K), dtype=dt, device="cuda"), d_y=torch.ones((rows, N), dtype=dt, device="cuda"), out=out,
+                             expert_off=torch.tensor(off, dtype=torch.int32, device="cuda"), order=order, **more)
+    nat.moer_expert_gemm(a, ws, 256)
+    assert nat.moer_ws_status(ws) == status
+    if op == "grad_weight":
+        assert (out == 0).all()
+    else:
+        assert (out[low:high] == 0).all() and (out[:low] == 7).all() and (out[high:] == 7).all()
 
 
 # ------------------------------------------------------------------ long calls
