@@ -2,14 +2,14 @@
 // to 16 bits and/or to e4m3 with a scale for each block of 128 columns.
 //
 // Sixteen lanes take a block of 128 columns, eight each; a half-warp has two blocks' loads in flight.
-// Bound by DRAM: 5.9 TB/s to 8 bits, 6.7 in the gradient (four blocks an SM: 201 us, three: 213,
-// 96,006 rows of 1,408).
+// Bound by DRAM: 5.8 TB/s to 8 bits, 6.7 in the gradient (four blocks an SM: 201 us, three: 213,
+// 96,006 rows of 1,408); rows of fp32 6.6 and 6.5 (246 and 414 us, the same rows).
 #include "rows.cuh"
 
 namespace moer {
 
 constexpr int ACT_THREADS = 256;
-constexpr int ACT_UNROLL = 2;  // blocks in flight a half-warp (four: 204 us where two take 176, 270,208 rows of 768 to 8 bits)
+constexpr int ACT_UNROLL = 2;  // blocks in flight a half-warp (four: 204 us where two took 176, 270,208 rows of 768 to 8 bits)
 
 // (row, block of 128 columns) of a half-warp's next unit, `step` units on.
 struct ActUnit {
@@ -17,9 +17,15 @@ struct ActUnit {
   int blk;
 };
 
-// To 2 + 1.2 |a| steps of the exponential and two of the division (an exact division: 352 us
-// where this took 213, 270,208 rows of 768 to 8 bits); 0 for an exponential past 2^126.
-__device__ __forceinline__ float sigmoid_of(float a) { return __fdividef(1.f, 1.f + __expf(-a)); }
+// Rows of fp32: the exponential to a step, then a rounded sum and division.  Rows of 16 bits: to 2 + 1.2 |a| steps
+// of the exponential and two of the division, at |a| = 20 a 500th of the output's rounding in bf16 and
+// a 70th in fp16; 0 for an exponential past 2^126, from a = -87.3 on.  (An exact division for them: 352 us where this
+// took 213, 270,208 rows of 768 to 8 bits.)
+template <typename T>
+__device__ __forceinline__ float sigmoid_of(float a) {
+  if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-a));
+  else return __fdividef(1.f, 1.f + __expf(-a));
+}
 
 template <typename T, bool VEC, bool GRAD>
 __global__ void __launch_bounds__(ACT_THREADS, GRAD ? 4 : 1) expert_act_kernel(const __grid_constant__ moer_expert_act_args a) {
@@ -62,7 +68,7 @@ __global__ void __launch_bounds__(ACT_THREADS, GRAD ? 4 : 1) expert_act_kernel(c
         float da[8], db[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float x = to_f32(va[i].v[j]), d = to_f32(vd[i].v[j]), s = sigmoid_of(x);
+          const float x = to_f32(va[i].v[j]), d = to_f32(vd[i].v[j]), s = sigmoid_of<T>(x);
           da[j] = d * to_f32(vb[i].v[j]) * s * (1.f + x * (1.f - s));
           db[j] = d * x * s;
         }
@@ -74,7 +80,7 @@ __global__ void __launch_bounds__(ACT_THREADS, GRAD ? 4 : 1) expert_act_kernel(c
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float x = to_f32(va[i].v[j]);
-          y[j] = x * sigmoid_of(x) * to_f32(vb[i].v[j]);
+          y[j] = x * sigmoid_of<T>(x) * to_f32(vb[i].v[j]);
         }
         if (a.y != nullptr) store8<T, VEC>(static_cast<T*>(a.y) + rw[i] * a.ld_y + col[i], pack8<T>(y), n);
         if (a.q != nullptr)

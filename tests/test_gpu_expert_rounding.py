@@ -107,3 +107,38 @@ def test_codes_of_the_largest_scales(env):
     nat.moer_rms_norm(nat.make_norm(T=1, H=384, dtype="f32", eps=0.0, x=x, weight=w.cuda(), y=y, q=q, scale=sc))
     assert torch.equal(y.cpu()[0], w) and w.isfinite().all()
     _same_codes(torch, y, q, sc)
+
+
+def _arguments(torch):
+    a = torch.cat([torch.linspace(-80, 80, 40001), torch.linspace(-2, 2, 8007)])
+    return a.view(-1, 8).float().cuda()
+
+
+def test_act_in_fp32(env):
+    """Rows of fp32: the exponential (one step, 2 U), the sum, the division and two products, U each, are 6 U of
+    the value; 8 U for terms of second order."""
+    torch, nat = env
+    a = _arguments(torch)
+    b = _rand(torch, a.shape, "f32", 3)
+    h, y = torch.cat([a, b], 1), torch.empty_like(a)
+    nat.moer_expert_act(nat.make_expert_act(rows=len(a), I=8, dtype="f32", h=h, y=y))
+    ref = ex.silu_gate(_np(h))
+    bad = ~(np.abs(_np(y) - ref) <= 8 * U * np.abs(ref))
+    assert not bad.any(), f"{bad.sum()} off, by {(np.abs(_np(y) - ref)[bad] / np.abs(ref)[bad]).max() / U} U"
+
+
+def test_act_grad_in_fp32(env):
+    """s is off by 4 U of itself, 1 - s by 4 U s + U, a (1 - s) by (4 s + 2) U |a|, 1 + a (1 - s) by that and U (1 + |a|),
+    the products d b s and that by 4 U + 3 U: 14 U of d b s (1 + 2 |a|) holds them; d a s has 4 U + 2 U of itself."""
+    torch, nat = env
+    a = _arguments(torch)
+    b, d = _rand(torch, a.shape, "f32", 3), _rand(torch, a.shape, "f32", 4)
+    h = torch.cat([a, b], 1)
+    dh = torch.empty_like(h)
+    nat.moer_expert_act_grad(nat.make_expert_act(rows=len(a), I=8, dtype="f32", h=h, d_y=d, d_h=dh))
+    ref = ex.silu_gate_grad(_np(h), _np(d))
+    av, bv, dv = _np(a), _np(b), _np(d)
+    s = ex.sigmoid(av)
+    mag = np.concatenate([np.abs(dv * bv) * s * (1 + 2 * np.abs(av)) * 14, np.abs(dv * av) * s * 8], 1)
+    bad = ~(np.abs(_np(dh) - ref) <= U * mag)
+    assert not bad.any(), f"{bad.sum()} off, by {(np.abs(_np(dh) - ref)[bad] / (U * mag[bad])).max()} of the bound"
