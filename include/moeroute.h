@@ -580,7 +580,7 @@ MOER_API moer_status moer_expert_order(const moer_dims* d, const uint8_t* topk, 
  * "or NULL" are optional; ld_* are elements between neighbouring rows).  Rows
  * that a call does not name are left as they were.  Sums are held in fp32 and
  * rounded once, to the type of the output.  A buffer may be given twice only
- * where its comment says so.
+ * where its comment says so (other rows of the same address: MOER_ESHAPE).
  *
  * 8-bit rows: a row of e4m3 values (largest 448) with one fp32 scale for each
  * block of 128 neighbouring columns (the last one may be shorter); column c
@@ -611,13 +611,14 @@ typedef struct moer_norm_args {
   const void* weight;   /* [H]                                                         */
   void* sum;            /* [T][H]: forward out or NULL (may be x or residual, with the
                            same rows); gradient in                                     */
-  void* y;              /* [T][H] out or NULL (may be x)                   forward     */
+  void* y;              /* [T][H] out or NULL (may be x, with the same rows) forward   */
   void* q;              /* [T][H] e4m3 out or NULL                         forward     */
   float* scale;         /* [T][blocks] out, with q                         forward     */
   float* rstd;          /* [T]: forward out or NULL; gradient in                       */
   const void* d_y;      /* [T][H] of dtype                                 gradient    */
   const void* d_sum;    /* [T][H] of dtype or NULL: the gradient by sum    gradient    */
-  void* d_x;            /* [T][H] of dtype out (may be d_y or d_sum)       gradient    */
+  void* d_x;            /* [T][H] of dtype out (may be d_y or d_sum, with the same
+                           rows)                                           gradient    */
   float* d_weight;      /* [H] out or NULL                                 gradient    */
 } moer_norm_args;
 

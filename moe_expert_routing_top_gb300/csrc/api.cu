@@ -226,6 +226,9 @@ moer_status check_matrices(std::initializer_list<Matrix> list) {
   return MOER_OK;
 }
 
+// Whether a call in place would write a row over others that it has yet to read: one buffer, rows that lie otherwise.
+bool other_rows(const Matrix& out, const Matrix& in) { return out.p != nullptr && out.p == in.p && out.rows > 1 && out.ld != in.ld; }
+
 bool is_float_dtype(int dtype) { return dtype == MOER_F32 || dtype == MOER_BF16 || dtype == MOER_F16; }
 constexpr int64_t MOST_ROWS = (int64_t(1) << 31) - 1;
 int64_t blocks128(int64_t n) { return (n + 127) / 128; }
@@ -838,6 +841,8 @@ moer_status moer_rms_norm(const moer_norm_args* a, void* ws, size_t ws_bytes, mo
       sc{a->scale, a->T, blocks128(a->H), a->ld_scale, 4, 4, a->q != nullptr}, rs{a->rstd, a->T, 1, 1, 4, 4, false};
   s = check_matrices({x, r, w, sum, y, q, sc, rs});
   if (s != MOER_OK) return s;
+  if (other_rows(sum, x) || other_rows(sum, r) || other_rows(y, x)) return MOER_ESHAPE;
+  if (a->sum != nullptr && a->sum == a->y) return MOER_EINVAL;
   s = check_extents({{x.p, extent_of(x)}, {r.p, extent_of(r)}, {w.p, extent_of(w)}, {sum.p, extent_of(sum)}, {y.p, extent_of(y)},
                      {q.p, extent_of(q)}, {q.p != nullptr ? sc.p : nullptr, extent_of(sc)}, {rs.p, extent_of(rs)}});
   if (s != MOER_OK) return s;
@@ -857,6 +862,7 @@ moer_status moer_rms_norm_grad(const moer_norm_args* a, void* ws, size_t ws_byte
   if (any) s = check_matrices({sum, w, rs, dy, ds, dx, dw});
   else s = check_matrices({dw});
   if (s != MOER_OK) return s;
+  if (any && (other_rows(dx, dy) || other_rows(dx, ds))) return MOER_ESHAPE;
   if (ws == nullptr || !aligned(ws, 16)) return MOER_EINVAL;
   if (ws_bytes < moer_rms_norm_workspace_bytes(a->T, a->H)) return MOER_ENOMEM;
   s = any ? check_extents({{sum.p, extent_of(sum)}, {w.p, extent_of(w)}, {rs.p, extent_of(rs)}, {dy.p, extent_of(dy)},
@@ -943,6 +949,7 @@ moer_status moer_expert_act_grad(const moer_expert_act_args* a, moer_stream_t st
       dh{a->d_h, a->rows, 2 * (int64_t)a->I, a->ld_d_h, eb, al, true};
   s = check_matrices({h, dy, dh});
   if (s != MOER_OK) return s;
+  if (other_rows(dh, h)) return MOER_ESHAPE;
   s = check_extents({{h.p, extent_of(h)}, {dy.p, extent_of(dy)}, {dh.p, extent_of(dh)}, {a->used, 4}});
   if (s != MOER_OK) return s;
   return moer::expert_act_launch(a, true, reinterpret_cast<cudaStream_t>(stream));
@@ -958,6 +965,7 @@ moer_status moer_expert_combine(const moer_expert_combine_args* a, void* ws, siz
       out{a->out, a->T, a->H, a->ld_out, eb, al, true};
   s = check_matrices({z, add, out});
   if (s != MOER_OK) return s;
+  if (other_rows(out, add)) return MOER_ESHAPE;
   s = check_extents({{z.p, extent_of(z)}, {add.p, extent_of(add)}, {out.p, extent_of(out)}, {a->inv, pairs * 4}, {a->weights, pairs * 4}, {ws, ws_bytes}});
   if (s != MOER_OK) return s;
   return moer::expert_combine_launch(a, false, ws, reinterpret_cast<cudaStream_t>(stream));
