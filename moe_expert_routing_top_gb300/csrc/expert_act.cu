@@ -11,12 +11,6 @@ namespace moer {
 constexpr int ACT_THREADS = 256;
 constexpr int ACT_UNROLL = 2;  // blocks in flight a half-warp (four: 204 us where two took 176, 270,208 rows of 768 to 8 bits)
 
-// (row, block of 128 columns) of a half-warp's next unit, `step` units on.
-struct ActUnit {
-  int64_t row;
-  int blk;
-};
-
 // Rows of fp32: the exponential to a step, then a rounded sum and division.  Rows of 16 bits: to 2 + 1.2 |a| steps
 // of the exponential and two of the division, at |a| = 20 a 500th of the output's rounding in bf16 and
 // a 70th in fp16; 0 for an exponential past 2^126, from a = -87.3 on.  (An exact division for them: 352 us where this

@@ -17,8 +17,8 @@
 // no permuted copy of x exists (one made first, in the workspace: 1,432 us for 262,144 rows of
 // 2,048 x 1,536, against 1,291), rows without a list in boxes of 32.  Where rows are contracted
 // (GRAD_WEIGHT), those past the segment or of padding are gathered from past the map's end, in both
-// operands: zeros.  Bound by the operands' arrival: 1.29 PFLOP/s there, 1.40 without a list
-// (1.71 sustained by a large library product).
+// operands: zeros.  Bound by the operands' arrival: 1.26 to 1.32 PFLOP/s there, 1.37 to 1.46 without a list
+// (1.74 sustained by a large library product).
 // Accumulators are fp32 in TMEM, two of 256 columns, drained by sixteen warps while the MMAs go
 // on.  TMEM sums are cut, not rounded, so that their error grows with their length: after
 // 8 blocks (512 terms) a sum is added to fp32 registers (weights' gradient over 1,500 rows: relative

@@ -3,8 +3,8 @@
 //
 // A row lies with W warps, eight columns a lane and step, at most four steps (gradient: two), and stays
 // in registers between the sum of squares and the outputs: each input is read once.  Bound by DRAM:
-// 65,536 rows of 2,048 bf16 with a residual to 16 and 8 bits in 179 us, 6.8 TB/s (eight steps a warp: 248).
-// The gradient of 30,011 rows takes 129 us (3.8 TB/s) and is bound by the latency from a row's loads to
+// 65,536 rows of 2,048 bf16 with a residual to 16 and 8 bits in 180 us, 6.7 TB/s (eight steps a warp: 248).
+// The gradient of 30,011 rows takes 128 us (3.9 TB/s) and is bound by the latency from a row's loads to
 // its stores; four steps a warp 144, eight 228, since fewer blocks then fit an SM.
 #include "rows.cuh"
 
@@ -233,7 +233,7 @@ cudaError_t norm_any(const moer_norm_args* a, bool grad, float* partial, int blo
   return norm_pick<__half>(a, grad, partial, blocks, st);
 }
 
-constexpr int NORM_GRAD_BLOCKS = 2 * 152;  // most blocks of the gradient (what fits at once), and rows of its partial sums
+constexpr int NORM_GRAD_BLOCKS = 2 * 152;  // most blocks of the gradient (two an SM, what fits at 128 registers), and rows of its partial sums
 }  // namespace
 
 size_t rms_norm_scratch_bytes(int32_t H) { return (size_t)NORM_GRAD_BLOCKS * H * 4; }

@@ -507,7 +507,8 @@ class ExpertLayer(_OnStream):
     w1 [E][2 I][H] (the halves a and b of the activation one after the other) and w2 [E][H][I], both
     bf16 or fp16; or both e4m3 with `scales` (of w1 and w2, from to_8bit_blocks), which serve only:
     the rows then go through both products in 8 bits.  Calls run on `stream` (the current one when
-    the layer is made, if none is given); inputs have to be ready there."""
+    the layer is made, if none is given); inputs have to be ready there, and a reader on another one
+    has to wait for it."""
 
     def __init__(self, w1, w2, scales=None, norm_weight=None, eps=1e-6, dtype=torch.bfloat16, stream=None):
         self.device = w1.device
@@ -667,7 +668,7 @@ class ExpertLayer(_OnStream):
             z = self._gemm("forward", self._new(rows, self.H), N=self.H, K=self.I, tokens=rows, x=a, w=self.w2, **lists, **more)
             out = self._combine(z, inv, weights, add)
             # its own copy of the weights: those of weights_for lie in the router's one buffer, which the next batch overwrites
-            kept = None if self.eight else ExpertPass(x, h, a, z, off, order, inv, None if weights is None else weights.clone())
+            kept = None if self.eight else ExpertPass(x, h, a, z, off, order, inv, None if weights is None else weights.detach().clone())
         self._results(out)
         return out, kept
 
