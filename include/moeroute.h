@@ -682,7 +682,7 @@ MOER_API moer_status moer_expert_gemm(const moer_expert_gemm_args* a, void* ws, 
  *   y = a / (1 + exp(-a)) * b, rounded to dtype and/or as 8-bit rows.
  * Gradient: d_h = [d_y * b * s * (1 + a * (1 - s)) | d_y * a * s], s = 1 / (1 + exp(-a)).
  * With fp32 rows s is off by 2^-22 of itself at most; with 16-bit rows by
- * (4 + 1.2 |a|) * 2^-23, and it is 0 from a = -87.3 on. */
+ * (5 + 1.2 |a|) * 2^-23, and it is 0 from a = -87.3 on. */
 typedef struct moer_expert_act_args {
   int64_t rows;         /* 0 .. 2^31 - 1                                                */
   int32_t I;            /* 1 .. 65536                                                   */
